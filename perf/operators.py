@@ -366,7 +366,7 @@ def _own_route(state):
                                      h["d_logits"], h["status"]))
         return h["d_logits"]
     B.check(B.moe_route_groups(h["desc"], h["groups"], None, None, state["logits"], state["k"],
-                               None, h["idx"], h["w"], h["load"], h["status"], None))
+                               None, h["idx"], h["w"], None, h["load"], h["status"], None))
     return {"idx": h["idx"], "w": h["w"], "load": h["load"]}
 
 
