@@ -33,7 +33,9 @@ EXPORTS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_gate_up", "moe
            "moe_cg_workspace_size", "moe_pack_proxy_rows", "moe_route_cg",
            "moe_layer_forward_cg", "moe_fold_decode", "moe_layer_forward_fold",
            "moe_cost_lookup", "moe_tier_schedule", "moe_layer_forward_paths",
-           "moe_layer_forward_host")
+           "moe_layer_forward_host", "moe_route_groups", "moe_route_backward",
+           "moe_layer_forward_groups", "moe_block_norm", "moe_block_norm_backward",
+           "moe_block_norm_workspace_size", "moe_lora_project", "moe_lora_workspace_size")
 
 
 class MoeLayerDesc(ctypes.Structure):
@@ -65,6 +67,28 @@ class MoeCostTable(ctypes.Structure):
     _fields_ = [("n_count", ctypes.c_int32), ("n_points", ctypes.c_void_p),
                 ("k_count", ctypes.c_int32), ("k_points", ctypes.c_void_p),
                 ("t_us", ctypes.c_void_p)]
+
+
+class MoeGroupRoute(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("select_bias", ctypes.c_void_p)]
+
+
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("residual_type", ctypes.c_int),
+                ("act_type", ctypes.c_int), ("gate_kind", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("w_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("ld_branch", ctypes.c_int64), ("ld_gate", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("ld_normed", ctypes.c_int64),
+                ("dev_status", ctypes.c_void_p)]
+
+
+class MoeLoraDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("n_adapters", ctypes.c_int32), ("r_max", ctypes.c_int32),
+                ("swiglu", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -118,6 +142,19 @@ def lib() -> ctypes.CDLL:
                                                    vp, vp, vp, ctypes.c_int32]),
             "moe_layer_forward_paths": (ctypes.c_int, [D, vp, vp, vp, i32p, i32p, vp, i32p, vp,
                                                        i32p, vp, vp]),
+            "moe_route_groups": (ctypes.c_int, [D, ctypes.POINTER(MoeGroupRoute), vp, vp, vp,
+                                                i32p, vp, i32p, vp, i32p, i32p, i32p, vp, vp]),
+            "moe_route_backward": (ctypes.c_int, [D, vp, i32p, vp, vp, i32p, vp]),
+            "moe_layer_forward_groups": (ctypes.c_int, [D, ctypes.POINTER(MoeGroupRoute), vp, vp,
+                                                        vp, vp, i32p, i32p, vp, i32p, vp, vp]),
+            "moe_block_norm": (ctypes.c_int, [ctypes.POINTER(MoeNormDesc), vp, vp, vp, vp, vp,
+                                              vp]),
+            "moe_block_norm_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(MoeNormDesc)]),
+            "moe_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(MoeNormDesc), vp, vp, vp,
+                                                       vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "moe_lora_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(MoeLoraDesc)]),
+            "moe_lora_project": (ctypes.c_int, [ctypes.POINTER(MoeLoraDesc), vp, vp, vp, vp, vp,
+                                                vp, i32p, vp, i32p, vp, vp]),
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         }
         for name, (res, args) in sig.items():
@@ -416,6 +453,126 @@ def moe_layer_forward_paths(desc, x, w_gate_up, w_down, src_idx, tgt_idx, beta, 
                                          _ptr(src_idx), _ptr(tgt_idx), _ptr(beta),
                                          _ptr(n_paths), _ptr(out), _ptr(dev_status),
                                          _ptr(workspace), _stream(stream))
+
+
+@dataclass
+class GroupRoute:
+    """Python mirror of moe_group_route (groups of units and the balance bias)."""
+    n_groups: int = 1
+    groups_kept: int = 1
+    group_best: int = 1
+    select_bias: Optional[torch.Tensor] = None   # fp32 [E_r]
+
+    def c(self) -> MoeGroupRoute:
+        return MoeGroupRoute(int(self.n_groups), int(self.groups_kept), int(self.group_best),
+                             _ptr(self.select_bias))
+
+
+def _c(desc):
+    """The ctypes form of a descriptor, which a caller may have built itself
+    once (desc.c()) to skip the conversion on every call."""
+    return desc if isinstance(desc, ctypes.Structure) else desc.c()
+
+
+def moe_route_groups(desc, groups, x, router_w, logits_in, k_per_token, logits_out, topk_idx,
+                     topk_w, k_out, load, dev_status, workspace, stream=None) -> int:
+    return lib().moe_route_groups(_c(desc), _c(groups), _ptr(x), _ptr(router_w), _ptr(logits_in),
+                                  _ptr(k_per_token), _ptr(logits_out), _ptr(topk_idx),
+                                  _ptr(topk_w), _ptr(k_out), _ptr(load), _ptr(dev_status),
+                                  _ptr(workspace), _stream(stream))
+
+
+def moe_route_backward(desc, logits, topk_idx, d_topk_w, d_logits, dev_status,
+                       stream=None) -> int:
+    return lib().moe_route_backward(_c(desc), _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w),
+                                    _ptr(d_logits), _ptr(dev_status), _stream(stream))
+
+
+def moe_layer_forward_groups(desc, groups, x, router_w, w_gate_up, w_down, k_per_token, load, out,
+                             dev_status, workspace, stream=None) -> int:
+    return lib().moe_layer_forward_groups(_c(desc), _c(groups), _ptr(x), _ptr(router_w),
+                                          _ptr(w_gate_up), _ptr(w_down), _ptr(k_per_token),
+                                          _ptr(load), _ptr(out), _ptr(dev_status),
+                                          _ptr(workspace), _stream(stream))
+
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+_GATE = {"none": 0, "channel": 1, "token": 2, "full": 3}
+
+
+@dataclass
+class BlockNormDesc:
+    """Python mirror of moe_norm_desc; the weights are kept alive by reference."""
+    T: int
+    H: int
+    residual_dtype: torch.dtype = torch.bfloat16
+    act_dtype: torch.dtype = torch.bfloat16
+    gate: str = "none"                       # "none" | "channel" | "token" | "full"
+    eps: float = 1e-6
+    weight_offset: float = 0.0
+    residual_scale: float = 1.0
+    branch_scale: float = 1.0
+    w_post: Optional[torch.Tensor] = None
+    w_pre: Optional[torch.Tensor] = None
+    ld_residual: int = 0
+    ld_branch: int = 0
+    ld_gate: int = 0
+    ld_out: int = 0
+    ld_normed: int = 0
+    dev_status: Optional[torch.Tensor] = None
+
+    def c(self) -> MoeNormDesc:
+        return MoeNormDesc(int(self.T), int(self.H), _DTYPE[self.residual_dtype],
+                           _DTYPE[self.act_dtype], _GATE[self.gate], float(self.eps),
+                           float(self.weight_offset), float(self.residual_scale),
+                           float(self.branch_scale), _ptr(self.w_post), _ptr(self.w_pre),
+                           int(self.ld_residual), int(self.ld_branch), int(self.ld_gate),
+                           int(self.ld_out), int(self.ld_normed), _ptr(self.dev_status))
+
+
+def moe_block_norm(desc, residual, branch, gate, residual_out, normed_out, stream=None) -> int:
+    return lib().moe_block_norm(_c(desc), _ptr(residual), _ptr(branch), _ptr(gate),
+                                _ptr(residual_out), _ptr(normed_out), _stream(stream))
+
+
+def moe_block_norm_workspace_size(desc) -> int:
+    return int(lib().moe_block_norm_workspace_size(_c(desc)))
+
+
+def moe_block_norm_backward(desc, residual, branch, gate, d_residual_out, d_normed, d_residual,
+                            d_branch, d_gate, d_w_post, d_w_pre, workspace, stream=None) -> int:
+    return lib().moe_block_norm_backward(_c(desc), _ptr(residual), _ptr(branch), _ptr(gate),
+                                         _ptr(d_residual_out), _ptr(d_normed), _ptr(d_residual),
+                                         _ptr(d_branch), _ptr(d_gate), _ptr(d_w_post),
+                                         _ptr(d_w_pre), _ptr(workspace), _stream(stream))
+
+
+@dataclass
+class LoraDesc:
+    """Python mirror of moe_lora_desc."""
+    T: int
+    K: int
+    N: int
+    n_adapters: int
+    r_max: int
+    swiglu: bool = False
+    ldx: int = 0
+    ldy: int = 0
+
+    def c(self) -> MoeLoraDesc:
+        return MoeLoraDesc(int(self.T), int(self.K), int(self.N), int(self.n_adapters),
+                           int(self.r_max), int(bool(self.swiglu)), int(self.ldx), int(self.ldy))
+
+
+def moe_lora_workspace_size(desc) -> int:
+    return int(lib().moe_lora_workspace_size(_c(desc)))
+
+
+def moe_lora_project(desc, x, w, lora_a, lora_b, ranks, scales, adapter_idx, y, dev_status,
+                     workspace, stream=None) -> int:
+    return lib().moe_lora_project(_c(desc), _ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b),
+                                  _ptr(ranks), _ptr(scales), _ptr(adapter_idx), _ptr(y),
+                                  _ptr(dev_status), _ptr(workspace), _stream(stream))
 
 
 def moe_get_device_status(dev_status, stream=None) -> int:

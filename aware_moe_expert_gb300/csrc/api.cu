@@ -739,6 +739,155 @@ moe_status do_route_cg(const moe_layer_desc* d, const moe_cg_router* cg, const v
                                            topk_idx, topk_w, status, s));
 }
 
+// ---------------------------------------------------------------- group-limited routing
+
+moe_status validate_groups(const moe_layer_desc* d, const moe_group_route* g) {
+  MOE_TRY(validate(d));
+  if (g == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  const int E_r = E_r_of(d);
+  if (g->n_groups < 1 || g->groups_kept < 1 || g->groups_kept > g->n_groups ||
+      (g->group_best != 1 && g->group_best != 2))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (E_r % g->n_groups != 0 || d->k_max > g->groups_kept * (E_r / g->n_groups))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (g->select_bias != nullptr) MOE_TRY(check_ptrs4({g->select_bias}));
+  return MOE_OK;
+}
+
+// Logits like do_route (tensor-core GEMM, else slices on the CUDA cores), then
+// the group selection, which adds partial sums and the expert bias itself.
+moe_status do_route_groups(const moe_layer_desc* d, const moe_group_route* g, const void* x,
+                           const void* router_w, const float* logits_in, const int32_t* kpt,
+                           float* logits_out, int32_t* topk_idx, float* topk_w, int32_t* k_out,
+                           int32_t* load, int32_t* status, void* ws, cudaStream_t s) {
+  const int E_r = E_r_of(d);
+  moe::GroupRouteArgs a{};
+  a.partial = logits_in;
+  a.S = 1;
+  a.n_sub = d->n_sub;
+  a.logits_out = logits_in != nullptr ? logits_out : nullptr;
+  if (logits_in == nullptr) {
+    const Layout l = layout_of(*d);
+    float* part = at<float>(ws, l.router_partial);
+    if (router_on_tensor_cores(*d)) {
+      int bn = 0, splits = 1;
+      moe::router_gemm_shape(d->T, d->H, E_r, &bn, &splits);
+      if (splits > 1) {
+        MOE_TRY(do_logits_gemm(d, x, router_w, part, status, s, splits, bn));
+        a.partial = part;
+        a.S = splits;
+        a.bias = d->expert_bias;
+        a.logits_out = logits_out;
+      } else {
+        float* dst = logits_out != nullptr ? logits_out : at<float>(ws, l.logits);
+        MOE_TRY(do_logits_gemm(d, x, router_w, dst, status, s, 1, bn));
+        a.partial = dst;
+      }
+    } else {
+      MOE_TRY(cuda_status(
+          moe::launch_router_logits_small(x, router_w, d->T, d->H, E_r, part, s)));
+      a.partial = part;
+      a.S = l.router_slices;
+      a.bias = d->expert_bias;
+      a.logits_out = logits_out;
+    }
+  }
+  a.k_per_token = kpt;
+  a.T = d->T;
+  a.E_r = E_r;
+  a.k_max = d->k_max;
+  a.score = d->score;
+  a.renorm = d->renorm;
+  a.route_scale = d->route_scale;
+  a.n_groups = g->n_groups;
+  a.groups_kept = g->groups_kept;
+  a.group_best = g->group_best;
+  a.select_bias = g->select_bias;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.k_out = k_out;
+  a.load = load;
+  a.status = status;
+  a.sm_count = sm_count();
+  return cuda_status(moe::launch_group_route(a, s));
+}
+
+// ---------------------------------------------------------------- block norms
+
+moe_status validate_norm(const moe_norm_desc* d) {
+  if (d == nullptr || d->T < 0 || d->H < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->residual_type != MOE_BF16 && d->residual_type != MOE_F32) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->act_type != MOE_BF16 && d->act_type != MOE_F32) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->gate_kind < MOE_GATE_NONE || d->gate_kind > MOE_GATE_FULL) return MOE_ERR_INVALID_ARGUMENT;
+  if (!(d->eps >= 0.f)) return MOE_ERR_INVALID_ARGUMENT;
+  for (int64_t ld : {d->ld_residual, d->ld_branch, d->ld_gate, d->ld_out, d->ld_normed})
+    if (ld != 0 && ld < d->H) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->H > moe::kNormMaxH || d->T > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (d->act_type == MOE_F32 && d->residual_type == MOE_BF16) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+// Pointers of one element type: given where `need` says so, aligned to it.
+moe_status check_norm_ptr(const void* p, bool need, moe_dtype t) {
+  if (p == nullptr) return need ? MOE_ERR_INVALID_ARGUMENT : MOE_OK;
+  const uintptr_t m = t == MOE_F32 ? 3u : 1u;
+  return (reinterpret_cast<uintptr_t>(p) & m) != 0 ? MOE_ERR_INVALID_ARGUMENT : MOE_OK;
+}
+
+moe_status norm_args(const moe_norm_desc* d, const void* residual, const void* branch,
+                     const void* gate, bool back, moe::BlockNormArgs* a) {
+  MOE_TRY(validate_norm(d));
+  if (!moe::block_norm_fits(d->H, d->residual_type == MOE_F32, d->act_type == MOE_F32,
+                            d->gate_kind == MOE_GATE_FULL, back))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  const bool some = d->T > 0;
+  MOE_TRY(check_norm_ptr(residual, some, d->residual_type));
+  MOE_TRY(check_norm_ptr(branch, some && (d->w_post != nullptr || d->gate_kind != MOE_GATE_NONE),
+                         d->act_type));
+  MOE_TRY(check_norm_ptr(gate, some && d->gate_kind != MOE_GATE_NONE, d->act_type));
+  if (gate != nullptr && d->gate_kind == MOE_GATE_NONE) return MOE_ERR_INVALID_ARGUMENT;
+  MOE_TRY(check_norm_ptr(d->w_post, false, d->act_type));
+  MOE_TRY(check_norm_ptr(d->w_pre, false, d->act_type));
+  auto ld = [d](int64_t v) { return static_cast<long long>(v != 0 ? v : d->H); };
+  a->T = d->T;
+  a->H = d->H;
+  a->residual_f32 = d->residual_type == MOE_F32;
+  a->act_f32 = d->act_type == MOE_F32;
+  a->gate_kind = d->gate_kind;
+  a->eps = d->eps;
+  a->weight_offset = d->weight_offset;
+  a->residual_scale = d->residual_scale;
+  a->branch_scale = d->branch_scale;
+  a->residual = residual;
+  a->branch = branch;
+  a->gate = gate;
+  a->w_post = d->w_post;
+  a->w_pre = d->w_pre;
+  a->ld_residual = ld(d->ld_residual);
+  a->ld_branch = ld(d->ld_branch);
+  a->ld_gate = ld(d->ld_gate);
+  a->ld_out = ld(d->ld_out);
+  a->ld_h = ld(d->ld_normed);
+  a->status = d->dev_status;
+  a->sm_count = sm_count();
+  return MOE_OK;
+}
+
+// ---------------------------------------------------------------- adapters
+
+moe_status validate_lora(const moe_lora_desc* d) {
+  if (d == nullptr || d->T < 0 || d->K < 1 || d->N < 1 || d->n_adapters < 0 || d->r_max < 1)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (d->ldx != 0 && d->ldx < d->K) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->ldy != 0 && d->ldy < (d->swiglu ? d->N / 2 : d->N)) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->K % 8 != 0 || d->ldx % 8 != 0 || d->r_max % 8 != 0 || d->r_max > 128)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (d->swiglu && d->N % 2 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (d->T > (1 << 24) || d->K > (1 << 20) || d->N > (1 << 20) || d->n_adapters > (1 << 16))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
 }  // namespace
 
 namespace moe {
@@ -1034,6 +1183,188 @@ moe_status moe_layer_forward_paths(const moe_layer_desc* desc, const void* x,
   MOE_TRY(check_ws(workspace));
   return do_layer_paths(desc, x, w_gate_up, w_down, src_idx, tgt_idx, beta, n_paths, out,
                         dev_status, workspace, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_route_groups(const moe_layer_desc* desc, const moe_group_route* groups,
+                            const void* x, const void* router_w, const float* logits_in,
+                            const int32_t* k_per_token, float* logits_out, int32_t* topk_idx,
+                            float* topk_w, int32_t* k_out, int32_t* load, int32_t* dev_status,
+                            void* workspace, void* stream) {
+  MOE_TRY(validate_groups(desc, groups));
+  if (load != nullptr) MOE_TRY(check_ptrs4({load}));
+  if (desc->T > 0) {
+    MOE_TRY(check_ptrs4({k_per_token, topk_idx, topk_w, dev_status}));
+    if (k_out != nullptr) MOE_TRY(check_ptrs4({k_out}));
+    if (logits_in != nullptr) {
+      MOE_TRY(check_ptrs4({logits_in}));
+      if (logits_out != nullptr) MOE_TRY(check_ptrs4({logits_out}));
+    } else {
+      MOE_TRY(check_ptrs({x, router_w}));
+      if (logits_out != nullptr) MOE_TRY(check_ptrs({logits_out}));
+      MOE_TRY(check_ws(workspace));
+    }
+  } else {
+    if (load == nullptr) return MOE_OK;
+    return cuda_status(cudaMemsetAsync(load, 0, sizeof(int32_t) * E_r_of(desc),
+                                       static_cast<cudaStream_t>(stream)));
+  }
+  return do_route_groups(desc, groups, x, router_w, logits_in, k_per_token, logits_out, topk_idx,
+                         topk_w, k_out, load, dev_status, workspace,
+                         static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_route_backward(const moe_layer_desc* desc, const float* logits,
+                              const int32_t* topk_idx, const float* d_topk_w, float* d_logits,
+                              int32_t* dev_status, void* stream) {
+  MOE_TRY(validate(desc));
+  if (desc->T == 0) return MOE_OK;
+  MOE_TRY(check_ptrs4({logits, topk_idx, d_topk_w, d_logits, dev_status}));
+  moe::RouteBackwardArgs a{};
+  a.logits = logits;
+  a.topk_idx = topk_idx;
+  a.d_topk_w = d_topk_w;
+  a.d_logits = d_logits;
+  a.T = desc->T;
+  a.E_r = E_r_of(desc);
+  a.k_max = desc->k_max;
+  a.score = desc->score;
+  a.renorm = desc->renorm;
+  a.route_scale = desc->route_scale;
+  a.status = dev_status;
+  a.sm_count = sm_count();
+  return cuda_status(moe::launch_route_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_layer_forward_groups(const moe_layer_desc* desc, const moe_group_route* groups,
+                                    const void* x, const void* router_w, const void* w_gate_up,
+                                    const void* w_down, const int32_t* k_per_token, int32_t* load,
+                                    void* out, int32_t* dev_status, void* workspace,
+                                    void* stream) {
+  MOE_TRY(validate_groups(desc, groups));
+  if (load != nullptr) MOE_TRY(check_ptrs4({load}));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (desc->T == 0)
+    return load == nullptr
+               ? MOE_OK
+               : cuda_status(cudaMemsetAsync(load, 0, sizeof(int32_t) * E_r_of(desc), s));
+  MOE_TRY(check_ptrs({x, router_w, w_gate_up, w_down, out}));
+  MOE_TRY(check_ptrs4({k_per_token, dev_status}));
+  MOE_TRY(check_ws(workspace));
+  const Layout l = layout_of(*desc);
+  int32_t* topk_idx = at<int32_t>(workspace, l.topk_idx);
+  float* topk_w = at<float>(workspace, l.topk_w);
+  int32_t* k_left = at<int32_t>(workspace, l.fold_k);   // budgets, as of a folded layer
+  int32_t* counts = at<int32_t>(workspace, l.counts);
+  int32_t* offsets = at<int32_t>(workspace, l.offsets);
+  int32_t* sorted_token = at<int32_t>(workspace, l.sorted_token);
+  int32_t* inv_row = at<int32_t>(workspace, l.inv_row);
+  void* yperm = at<void>(workspace, l.yperm);
+  void* ysh = desc->I_shared > 0 ? at<void>(workspace, l.ysh) : nullptr;
+  MOE_TRY(do_route_groups(desc, groups, x, router_w, nullptr, k_per_token, nullptr, topk_idx,
+                          topk_w, k_left, load, dev_status, workspace, s));
+  MOE_TRY(do_permute(desc, topk_idx, k_left, counts, offsets, sorted_token, inv_row, dev_status,
+                     workspace, s));
+  if (ysh != nullptr) MOE_TRY(do_shared(desc, x, ysh, dev_status, workspace, s));
+  MOE_TRY(do_grouped_ffn(desc, x, sorted_token, offsets, w_gate_up, w_down, yperm, dev_status,
+                         workspace, s));
+  return do_combine(desc, yperm, ysh, inv_row, topk_w, k_left, out, dev_status, s);
+}
+
+moe_status moe_block_norm(const moe_norm_desc* desc, const void* residual, const void* branch,
+                          const void* gate, void* residual_out, void* normed_out, void* stream) {
+  moe::BlockNormArgs a{};
+  MOE_TRY(norm_args(desc, residual, branch, gate, false, &a));
+  const bool some = desc->T > 0;
+  MOE_TRY(check_norm_ptr(residual_out, some && branch != nullptr, desc->residual_type));
+  MOE_TRY(check_norm_ptr(normed_out, some && desc->w_pre != nullptr, desc->act_type));
+  if (normed_out != nullptr && desc->w_pre == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (!some) return MOE_OK;
+  a.out = residual_out;
+  a.h = normed_out;
+  return cuda_status(moe::launch_block_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_block_norm_workspace_size(const moe_norm_desc* desc) {
+  if (validate_norm(desc) != MOE_OK) return 0;
+  return align_up(moe::block_norm_part_bytes(desc->T, desc->H, 3));
+}
+
+moe_status moe_block_norm_backward(const moe_norm_desc* desc, const void* residual,
+                                   const void* branch, const void* gate,
+                                   const void* d_residual_out, const void* d_normed,
+                                   void* d_residual, void* d_branch, void* d_gate,
+                                   float* d_w_post, float* d_w_pre, void* workspace,
+                                   void* stream) {
+  moe::BlockNormArgs a{};
+  MOE_TRY(norm_args(desc, residual, branch, gate, true, &a));
+  const bool some = desc->T > 0;
+  MOE_TRY(check_norm_ptr(d_residual_out, false, desc->residual_type));
+  MOE_TRY(check_norm_ptr(d_normed, some && desc->w_pre != nullptr, desc->act_type));
+  if (d_normed != nullptr && desc->w_pre == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  MOE_TRY(check_norm_ptr(d_residual, some, desc->residual_type));
+  MOE_TRY(check_norm_ptr(d_branch, some && branch != nullptr, desc->act_type));
+  const bool full = desc->gate_kind == MOE_GATE_FULL;
+  MOE_TRY(check_norm_ptr(d_gate, desc->gate_kind != MOE_GATE_NONE && (some || !full),
+                         full ? desc->act_type : MOE_F32));
+  MOE_TRY(check_norm_ptr(d_w_post, desc->w_post != nullptr, MOE_F32));
+  MOE_TRY(check_norm_ptr(d_w_pre, desc->w_pre != nullptr, MOE_F32));
+  MOE_TRY(check_ws(workspace));
+  a.back = true;
+  a.out = d_residual;
+  a.h = d_branch;
+  a.ld_dout = a.ld_out;
+  a.ld_dh = a.ld_h;
+  a.ld_h = a.ld_branch;
+  a.d_out = d_residual_out;
+  a.d_h = d_normed;
+  a.d_gate = d_gate;
+  a.d_w_post = d_w_post;
+  a.d_w_pre = d_w_pre;
+  a.part = static_cast<float*>(workspace);
+  return cuda_status(moe::launch_block_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_lora_workspace_size(const moe_lora_desc* desc) {
+  if (validate_lora(desc) != MOE_OK) return 0;
+  return align_up(moe::lora_workspace_bytes(desc->T, desc->K, desc->N, desc->n_adapters,
+                                            desc->r_max) + 1);
+}
+
+moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void* w,
+                            const void* lora_a, const void* lora_b, const int32_t* ranks,
+                            const float* scales, const int32_t* adapter_idx, void* y,
+                            int32_t* dev_status, void* workspace, void* stream) {
+  MOE_TRY(validate_lora(desc));
+  if (desc->T == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({x, w}));
+  if (y == nullptr || (reinterpret_cast<uintptr_t>(y) & 1u) != 0) return MOE_ERR_INVALID_ARGUMENT;
+  MOE_TRY(check_ptrs4({dev_status}));
+  if (desc->n_adapters > 0) {
+    MOE_TRY(check_ptrs({lora_a, lora_b}));
+    MOE_TRY(check_ptrs4({ranks, scales, adapter_idx}));
+  }
+  MOE_TRY(check_ws(workspace));
+  moe::LoraArgs g{};
+  g.x = x;
+  g.w = w;
+  g.a = lora_a;
+  g.b = lora_b;
+  g.ranks = ranks;
+  g.scales = scales;
+  g.adapter = adapter_idx;
+  g.y = y;
+  g.ws = workspace;
+  g.ldx = desc->ldx != 0 ? desc->ldx : desc->K;
+  g.ldy = desc->ldy != 0 ? desc->ldy : (desc->swiglu ? desc->N / 2 : desc->N);
+  g.T = desc->T;
+  g.K = desc->K;
+  g.N = desc->N;
+  g.n_adapters = desc->n_adapters;
+  g.r_max = desc->r_max;
+  g.swiglu = desc->swiglu;
+  g.status = dev_status;
+  g.sm_count = sm_count();
+  return cuda_status(moe::launch_lora_project(g, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_get_device_status(const int32_t* dev_status, void* stream) {

@@ -1,0 +1,510 @@
+// Group-limited routing with a balance bias, and the gradient of its weights.
+//
+// Per token, over the E_r units u with logit l_u (fp32):
+//   s_u = 1 / (1 + exp(-l_u))            or  exp(l_u - max l) / sum exp(l - max l)
+//   c_u = s_u + b_u                       b: balance bias, selection only
+//   G_g = sum of the group_best (1 or 2) largest c of group g (consecutive units)
+//   the groups_kept best groups stay; the k_t largest c inside them are selected
+//   w_u = route_scale * s_u / (renorm ? sum of the selected s : 1)
+// Ties go to the lower group and the lower unit.  A logit of -inf takes its
+// unit out (NaN and +inf do too, and are reported).
+//
+// Gradient, with g_j the gradient of w_j (the selection is held fixed):
+//   sigmoid          dl_j = route_scale g_j s_j (1 - s_j)
+//   sigmoid, renorm  dl_j = route_scale w'_j (1 - s_j) (g_j - sum_i g_i w'_i)
+//   softmax          dl_u = s_u (d_u - sum_i d_i s_i),  d_j = route_scale g_j, else 0
+//   softmax, renorm  dl_j = route_scale w'_j (g_j - sum_i g_i w'_i)
+// with w' = s / (sum of the selected s).  A softmax renormalised over the
+// selection is the softmax of the selected logits alone, so that form needs
+// neither the other logits nor their sum.  A renormalised sigmoid takes the
+// common factor exp(m), m = min(max selected l, 0), out of every s.  Neither can
+// divide by a sum that underflowed.
+#include "moe_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWarps = 8;            // tokens of a CTA at a time
+constexpr int kMaxUnits = 256;
+constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ float warp_max_f32(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ float warp_sum_f32(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  return v;
+}
+
+// Scores for the comparison: expf and one approximate reciprocal (relative
+// error below 4e-7).  The weights that leave the kernel are computed again
+// with the correctly rounded division.
+__device__ __forceinline__ float sigmoid_fast(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
+
+// s(l) exp(-m) with m = min(largest selected l, 0): l > 0 only where m = 0.
+__device__ __forceinline__ float sigmoid_over(float l, float m) {
+  return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
+}
+
+struct GroupParams {
+  const float* P;         // S partial logit arrays [S][T][E]
+  int S;
+  long long slice;        // T * E
+  const float* bias;      // nullable: added to the logits of unit u, bias[u / n_sub]
+  int n_sub;
+  float* logits_out;      // nullable
+  const int32_t* kpt;
+  int T, E, k_max, score, renorm;
+  float scale;
+  int G, kept, best;
+  const float* sel_bias;  // nullable
+  int size;               // units per group
+  int L;                  // lanes per group (MANY: 1)
+  int gpl;                // groups per lane (1 unless MANY)
+  int per;                // units per lane
+  int vec;                // lanes hold aligned multiples of four units: 16-byte loads
+  int32_t* idx;
+  float* w;
+  int32_t* k_out;         // nullable
+  int32_t* load;          // nullable; zeroed before the launch unless the grid is one CTA
+  int32_t* status;
+};
+
+// Descending compare-exchange; on equal scores the lower unit stays first.
+__device__ __forceinline__ void cas(float& a, int& ia, float& b, int& ib) {
+  const bool sw = b > a || (b == a && ib < ia);
+  const float ta = sw ? b : a, tb = sw ? a : b;
+  const int ja = sw ? ib : ia, jb = sw ? ia : ib;
+  a = ta;
+  b = tb;
+  ia = ja;
+  ib = jb;
+}
+
+// Batcher's odd-even merge sort of a lane's IPL entries (a power of two).
+template <int IPL>
+__device__ __forceinline__ void lane_sort(float (&c)[IPL], int (&u)[IPL]) {
+#pragma unroll
+  for (int p = 1; p < IPL; p <<= 1) {
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1) {
+#pragma unroll
+      for (int j = q % p; j + q < IPL; j += 2 * q) {
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < IPL && (i + j) / (2 * p) == (i + j + q) / (2 * p))
+            cas(c[i + j], u[i + j], c[i + j + q], u[i + j + q]);
+      }
+    }
+  }
+}
+
+// One warp per token.  G <= 32: a group takes L = floor(32 / G) neighbouring
+// lanes, each with `per` consecutive units, so units ascend with the lanes and
+// a group's two best come from its lanes' sorted heads.  MANY (G > 32): a lane
+// holds whole groups, at most 16 units.
+template <int IPL, bool MANY>
+__global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupParams p) {
+  __shared__ int32_t s_load[kMaxUnits];
+  __shared__ float s_row[kWarps][kMaxUnits];
+  __shared__ float s_rank[MANY ? kWarps : 1][kMaxUnits];
+  pdl_wait_and_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.load != nullptr) {
+    for (int i = threadIdx.x; i < p.E; i += blockDim.x) s_load[i] = 0;
+    __syncthreads();
+  }
+  // this lane's units [u0, u0 + n)
+  const int g = MANY ? lane * p.gpl : lane / p.L;
+  const int j = MANY ? 0 : lane - g * p.L;
+  int u0 = g * p.size + j * p.per, n;
+  if (MANY)
+    n = max(0, min(p.per, p.E - u0));
+  else
+    n = g < p.G ? max(0, min(p.per, p.size - j * p.per)) : 0;
+  if (n == 0) u0 = 0;
+  float b[IPL];
+#pragma unroll
+  for (int i = 0; i < IPL; ++i)
+    b[i] = i < n && p.sel_bias != nullptr ? __ldg(p.sel_bias + u0 + i) : 0.f;
+  float* row_s = s_row[warp];
+
+  for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
+    int k = p.kpt != nullptr ? __ldg(p.kpt + t) : p.k_max;
+    const float* row = p.P + static_cast<size_t>(t) * p.E + u0;
+    float c[IPL];
+    if (p.vec) {
+#pragma unroll
+      for (int i = 0; i < IPL; i += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) v = __ldg(reinterpret_cast<const float4*>(row + i));
+        c[i] = v.x;
+        if (i + 1 < IPL) c[i + 1] = v.y;
+        if (i + 2 < IPL) c[i + 2] = v.z;
+        if (i + 3 < IPL) c[i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < IPL; ++i) c[i] = i < n ? __ldg(row + i) : 0.f;
+    }
+    for (int s = 1; s < p.S; ++s) {
+#pragma unroll
+      for (int i = 0; i < IPL; ++i)
+        if (i < n) c[i] += __ldg(row + s * p.slice + i);
+    }
+    if (p.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < IPL; ++i)
+        if (i < n) c[i] += __ldg(p.bias + (u0 + i) / p.n_sub);
+    }
+    if (p.logits_out != nullptr) {
+      float* lo = p.logits_out + static_cast<size_t>(t) * p.E + u0;
+#pragma unroll
+      for (int i = 0; i < IPL; ++i)
+        if (i < n) lo[i] = c[i];
+    }
+    if (k < 1 || k > p.k_max) {
+      if (lane == 0) report(p.status, MOE_ERR_K_RANGE);
+      k = min(max(k, 0), p.k_max);
+    }
+    // NaN and +inf are reported and leave the unit out, like -inf
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < IPL; ++i) {
+      if (i < n) {
+        if (!(c[i] < INFINITY)) {
+          bad = true;
+          c[i] = -INFINITY;
+        }
+        row_s[u0 + i] = c[i];
+      } else {
+        c[i] = -INFINITY;
+      }
+    }
+    float mx = 0.f, sum = 1.f;
+    if (p.score == MOE_SCORE_SOFTMAX) {
+      mx = c[0];
+#pragma unroll
+      for (int i = 1; i < IPL; ++i) mx = fmaxf(mx, c[i]);
+      mx = warp_max_f32(mx);
+      const float m0 = mx > -INFINITY ? mx : 0.f;
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < IPL; ++i) {
+        const float e = expf(c[i] - m0);
+        part += e;
+        c[i] = c[i] > -INFINITY ? e : -INFINITY;
+      }
+      sum = warp_sum_f32(part);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int i = 0; i < IPL; ++i) c[i] = c[i] * inv + b[i];   // -inf stays -inf
+    } else {
+#pragma unroll
+      for (int i = 0; i < IPL; ++i) c[i] = c[i] > -INFINITY ? sigmoid_fast(c[i]) + b[i] : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < IPL; ++i) {
+      if (c[i] != c[i]) {     // a NaN bias, or -inf * 0 of a row with nothing left
+        bad |= b[i] != b[i];
+        c[i] = -INFINITY;
+      }
+    }
+    if (__any_sync(kAll, bad) && lane == 0) report(p.status, MOE_ERR_NONFINITE);
+
+    if (MANY && p.kept < p.G) {
+      float* rank = s_rank[warp];
+      for (int q = 0; q < p.gpl; ++q) {
+        float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+          if (i < n && i / p.size == q) {
+            a2 = fmaxf(a2, fminf(a1, c[i]));
+            a1 = fmaxf(a1, c[i]);
+          }
+        if (g + q < p.G) rank[g + q] = a1 + (p.best == 2 && a2 > -INFINITY ? a2 : 0.f);
+      }
+      __syncwarp();
+      for (int q = 0; q < p.gpl; ++q) {
+        if (g + q >= p.G) break;
+        const float mine = rank[g + q];
+        int ahead = 0;
+        for (int o = 0; o < p.G; ++o) ahead += rank[o] > mine || (rank[o] == mine && o < g + q);
+        if (ahead >= p.kept) {
+#pragma unroll
+          for (int i = 0; i < IPL; ++i)
+            if (i / p.size == q) c[i] = -INFINITY;
+        }
+      }
+    }
+    int u[IPL];
+#pragma unroll
+    for (int i = 0; i < IPL; ++i) u[i] = u0 + i;
+    lane_sort<IPL>(c, u);
+    if (!MANY && p.kept < p.G) {
+      float a1 = c[0], a2 = IPL > 1 ? c[IPL > 1 ? 1 : 0] : -INFINITY;
+      if ((p.L & (p.L - 1)) == 0) {
+        for (int off = 1; off < p.L; off <<= 1) {
+          const float b1 = __shfl_xor_sync(kAll, a1, off), b2 = __shfl_xor_sync(kAll, a2, off);
+          a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+          a1 = fmaxf(a1, b1);
+        }
+      } else {
+        const float h1 = a1, h2 = a2;
+        a1 = a2 = -INFINITY;
+        for (int o = 0; o < p.L; ++o) {
+          const int from = min(g * p.L + o, 31);
+          const float b1 = __shfl_sync(kAll, h1, from), b2 = __shfl_sync(kAll, h2, from);
+          a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+          a1 = fmaxf(a1, b1);
+        }
+      }
+      const float rank = a1 + (p.best == 2 && a2 > -INFINITY ? a2 : 0.f);
+      int ahead = 0;
+      for (int o = 0; o < p.G; ++o) {
+        const float other = __shfl_sync(kAll, rank, o * p.L);
+        ahead += other > rank || (other == rank && o < g);
+      }
+      if (ahead >= p.kept) {
+#pragma unroll
+        for (int i = 0; i < IPL; ++i) c[i] = -INFINITY;
+      }
+    }
+    // k rounds: the largest head of the warp, lowest lane (= lowest unit) on ties
+    int mine = -1, got = 0;
+    for (; got < k; ++got) {
+      const float m = warp_max_f32(c[0]);
+      if (!(m > -INFINITY)) break;
+      const int who = __ffs(__ballot_sync(kAll, c[0] == m)) - 1;
+      const int unit = __shfl_sync(kAll, u[0], who);
+      if (lane == got) mine = unit;
+      if (lane == who) {
+#pragma unroll
+        for (int i = 0; i + 1 < IPL; ++i) {
+          c[i] = c[i + 1];
+          u[i] = u[i + 1];
+        }
+        c[IPL - 1] = -INFINITY;
+      }
+    }
+    __syncwarp();
+    // weights of the selected units, one per lane
+    const bool sel = lane < got;
+    const float l = sel ? row_s[mine] : -INFINITY;
+    float wt = 0.f;
+    if (p.score == MOE_SCORE_SOFTMAX) {
+      const float top = p.renorm ? warp_max_f32(l) : mx;
+      const float e = sel ? expf(l - top) : 0.f;
+      const float total = p.renorm ? warp_sum_f32(e) : sum;
+      if (sel) wt = e / total;
+    } else {
+      const float m = p.renorm ? fminf(warp_max_f32(l), 0.f) : 0.f;
+      const float s = sel ? sigmoid_over(l, m) : 0.f;
+      const float total = p.renorm ? warp_sum_f32(s) : 1.f;
+      if (sel) wt = s / total;
+    }
+    if (lane < p.k_max) {
+      const size_t o = static_cast<size_t>(t) * p.k_max + lane;
+      p.idx[o] = sel ? mine : -1;
+      p.w[o] = wt * p.scale;
+    }
+    if (p.k_out != nullptr && lane == 0) p.k_out[t] = got;
+    if (p.load != nullptr && sel) atomicAdd(&s_load[mine], 1);
+    __syncwarp();   // the row and rank buffers are written again for the next token
+  }
+  if (p.load != nullptr) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.E; i += blockDim.x) {
+      const int v = s_load[i];
+      if (gridDim.x == 1)
+        p.load[i] = v;
+      else if (v != 0)
+        atomicAdd(p.load + i, v);
+    }
+  }
+}
+
+struct RouteBackParams {
+  const float* logits;
+  const int32_t* idx;
+  const float* d_w;
+  float* d_logits;
+  int T, E, k_max, score, renorm;
+  float scale;
+  int vec;                // E % 4 == 0 and 16-byte aligned rows
+  int32_t* status;
+};
+
+// One warp per token: lane j takes slot j; the row leaves through shared
+// memory, whole.
+__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const RouteBackParams p) {
+  __shared__ __align__(16) float s_row[kWarps][kMaxUnits];
+  pdl_wait_and_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* d = s_row[warp];
+  const bool dense = p.score == MOE_SCORE_SOFTMAX && !p.renorm;
+  for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
+    const float* row = p.logits + static_cast<size_t>(t) * p.E;
+    float* out = p.d_logits + static_cast<size_t>(t) * p.E;
+    int u = -1;
+    float gw = 0.f;
+    if (lane < p.k_max) {
+      const size_t o = static_cast<size_t>(t) * p.k_max + lane;
+      u = p.idx[o];
+      gw = p.d_w[o];
+    }
+    const unsigned same = __match_any_sync(kAll, u);
+    if (u >= p.E || u < -1 || (u >= 0 && same != (1u << lane))) {
+      report(p.status, MOE_ERR_BAD_INDEX);
+      if (u >= p.E || u < -1 || (same & ((1u << lane) - 1u)) != 0u) u = -1;
+    }
+    float l = u >= 0 ? __ldg(row + u) : -INFINITY;
+    bool bad = !(l < INFINITY);
+    if (bad) l = -INFINITY;
+    const bool sel = u >= 0 && l > -INFINITY;
+    if (!sel) gw = 0.f;
+    for (int i = lane; i < p.E; i += 32) d[i] = 0.f;
+    __syncwarp();
+    if (dense) {
+      float mx = -INFINITY;
+      for (int i = lane; i < p.E; i += 32) {
+        const float v = __ldg(row + i);
+        bad |= !(v < INFINITY);
+        if (v < INFINITY) mx = fmaxf(mx, v);
+      }
+      mx = warp_max_f32(mx);
+      if (sel) d[u] = gw * p.scale;
+      __syncwarp();
+      float sum = 0.f, dot = 0.f;
+      for (int i = lane; i < p.E; i += 32) {
+        const float v = __ldg(row + i);
+        const float e = v < INFINITY && mx > -INFINITY ? expf(v - mx) : 0.f;
+        sum += e;
+        dot += e * d[i];
+      }
+      sum = warp_sum_f32(sum);
+      dot = warp_sum_f32(dot);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      dot *= inv;
+      for (int i = lane; i < p.E; i += 32) {
+        const float v = __ldg(row + i);
+        const float e = v < INFINITY && mx > -INFINITY ? expf(v - mx) * inv : 0.f;
+        out[i] = e * (d[i] - dot);
+      }
+    } else {
+      float dl;
+      if (p.score == MOE_SCORE_SOFTMAX) {
+        const float top = warp_max_f32(l);
+        const float e = sel ? expf(l - top) : 0.f;
+        const float total = warp_sum_f32(e);
+        const float wt = sel ? e / total : 0.f;
+        const float dot = warp_sum_f32(gw * wt);
+        dl = p.scale * wt * (gw - dot);
+      } else {
+        const float m = p.renorm ? fminf(warp_max_f32(l), 0.f) : 0.f;
+        const float s = sel ? sigmoid_over(l, m) : 0.f;
+        const float ms = 1.f / (1.f + expf(l));        // 1 - s without cancellation
+        float wt = s, dot = 0.f;
+        if (p.renorm) {
+          const float total = warp_sum_f32(s);
+          if (sel) wt = s / total;
+          dot = warp_sum_f32(gw * wt);
+        }
+        dl = p.scale * wt * ms * (gw - dot);
+      }
+      if (sel) d[u] = dl;
+      __syncwarp();
+      if (p.vec) {
+        for (int i = lane; i < p.E / 4; i += 32)
+          reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(d)[i];
+      } else {
+        for (int i = lane; i < p.E; i += 32) out[i] = d[i];
+      }
+    }
+    if (bad) report(p.status, MOE_ERR_NONFINITE);
+    __syncwarp();
+  }
+}
+
+inline bool aligned16p(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
+
+}  // namespace
+
+cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
+  if (a.T == 0) {
+    if (a.load != nullptr) return cudaMemsetAsync(a.load, 0, sizeof(int32_t) * a.E_r, s);
+    return cudaSuccess;
+  }
+  GroupParams p{};
+  p.P = a.partial;
+  p.S = a.S;
+  p.slice = static_cast<long long>(a.T) * a.E_r;
+  p.bias = a.bias;
+  p.n_sub = a.n_sub;
+  p.logits_out = a.logits_out;
+  p.kpt = a.k_per_token;
+  p.T = a.T;
+  p.E = a.E_r;
+  p.k_max = a.k_max;
+  p.score = a.score;
+  p.renorm = a.renorm;
+  p.scale = a.route_scale;
+  p.G = a.n_groups;
+  p.kept = a.groups_kept;
+  p.best = a.group_best;
+  // with every group kept the grouping decides nothing
+  if (p.kept == p.G) p.G = p.kept = 1;
+  p.sel_bias = a.select_bias;
+  p.size = p.E / p.G;
+  const bool many = p.G > 32;
+  p.L = many ? 1 : 32 / p.G;
+  p.gpl = many ? (p.G + 31) / 32 : 1;
+  p.per = many ? p.gpl * p.size : (p.size + p.L - 1) / p.L;
+  p.vec = p.per % 4 == 0 && p.size % 4 == 0 && aligned16p(a.partial);
+  p.idx = a.topk_idx;
+  p.w = a.topk_w;
+  p.k_out = a.k_out;
+  p.load = a.load;
+  p.status = a.status;
+  const int blocks = (a.T + kWarps - 1) / kWarps;
+  const int grid = blocks < 4 * a.sm_count ? blocks : 4 * a.sm_count;
+  if (a.load != nullptr && grid > 1) {
+    const cudaError_t e = cudaMemsetAsync(a.load, 0, sizeof(int32_t) * a.E_r, s);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 g(grid), b(kWarps * 32);
+  if (many) return launch_pdl(group_route_kernel<16, true>, g, b, 0, s, p);
+  if (p.per <= 1) return launch_pdl(group_route_kernel<1, false>, g, b, 0, s, p);
+  if (p.per <= 2) return launch_pdl(group_route_kernel<2, false>, g, b, 0, s, p);
+  if (p.per <= 4) return launch_pdl(group_route_kernel<4, false>, g, b, 0, s, p);
+  if (p.per <= 8) return launch_pdl(group_route_kernel<8, false>, g, b, 0, s, p);
+  return launch_pdl(group_route_kernel<16, false>, g, b, 0, s, p);
+}
+
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  RouteBackParams p{};
+  p.logits = a.logits;
+  p.idx = a.topk_idx;
+  p.d_w = a.d_topk_w;
+  p.d_logits = a.d_logits;
+  p.T = a.T;
+  p.E = a.E_r;
+  p.k_max = a.k_max;
+  p.score = a.score;
+  p.renorm = a.renorm;
+  p.scale = a.route_scale;
+  p.vec = a.E_r % 4 == 0 && aligned16p(a.logits) && aligned16p(a.d_logits);
+  p.status = a.status;
+  const int blocks = (a.T + kWarps - 1) / kWarps;
+  const int grid = blocks < 8 * a.sm_count ? blocks : 8 * a.sm_count;
+  return launch_pdl(route_backward_kernel, dim3(grid), dim3(kWarps * 32), 0, s, p);
+}
+
+}  // namespace moe

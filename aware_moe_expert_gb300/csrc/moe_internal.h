@@ -219,6 +219,89 @@ cudaError_t launch_decode_ffn(const DecodeFfnArgs& a, cudaStream_t s);
 constexpr int kFfnPartSlots = 256;
 bool decode_ffn_supports(int H, int I_sub);
 
+// ---- group_route.cu: group-limited routing with a balance bias, and its gradient
+struct GroupRouteArgs {
+  const float* partial;        // S partial logit arrays [S, T, E_r] (S = 1: finished logits)
+  int S;
+  const float* bias;           // nullable: bias[u / n_sub] joins the logits
+  int n_sub;
+  float* logits_out;           // nullable
+  const int32_t* k_per_token;
+  int T, E_r, k_max, score, renorm;
+  float route_scale;
+  int n_groups, groups_kept, group_best;
+  const float* select_bias;    // nullable [E_r]
+  int32_t* topk_idx;
+  float* topk_w;
+  int32_t* k_out;              // nullable [T]
+  int32_t* load;               // nullable [E_r]
+  int32_t* status;
+  int sm_count;
+};
+cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s);
+
+struct RouteBackwardArgs {
+  const float* logits;         // [T, E_r]
+  const int32_t* topk_idx;     // [T, k_max]
+  const float* d_topk_w;       // [T, k_max]
+  float* d_logits;             // [T, E_r]
+  int T, E_r, k_max, score, renorm;
+  float route_scale;
+  int32_t* status;
+  int sm_count;
+};
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s);
+
+// ---- block_norm.cu: the norms around a residual block and their gradients
+constexpr int kNormMaxCtas = 160;   // CTAs of a launch (one per SM), rows of the partial sums
+constexpr int kNormMaxH = 16384;
+struct BlockNormArgs {
+  bool back;
+  int T, H;
+  bool residual_f32, act_f32;
+  int gate_kind;
+  float eps, weight_offset, residual_scale, branch_scale;
+  const void* residual;
+  const void* branch;          // nullable
+  const void* gate;
+  const void* w_post;          // nullable
+  const void* w_pre;           // nullable
+  void* out;                   // r', or dr
+  void* h;                     // normed output, or dy
+  const void* d_out;           // nullable
+  const void* d_h;             // nullable without w_pre
+  void* d_gate;
+  float* d_w_post;
+  float* d_w_pre;
+  float* part;                 // block_norm_part_bytes
+  long long ld_residual, ld_branch, ld_gate, ld_out, ld_h, ld_dout, ld_dh;
+  int32_t* status;             // nullable
+  int sm_count;
+};
+// Whether one row of every tensor fits the shared memory of a CTA together.
+bool block_norm_fits(int H, bool residual_f32, bool act_f32, bool full_gate, bool back);
+size_t block_norm_part_bytes(int T, int H, int n_part);
+cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s);
+
+// ---- lora.cu: a shared projection with an adapter per request
+struct LoraArgs {
+  const void* x;
+  const void* w;
+  const void* a;
+  const void* b;
+  const int32_t* ranks;
+  const float* scales;
+  const int32_t* adapter;
+  void* y;
+  void* ws;
+  long long ldx, ldy;
+  int T, K, N, n_adapters, r_max, swiglu;
+  int32_t* status;
+  int sm_count;
+};
+size_t lora_workspace_bytes(int T, int K, int N, int n_adapters, int r_max);
+cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s);
+
 // bf16 [rows, cols] row-major tensor map: box of 64 columns x box_rows rows,
 // 128-byte swizzle, zero fill out of bounds.
 bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);

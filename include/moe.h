@@ -377,6 +377,157 @@ moe_status moe_layer_forward_cg(const moe_layer_desc* desc, const moe_cg_router*
                                 const int32_t* k_per_token, void* out, int32_t* dev_status,
                                 void* workspace, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Group-limited routing with a balance bias.  Over the E_r units of a token,
+ * with its logits L (as moe_route computes them, or logits_in):
+ *     s_u = softmax or sigmoid score of L_u            (desc->score)
+ *     c_u = s_u + select_bias[u]                       ranks the units, only that
+ *     G_g = sum of the group_best largest c of group g (one if only one is left)
+ * the groups_kept best groups stay, and the k_t units with the largest c inside
+ * them are selected; their weight is s_u, divided by the selected sum with
+ * desc->renorm (also where every one of them underflows), times desc->route_scale.  Equal scores go
+ * to the lower group and the lower unit.
+ * A logit of -inf takes its unit out: it is never selected, is no part of the
+ * softmax and counts in no group.  NaN and +inf do the same and are reported
+ * (MOE_ERR_NONFINITE), and so is a NaN bias; a bias of -inf takes a unit out of
+ * the selection.  A token with fewer than k_t units left gets those.
+ * Scores are compared in fp32, each within 1e-6 of its value.
+ */
+typedef struct {
+  int32_t n_groups;           /* groups of E_r / n_groups consecutive units; divides E_r  */
+  int32_t groups_kept;        /* 1..n_groups, with k_max <= groups_kept * group size       */
+  int32_t group_best;         /* 1 or 2: the units whose scores rank a group               */
+  const float* select_bias;   /* nullable device fp32 [E_r]: the balance bias              */
+} moe_group_route;
+
+/*   x, router_w, logits_in, k_per_token, logits_out, workspace  as for moe_route
+ *   topk_idx  int32 [T, k_max]: selected units, best first; -1 after the last
+ *   topk_w    fp32 [T, k_max]: their weights; 0 after the last
+ *   k_out     nullable int32 [T]: units selected for each token (k_t, or fewer);
+ *             the budgets to hand to moe_permute and moe_combine
+ *   load      nullable int32 [E_r]: assignments per unit in this call, what a
+ *             balancing step compares with its mean to move select_bias */
+moe_status moe_route_groups(const moe_layer_desc* desc, const moe_group_route* groups,
+                            const void* x, const void* router_w, const float* logits_in,
+                            const int32_t* k_per_token, float* logits_out, int32_t* topk_idx,
+                            float* topk_w, int32_t* k_out, int32_t* load, int32_t* dev_status,
+                            void* workspace, void* stream);
+
+/* Gradient of the weights of moe_route_groups or moe_route with respect to the
+ * logits, the selection held fixed (the balance bias has none: it only selects).
+ *   logits    fp32 [T, E_r]: the logits that were routed
+ *   topk_idx  int32 [T, k_max] from the forward call; -1 slots have no part;
+ *             a unit out of range or twice in a token -> MOE_ERR_BAD_INDEX (the
+ *             slot is left out)
+ *   d_topk_w  fp32 [T, k_max]
+ *   d_logits  fp32 [T, E_r], every element written
+ * Reads desc->T, the unit counts, k_max, score, renorm and route_scale. */
+moe_status moe_route_backward(const moe_layer_desc* desc, const float* logits,
+                              const int32_t* topk_idx, const float* d_topk_w, float* d_logits,
+                              int32_t* dev_status, void* stream);
+
+/* The whole layer with this router: route_groups -> permute -> [shared FFN] ->
+ * grouped FFN -> combine.  load as above (nullable).  A token that has no unit
+ * left gets the shared expert's output alone and reports MOE_ERR_K_RANGE.
+ * Workspace: moe_workspace_size. */
+moe_status moe_layer_forward_groups(const moe_layer_desc* desc, const moe_group_route* groups,
+                                    const void* x, const void* router_w, const void* w_gate_up,
+                                    const void* w_down, const int32_t* k_per_token, int32_t* load,
+                                    void* out, int32_t* dev_status, void* workspace,
+                                    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms around a residual block, fused with its gate and scales:
+ *     z  = w_post' * y / rms(y)                  (z = y without w_post)
+ *     r' = residual_scale * r + branch_scale * gate * z
+ *     h  = w_pre' * r' / rms(r')                 the next block's input
+ * rms(v) = sqrt(mean of v^2 + eps) over the H values of a row, w' = w +
+ * weight_offset.  With no branch (y null) r' = residual_scale * r.  Everything
+ * is computed in fp32 from the loaded values; r' and h are rounded once (h from
+ * the unrounded r').
+ */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,       /* gate [H]                                               */
+  MOE_GATE_TOKEN = 2,         /* gate [T]                                               */
+  MOE_GATE_FULL = 3           /* gate [T, H]                                            */
+} moe_gate_kind;
+
+typedef struct {
+  int32_t T, H;               /* T >= 0, 1 <= H <= 16384, and a row of every [T, H]
+                                 tensor a call reads within 200 KB together (else
+                                 MOE_ERR_UNSUPPORTED_SHAPE)                             */
+  moe_dtype residual_type;    /* r, r' and their gradients                              */
+  moe_dtype act_type;         /* y, gate, w_post, w_pre, h and dy, dh (bf16 unless the
+                                 residual is fp32)                                      */
+  moe_gate_kind gate_kind;
+  float eps, weight_offset, residual_scale, branch_scale;
+  const void* w_post;         /* nullable [H]: norm of the branch output                */
+  const void* w_pre;          /* nullable [H]: norm of the new residual                 */
+  /* elements between rows; 0 = H, else >= H */
+  int64_t ld_residual, ld_branch, ld_gate, ld_out, ld_normed;
+  int32_t* dev_status;        /* nullable: MOE_ERR_DEVICE_TIMEOUT of a bounded wait     */
+} moe_norm_desc;
+/* Pointers need the alignment of their type only; rows that are 16-byte aligned
+ * with H % 8 == 0 run fastest. */
+
+/*   residual [T, H], branch [T, H] (nullable without w_post and gate)
+ *   residual_out [T, H] (may be residual itself; nullable without a branch)
+ *   normed_out [T, H]: required exactly with w_pre */
+moe_status moe_block_norm(const moe_norm_desc* desc, const void* residual, const void* branch,
+                          const void* gate, void* residual_out, void* normed_out, void* stream);
+
+/* Bytes moe_block_norm_backward needs for this desc (0 on a bad desc). */
+size_t moe_block_norm_workspace_size(const moe_norm_desc* desc);
+
+/* Gradients of moe_block_norm from its inputs (nothing is saved forward):
+ *   d_residual_out  nullable [T, H]: gradient at r'
+ *   d_normed        [T, H]: gradient at h; required exactly with w_pre
+ *   d_residual [T, H]; d_branch [T, H] (with a branch)
+ *   d_gate    channel: fp32 [H], token: fp32 [T], full: act_type [T, H]
+ *   d_w_post, d_w_pre  fp32 [H], where the weight is given
+ * d_residual and d_residual_out share residual_out's row stride, d_normed has
+ * normed_out's, d_branch branch's, a full d_gate gate's.  The sums over tokens
+ * are taken in a fixed order.  d_residual may be d_residual_out. */
+moe_status moe_block_norm_backward(const moe_norm_desc* desc, const void* residual,
+                                   const void* branch, const void* gate,
+                                   const void* d_residual_out, const void* d_normed,
+                                   void* d_residual, void* d_branch, void* d_gate,
+                                   float* d_w_post, float* d_w_pre, void* workspace,
+                                   void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A projection that all requests share, with a low-rank adapter per request:
+ *     y_t = x_t W^T + scale_a (x_t A_a^T) B_a^T,      a = adapter_idx[t], or none (-1)
+ * and with `swiglu` SiLU(y[0, N/2)) * y[N/2, N) (the gate|up projection of a
+ * shared expert).  Sums in fp32; the low-rank intermediate is rounded to bf16
+ * as a tensor-core operand, y once at the end.
+ */
+typedef struct {
+  int32_t T, K, N;            /* tokens, input and output features; K % 8 == 0          */
+  int32_t n_adapters;         /* adapters in the pool, >= 0                             */
+  int32_t r_max;              /* rows of an adapter's A, 8..128, a multiple of 8        */
+  int32_t swiglu;             /* 1: W and B rows are N/2 gate, then N/2 up; N even      */
+  int64_t ldx, ldy;           /* elements between rows; 0 = contiguous; ldx % 8 == 0    */
+} moe_lora_desc;
+
+/* Bytes of workspace moe_lora_project needs (0 on a bad desc). */
+size_t moe_lora_workspace_size(const moe_lora_desc* desc);
+
+/*   x bf16 [T, K], w bf16 [N, K], y bf16 [T, N] ([T, N/2] with swiglu)
+ *   lora_a bf16 [n_adapters, r_max, K], lora_b bf16 [n_adapters, N, r_max]
+ *   ranks int32 [n_adapters]: rows of A and columns of B in use, 0..r_max; what
+ *         lies past them has no part in the result
+ *   scales fp32 [n_adapters]
+ *   adapter_idx int32 [T]: -1 for none; an index or a rank out of range ->
+ *         MOE_ERR_BAD_INDEX, and none is used
+ * The pool arguments may be null when n_adapters is 0. */
+moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void* w,
+                            const void* lora_a, const void* lora_b, const int32_t* ranks,
+                            const float* scales, const int32_t* adapter_idx, void* y,
+                            int32_t* dev_status, void* workspace, void* stream);
+
 /* Synchronises `stream`, then returns the code stored in *dev_status
  * (MOE_OK if zero), or MOE_ERR_CUDA if the synchronisation itself failed. */
 moe_status moe_get_device_status(const int32_t* dev_status, void* stream);
