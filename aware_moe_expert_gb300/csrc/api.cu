@@ -883,7 +883,7 @@ moe_status validate_lora(const moe_lora_desc* d) {
   if (d->K % 8 != 0 || d->ldx % 8 != 0 || d->r_max % 8 != 0 || d->r_max > 128)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (d->swiglu && d->N % 2 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (d->T > (1 << 24) || d->K > (1 << 20) || d->N > (1 << 20) || d->n_adapters > (1 << 16))
+  if (d->T > (1 << 23) || d->K > (1 << 20) || d->N > (1 << 20) || d->n_adapters > (1 << 16))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
@@ -1326,8 +1326,7 @@ moe_status moe_block_norm_backward(const moe_norm_desc* desc, const void* residu
 
 size_t moe_lora_workspace_size(const moe_lora_desc* desc) {
   if (validate_lora(desc) != MOE_OK) return 0;
-  return align_up(moe::lora_workspace_bytes(desc->T, desc->K, desc->N, desc->n_adapters,
-                                            desc->r_max) + 1);
+  return align_up(moe::lora_workspace_bytes(desc->T, desc->r_max) + 1);
 }
 
 moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void* w,

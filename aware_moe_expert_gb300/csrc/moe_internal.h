@@ -299,12 +299,16 @@ struct LoraArgs {
   int32_t* status;
   int sm_count;
 };
-size_t lora_workspace_bytes(int T, int K, int N, int n_adapters, int r_max);
+size_t lora_workspace_bytes(int T, int r_max);
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s);
 
 // bf16 [rows, cols] row-major tensor map: box of 64 columns x box_rows rows,
 // 128-byte swizzle, zero fill out of bounds.
 bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);
+// The same with ld elements between rows (a multiple of 8), encoded anew on
+// every call.
+bool encode_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, long long ld,
+                      int box_rows);
 bool gemm_supports_f32_router(int E_r);
 // Output columns per tile and K splits of the tensor-core router GEMM for T
 // tokens: small batches take 64-column tiles, and K is split until about 128
