@@ -6,19 +6,27 @@
 // A [n, r_max, K], B [n, N, r_max] bf16, fp32 sums; of an adapter rank_a <= r_max
 // rows of A and columns of B count.
 //
-// The adapters extend the reduction axis.  Of a tile of tokens, the distinct
-// adapters' columns of B, in groups of 16, follow the K columns of W:
-//
-//   y[t, :] = [x_t | v_t placed in its adapter's columns, 0 elsewhere] [W | B_a0 | B_a1 ...]^T
-//
-// so a tile's adapters cost ceil(sum of their ranks / 64) more k-blocks of the
-// same MMA loop, whatever the tokens' order, and no token is sorted or copied.
-// The zeros only hide what is finite: a factor that is Inf or NaN counts as 0
-// for everyone and is reported, so one request's adapter cannot reach another.
-//
-// v is rounded to bf16 once, being an MMA operand: 2^-9 of the adapter's term,
-// below the rounding of y unless that term outgrows y.
+// First a launch computes v, then one the projection; programmatic dependent
+// launch lets the projection stream W meanwhile and meet v at its end.
+//   few tokens   (lora_swap_kernel) the weight stream is the bound: v B_a^T is
+//                computed by otherwise idle warps on CUDA cores, in fp32, each
+//                token with its own adapter, while the tensor cores work on W
+//   many tokens  (lora_pair_kernel) the adapters extend the reduction axis: of
+//                a tile of tokens, the distinct adapters' columns of B, in
+//                groups of 16, follow the K columns of W,
+//                  y[t, :] = [x_t | v_t in its adapter's columns, 0 elsewhere]
+//                            [W | B_a0 | B_a1 ...]^T
+//                so a tile's adapters cost ceil(sum of their ranks / 64) more
+//                k-blocks of the same MMA loop, whatever the tokens' order.
+//                v is rounded to bf16 there, being an MMA operand: 2^-9 of the
+//                adapter's term, below the rounding of y unless that term
+//                outgrows y.  The zeros only hide what is finite, so a factor
+//                that is Inf or NaN counts as 0 and is reported.
+// No token is sorted or copied, and no token's result depends on another's
+// adapter or activations.
 #include <cudaTypedefs.h>
+
+#include <cmath>
 
 #include "gemm_common.cuh"
 #include "moe_internal.h"
@@ -34,17 +42,18 @@ constexpr uint32_t kTile = kRows * kBK * 2;
 constexpr int kWorkers = 128;           // threads that fill adapter k-blocks
 constexpr int kMaxTileTokens = 256;
 
-struct LoraParams {
+struct LoraParams {   // what the kernels share
   const __nv_bfloat16* b;
   const int32_t* ranks;
   const float* scales;
   const int32_t* adapter;
-  __nv_bfloat16* v;                     // [T, r_max]
+  void* v;                              // [T, r_max], fp32 or (v_bf16) bf16
+  int v_bf16;
   __nv_bfloat16* y;
   long long ldy;
   int T, K, N, outs, n, r_max, swiglu;
   int wait_first;                       // no kernel of this call runs before this one
-  int vec_y;                            // swap: 8-byte stores; pair: TMA stores
+  int vec_y;                            // pair: y is aligned for TMA stores
   int32_t* status;
 };
 
@@ -55,7 +64,7 @@ __device__ __forceinline__ int grp_cols(uint32_t g) { return static_cast<int>(g 
 
 __device__ __forceinline__ int adapter_of(const LoraParams& p, int t) {
   if (p.n == 0) return -1;
-  const int a = __ldg(p.adapter + t);
+  const int a = __ldcg(p.adapter + t);
   if (a < -1 || a >= p.n) {
     report(p.status, MOE_ERR_BAD_INDEX);
     return -1;
@@ -71,36 +80,66 @@ __device__ __forceinline__ int rank_of(const LoraParams& p, int a) {
   return r;
 }
 
+__device__ __forceinline__ void store_v(const LoraParams& p, int t, int col, float v) {
+  const long long at = static_cast<long long>(t) * p.r_max + col;
+  if (p.v_bf16)
+    static_cast<__nv_bfloat16*>(p.v)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(p.v)[at] = v;
+}
+
 __device__ __forceinline__ void workers_sync() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
 // Built by the 128 workers (e = 0..127): s_ad[n] the tokens' adapters, s_grp
 // the groups of the distinct adapters in the order of their first token.
-// Returns the number of groups.  s_sum: four words.
+// Returns the number of groups.  A hash table of the tile's adapters (4 NT
+// keys and their first tokens, in s_grp's space, 8 NT words) finds the first
+// tokens in a probe or two each; comparing every token with those before it
+// took several us at 256 tokens.  s_sum: four words.
 template <int NT>
 __device__ __forceinline__ int build_groups(const LoraParams& p, int t0, int e, int* s_ad,
                                             uint32_t* s_grp, int* s_sum) {
   constexpr int PER = NT > kWorkers ? NT / kWorkers : 1;
+  constexpr unsigned kSlots = 4 * NT;
   const int lane = e & 31, warp = e >> 5;
+  int* key = reinterpret_cast<int*>(s_grp);
+  int* first = key + kSlots;
+  int ad[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int n = e * PER + i;
-    if (n < NT) s_ad[n] = t0 + n < p.T ? adapter_of(p, t0 + n) : -1;
+    ad[i] = n < NT && t0 + n < p.T ? adapter_of(p, t0 + n) : -1;
+    if (n < NT) s_ad[n] = ad[i];
+  }
+  int rank[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) rank[i] = ad[i] >= 0 ? rank_of(p, ad[i]) : 0;
+  for (int i = e; i < static_cast<int>(kSlots); i += kWorkers) {
+    key[i] = -1;
+    first[i] = NT;
   }
   workers_sync();
-  int rank[PER], mine = 0;
+  unsigned at[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int n = e * PER + i;
-    rank[i] = 0;
-    if (n < NT) {
-      const int a = s_ad[n];
-      bool first = a >= 0 && (n == 0 || s_ad[n - 1] != a);
-      for (int m = 0; first && m + 1 < n; ++m) first = s_ad[m] != a;
-      if (first) rank[i] = rank_of(p, a);
-      mine += (rank[i] + kGroup - 1) / kGroup;
+    at[i] = (static_cast<unsigned>(ad[i]) * 2654435761u >> 16) & (kSlots - 1);
+    if (ad[i] >= 0) {
+      for (;;) {      // ends: at most NT distinct keys in 4 NT slots
+        const int was = atomicCAS(&key[at[i]], -1, ad[i]);
+        if (was == -1 || was == ad[i]) break;
+        at[i] = (at[i] + 1) & (kSlots - 1);
+      }
+      atomicMin(&first[at[i]], e * PER + i);
     }
+  }
+  workers_sync();
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (ad[i] >= 0 && first[at[i]] != e * PER + i) rank[i] = 0;
+    mine += (rank[i] + kGroup - 1) / kGroup;
   }
   int incl = mine;
 #pragma unroll
@@ -109,16 +148,16 @@ __device__ __forceinline__ int build_groups(const LoraParams& p, int t0, int e, 
     if (lane >= off) incl += o;
   }
   if (lane == 31) s_sum[warp] = incl;
-  workers_sync();
-  int at = incl - mine, total = 0;
+  workers_sync();     // everyone is done with the hash table, too
+  int to = incl - mine, total = 0;
   for (int w = 0; w < 4; ++w) {
-    if (w < warp) at += s_sum[w];
+    if (w < warp) to += s_sum[w];
     total += s_sum[w];
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     for (int j = 0; j * kGroup < rank[i]; ++j)
-      s_grp[at++] = static_cast<uint32_t>(s_ad[e * PER + i]) | (static_cast<uint32_t>(j) << 16) |
+      s_grp[to++] = static_cast<uint32_t>(ad[i]) | (static_cast<uint32_t>(j) << 16) |
                     (static_cast<uint32_t>(min(kGroup, rank[i] - j * kGroup)) << 20);
   workers_sync();
   return total;
@@ -145,179 +184,376 @@ __device__ __forceinline__ uint4 clean8(uint4 q, int cols, bool& bad) {
   return q;
 }
 
-// One k-block of four groups [g0, g0 + 4) of adapter columns, in the 128-byte
-// swizzle that the MMA descriptors expect: the factor rows (128 rows, row i of
-// W's row map(i), or none if map(i) < 0) and the tokens' v (VROWS rows).
-template <int VROWS, typename Map>
-__device__ __forceinline__ void fill_block(const LoraParams& p, int e, uint8_t* s_b, uint8_t* s_v,
-                                           const int* s_ad, const uint32_t* s_grp, int g0, int groups,
-                                           int t0, Map map) {
-  const int c = e & 7, r0 = e >> 3;                    // 16-byte chunk of a row, first row
-  const int gi = g0 + (c >> 1), half = (c & 1) * 8;
-  const bool live = gi < groups;
-  const uint32_t g = live ? s_grp[gi] : 0u;
-  const int a = live ? grp_adapter(g) : -2;
-  const int col = grp_first(g) + half, cols = live ? grp_cols(g) - half : 0;
-  bool bad = false;
-  uint4 q[8];
+// A worker's part of one k-block of four groups [4 j, 4 j + 4) of adapter
+// columns: the 16-byte chunk c of every sixteenth factor row and token row.
+// The loads are issued a block ahead of the stores, the factors even before
+// the kernel that computes v has finished.
+template <int VROWS>
+struct Block {
+  uint4 b[8], v[VROWS / 16];
+  int a, col, cols;
+
+  // factor row i is row map(i) of W (none if negative)
+  template <typename Map>
+  __device__ __forceinline__ void load_b(const LoraParams& p, int e, const uint32_t* s_grp, int j,
+                                         int groups, Map map) {
+    const int c = e & 7, r0 = e >> 3;
+    const int gi = 4 * j + (c >> 1), half = (c & 1) * 8;
+    const bool live = gi < groups;
+    const uint32_t g = live ? s_grp[gi] : 0u;
+    a = live ? grp_adapter(g) : -2;
+    col = grp_first(g) + half;
+    cols = live ? grp_cols(g) - half : 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int wr = map(r0 + 16 * i);
-    q[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (cols > 0 && wr >= 0)
-      q[i] = __ldg(reinterpret_cast<const uint4*>(
-          p.b + (static_cast<long long>(a) * p.N + wr) * p.r_max + col));
+    for (int i = 0; i < 8; ++i) {
+      const int wr = map(r0 + 16 * i);
+      b[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (cols > 0 && wr >= 0)
+        b[i] = __ldg(reinterpret_cast<const uint4*>(
+            p.b + (static_cast<long long>(a) * p.N + wr) * p.r_max + col));
+    }
   }
+  __device__ __forceinline__ void load_v(const LoraParams& p, int e, const int* s_ad, int t0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = r0 + 16 * i;
-    *reinterpret_cast<uint4*>(s_b + r * 128 + ((c ^ (r & 7)) << 4)) = clean8(q[i], cols, bad);
+    for (int i = 0; i < VROWS / 16; ++i) {
+      const int r = (e >> 3) + 16 * i;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (cols > 0 && s_ad[r] == a)
+        v[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) +
+                                                     static_cast<long long>(t0 + r) * p.r_max + col));
+    }
   }
-#pragma unroll 8
-  for (int i = 0; i < VROWS / 16; ++i) {
-    const int r = r0 + 16 * i;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (cols > 0 && s_ad[r] == a)
-      w = __ldcg(reinterpret_cast<const uint4*>(p.v + static_cast<long long>(t0 + r) * p.r_max + col));
-    *reinterpret_cast<uint4*>(s_v + r * 128 + ((c ^ (r & 7)) << 4)) = w;
+  // in the 128-byte swizzle that the MMA descriptors expect
+  __device__ __forceinline__ void store(const LoraParams& p, int e, uint8_t* s_b, uint8_t* s_v) {
+    const int c = e & 7, r0 = e >> 3;
+    const uint32_t at = static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(s_b + at + i * 2048) = clean8(b[i], cols, bad);
+#pragma unroll
+    for (int i = 0; i < VROWS / 16; ++i) *reinterpret_cast<uint4*>(s_v + at + i * 2048) = v[i];
+    if (bad) report(p.status, MOE_ERR_NONFINITE);
+    fence_proxy_async_smem();
   }
-  if (bad) report(p.status, MOE_ERR_NONFINITE);
-}
+};
 
 // ---------------------------------------------------------------- v, few tokens
-// v[t, i] = scale_a x_t . A_a[i]: 128 threads a (token, rank), all loads of a
-// thread's slice in flight.  Columns past the rank are 0; a token without an
-// adapter is left out (nothing reads its v).
-constexpr int kDotThreads = 128;
+// v[t, i] = scale_a x_t . A_a[i]: a CTA for a token and eight ranks, x read once
+// for the eight.  Columns past the rank are 0; a token without an adapter is
+// left out (nothing reads its v).  The chain of dependent loads is two long:
+// the adapter's index, then its rank, scale and rows together (rows past the
+// rank exist in the pool and are not used).
+constexpr int kDotThreads = 256;
+constexpr int kDotRanks = 8;
+constexpr int kDotVecs = 2;      // 16-byte vectors of a row a thread has in flight
 
-__global__ void __launch_bounds__(kDotThreads) lora_dot_kernel(const LoraParams p,
-                                                               const __nv_bfloat16* __restrict__ x,
-                                                               const __nv_bfloat16* __restrict__ fa,
-                                                               long long ldx) {
-  __shared__ float s_part[kDotThreads / 32];
+__global__ void __launch_bounds__(kDotThreads, 2)
+    lora_dot_kernel(const LoraParams p, const __nv_bfloat16* __restrict__ x,
+                    const __nv_bfloat16* __restrict__ fa, long long ldx) {
+  __shared__ float s_part[kDotThreads / 32][kDotRanks];
   pdl_wait_and_trigger();
-  const int i = blockIdx.x, t = blockIdx.y;
+  const int i0 = blockIdx.x * kDotRanks, t = blockIdx.y;
+  const int nv = p.K / 8;
+  const uint4* xr = reinterpret_cast<const uint4*>(x + t * ldx);
   const int a = adapter_of(p, t);
   if (a < 0) return;
+  const float scale = __ldg(p.scales + a);
   const int rank = rank_of(p, a);
-  float v = 0.f;
-  if (i < rank) {
-    const uint4* xr = reinterpret_cast<const uint4*>(x + t * ldx);
-    const uint4* ar = reinterpret_cast<const uint4*>(fa + (static_cast<long long>(a) * p.r_max + i) * p.K);
-    const int nv = p.K / 8;
-    for (int q0 = threadIdx.x; q0 < nv; q0 += 8 * kDotThreads) {
-      uint4 xv[8], av[8];
+  const uint4* ar = reinterpret_cast<const uint4*>(fa + (static_cast<long long>(a) * p.r_max + i0) * p.K);
+  float v[kDotRanks] = {};
+  for (int q0 = threadIdx.x; q0 < nv; q0 += kDotVecs * kDotThreads) {
+    uint4 xv[kDotVecs], av[kDotVecs][kDotRanks];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int q = q0 + j * kDotThreads;
-        xv[j] = q < nv ? __ldg(xr + q) : make_uint4(0u, 0u, 0u, 0u);
-        av[j] = q < nv ? __ldg(ar + q) : make_uint4(0u, 0u, 0u, 0u);
-      }
+    for (int j = 0; j < kDotVecs; ++j) {
+      const int q = q0 + j * kDotThreads;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      xv[j] = q < nv ? __ldg(xr + q) : zero;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t* xs = &xv[j].x;
-        const uint32_t* as = &av[j].x;
+      for (int i = 0; i < kDotRanks; ++i)
+        av[j][i] = q < nv ? __ldg(ar + static_cast<long long>(i) * nv + q) : zero;
+    }
+#pragma unroll
+    for (int j = 0; j < kDotVecs; ++j) {
+      const uint32_t* xs = &xv[j].x;
+#pragma unroll
+      for (int i = 0; i < kDotRanks; ++i) {
+        const uint32_t* as = &av[j][i].x;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          v = fmaf(bf16lo(xs[k]), bf16lo(as[k]), v);
-          v = fmaf(bf16hi(xs[k]), bf16hi(as[k]), v);
+          v[i] = fmaf(bf16lo(xs[k]), bf16lo(as[k]), v[i]);
+          v[i] = fmaf(bf16hi(xs[k]), bf16hi(as[k]), v[i]);
         }
       }
     }
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+  for (int i = 0; i < kDotRanks; ++i)
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < kDotRanks; ++i) s_part[threadIdx.x >> 5][i] = v[i];
+  }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    v = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
-    p.v[static_cast<long long>(t) * p.r_max + i] =
-        __float2bfloat16_rn(i < rank ? v * __ldg(p.scales + a) : 0.f);
+  if (threadIdx.x < kDotRanks) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDotThreads / 32; ++w) sum += s_part[w][threadIdx.x];
+    const int i = i0 + threadIdx.x;
+    store_v(p, t, i, i < rank ? sum * scale : 0.f);
   }
 }
 
 // ---------------------------------------------------------------- swapped operands
 // D[128 rows of W (or of the adapters' A), NT tokens]: the weight rows are the
 // MMA's M, so few tokens waste no tensor work and the weights stream once per
-// token tile.  K is split over the S CTAs of a cluster; each leaves its fp32
-// partial tile in shared memory and sums a slice of the tokens over the
-// cluster in rank order.
+// token tile.  K is split over the S CTAs of a cluster; rank q owns tokens
+// [q NT/S, (q+1) NT/S) of the tile: every CTA pushes its fp32 partial sums of
+// them into q's shared memory (stores need no round trip; reading them from
+// the other CTAs took 6 us for 64 tokens of four), and q adds them in rank order.
 //   SHRINK   rows = eight groups of factor rows (a TMA box of 16 rows each);
 //            the sums are scaled and go to v where the token has that adapter
-//   else     rows = 128 rows of W (swiglu: 64 gate and their 64 up rows), then
-//            the adapters' k-blocks, filled by warps 2-5
-// Warps: 0 TMA, 1 MMA, 2-5 adapter blocks, sums and stores.
-template <int NT>
+//   else     rows = 128 rows of W (swiglu: 64 gate and their 64 up rows)
+// Warps: 0 TMA, 1 MMA, 2-5 the adapters' terms of the CTA's own tokens while W
+// streams (kept in TMEM behind the accumulator), then sums and stores: a thread
+// has the row of its TMEM lane.
+template <int NT, bool SHRINK>
 struct SwapCfg {
   static constexpr uint32_t kStage = kTile + NT * 128;
-  static constexpr int kStages = NT >= 256 ? 3 : (NT >= 128 ? 4 : (NT >= 64 ? 6 : 8));
-  static constexpr uint32_t kOffSlot = kStages * kStage;          // one adapter k-block
-  static constexpr uint32_t kPitch = 132;                         // floats per token of the tile
-  static constexpr uint32_t kRing = kOffSlot + kStage;
-  static constexpr uint32_t kPart = NT * kPitch * 4;              // reuses the ring
-  static constexpr uint32_t kOffBar = kRing > kPart ? kRing : kPart;
-  static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 3) * 8;
+  static constexpr int kStages = NT >= 256 ? 4 : (NT >= 128 ? 6 : 8);
+  static constexpr uint32_t kVBytes = SHRINK ? 0 : 16384;         // v of the CTA's tokens
+  static constexpr uint32_t kOffV = kStages * kStage;
+  static constexpr uint32_t kOffBar = kOffV + kVBytes;
+  static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 1) * 8;
   static constexpr uint32_t kOffAd = kOffMisc + 64;
   static constexpr uint32_t kOffGrp = kOffAd + NT * 4;
-  static constexpr uint32_t kUsed = kOffGrp + NT * 8 * 4;         // r_max 128: 8 groups a token
+  static constexpr uint32_t kUsed = kOffGrp + NT * (SHRINK ? 8 : 1) * 4;   // groups; else ranks
   static constexpr uint32_t kSmem = kUsed + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static constexpr uint32_t kTmem = NT < 32 ? 32 : NT;
+  static_assert(NT * kRows * 4 <= kOffV, "the partial sums reuse the ring");
+  // sums, and for the projection the adapters' terms from column NT; loads read 32
+  static constexpr uint32_t kTmem = SHRINK ? (NT < 32 ? 32 : NT) : (NT < 32 ? 64 : 2 * NT);
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ void store4(__nv_bfloat16* dst, float4 v, int left, bool vec) {
-  if (vec && left >= 4) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+__device__ __forceinline__ float dot8(uint4 b, const float4& lo, const float4& hi, float acc) {
+  acc = fmaf(bf16lo(b.x), lo.x, acc);
+  acc = fmaf(bf16hi(b.x), lo.y, acc);
+  acc = fmaf(bf16lo(b.y), lo.z, acc);
+  acc = fmaf(bf16hi(b.y), lo.w, acc);
+  acc = fmaf(bf16lo(b.z), hi.x, acc);
+  acc = fmaf(bf16hi(b.z), hi.y, acc);
+  acc = fmaf(bf16lo(b.w), hi.z, acc);
+  return fmaf(bf16hi(b.w), hi.w, acc);
+}
+
+// Columns of a factor at and past `cols` (<= 0: all) become 0.
+__device__ __forceinline__ uint4 keep8(uint4 q, int cols) {
+  uint32_t* w = &q.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (2 * i >= cols) w[i] = 0u;
+    else if (2 * i + 1 >= cols) w[i] &= 0xffffu;
+  }
+  return q;
+}
+
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr),
+               "r"(__float_as_uint(v))
+               : "memory");
+}
+
+// 32 columns of the factor rows of four tokens, those of their ranks only; a
+// token with the adapter of the one before takes its copy.
+struct Pieces {
+  uint4 q[4][4];
+  __device__ __forceinline__ void load(const LoraParams& p, int row, int c, const int (&ad)[4],
+                                       const int (&rank)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool same = j > 0 && ad[j] == ad[j > 0 ? j - 1 : 0];
+      const __nv_bfloat16* b = p.b + (static_cast<long long>(ad[j]) * p.N + row) * p.r_max + c;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (same) {
+          q[j][k] = q[j > 0 ? j - 1 : 0][k];
+        } else {
+          q[j][k] = make_uint4(0u, 0u, 0u, 0u);
+          if (row >= 0 && c + 8 * k < rank[j]) q[j][k] = __ldg(reinterpret_cast<const uint4*>(b + 8 * k));
+        }
+      }
+    }
+  }
+};
+
+// v_t . B_a[row] of the CTA's own tokens first + n into TMEM column term + n:
+// each thread has the factor row of its TMEM lane (none if row < 0).  Tokens go
+// by fours, the next four's factors in flight under this four's products.
+__device__ __forceinline__ void adapter_terms(const LoraParams& p, int first, int count, int row, int e,
+                                              const int* s_ad, const int* s_rank, float* s_v,
+                                              uint32_t term) {
+  const float* v = static_cast<const float*>(p.v);
+  const int lane = e & 31, vecs = p.r_max / 4;
+  for (int l0 = 0; l0 < count; l0 += 32) {
+    const int m = min(32, count - l0);
+    const int my_ad = lane < m ? s_ad[l0 + lane] : -1;
+    const int my_rank = lane < m ? s_rank[l0 + lane] : 0;
+    auto take = [&](int i, int (&ad)[4], int (&rank)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ad[j] = __shfl_sync(0xffffffffu, my_ad, (i + j) & 31);
+        rank[j] = __shfl_sync(0xffffffffu, my_rank, (i + j) & 31);
+        if (i + j >= m) rank[j] = 0;
+        if (rank[j] == 0) ad[j] = -1;
+      }
+    };
+    int ad[4], rank[4];
+    Pieces cur, next;
+    take(0, ad, rank);
+    cur.load(p, row, 0, ad, rank);
+    workers_sync();           // the last tokens' v is read
+    for (int i = e; i < m * vecs; i += kWorkers) {
+      const int n = i / vecs, c = (i - n * vecs) * 4;
+      if ((c & ~7) < s_rank[l0 + n])        // whole chunks of eight: v is 0 past the rank
+        *reinterpret_cast<float4*>(s_v + n * p.r_max + c) = *reinterpret_cast<const float4*>(
+            v + static_cast<long long>(first + l0 + n) * p.r_max + c);
+    }
+    workers_sync();
+    for (int i = 0; i < m; i += 4) {
+      int ad1[4], rank1[4];
+      take(i + 4, ad1, rank1);
+      next.load(p, row, 0, ad1, rank1);
+      float acc[4] = {};
+      const int most = max(max(rank[0], rank[1]), max(rank[2], rank[3]));
+      for (int c0 = 0;;) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int left = rank[j] - c0 - 8 * k;
+            if (left > 0) {
+              const float4* w = reinterpret_cast<const float4*>(s_v + (i + j) * p.r_max + c0 + 8 * k);
+              acc[j] = dot8(left < 8 ? keep8(cur.q[j][k], left) : cur.q[j][k], w[0], w[1], acc[j]);
+            }
+          }
+        c0 += 32;
+        if (c0 >= most) break;
+        cur.load(p, row, c0, ad, rank);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < m) tmem_st1(term + static_cast<uint32_t>(l0 + i + j), acc[j]);
+      cur = next;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ad[j] = ad1[j];
+        rank[j] = rank1[j];
+      }
+    }
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Sums the S partial rows of this CTA's tokens, in rank order, adds the
+// adapters' terms (TMEM column term + n, 0: none) and stores them.  A thread
+// has row `row` of the tile, its TMEM lane.
+template <bool SHRINK, int S>
+__device__ __forceinline__ void finish(const LoraParams& p, float* part, const int* ad,
+                                       const uint32_t* grp, int ng, int first, int count, int per,
+                                       int blk, int row, uint32_t term) {
+  auto sum = [&](int n) {
+    float w[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) w[s] = part[(s * per + n) * kRows + row];
+    float v = w[0];
+#pragma unroll
+    for (int s = 1; s < S; ++s) v += w[s];
+    return v;
+  };
+  if (SHRINK) {
+    const int g = row / kGroup;
+    if (g >= ng) return;
+    const uint32_t gr = grp[g];
+    const int i = row % kGroup, a = grp_adapter(gr), col = grp_first(gr) + i;
+    const float sc = __ldg(p.scales + a);
+    if (col >= p.r_max) return;
+#pragma unroll 4
+    for (int n = 0; n < count; ++n) {
+      const float v = sum(n);
+      if (ad[n] == a) store_v(p, first + n, col, i < grp_cols(gr) ? v * sc : 0.f);
+    }
     return;
   }
-  if (left > 0) dst[0] = __float2bfloat16_rn(v.x);
-  if (left > 1) dst[1] = __float2bfloat16_rn(v.y);
-  if (left > 2) dst[2] = __float2bfloat16_rn(v.z);
-  if (left > 3) dst[3] = __float2bfloat16_rn(v.w);
+  const int o = blk * kRows + row;
+  __nv_bfloat16* y = p.y + first * p.ldy + o;
+  const bool store = !p.swiglu && o < p.outs;
+  for (int n0 = 0; n0 < count; n0 += 32) {
+    float w[32];
+    if (term != 0u) {
+      uint32_t t[32];
+      tmem_ld32(term + static_cast<uint32_t>(n0), t);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = __uint_as_float(t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (n0 + i < count) {
+        const float v = sum(n0 + i) + w[i];
+        if (store) y[(n0 + i) * p.ldy] = __float2bfloat16_rn(v);
+        if (p.swiglu) part[(n0 + i) * kRows + row] = v;    // only this thread reads or writes it
+      }
+    }
+  }
+  if (!p.swiglu) return;
+  workers_sync();
+  const int c = row & 63, q = blk * 64 + c;
+  if (q >= p.outs) return;
+#pragma unroll 4
+  for (int n = row >> 6; n < count; n += 2) {
+    const float g = part[n * kRows + c], u = part[n * kRows + c + 64];
+    p.y[(first + n) * p.ldy + q] = __float2bfloat16_rn(silu_f(g) * u);
+  }
 }
 
 template <int NT, bool SHRINK>
 __global__ void __launch_bounds__(192, 1)
     lora_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                      const LoraParams p) {
-  using C = SwapCfg<NT>;
+  using C = SwapCfg<NT, SHRINK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* empty = full + C::kStages;
-  uint64_t* lfull = empty + C::kStages;    // an adapter block is in its slot (or there is none)
-  uint64_t* lempty = lfull + 1;
-  uint64_t* tfull = lfull + 2;             // the accumulator is complete
+  uint64_t* tfull = empty + C::kStages;    // the accumulator is complete
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int* s_last = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   int* s_total = reinterpret_cast<int*>(smem + C::kOffMisc + 12);
   int* s_sum = reinterpret_cast<int*>(smem + C::kOffMisc + 16);
   int* s_ad = reinterpret_cast<int*>(smem + C::kOffAd);
   uint32_t* s_grp = reinterpret_cast<uint32_t*>(smem + C::kOffGrp);
+  float* part = reinterpret_cast<float*>(smem);           // [S][own tokens][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = gridDim.x, rank = blockIdx.x;
   const int t0 = blockIdx.z * NT;
+  const int per = NT / S;                  // tokens of this CTA: a power of two
+  const int lg = 31 - __clz(per);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(lfull, 4);
-    mbar_init(lempty, 1);
     mbar_init(tfull, 1);
     *s_abort = 0;
-    *s_last = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
@@ -380,7 +616,7 @@ __global__ void __launch_bounds__(192, 1)
         }
         if (!ok) {
           fail(s_abort, p.status);
-          // the copies issued into the other slots end before the CTA does
+          // the copies issued into the slots end before the CTA does
           for (int s = 0; s < C::kStages; ++s) mbar_wait(&full[s], s < stage ? phase : phase ^ 1u, nullptr);
         }
       }
@@ -406,134 +642,93 @@ __global__ void __launch_bounds__(192, 1)
             phase ^= 1u;
           }
         }
-        if (!SHRINK) {
-          const uint64_t ad = sdesc_sw128(smem_u32(smem + C::kOffSlot));
-          const uint64_t bd = sdesc_sw128(smem_u32(smem + C::kOffSlot + kTile));
-          for (uint32_t lp = 0; ok; lp ^= 1u) {
-            if (!mbar_wait(lfull, lp, s_abort)) {
-              ok = false;
-              break;
-            }
-            if (*s_last == 2) break;       // nothing in the slot, nothing to follow
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) umma_bf16(tmem, ad + 2u * k, bd + 2u * k, idesc, 1u);
-            umma_commit(lempty);
-          }
-        }
         if (!ok) fail(s_abort, p.status);
         umma_commit(tfull);
         if (!ok) mbar_wait(tfull, pass_parity, nullptr);
       }
       __syncwarp();
-    } else {
+    } else if (!SHRINK) {
       const int e = threadIdx.x - 64;
-      if (!SHRINK) {
-        if (!p.wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
-        groups = build_groups<NT>(p, t0, e, s_ad, s_grp, s_sum);
-        const int blocks = (groups + 3) / 4, half = p.swiglu ? 64 : kRows;
-        auto map = [&](int i) {
-          const int o = i < half ? blk * half + i : blk * half + i - half;
-          return o < p.outs ? (i < half ? o : p.outs + o) : -1;
-        };
-        uint32_t lp = 0;
-        for (int j = rank;; j += S) {
-          int ok = 1;
-          if (lane == 0) ok = mbar_wait(lempty, lp ^ 1u, s_abort) ? 1 : 0;
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
-            if (lane == 0) fail(s_abort, p.status);
-            break;
-          }
-          const bool more = j < blocks;
-          if (more) {
-            fill_block<NT>(p, e, smem + C::kOffSlot, smem + C::kOffSlot + kTile, s_ad, s_grp, 4 * j,
-                           groups, t0, map);
-            fence_proxy_async_smem();
-          } else if (e == 0) {
-            *s_last = 2;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(lfull);
-          lp ^= 1u;
-          if (!more) break;
+      if (p.n > 0) {
+        const int half = p.swiglu ? 64 : kRows;
+        const int lr = (warp & 3) * 32 + lane;      // the TMEM lane this thread writes
+        const int o = blk * half + (lr < half ? lr : lr - half);
+        const int row = o < p.outs ? (lr < half ? o : p.outs + o) : -1;
+        int* s_rank = reinterpret_cast<int*>(s_grp);
+        const int first = t0 + rank * per, count = min(per, p.T - first);
+        for (int n = e; n < count; n += kWorkers) {
+          const int a = adapter_of(p, first + n);
+          s_ad[n] = a;
+          s_rank[n] = a >= 0 ? rank_of(p, a) : 0;
         }
+        workers_sync();
+        // the factors into L2 while v is still being computed
+        for (int n = 0, last = -1; n < count; ++n) {
+          const int a = s_ad[n], r = s_rank[n];
+          if (a != last && row >= 0) {
+            const __nv_bfloat16* b = p.b + (static_cast<long long>(a) * p.N + row) * p.r_max;
+            for (int c = 0; c < r; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + c));
+          }
+          last = a;
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        adapter_terms(p, first, count, row, e, s_ad, s_rank, reinterpret_cast<float*>(smem + C::kOffV),
+                      tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + NT);
       }
+    }
+    if (warp >= 2) {
       int ok = 1;
       if (lane == 0) ok = mbar_wait(tfull, pass_parity, s_abort) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      tc_fence_after();
-      if (ok) {
-        const int q = warp & 3;
-        float* part = reinterpret_cast<float*>(smem);
-#pragma unroll 1
-        for (int n0 = 0; n0 < NT; n0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + n0, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n0 + i < NT) part[(n0 + i) * C::kPitch + q * 32 + lane] = __uint_as_float(v[i]);
-        }
-      } else if (lane == 0) {
-        fail(s_abort, p.status);
-      }
-      tc_fence_before();
+      if (lane == 0 && !ok) fail(s_abort, p.status);
     }
     pass_parity ^= 1u;
     __syncwarp();
-    cluster_sync_all();      // every CTA's partial tile is in its shared memory
+    if (S > 1) cluster_sync_all();   // every ring of the cluster is free
     if (warp >= 2) {
-      const int per = NT / S;
-      const uint32_t base = smem_u32(smem) + static_cast<uint32_t>(lane * 16);
-      for (int n = rank * per + warp - 2; n < (rank + 1) * per; n += 4) {
-        const int t = t0 + n;
-        if (t >= p.T) break;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q = 0; q < S; ++q) {
-          const float4 w = ld_cluster_f4(
-              mapa_shared(base + static_cast<uint32_t>(n) * C::kPitch * 4, static_cast<uint32_t>(q)));
-          v.x += w.x;
-          v.y += w.y;
-          v.z += w.z;
-          v.w += w.w;
-        }
-        if (SHRINK) {
-          const int g = blk * 8 + lane / 4;        // four rows of one group a lane
-          if (lane / 4 < ng) {
-            const uint32_t gr = s_grp[g];
-            const int i0 = (lane & 3) * 4, cols = grp_cols(gr);
-            if (s_ad[n] == grp_adapter(gr) && grp_first(gr) + i0 < p.r_max) {
-              const float sc = __ldg(p.scales + grp_adapter(gr));
-              v.x = i0 < cols ? v.x * sc : 0.f;
-              v.y = i0 + 1 < cols ? v.y * sc : 0.f;
-              v.z = i0 + 2 < cols ? v.z * sc : 0.f;
-              v.w = i0 + 3 < cols ? v.w * sc : 0.f;
-              store4(p.v + static_cast<long long>(t) * p.r_max + grp_first(gr) + i0, v, 4, true);
-            }
-          }
-        } else if (p.swiglu) {
-          float4 u;
-          u.x = __shfl_down_sync(0xffffffffu, v.x, 16);
-          u.y = __shfl_down_sync(0xffffffffu, v.y, 16);
-          u.z = __shfl_down_sync(0xffffffffu, v.z, 16);
-          u.w = __shfl_down_sync(0xffffffffu, v.w, 16);
-          v.x = silu_f(v.x) * u.x;
-          v.y = silu_f(v.y) * u.y;
-          v.z = silu_f(v.z) * u.z;
-          v.w = silu_f(v.w) * u.w;
-          const int o = blk * 64 + lane * 4;
-          if (lane < 16) store4(p.y + t * p.ldy + o, v, p.outs - o, p.vec_y);
-        } else {
-          const int o = blk * kRows + lane * 4;
-          store4(p.y + t * p.ldy + o, v, p.outs - o, p.vec_y);
+      tc_fence_after();
+      const int q = warp & 3;
+      const uint32_t mine = smem_u32(part) + static_cast<uint32_t>((rank * per * kRows + q * 32 + lane) * 4);
+#pragma unroll 1
+      for (int n0 = 0; n0 < NT && t0 + n0 < p.T; n0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + n0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int n = n0 + i, owner = n >> lg;
+          if (n < NT && t0 + n < p.T)
+            st_cluster_f32(mapa_shared(mine + static_cast<uint32_t>((n & (per - 1)) * kRows * 4),
+                                       static_cast<uint32_t>(owner)),
+                           __uint_as_float(v[i]));
         }
       }
+      tc_fence_before();
     }
-    fence_proxy_async_smem();   // the next pass's copies land where the sums were
     __syncwarp();
-    cluster_sync_all();      // nobody reads this CTA's tile any more
+    if (S > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
+    if (warp >= 2) {
+      const int lr = (warp & 3) * 32 + lane, first = t0 + rank * per, count = min(per, p.T - first);
+      const int* ad = SHRINK ? s_ad + rank * per : s_ad;
+      const uint32_t* grp = s_grp + (SHRINK ? blk * 8 : 0);
+      const uint32_t term =
+          !SHRINK && p.n > 0 ? tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + NT : 0u;
+      switch (S) {
+        case 1: finish<SHRINK, 1>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
+        case 2: finish<SHRINK, 2>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
+        case 4: finish<SHRINK, 4>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
+        default: finish<SHRINK, 8>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
+      }
+    }
+    if (SHRINK) {
+      fence_proxy_async_smem();   // the next block's copies land where the sums were
+      __syncthreads();
+    }
   }
+  tc_fence_before();
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
@@ -771,7 +966,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t tbase =
           tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kPairN);
       const int row0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;
-      const int t = row0 + lane;
 #pragma unroll 1
       for (int ci = 0; ci < per_n / 32; ++ci) {
         uint32_t pk[16];
@@ -811,13 +1005,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               bulk_commit();
             }
           }
-        } else if (t < p.T) {
-          __nv_bfloat16* dst = p.y + t * p.ldy + col;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col + i < p.outs)
-              dst[i] = __ushort_as_bfloat16(
-                  static_cast<unsigned short>((i & 1) ? pk[i / 2] >> 16 : pk[i / 2] & 0xffffu));
+        } else {
+          // rows the map cannot describe: through the buffer, so that a warp
+          // stores 64 neighbouring columns of a row at a time
+          stage_row_32(sbuf, lane, (ci & 1) * 4, pk);
+          if ((ci & 1) != 0) {
+            __syncwarp();
+            const int c0 = col - 32 + lane;
+#pragma unroll 4
+            for (int r = 0; r < 32 && row0 + r < p.T; ++r) {
+              const __nv_bfloat16* from = reinterpret_cast<const __nv_bfloat16*>(sbuf + r * 128);
+              __nv_bfloat16* dst = p.y + (row0 + r) * p.ldy;
+              // element k of row r: chunk k / 8 at (k / 8) ^ (r % 8)
+              const int lo = (((lane >> 3) ^ (r & 7)) << 3) + (lane & 7);
+              const int hi = ((((lane >> 3) + 4) ^ (r & 7)) << 3) + (lane & 7);
+              if (c0 < p.outs) dst[c0] = from[lo];
+              if (c0 + 32 < p.outs) dst[c0 + 32] = from[hi];
+            }
+            __syncwarp();
+          }
         }
       }
       tc_fence_before();
@@ -833,9 +1039,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     const int e = threadIdx.x - 192;
     const uint32_t lfull_l = mapa_shared(smem_u32(lfull), 0);
-    if (!p.wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool waited = p.wait_first != 0;
     uint32_t lp = 0;
     int built = -1, groups = 0;
+    Block<kRows> f;
     bool run = true;   // after a wait that gave up: keep the workers' barriers, touch nothing
     for (int w = cid; w < total; w += ncl) {
       const int mt = w / n_tiles, nt = w - mt * n_tiles;
@@ -851,6 +1058,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         return o < p.outs ? (i < half ? o : p.outs + o) : -1;
       };
       const int blocks = (groups + 3) / 4;
+      const int row0 = static_cast<int>(rank) * 128;
+      f.load_b(p, e, s_grp, 0, groups, map);
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+      f.load_v(p, e, s_ad + row0, mt * 256 + row0);
       for (int j = 0; run && j <= blocks; ++j) {
         int ok = 1;
         if (lane == 0) ok = mbar_wait(lempty, lp ^ 1u, s_abort) ? 1 : 0;
@@ -859,16 +1071,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (lane == 0) fail(s_abort, p.status);
           break;
         }
-        if (j < blocks) {
-          fill_block<kRows>(p, e, smem + C::kOffSlot + kTile, smem + C::kOffSlot,
-                            s_ad + static_cast<int>(rank) * 128, s_grp, 4 * j, groups,
-                            mt * 256 + static_cast<int>(rank) * 128, map);
-          fence_proxy_async_smem();
-        }
+        if (j < blocks) f.store(p, e, smem + C::kOffSlot + kTile, smem + C::kOffSlot);
         if (e == 0) *s_more = j < blocks ? 1 : 0;
         __syncwarp();
         if (lane == 0) arrive_release_cluster(lfull_l);
         lp ^= 1u;
+        if (j + 1 < blocks) {
+          f.load_b(p, e, s_grp, j + 1, groups, map);
+          f.load_v(p, e, s_ad + row0, mt * 256 + row0);
+        }
       }
     }
     // the last commit on this CTA's lempty has arrived
@@ -907,23 +1118,57 @@ cudaError_t launch_cluster(K kern, dim3 grid, int threads, int smem, int cluster
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Tokens per tile of the swapped kernel.
-int tile_tokens(int T) {
-  if (T <= 16) return 16;
-  if (T <= 32) return 32;
-  if (T <= 64) return 64;
-  if (T <= 128) return 128;
-  return 256;
+// Tokens per tile, splits of K and kernel, by an estimate of the time in us:
+// rounds of CTAs x k-blocks x the slowest of
+//   the weight tiles' way from HBM (16 KB per CTA, shared by the token tiles),
+//   the bytes into an SM (120 GB/s each measured with all SMs at it),
+//   the MMA (0.33 us for 128 x 256 x 64 in one CTA; less falls slower than N)
+// plus what a CTA does before and after its loop, which grows with its tokens
+// and, for the cluster's exchange of partial sums, with them again.
+struct Shape {
+  int nt, splits;      // nt = 0: CTA pairs
+};
+
+Shape pick_shape(int T, int K, int outs, int rows_per_tile, int sm) {
+  const double KB = (K + kBK - 1) / kBK;
+  Shape best{0, 1};
+  const double pair_tiles = static_cast<double>((T + 255) / 256) * ((outs + 2 * rows_per_tile - 1) / (2 * rows_per_tile));
+  const double pairs = sm / 2;
+  double least = std::ceil(pair_tiles / pairs) * KB * 0.33 + 6.0;
+  const int rows = (outs + rows_per_tile - 1) / rows_per_tile;
+  for (int nt = 16; nt <= 256; nt *= 2) {
+    const int tt = (T + nt - 1) / nt;
+    if (tt > 64) continue;
+    for (int S = 1; S <= 8 && S <= KB; S *= 2) {
+      const double ctas = static_cast<double>(rows) * tt * S;
+      const double rounds = std::ceil(ctas / sm), busy = ctas < sm ? ctas : sm;
+      const double hbm = 16384.0 * busy / tt / 7.0e6, in = (16384.0 + 128.0 * nt) / 1.2e5;
+      const double mma = 0.12 + nt * 0.0008;
+      const double block = hbm > in ? (hbm > mma ? hbm : mma) : (in > mma ? in : mma);
+      const double us = rounds * (std::ceil(KB / S) * block + 3.0 + nt * 0.01 +
+                                  (S > 1 ? 0.8 + nt * 0.015 : 0.0));
+      if (us < least) {
+        least = us;
+        best = Shape{nt, S};
+      }
+    }
+  }
+  return best;
 }
 
-// From here up 256-token tiles of CTA pairs have enough tiles to fill the GPU.
-constexpr int kPairMinT = 1025;
-// Up to here (tokens x r_max) v is a dot product per (token, rank).
-constexpr long long kDotMax = 2048;
+// Tokens per tile where the factors of A are the rows.
+int tile_tokens(int T) {
+  int nt = 16;
+  while (nt < T && nt < 256) nt *= 2;
+  return nt;
+}
+
+// Up to here (tokens x r_max) v is a dot product per token and rank.
+constexpr long long kDotMax = 8192;
 
 template <int NT, bool SHRINK>
-cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
-  using C = SwapCfg<NT>;
+cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t s) {
+  using C = SwapCfg<NT, SHRINK>;
   CUtensorMap tw, tx;
   if (SHRINK) {
     if (!encode_tmap_bf16(&tw, g.a, static_cast<long long>(g.n_adapters) * g.r_max, g.K, g.K, kGroup))
@@ -936,17 +1181,18 @@ cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
   const int tt = (g.T + NT - 1) / NT;
   int rows;                               // blocks of 128 rows
   if (SHRINK) {
+    // how many blocks a tile has is known on the device only: K is split as
+    // far as the tiles leave SMs, and the blocks take what is left
     const long long adapters = g.n_adapters < NT ? g.n_adapters : NT;
     const long long most = (adapters * ((g.r_max + kGroup - 1) / kGroup) + 7) / 8;
-    const long long room = (2ll * g.sm_count + tt - 1) / tt;   // clusters walk over the rest
+    while (S < 8 && S * 2 <= KB && static_cast<long long>(tt) * S * 2 <= g.sm_count) S *= 2;
+    const long long room = g.sm_count / (static_cast<long long>(tt) * S);
     rows = static_cast<int>(most < room ? most : room);
     if (rows < 1) rows = 1;
   } else {
     const int per = g.swiglu ? 64 : kRows;
     rows = (p.outs + per - 1) / per;
   }
-  int S = 1;
-  while (S < 8 && S * 2 <= KB && static_cast<long long>(rows) * tt * S * 2 <= g.sm_count) S *= 2;
   auto kern = lora_swap_kernel<NT, SHRINK>;
   static bool done[64] = {false};
   const cudaError_t e = set_smem_once(kern, static_cast<int>(C::kSmem), done);
@@ -954,14 +1200,23 @@ cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
   return launch_cluster(kern, dim3(S, rows, tt), 192, static_cast<int>(C::kSmem), S, s, tw, tx, p);
 }
 
-template <bool SHRINK>
-cudaError_t pick_swap(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
+cudaError_t run_shrink(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
   switch (tile_tokens(g.T)) {
-    case 16: return run_swap<16, SHRINK>(g, p, s);
-    case 32: return run_swap<32, SHRINK>(g, p, s);
-    case 64: return run_swap<64, SHRINK>(g, p, s);
-    case 128: return run_swap<128, SHRINK>(g, p, s);
-    default: return run_swap<256, SHRINK>(g, p, s);
+    case 16: return run_swap<16, true>(g, p, 1, s);
+    case 32: return run_swap<32, true>(g, p, 1, s);
+    case 64: return run_swap<64, true>(g, p, 1, s);
+    case 128: return run_swap<128, true>(g, p, 1, s);
+    default: return run_swap<256, true>(g, p, 1, s);
+  }
+}
+
+cudaError_t run_project(const LoraArgs& g, const LoraParams& p, Shape shape, cudaStream_t s) {
+  switch (shape.nt) {
+    case 16: return run_swap<16, false>(g, p, shape.splits, s);
+    case 32: return run_swap<32, false>(g, p, shape.splits, s);
+    case 64: return run_swap<64, false>(g, p, shape.splits, s);
+    case 128: return run_swap<128, false>(g, p, shape.splits, s);
+    default: return run_swap<256, false>(g, p, shape.splits, s);
   }
 }
 
@@ -988,7 +1243,7 @@ cudaError_t run_pair(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t lora_workspace_bytes(int T, int r_max) { return static_cast<size_t>(T) * r_max * 2; }
+size_t lora_workspace_bytes(int T, int r_max) { return static_cast<size_t>(T) * r_max * 4; }
 
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   LoraParams p{};
@@ -996,7 +1251,7 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   p.ranks = g.ranks;
   p.scales = g.scales;
   p.adapter = g.adapter;
-  p.v = static_cast<__nv_bfloat16*>(g.ws);
+  p.v = g.ws;
   p.y = static_cast<__nv_bfloat16*>(g.y);
   p.ldy = g.ldy;
   p.T = g.T;
@@ -1009,23 +1264,22 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   p.status = g.status;
   p.wait_first = g.n_adapters == 0 ? 1 : 0;
   if (g.T == 0) return cudaSuccess;
+  const Shape shape = pick_shape(g.T, g.K, p.outs, g.swiglu ? 64 : kRows, g.sm_count);
+  const bool pair = shape.nt == 0;
+  p.v_bf16 = pair;
   if (g.n_adapters > 0) {
     cudaError_t e;
     if (static_cast<long long>(g.T) * g.r_max <= kDotMax)
-      e = launch_pdl(lora_dot_kernel, dim3(g.r_max, g.T), dim3(kDotThreads), 0, s, p,
+      e = launch_pdl(lora_dot_kernel, dim3(g.r_max / kDotRanks, g.T), dim3(kDotThreads), 0, s, p,
                      static_cast<const __nv_bfloat16*>(g.x), static_cast<const __nv_bfloat16*>(g.a),
                      g.ldx);
     else
-      e = pick_swap<true>(g, p, s);
+      e = run_shrink(g, p, s);
     if (e != cudaSuccess) return e;
   }
-  const uintptr_t y = reinterpret_cast<uintptr_t>(g.y);
-  if (g.T >= kPairMinT) {
-    p.vec_y = (y & 15u) == 0 && g.ldy % 8 == 0;
-    return run_pair(g, p, s);
-  }
-  p.vec_y = (y & 7u) == 0 && g.ldy % 4 == 0;
-  return pick_swap<false>(g, p, s);
+  if (!pair) return run_project(g, p, shape, s);
+  p.vec_y = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0;
+  return run_pair(g, p, s);
 }
 
 }  // namespace moe
