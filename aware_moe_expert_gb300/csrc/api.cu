@@ -883,7 +883,8 @@ moe_status validate_lora(const moe_lora_desc* d) {
   if (d->K % 8 != 0 || d->ldx % 8 != 0 || d->r_max % 8 != 0 || d->r_max > 128)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (d->swiglu && d->N % 2 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (d->T > (1 << 23) || d->K > (1 << 20) || d->N > (1 << 20) || d->n_adapters > (1 << 16))
+  if (d->T > (1 << 23) || d->K > (1 << 20) || d->N > (1 << 20) || d->n_adapters > (1 << 16) ||
+      static_cast<long long>(d->n_adapters) * d->N > 0x7fffffffll)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }

@@ -7,23 +7,22 @@
 // rows of A and columns of B count.
 //
 // First a launch computes v, then one the projection; programmatic dependent
-// launch lets the projection stream W meanwhile and meet v at its end.
-//   few tokens   (lora_swap_kernel) the weight stream is the bound: v B_a^T is
-//                computed by otherwise idle warps on CUDA cores, in fp32, each
-//                token with its own adapter, while the tensor cores work on W
-//   many tokens  (lora_pair_kernel) the adapters extend the reduction axis: of
-//                a tile of tokens, the distinct adapters' columns of B, in
-//                groups of 16, follow the K columns of W,
-//                  y[t, :] = [x_t | v_t in its adapter's columns, 0 elsewhere]
-//                            [W | B_a0 | B_a1 ...]^T
-//                so a tile's adapters cost ceil(sum of their ranks / 64) more
-//                k-blocks of the same MMA loop, whatever the tokens' order.
-//                v is rounded to bf16 there, being an MMA operand: 2^-9 of the
-//                adapter's term, below the rounding of y unless that term
-//                outgrows y.  The zeros only hide what is finite, so a factor
-//                that is Inf or NaN counts as 0 and is reported.
-// No token is sorted or copied, and no token's result depends on another's
-// adapter or activations.
+// launch lets the projection stream W meanwhile and meet v at its end.  There
+// the adapters extend the reduction axis: of a tile of tokens, the distinct
+// adapters' columns of B, in groups of 16, follow the K columns of W,
+//   y[t, :] = [x_t | v_t in its adapter's columns, 0 elsewhere] [W | B_a0 | B_a1 ...]^T
+// so a tile's adapters cost ceil(sum of their ranks / 64) more k-blocks of the
+// same MMA loop, whatever the tokens' order; no token is sorted or copied.
+//   few tokens   lora_swap_kernel: W's rows are the MMA's M, the weight stream
+//                is the bound
+//   many tokens  lora_pair_kernel: CTA pairs, the tensor cores are the bound
+// v is rounded to bf16, being an MMA operand: 2^-9 of the adapter's term, below
+// the rounding of y unless that term outgrows y.
+// The zeros only hide what is finite.  So that no token's result depends on
+// another's adapter, a factor that is Inf or NaN counts as 0 and is reported:
+// the pair kernel's warps look at the factors as they place them; the swapped
+// kernel, which lets the TMA place them, keeps the adapters' sums apart and
+// computes a tile's again with looked-over factors if one is not finite.
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -47,8 +46,7 @@ struct LoraParams {   // what the kernels share
   const int32_t* ranks;
   const float* scales;
   const int32_t* adapter;
-  void* v;                              // [T, r_max], fp32 or (v_bf16) bf16
-  int v_bf16;
+  __nv_bfloat16* v;                     // [T, r_max]
   __nv_bfloat16* y;
   long long ldy;
   int T, K, N, outs, n, r_max, swiglu;
@@ -78,14 +76,6 @@ __device__ __forceinline__ int rank_of(const LoraParams& p, int a) {
     return 0;
   }
   return r;
-}
-
-__device__ __forceinline__ void store_v(const LoraParams& p, int t, int col, float v) {
-  const long long at = static_cast<long long>(t) * p.r_max + col;
-  if (p.v_bf16)
-    static_cast<__nv_bfloat16*>(p.v)[at] = __float2bfloat16_rn(v);
-  else
-    static_cast<float*>(p.v)[at] = v;
 }
 
 __device__ __forceinline__ void workers_sync() {
@@ -197,13 +187,8 @@ struct Block {
   template <typename Map>
   __device__ __forceinline__ void load_b(const LoraParams& p, int e, const uint32_t* s_grp, int j,
                                          int groups, Map map) {
-    const int c = e & 7, r0 = e >> 3;
-    const int gi = 4 * j + (c >> 1), half = (c & 1) * 8;
-    const bool live = gi < groups;
-    const uint32_t g = live ? s_grp[gi] : 0u;
-    a = live ? grp_adapter(g) : -2;
-    col = grp_first(g) + half;
-    cols = live ? grp_cols(g) - half : 0;
+    const int r0 = e >> 3;
+    place(e, s_grp, j, groups);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int wr = map(r0 + 16 * i);
@@ -219,9 +204,24 @@ struct Block {
       const int r = (e >> 3) + 16 * i;
       v[i] = make_uint4(0u, 0u, 0u, 0u);
       if (cols > 0 && s_ad[r] == a)
-        v[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) +
-                                                     static_cast<long long>(t0 + r) * p.r_max + col));
+        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.v + static_cast<long long>(t0 + r) * p.r_max + col));
     }
+  }
+  // the chunk's place among the groups only, without the factors
+  __device__ __forceinline__ void place(int e, const uint32_t* s_grp, int j, int groups) {
+    const int gi = 4 * j + ((e & 7) >> 1), half = (e & 1) * 8;
+    const bool live = gi < groups;
+    const uint32_t g = live ? s_grp[gi] : 0u;
+    a = live ? grp_adapter(g) : -2;
+    col = grp_first(g) + half;
+    cols = live ? grp_cols(g) - half : 0;
+  }
+  __device__ __forceinline__ void store_v(int e, uint8_t* s_v) {
+    const int c = e & 7, r0 = e >> 3;
+    const uint32_t at = static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+#pragma unroll
+    for (int i = 0; i < VROWS / 16; ++i) *reinterpret_cast<uint4*>(s_v + at + i * 2048) = v[i];
+    fence_proxy_async_smem();
   }
   // in the 128-byte swizzle that the MMA descriptors expect
   __device__ __forceinline__ void store(const LoraParams& p, int e, uint8_t* s_b, uint8_t* s_v) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kDotThreads, 2)
 #pragma unroll
     for (int w = 0; w < kDotThreads / 32; ++w) sum += s_part[w][threadIdx.x];
     const int i = i0 + threadIdx.x;
-    store_v(p, t, i, i < rank ? sum * scale : 0.f);
+    p.v[static_cast<long long>(t) * p.r_max + i] = __float2bfloat16_rn(i < rank ? sum * scale : 0.f);
   }
 }
 
@@ -315,161 +315,58 @@ __global__ void __launch_bounds__(kDotThreads, 2)
 //   SHRINK   rows = eight groups of factor rows (a TMA box of 16 rows each);
 //            the sums are scaled and go to v where the token has that adapter
 //   else     rows = 128 rows of W (swiglu: 64 gate and their 64 up rows)
-// Warps: 0 TMA, 1 MMA, 2-5 the adapters' terms of the CTA's own tokens while W
-// streams (kept in TMEM behind the accumulator), then sums and stores: a thread
-// has the row of its TMEM lane.
+// The adapters' k-blocks are dealt to the CTAs of the cluster and come through
+// the same ring behind the K columns (factor rows in TMA boxes of 16 columns);
+// their sums have columns of their own in TMEM.  How much of W is in flight is
+// kept to what the bandwidth needs: with 16 MB of it, every other load waited
+// 2-3 us, and v with its chain of loads came late.
+// Warps: 0 TMA, 1 MMA, 2-5 v tiles, sums and stores: a thread has the row of
+// its TMEM lane.
 template <int NT, bool SHRINK>
 struct SwapCfg {
   static constexpr uint32_t kStage = kTile + NT * 128;
-  static constexpr int kStages = NT >= 256 ? 4 : (NT >= 128 ? 6 : 8);
-  static constexpr uint32_t kVBytes = SHRINK ? 0 : 16384;         // v of the CTA's tokens
+  static constexpr int kStages = NT >= 256 ? (SHRINK ? 4 : 3) : (NT >= 128 ? 5 : 6);
+  static constexpr int kVSlots = SHRINK ? 0 : (NT >= 128 ? 2 : 4);  // v tiles of adapter k-blocks
   static constexpr uint32_t kOffV = kStages * kStage;
-  static constexpr uint32_t kOffBar = kOffV + kVBytes;
-  static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 1) * 8;
+  static constexpr uint32_t kOffBar = kOffV + kVSlots * NT * 128;
+  static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 3 + 2 * 4) * 8;
   static constexpr uint32_t kOffAd = kOffMisc + 64;
   static constexpr uint32_t kOffGrp = kOffAd + NT * 4;
-  static constexpr uint32_t kUsed = kOffGrp + NT * (SHRINK ? 8 : 1) * 4;   // groups; else ranks
+  static constexpr uint32_t kUsed = kOffGrp + NT * 8 * 4;
   static constexpr uint32_t kSmem = kUsed + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(NT * kRows * 4 <= kOffV, "the partial sums reuse the ring");
-  // sums, and for the projection the adapters' terms from column NT; loads read 32
-  static constexpr uint32_t kTmem = SHRINK ? (NT < 32 ? 32 : NT) : (NT < 32 ? 64 : 2 * NT);
+  static constexpr uint32_t kCols = NT < 32 ? 32 : NT;            // loads read 32 columns
+  static constexpr uint32_t kTmem = SHRINK ? kCols : 2 * kCols;   // projection: the adapters' sums, too
 };
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ float dot8(uint4 b, const float4& lo, const float4& hi, float acc) {
-  acc = fmaf(bf16lo(b.x), lo.x, acc);
-  acc = fmaf(bf16hi(b.x), lo.y, acc);
-  acc = fmaf(bf16lo(b.y), lo.z, acc);
-  acc = fmaf(bf16hi(b.y), lo.w, acc);
-  acc = fmaf(bf16lo(b.z), hi.x, acc);
-  acc = fmaf(bf16hi(b.z), hi.y, acc);
-  acc = fmaf(bf16lo(b.w), hi.z, acc);
-  return fmaf(bf16hi(b.w), hi.w, acc);
+// Descriptor of a K-major tile of 16 bf16 columns (rows of 32 bytes, 32-byte
+// swizzle, groups of eight rows 256 bytes apart), as a TMA load with
+// CU_TENSOR_MAP_SWIZZLE_32B writes it.
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(256 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(6) << 61;
+  return d;
 }
 
-// Columns of a factor at and past `cols` (<= 0: all) become 0.
-__device__ __forceinline__ uint4 keep8(uint4 q, int cols) {
-  uint32_t* w = &q.x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (2 * i >= cols) w[i] = 0u;
-    else if (2 * i + 1 >= cols) w[i] &= 0xffffu;
-  }
-  return q;
-}
-
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr),
-               "r"(__float_as_uint(v))
-               : "memory");
-}
-
-// 32 columns of the factor rows of four tokens, those of their ranks only; a
-// token with the adapter of the one before takes its copy.
-struct Pieces {
-  uint4 q[4][4];
-  __device__ __forceinline__ void load(const LoraParams& p, int row, int c, const int (&ad)[4],
-                                       const int (&rank)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool same = j > 0 && ad[j] == ad[j > 0 ? j - 1 : 0];
-      const __nv_bfloat16* b = p.b + (static_cast<long long>(ad[j]) * p.N + row) * p.r_max + c;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (same) {
-          q[j][k] = q[j > 0 ? j - 1 : 0][k];
-        } else {
-          q[j][k] = make_uint4(0u, 0u, 0u, 0u);
-          if (row >= 0 && c + 8 * k < rank[j]) q[j][k] = __ldg(reinterpret_cast<const uint4*>(b + 8 * k));
-        }
-      }
-    }
-  }
-};
-
-// v_t . B_a[row] of the CTA's own tokens first + n into TMEM column term + n:
-// each thread has the factor row of its TMEM lane (none if row < 0).  Tokens go
-// by fours, the next four's factors in flight under this four's products.
-__device__ __forceinline__ void adapter_terms(const LoraParams& p, int first, int count, int row, int e,
-                                              const int* s_ad, const int* s_rank, float* s_v,
-                                              uint32_t term) {
-  const float* v = static_cast<const float*>(p.v);
-  const int lane = e & 31, vecs = p.r_max / 4;
-  for (int l0 = 0; l0 < count; l0 += 32) {
-    const int m = min(32, count - l0);
-    const int my_ad = lane < m ? s_ad[l0 + lane] : -1;
-    const int my_rank = lane < m ? s_rank[l0 + lane] : 0;
-    auto take = [&](int i, int (&ad)[4], int (&rank)[4]) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ad[j] = __shfl_sync(0xffffffffu, my_ad, (i + j) & 31);
-        rank[j] = __shfl_sync(0xffffffffu, my_rank, (i + j) & 31);
-        if (i + j >= m) rank[j] = 0;
-        if (rank[j] == 0) ad[j] = -1;
-      }
-    };
-    int ad[4], rank[4];
-    Pieces cur, next;
-    take(0, ad, rank);
-    cur.load(p, row, 0, ad, rank);
-    workers_sync();           // the last tokens' v is read
-    for (int i = e; i < m * vecs; i += kWorkers) {
-      const int n = i / vecs, c = (i - n * vecs) * 4;
-      if ((c & ~7) < s_rank[l0 + n])        // whole chunks of eight: v is 0 past the rank
-        *reinterpret_cast<float4*>(s_v + n * p.r_max + c) = *reinterpret_cast<const float4*>(
-            v + static_cast<long long>(first + l0 + n) * p.r_max + c);
-    }
-    workers_sync();
-    for (int i = 0; i < m; i += 4) {
-      int ad1[4], rank1[4];
-      take(i + 4, ad1, rank1);
-      next.load(p, row, 0, ad1, rank1);
-      float acc[4] = {};
-      const int most = max(max(rank[0], rank[1]), max(rank[2], rank[3]));
-      for (int c0 = 0;;) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int left = rank[j] - c0 - 8 * k;
-            if (left > 0) {
-              const float4* w = reinterpret_cast<const float4*>(s_v + (i + j) * p.r_max + c0 + 8 * k);
-              acc[j] = dot8(left < 8 ? keep8(cur.q[j][k], left) : cur.q[j][k], w[0], w[1], acc[j]);
-            }
-          }
-        c0 += 32;
-        if (c0 >= most) break;
-        cur.load(p, row, c0, ad, rank);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j < m) tmem_st1(term + static_cast<uint32_t>(l0 + i + j), acc[j]);
-      cur = next;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ad[j] = ad1[j];
-        rank[j] = rank1[j];
-      }
-    }
-  }
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Sums the S partial rows of this CTA's tokens, in rank order, adds the
-// adapters' terms (TMEM column term + n, 0: none) and stores them.  A thread
-// has row `row` of the tile, its TMEM lane.
+// Sums the S partial rows of this CTA's tokens, in rank order, and stores them;
+// a thread has row `row` of the tile.
 template <bool SHRINK, int S>
-__device__ __forceinline__ void finish(const LoraParams& p, float* part, const int* ad,
+__device__ __forceinline__ void finish(const LoraParams& p, const float* part, const int* ad,
                                        const uint32_t* grp, int ng, int first, int count, int per,
-                                       int blk, int row, uint32_t term) {
-  auto sum = [&](int n) {
+                                       int blk, int row) {
+  auto sum = [&](int n, int r) {
     float w[S];
 #pragma unroll
-    for (int s = 0; s < S; ++s) w[s] = part[(s * per + n) * kRows + row];
+    for (int s = 0; s < S; ++s) w[s] = part[(s * per + n) * kRows + r];
     float v = w[0];
 #pragma unroll
     for (int s = 1; s < S; ++s) v += w[s];
@@ -484,57 +381,103 @@ __device__ __forceinline__ void finish(const LoraParams& p, float* part, const i
     if (col >= p.r_max) return;
 #pragma unroll 4
     for (int n = 0; n < count; ++n) {
-      const float v = sum(n);
-      if (ad[n] == a) store_v(p, first + n, col, i < grp_cols(gr) ? v * sc : 0.f);
+      const float v = sum(n, row);
+      if (ad[n] == a)
+        p.v[static_cast<long long>(first + n) * p.r_max + col] =
+            __float2bfloat16_rn(i < grp_cols(gr) ? v * sc : 0.f);
     }
-    return;
-  }
-  const int o = blk * kRows + row;
-  __nv_bfloat16* y = p.y + first * p.ldy + o;
-  const bool store = !p.swiglu && o < p.outs;
-  for (int n0 = 0; n0 < count; n0 += 32) {
-    float w[32];
-    if (term != 0u) {
-      uint32_t t[32];
-      tmem_ld32(term + static_cast<uint32_t>(n0), t);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = __uint_as_float(t[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (n0 + i < count) {
-        const float v = sum(n0 + i) + w[i];
-        if (store) y[(n0 + i) * p.ldy] = __float2bfloat16_rn(v);
-        if (p.swiglu) part[(n0 + i) * kRows + row] = v;    // only this thread reads or writes it
-      }
-    }
-  }
-  if (!p.swiglu) return;
-  workers_sync();
-  const int c = row & 63, q = blk * 64 + c;
-  if (q >= p.outs) return;
+  } else if (p.swiglu) {
+    const int o = blk * 64 + (row & 63);
+    if (o >= p.outs) return;
+    __nv_bfloat16* y = p.y + first * p.ldy + o;
 #pragma unroll 4
-  for (int n = row >> 6; n < count; n += 2) {
-    const float g = part[n * kRows + c], u = part[n * kRows + c + 64];
-    p.y[(first + n) * p.ldy + q] = __float2bfloat16_rn(silu_f(g) * u);
+    for (int n = row >> 6; n < count; n += 2)
+      y[n * p.ldy] = __float2bfloat16_rn(silu_f(sum(n, row & 63)) * sum(n, (row & 63) + 64));
+  } else {
+    const int o = blk * kRows + row;
+    if (o >= p.outs) return;
+    __nv_bfloat16* y = p.y + first * p.ldy + o;
+#pragma unroll 8
+    for (int n = 0; n < count; ++n) y[n * p.ldy] = __float2bfloat16_rn(sum(n, row));
+  }
+}
+
+// Row i of a tile of W (swiglu: 64 gate rows, then their up rows) as a row of W,
+// or -1.
+__device__ __forceinline__ int tile_row(const LoraParams& p, int blk, int i) {
+  const int half = p.swiglu ? 64 : kRows;
+  const int o = blk * half + (i < half ? i : i - half);
+  return o < p.outs ? (i < half ? o : p.outs + o) : -1;
+}
+
+// By the workers, once every MMA of the CTA is complete: if one of its
+// adapters' sums is not finite, they are all computed again with factors that
+// were looked over.  The same k-steps in the same order: what was finite keeps
+// its bits.  The ring is free by then.
+template <int NT>
+__device__ __forceinline__ void look_over(const LoraParams& p, uint8_t* smem, const int* s_ad,
+                                          const uint32_t* s_grp, int* s_sum, uint64_t* redo,
+                                          volatile int* s_abort, uint32_t tmem, int blk, int t0,
+                                          int rank, int S, int groups, int e) {
+  using C = SwapCfg<NT, false>;
+  const int warp = e >> 5, lane = e & 31, q = (warp + 2) & 3;
+  tc_fence_after();
+  bool bad = false;
+  const bool used = tile_row(p, blk, q * 32 + lane) >= 0;
+#pragma unroll 1
+  for (int n0 = 0; n0 < NT; n0 += 32) {
+    uint32_t w[32];
+    tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + C::kCols + n0, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      bad |= n0 + i < NT && !(fabsf(__uint_as_float(w[i])) < INFINITY);
+  }
+  bad = __any_sync(0xffffffffu, bad && used);
+  if (lane == 0) s_sum[warp] = bad;
+  workers_sync();
+  if ((s_sum[0] | s_sum[1] | s_sum[2] | s_sum[3]) == 0) return;
+  Block<NT> f;
+  bool run = true;
+  const int blocks = (groups + 3) / 4;
+  for (int j = rank, i = 0; j < blocks; j += S, ++i) {
+    f.load_b(p, e, s_grp, j, groups, [&](int r) { return tile_row(p, blk, r); });
+    f.load_v(p, e, s_ad, t0);
+    f.store(p, e, smem, smem + C::kOffV);
+    tc_fence_before();
+    workers_sync();
+    if (e == 0) {
+      tc_fence_after();
+      const uint64_t ad = sdesc_sw128(smem_u32(smem)), bd = sdesc_sw128(smem_u32(smem + C::kOffV));
+#pragma unroll
+      for (int k = 0; k < kBK / 16; ++k)
+        umma_bf16(tmem + C::kCols, ad + 2u * k, bd + 2u * k, idesc_bf16_f32(kRows, NT),
+                  (i | k) != 0 ? 1u : 0u);
+      umma_commit(redo);
+    }
+    int ok = 1;
+    if (lane == 0 && run) ok = mbar_wait(redo, i & 1, s_abort) ? 1 : 0;
+    if (lane == 0 && !ok) fail(s_abort, p.status);
+    run = __shfl_sync(0xffffffffu, ok, 0) != 0 && run;
+    tc_fence_after();
   }
 }
 
 template <int NT, bool SHRINK>
 __global__ void __launch_bounds__(192, 1)
     lora_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                     const LoraParams p) {
+                     const __grid_constant__ CUtensorMap tmB, const LoraParams p) {
   using C = SwapCfg<NT, SHRINK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* empty = full + C::kStages;
-  uint64_t* tfull = empty + C::kStages;    // the accumulator is complete
+  uint64_t* tfull = empty + C::kStages;    // the accumulators are complete
+  uint64_t* tbl = tfull + 1;               // the groups are listed
+  uint64_t* vfull = tfull + 2;             // a v tile is in its slot
+  uint64_t* vempty = vfull + 4;
+  uint64_t* redo = vempty + 4;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   int* s_total = reinterpret_cast<int*>(smem + C::kOffMisc + 12);
@@ -553,10 +496,18 @@ __global__ void __launch_bounds__(192, 1)
       mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
+    mbar_init(tbl, 4);
+    mbar_init(redo, 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&vfull[s], 4);
+      mbar_init(&vempty[s], 1);
+    }
     *s_abort = 0;
+    if (!SHRINK) *s_total = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
+    if (!SHRINK) tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
     tmem_alloc(s_tmem, C::kTmem);
@@ -614,6 +565,34 @@ __global__ void __launch_bounds__(192, 1)
             phase ^= 1u;
           }
         }
+        if (!SHRINK && ok && p.n > 0) {
+          ok = mbar_wait(tbl, 0u, s_abort);
+          const int total = ok ? *s_total : 0, blocks = (total + 3) / 4;
+          for (int j = rank; ok && j < blocks; j += S) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
+              ok = false;
+              break;
+            }
+            uint8_t* sa = smem + stage * C::kStage;
+            const int n = min(4, total - 4 * j);
+            mbar_expect_tx(&full[stage], static_cast<uint32_t>(n) * kRows * kGroup * 2);
+            for (int g = 0; g < n; ++g) {
+              const uint32_t gr = s_grp[4 * j + g];
+              const int row = grp_adapter(gr) * p.N;
+              uint8_t* to = sa + g * kRows * kGroup * 2;
+              if (p.swiglu) {
+                tma_load_2d(to, &tmB, &full[stage], grp_first(gr), row + blk * 64);
+                tma_load_2d(to + kRows * kGroup, &tmB, &full[stage], grp_first(gr), row + p.outs + blk * 64);
+              } else {
+                tma_load_2d(to, &tmB, &full[stage], grp_first(gr), row + blk * kRows);
+              }
+            }
+            if (++stage == C::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
         if (!ok) {
           fail(s_abort, p.status);
           // the copies issued into the slots end before the CTA does
@@ -642,6 +621,31 @@ __global__ void __launch_bounds__(192, 1)
             phase ^= 1u;
           }
         }
+        if (!SHRINK && ok && p.n > 0) {
+          ok = mbar_wait(tbl, 0u, s_abort);
+          const int total = ok ? *s_total : 0, blocks = (total + 3) / 4;
+          for (int j = rank, i = 0; ok && j < blocks; j += S, ++i) {
+            const int sl = i % C::kVSlots;
+            if (!mbar_wait(&full[stage], phase, s_abort) ||
+                !mbar_wait(&vfull[sl], (i / C::kVSlots) & 1, s_abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * C::kStage);
+            const uint64_t bd = sdesc_sw128(smem_u32(smem + C::kOffV + sl * NT * 128));
+            const int n = min(4, total - 4 * j);
+            for (int k = 0; k < n; ++k)     // a group is one k-step
+              umma_bf16(tmem + C::kCols, sdesc_sw32(sa + k * kRows * kGroup * 2), bd + 2u * k, idesc,
+                        (i | k) != 0 ? 1u : 0u);
+            umma_commit(&empty[stage]);
+            umma_commit(&vempty[sl]);
+            if (++stage == C::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
         if (!ok) fail(s_abort, p.status);
         umma_commit(tfull);
         if (!ok) mbar_wait(tfull, pass_parity, nullptr);
@@ -650,36 +654,40 @@ __global__ void __launch_bounds__(192, 1)
     } else if (!SHRINK) {
       const int e = threadIdx.x - 64;
       if (p.n > 0) {
-        const int half = p.swiglu ? 64 : kRows;
-        const int lr = (warp & 3) * 32 + lane;      // the TMEM lane this thread writes
-        const int o = blk * half + (lr < half ? lr : lr - half);
-        const int row = o < p.outs ? (lr < half ? o : p.outs + o) : -1;
-        int* s_rank = reinterpret_cast<int*>(s_grp);
-        const int first = t0 + rank * per, count = min(per, p.T - first);
-        for (int n = e; n < count; n += kWorkers) {
-          const int a = adapter_of(p, first + n);
-          s_ad[n] = a;
-          s_rank[n] = a >= 0 ? rank_of(p, a) : 0;
-        }
-        workers_sync();
-        // the factors into L2 while v is still being computed
-        for (int n = 0, last = -1; n < count; ++n) {
-          const int a = s_ad[n], r = s_rank[n];
-          if (a != last && row >= 0) {
-            const __nv_bfloat16* b = p.b + (static_cast<long long>(a) * p.N + row) * p.r_max;
-            for (int c = 0; c < r; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + c));
-          }
-          last = a;
-        }
+        // the adapters' indexes and ranks are inputs: read before v is there
+        groups = build_groups<NT>(p, t0, e, s_ad, s_grp, s_sum);
+        if (e == 0) *s_total = groups;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tbl);
+        const int blocks = (groups + 3) / 4;
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        adapter_terms(p, first, count, row, e, s_ad, s_rank, reinterpret_cast<float*>(smem + C::kOffV),
-                      tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + NT);
+        Block<NT> f;
+        f.place(e, s_grp, rank, groups);
+        f.load_v(p, e, s_ad, t0);
+        for (int j = rank, i = 0; j < blocks; j += S, ++i) {
+          const int sl = i % C::kVSlots;
+          int ok = 1;
+          if (lane == 0) ok = mbar_wait(&vempty[sl], ((i / C::kVSlots) & 1) ^ 1, s_abort) ? 1 : 0;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            if (lane == 0) fail(s_abort, p.status);
+            break;
+          }
+          f.store_v(e, smem + C::kOffV + sl * NT * 128);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vfull[sl]);
+          f.place(e, s_grp, j + S, groups);
+          f.load_v(p, e, s_ad, t0);
+        }
       }
     }
     if (warp >= 2) {
       int ok = 1;
       if (lane == 0) ok = mbar_wait(tfull, pass_parity, s_abort) ? 1 : 0;
       if (lane == 0 && !ok) fail(s_abort, p.status);
+      __syncwarp();
+      if (!SHRINK && 4 * rank < groups) look_over<NT>(p, smem, s_ad, s_grp, s_sum, redo, s_abort, tmem,
+                                                      blk, t0, rank, S, groups, threadIdx.x - 64);
     }
     pass_parity ^= 1u;
     __syncwarp();
@@ -692,6 +700,14 @@ __global__ void __launch_bounds__(192, 1)
       for (int n0 = 0; n0 < NT && t0 + n0 < p.T; n0 += 32) {
         uint32_t v[32];
         tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + n0, v);
+        if (!SHRINK && 4 * rank < groups) {      // this CTA had adapter k-blocks
+          uint32_t w[32];
+          tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + C::kCols + n0, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+        }
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -711,15 +727,13 @@ __global__ void __launch_bounds__(192, 1)
       __syncthreads();
     if (warp >= 2) {
       const int lr = (warp & 3) * 32 + lane, first = t0 + rank * per, count = min(per, p.T - first);
-      const int* ad = SHRINK ? s_ad + rank * per : s_ad;
+      const int* ad = s_ad + rank * per;
       const uint32_t* grp = s_grp + (SHRINK ? blk * 8 : 0);
-      const uint32_t term =
-          !SHRINK && p.n > 0 ? tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + NT : 0u;
       switch (S) {
-        case 1: finish<SHRINK, 1>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
-        case 2: finish<SHRINK, 2>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
-        case 4: finish<SHRINK, 4>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
-        default: finish<SHRINK, 8>(p, part, ad, grp, ng, first, count, per, blk, lr, term); break;
+        case 1: finish<SHRINK, 1>(p, part, ad, grp, ng, first, count, per, blk, lr); break;
+        case 2: finish<SHRINK, 2>(p, part, ad, grp, ng, first, count, per, blk, lr); break;
+        case 4: finish<SHRINK, 4>(p, part, ad, grp, ng, first, count, per, blk, lr); break;
+        default: finish<SHRINK, 8>(p, part, ad, grp, ng, first, count, per, blk, lr); break;
       }
     }
     if (SHRINK) {
@@ -1133,7 +1147,7 @@ Shape pick_shape(int T, int K, int outs, int rows_per_tile, int sm) {
   const double KB = (K + kBK - 1) / kBK;
   Shape best{0, 1};
   const double pair_tiles = static_cast<double>((T + 255) / 256) * ((outs + 2 * rows_per_tile - 1) / (2 * rows_per_tile));
-  const double pairs = sm / 2;
+  const double pairs = sm > 1 ? sm / 2 : 1;
   double least = std::ceil(pair_tiles / pairs) * KB * 0.33 + 6.0;
   const int rows = (outs + rows_per_tile - 1) / rows_per_tile;
   for (int nt = 16; nt <= 256; nt *= 2) {
@@ -1169,7 +1183,7 @@ constexpr long long kDotMax = 8192;
 template <int NT, bool SHRINK>
 cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t s) {
   using C = SwapCfg<NT, SHRINK>;
-  CUtensorMap tw, tx;
+  CUtensorMap tw, tx, tb;
   if (SHRINK) {
     if (!encode_tmap_bf16(&tw, g.a, static_cast<long long>(g.n_adapters) * g.r_max, g.K, g.K, kGroup))
       return cudaErrorInvalidValue;
@@ -1177,6 +1191,11 @@ cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t
     return cudaErrorInvalidValue;
   }
   if (!encode_tmap_bf16(&tx, g.x, g.T, g.K, g.ldx, NT)) return cudaErrorInvalidValue;
+  if (SHRINK || g.n_adapters == 0)
+    tb = tx;                              // not used
+  else if (!encode_tmap_bf16(&tb, g.b, static_cast<long long>(g.n_adapters) * g.N, g.r_max, g.r_max,
+                             g.swiglu ? 64 : kRows, kGroup))
+    return cudaErrorInvalidValue;
   const int KB = (g.K + kBK - 1) / kBK;
   const int tt = (g.T + NT - 1) / NT;
   int rows;                               // blocks of 128 rows
@@ -1197,7 +1216,7 @@ cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t
   static bool done[64] = {false};
   const cudaError_t e = set_smem_once(kern, static_cast<int>(C::kSmem), done);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kern, dim3(S, rows, tt), 192, static_cast<int>(C::kSmem), S, s, tw, tx, p);
+  return launch_cluster(kern, dim3(S, rows, tt), 192, static_cast<int>(C::kSmem), S, s, tw, tx, tb, p);
 }
 
 cudaError_t run_shrink(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
@@ -1243,7 +1262,7 @@ cudaError_t run_pair(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t lora_workspace_bytes(int T, int r_max) { return static_cast<size_t>(T) * r_max * 4; }
+size_t lora_workspace_bytes(int T, int r_max) { return static_cast<size_t>(T) * r_max * 2; }
 
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   LoraParams p{};
@@ -1251,7 +1270,7 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   p.ranks = g.ranks;
   p.scales = g.scales;
   p.adapter = g.adapter;
-  p.v = g.ws;
+  p.v = static_cast<__nv_bfloat16*>(g.ws);
   p.y = static_cast<__nv_bfloat16*>(g.y);
   p.ldy = g.ldy;
   p.T = g.T;
@@ -1266,7 +1285,6 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   if (g.T == 0) return cudaSuccess;
   const Shape shape = pick_shape(g.T, g.K, p.outs, g.swiglu ? 64 : kRows, g.sm_count);
   const bool pair = shape.nt == 0;
-  p.v_bf16 = pair;
   if (g.n_adapters > 0) {
     cudaError_t e;
     if (static_cast<long long>(g.T) * g.r_max <= kDotMax)

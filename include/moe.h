@@ -501,12 +501,10 @@ moe_status moe_block_norm_backward(const moe_norm_desc* desc, const void* residu
  * A projection that all requests share, with a low-rank adapter per request:
  *     y_t = x_t W^T + scale_a (x_t A_a^T) B_a^T,      a = adapter_idx[t], or none (-1)
  * and with `swiglu` SiLU(y[0, N/2)) * y[N/2, N) (the gate|up projection of a
- * shared expert).  Sums in fp32; y is rounded once, and with many tokens the
- * low-rank intermediate is rounded to bf16 as a tensor-core operand.  Whatever
- * is in one adapter or one token's x, the other tokens' results are what they
- * are without it.  An element of B in use that is Inf or NaN leaves its own
- * adapter's tokens without a defined result; with many tokens it is also
- * reported (MOE_ERR_NONFINITE).
+ * shared expert).  Sums in fp32; the low-rank intermediate is rounded to bf16
+ * as a tensor-core operand, y once at the end.  An element of B in use that is
+ * Inf or NaN counts as 0 and is reported (MOE_ERR_NONFINITE); whatever is in one
+ * adapter or one token's x, the other tokens' results are what they are without.
  */
 typedef struct {
   int32_t T, K, N;            /* tokens, input and output features; K % 8 == 0          */
