@@ -13,12 +13,14 @@
 //   dw_post = sum_t dz n;   dw_pre = sum_t dh m
 // r' and both rstd are computed again from r, y and g: the row is in shared
 // memory anyway, so the backward pass reads nothing that the forward pass
-// would have had to store.
+// would have had to store.  The sums of both norms' gradients are taken in one
+// round, which rearranges a(dz w_post n) into three sums over r'.
 //
 // Bound: memory.  A group of TPR threads owns a row, EPT elements a thread, and
-// walks over rows with a ring of row slots that bulk copies fill ahead, so the
-// loads of the next rows run under the two (three backward) row sums of this
-// one.  Rows of any alignment are copied as the 16-byte granules around them.
+// walks over rows with a ring of row slots that bulk copies fill ahead.  Row
+// sums cost a barrier each, so there is one round of them per row: sum(y^2) of
+// the next row is taken with the sums of this one.  Rows of any alignment are
+// copied as the 16-byte granules around them.
 // Sums and everything between load and store are fp32; each output is rounded
 // once.
 #include "moe_common.cuh"
@@ -28,7 +30,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxThreads = 1024;
 constexpr uint32_t kSmemBudget = 200 * 1024;
 
 template <typename T>
@@ -113,6 +114,53 @@ __device__ __forceinline__ void store_row(T* __restrict__ p, const Cols<VEC>& c,
   }
 }
 
+// A thread's elements of a row as they are in memory (bf16 two to a register),
+// for what is kept across rows or sums.
+template <typename T, int VEC, int EPT>
+struct Kept;
+template <int VEC, int EPT>
+struct Kept<float, VEC, EPT> {
+  float v[EPT];
+  __device__ __forceinline__ void load(const float* p, const Cols<VEC>& c) {
+    load_row<float, VEC, EPT>(p, c, v);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) v[e] = 0.f;
+  }
+  __device__ __forceinline__ float operator[](int e) const { return v[e]; }
+};
+template <int VEC, int EPT>
+struct Kept<__nv_bfloat16, VEC, EPT> {
+  uint32_t v[EPT / 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const Cols<VEC>& c) {
+    if constexpr (VEC == 1) {
+      const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+      for (int e = 0; e < EPT; e += 2)
+        v[e / 2] = (c.col(e) < c.H ? u[c.col(e)] : 0u) |
+                   (c.col(e + 1) < c.H ? static_cast<uint32_t>(u[c.col(e + 1)]) << 16 : 0u);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPT; e += 8) {
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (c.col(e) < c.H) q = *reinterpret_cast<const uint4*>(p + c.col(e));
+        v[e / 2] = q.x;
+        v[e / 2 + 1] = q.y;
+        v[e / 2 + 2] = q.z;
+        v[e / 2 + 3] = q.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < EPT / 2; ++e) v[e] = 0u;
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    return (e & 1) ? bf16hi(v[e / 2]) : bf16lo(v[e / 2]);
+  }
+};
+
 struct NormParams {
   int T, H;
   int tpr, groups, slots;       // threads per row, row groups per CTA, ring slots per group
@@ -157,35 +205,60 @@ __device__ __forceinline__ uint32_t skew(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
 }
 
-// Sums N values over the group's threads; every thread gets the sums.  `red`
-// holds one buffer per parity: a buffer is written again only two sums later,
-// behind the barrier of the sum between, which follows everyone's reads.
+constexpr int kSumFloats = 8 * 32;    // up to eight sums of up to 32 warps
+
+// Sums N (2 or 8) values over the group's threads, in a fixed order; every
+// thread gets the sums.  `red` holds one buffer per parity: a buffer is written
+// again only two sums later, behind the barrier of the sum between, which
+// follows everyone's reads.
+// Eight values fold into one per lane quad while they are added (9 shuffles
+// instead of 40).
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], int tpr, int bar, int tid, float* red,
                                           int& parity) {
+  static_assert(N == 2 || N == 8, "two or eight sums");
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = tid & 31;
+  // lane holds the sum of value lane * N / 32 over its warp
+  float part;
+  if constexpr (N == 8) {
+    float a[4], b[2];
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+    for (int i = 0; i < 4; ++i) {
+      const float keep = (lane & 16) ? v[i + 4] : v[i], send = (lane & 16) ? v[i] : v[i + 4];
+      a[i] = keep + __shfl_xor_sync(kAll, send, 16);
+    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-  if (tpr == 32) {
-    __syncwarp();
-    return;
+    for (int i = 0; i < 2; ++i) {
+      const float keep = (lane & 8) ? a[i + 2] : a[i], send = (lane & 8) ? a[i] : a[i + 2];
+      b[i] = keep + __shfl_xor_sync(kAll, send, 8);
+    }
+    const float keep = (lane & 4) ? b[1] : b[0], send = (lane & 4) ? b[0] : b[1];
+    part = keep + __shfl_xor_sync(kAll, send, 4);
+  } else {
+    const float keep = (lane & 16) ? v[1] : v[0], send = (lane & 16) ? v[0] : v[1];
+    part = keep + __shfl_xor_sync(kAll, send, 16);
+    part += __shfl_xor_sync(kAll, part, 8);
+    part += __shfl_xor_sync(kAll, part, 4);
   }
-  float* buf = red + parity * 64;
-  parity ^= 1;
-  const int warp = tid >> 5, nw = tpr >> 5;
-  if ((tid & 31) == 0) {
+  part += __shfl_xor_sync(kAll, part, 2);
+  part += __shfl_xor_sync(kAll, part, 1);
+  if (tpr > 32) {
+    constexpr int kLanes = 32 / N;      // lanes of a value
+    float* buf = red + parity * kSumFloats;
+    parity ^= 1;
+    const int warp = tid >> 5, nw = tpr >> 5, value = lane / kLanes;
+    if (lane % kLanes == 0) buf[value * 32 + warp] = part;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+    part = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) buf[i * 32 + warp] = v[i];
+    for (int w = 0; w < 32; w += kLanes)
+      if (w + lane % kLanes < nw) part += buf[value * 32 + w + lane % kLanes];
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) part += __shfl_xor_sync(kAll, part, off);
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float t = (tid & 31) < nw ? buf[i * 32 + (tid & 31)] : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    v[i] = t;
-  }
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kAll, part, i * (32 / N));
 }
 
 // Shared memory: [groups][slots] row slots, then the sum buffers, then barriers.
@@ -196,7 +269,7 @@ __host__ __device__ inline NormSmem norm_smem(uint32_t slot_bytes, int slots, in
   NormSmem o;
   uint32_t b = slot_bytes * static_cast<uint32_t>(slots) * static_cast<uint32_t>(groups);
   o.red = b;
-  b += static_cast<uint32_t>(groups) * 128 * 4;
+  b += static_cast<uint32_t>(groups) * 2 * kSumFloats * 4;
   o.bars = b;
   b += static_cast<uint32_t>(groups * slots) * 8;
   o.total = b;
@@ -258,13 +331,13 @@ struct Ring {
   }
 };
 
-template <typename R, typename A, int VEC, int EPT>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormParams p) {
+template <typename R, typename A, int VEC, int EPT, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const NormSmem L = norm_smem(p.slot_bytes, p.slots, p.groups);
   const int group = threadIdx.x / p.tpr, tid = threadIdx.x - group * p.tpr;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
-  float* red = reinterpret_cast<float*>(smem + L.red) + group * 128;
+  float* red = reinterpret_cast<float*>(smem + L.red) + group * 2 * kSumFloats;
   Ring<R, A, false> ring;
   ring.base = smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes;
   ring.full = bars + group * p.slots;
@@ -283,67 +356,78 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormParam
     for (int s = 0; s < p.slots; ++s)
       if (first + s * step < p.T) ring.fill(s, first + s * step);
   const Cols<VEC> c{tid, p.tpr, p.H};
-  float w_post[EPT], w_pre[EPT], gate[EPT];
   const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr;
-  if (post) load_row<A, VEC, EPT>(static_cast<const A*>(p.w_post), c, w_post);
-  if (pre) load_row<A, VEC, EPT>(static_cast<const A*>(p.w_pre), c, w_pre);
-  if (p.gate == MOE_GATE_CHANNEL) load_row<A, VEC, EPT>(static_cast<const A*>(p.gate_p), c, gate);
-#pragma unroll
-  for (int e = 0; e < EPT; ++e) {
-    w_post[e] = post ? w_post[e] + p.offset : 1.f;
-    w_pre[e] = pre ? w_pre[e] + p.offset : 1.f;
-    if (p.gate == MOE_GATE_CHANNEL) w_post[e] *= gate[e];
-    w_post[e] *= p.bs;
-  }
+  Kept<A, VEC, EPT> w_post, w_pre;
+  w_post.zero();
+  w_pre.zero();
+  if (post) w_post.load(static_cast<const A*>(p.w_post), c);
+  if (pre) w_pre.load(static_cast<const A*>(p.w_pre), c);
   const float inv_h = 1.f / static_cast<float>(p.H);
+  const bool ahead = p.slots > 1;     // the next row is there while this one is at work
   int slot = 0, parity = 0;
   uint32_t phase = 0;
+  Kept<A, VEC, EPT> x;                // y of the row
+  float sq = 0.f;                     // its sum of squares
+  auto take_y = [&](int t, int sl, uint32_t ph) {
+    if (!mbar_wait(ring.full + sl, ph, nullptr)) report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+    const uint8_t* at = ring.base + static_cast<uint32_t>(sl) * p.slot_bytes + p.pitch_r;
+    x.zero();
+    if (p.y != nullptr) x.load(reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.y_row(t)) : 0)), c);
+    float q = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) q += x[e] * x[e];
+    return q;
+  };
   for (int t = first; t < p.T; t += step) {
-    float tg = 1.f;
-    if (p.gate == MOE_GATE_TOKEN) tg = to_f<A>(static_cast<const A*>(p.gate_p)[t]);
-    if (!mbar_wait(ring.full + slot, phase, nullptr)) report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+    if (t == first || !ahead) {
+      float q[2] = {take_y(t, slot, phase), 0.f};
+      group_sum<2>(q, p.tpr, 1 + group, tid, red, parity);
+      sq = q[0];
+    }
+    float scale = p.bs;
+    if (p.gate == MOE_GATE_TOKEN) scale *= to_f<A>(static_cast<const A*>(p.gate_p)[t]);
+    if (post) scale *= rsqrtf(sq * inv_h + p.eps);
     const uint8_t* at = ring.base + static_cast<uint32_t>(slot) * p.slot_bytes;
-    float v[EPT], x[EPT];
+    float v[EPT];
     load_row<R, VEC, EPT>(reinterpret_cast<const R*>(at + (VEC == 1 ? skew(ring.r_row(t)) : 0)), c, v);
-    at += p.pitch_r;
-    float q[1] = {0.f};
-    if (p.y != nullptr) {
-      load_row<A, VEC, EPT>(reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.y_row(t)) : 0)), c, x);
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) q[0] += x[e] * x[e];
-    }
-    at += p.pitch_a;
+    at += p.pitch_r + p.pitch_a;
+    const A* gate = nullptr;
     if (p.gate == MOE_GATE_FULL)
-      load_row<A, VEC, EPT>(reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.g_row(t)) : 0)), c, gate);
-    // every thread has its part of the slot behind this barrier
-    group_sum<1>(q, p.tpr, 1 + group, tid, red, parity);
-    if (tid == 0 && t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
-    if (++slot == p.slots) {
-      slot = 0;
-      phase ^= 1u;
-    }
-    if (p.y != nullptr) {
-      const float f = (post ? rsqrtf(q[0] * inv_h + p.eps) : 1.f) * tg;
+      gate = reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.g_row(t)) : 0));
+    else if (p.gate == MOE_GATE_CHANNEL)
+      gate = static_cast<const A*>(p.gate_p);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        float z = x[e] * f * w_post[e];
-        if (p.gate == MOE_GATE_FULL) z *= gate[e];
-        v[e] = p.rs * v[e] + z;
-      }
+    for (int e = 0; e < EPT; ++e) v[e] *= p.rs;
+    if (gate != nullptr) {
+      Kept<A, VEC, EPT> g;
+      g.load(gate, c);
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) v[e] += x[e] * scale * (post ? w_post[e] + p.offset : 1.f) * g[e];
+    } else if (post) {
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) v[e] += x[e] * scale * (w_post[e] + p.offset);
     } else {
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] *= p.rs;
+      for (int e = 0; e < EPT; ++e) v[e] += x[e] * scale;
     }
     if (p.out != nullptr)
       store_row<R, VEC, EPT>(static_cast<R*>(p.out) + static_cast<long long>(t) * p.ld_out, c, v);
-    if (pre) {
-      q[0] = 0.f;
+    float q[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) q[0] += v[e] * v[e];
-      group_sum<1>(q, p.tpr, 1 + group, tid, red, parity);
+    for (int e = 0; e < EPT; ++e) q[0] += v[e] * v[e];
+    const int next = slot + 1 == p.slots ? 0 : slot + 1;
+    const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+    if (ahead && t + step < p.T) q[1] = take_y(t + step, next, next_phase);
+    // behind this barrier every thread has its part of the slot
+    group_sum<2>(q, p.tpr, 1 + group, tid, red, parity);
+    if (tid == 0 && t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
+    slot = next;
+    phase = next_phase;
+    sq = q[1];
+    if (pre) {
       const float f = rsqrtf(q[0] * inv_h + p.eps);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] *= f * w_pre[e];
+      for (int e = 0; e < EPT; ++e) v[e] *= f * (w_pre[e] + p.offset);
       store_row<A, VEC, EPT>(static_cast<A*>(p.h) + static_cast<long long>(t) * p.ld_h, c, v);
     }
   }
@@ -371,13 +455,13 @@ __device__ __forceinline__ void cta_columns(float* buf, float* dst, const Cols<V
   }
 }
 
-template <typename R, typename A, int VEC, int EPT>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_backward_kernel(const NormParams p) {
+template <typename R, typename A, int VEC, int EPT, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const NormSmem L = norm_smem(p.slot_bytes, p.slots, p.groups);
   const int group = threadIdx.x / p.tpr, tid = threadIdx.x - group * p.tpr;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
-  float* red = reinterpret_cast<float*>(smem + L.red) + group * 128;
+  float* red = reinterpret_cast<float*>(smem + L.red) + group * 2 * kSumFloats;
   Ring<R, A, true> ring;
   ring.base = smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes;
   ring.full = bars + group * p.slots;
@@ -396,22 +480,50 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_backward_kernel(const 
     for (int s = 0; s < p.slots; ++s)
       if (first + s * step < p.T) ring.fill(s, first + s * step);
   const Cols<VEC> c{tid, p.tpr, p.H};
-  const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr;
+  const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr, branch = p.y != nullptr;
   const float inv_h = 1.f / static_cast<float>(p.H);
   float a_post[EPT], a_pre[EPT], a_gate[EPT];   // column sums of dw_post, dw_pre, dg
 #pragma unroll
   for (int e = 0; e < EPT; ++e) a_post[e] = a_pre[e] = a_gate[e] = 0.f;
-  int slot = 0, parity = 0;
+  Kept<A, VEC, EPT> w_post, w_pre;
+  w_post.zero();
+  w_pre.zero();
+  if (post) w_post.load(static_cast<const A*>(p.w_post), c);
+  if (pre) w_pre.load(static_cast<const A*>(p.w_pre), c);
+  // Rows behind this one's sums: a slot is filled again behind the sums of the
+  // next row, so three are needed for sum(y^2) to run a row ahead.
+  const bool ahead = p.slots > 2;
+  auto wait = [&](int sl, uint32_t ph) {
+    if (!mbar_wait(ring.full + sl, ph, nullptr)) report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+  };
+  auto y_at = [&](int t, int sl) {
+    return reinterpret_cast<const A*>(ring.base + static_cast<uint32_t>(sl) * p.slot_bytes + p.pitch_r +
+                                      (VEC == 1 ? skew(ring.y_row(t)) : 0));
+  };
+  auto squares = [&](int t, int sl) {
+    Kept<A, VEC, EPT> y;
+    y.load(y_at(t, sl), c);
+    float q = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) q += y[e] * y[e];
+    return q;
+  };
+  int slot = 0, parity = 0, before = 0;
   uint32_t phase = 0;
+  float sq = 0.f;                               // sum of squares of the row's y
   for (int t = first; t < p.T; t += step) {
-    float tg = 1.f;
+    if (t == first || !ahead) {
+      wait(slot, phase);
+      float q[2] = {post ? squares(t, slot) : 0.f, 0.f};
+      if (post) group_sum<2>(q, p.tpr, 1 + group, tid, red, parity);
+      sq = q[0];
+    }
+    const float fy = post ? rsqrtf(sq * inv_h + p.eps) : 1.f;
+    float tg = 1.f;                             // gate of the token
     if (p.gate == MOE_GATE_TOKEN) tg = to_f<A>(static_cast<const A*>(p.gate_p)[t]);
-    if (!mbar_wait(ring.full + slot, phase, nullptr)) report(p.status, MOE_ERR_DEVICE_TIMEOUT);
     const uint8_t* at = ring.base + static_cast<uint32_t>(slot) * p.slot_bytes;
     const R* s_r = reinterpret_cast<const R*>(at + (VEC == 1 ? skew(ring.r_row(t)) : 0));
-    at += p.pitch_r;
-    const A* s_y = reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.y_row(t)) : 0));
-    at += p.pitch_a;
+    at += p.pitch_r + p.pitch_a;
     const A* s_g = nullptr;
     if (p.gate == MOE_GATE_FULL) {
       s_g = reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.g_row(t)) : 0));
@@ -423,121 +535,101 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_backward_kernel(const 
     at += p.pitch_r;
     const A* s_dh = reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.dh_row(t)) : 0));
 
-    float n[EPT], w[EPT], z[EPT], d[EPT];   // n = y rstd(y), z = n w_post
-    float fy = 1.f;
-    if (p.y != nullptr) {
-      load_row<A, VEC, EPT>(s_y, c, n);
-      if (post) {
-        float q[1] = {0.f};
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) q[0] += n[e] * n[e];
-        group_sum<1>(q, p.tpr, 1 + group, tid, red, parity);
-        fy = rsqrtf(q[0] * inv_h + p.eps);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) n[e] = 0.f;
+    // n = y rstd(y) and u = bs g n w_post (without the token's gate), element
+    // by element again in both passes below
+    Kept<A, VEC, EPT> y, g, dh;
+    Kept<R, VEC, EPT> dr, r;
+    y.zero();
+    dr.zero();
+    r.zero();
+    dh.zero();
+    if (branch) y.load(y_at(t, slot), c);
+    if (s_g != nullptr) g.load(s_g, c);
+    if (p.d_out != nullptr) dr.load(s_do, c);
+    if (pre) {
+      r.load(s_r, c);
+      dh.load(s_dh, c);
     }
+    const float su = p.bs * fy;
+    auto u_of = [&](int e) {
+      float u = y[e] * su;
+      if (post) u *= w_post[e] + p.offset;
+      if (s_g != nullptr) u *= g[e];
+      return u;
+    };
+    // one round of sums for both norms: with m~ = r', d = dh w_pre,
+    //   mean(d m) = f^2 sum(d m~) / H,  f = rstd(r')
+    //   sum(D u) = sum(dr' u) + f sum(d u) - f mean sum(m~ u)
+    float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
-      n[e] *= fy;
-      z[e] = n[e];
+      const float u = u_of(e), m = p.rs * r[e] + tg * u, d = dh[e] * (w_pre[e] + p.offset);
+      q[0] += m * m;
+      q[1] += d * m;
+      q[2] += dr[e] * u;
+      q[3] += d * u;
+      q[4] += m * u;
     }
-    if (post) {
-      load_row<A, VEC, EPT>(static_cast<const A*>(p.w_post), c, w);
+    const int next = slot + 1 == p.slots ? 0 : slot + 1;
+    const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+    if (ahead && t + step < p.T) {
+      wait(next, next_phase);
+      if (post) q[5] = squares(t + step, next);
+    }
+    // behind this barrier everyone is done with the row before
+    group_sum<8>(q, p.tpr, 1 + group, tid, red, parity);
+    if (ahead && tid == 0 && t != first && t + (p.slots - 1) * step < p.T)
+      ring.fill(before, t + (p.slots - 1) * step);
+    sq = q[5];
+    const float f = pre ? rsqrtf(q[0] * inv_h + p.eps) : 0.f, mean_h = q[1] * inv_h * f * f;
+    const float sum_u = q[2] + f * (q[3] - mean_h * q[4]);
+    if (p.gate == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(p.d_gate)[t] = sum_u;
+    float D[EPT], o[EPT];                       // the whole gradient at r'
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) z[e] *= w[e] + p.offset;
+    for (int e = 0; e < EPT; ++e) {
+      const float m = p.rs * r[e] + tg * u_of(e);
+      a_pre[e] += dh[e] * m * f;
+      D[e] = dr[e] + f * (dh[e] * (w_pre[e] + p.offset) - m * mean_h);
+      o[e] = p.rs * D[e];
     }
-    if (p.d_out != nullptr) {
-      load_row<R, VEC, EPT>(s_do, c, d);
-    } else {
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) d[e] = 0.f;
-    }
-    if (pre) {
-      float m[EPT], dm[EPT];
-      load_row<R, VEC, EPT>(s_r, c, m);
+    store_row<R, VEC, EPT>(static_cast<R*>(p.out) + static_cast<long long>(t) * p.ld_out, c, o);
+    if (branch) {
       if (s_g != nullptr) {
-        load_row<A, VEC, EPT>(s_g, c, dm);
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) m[e] = p.rs * m[e] + p.bs * dm[e] * z[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) m[e] = p.rs * m[e] + p.bs * tg * z[e];
-      }
-      load_row<A, VEC, EPT>(s_dh, c, dm);
-      load_row<A, VEC, EPT>(static_cast<const A*>(p.w_pre), c, w);
-      float q[2] = {0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        q[0] += m[e] * m[e];
-        q[1] += dm[e] * (w[e] + p.offset) * m[e];
-      }
-      group_sum<2>(q, p.tpr, 1 + group, tid, red, parity);
-      const float f = rsqrtf(q[0] * inv_h + p.eps);
-      const float mean = q[1] * inv_h * f * f;   // mean(dh w m~) rstd^2 with m~ = r'
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        a_pre[e] += dm[e] * m[e] * f;
-        d[e] += f * (dm[e] * (w[e] + p.offset) - m[e] * mean);
-      }
-    }
-    {
-      float dr[EPT];
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) dr[e] = p.rs * d[e];
-      store_row<R, VEC, EPT>(static_cast<R*>(p.out) + static_cast<long long>(t) * p.ld_out, c, dr);
-    }
-    if (p.y != nullptr) {
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) d[e] *= p.bs;
-      float q[2] = {0.f, 0.f};   // sum d z (token gate), sum dz w n
-      if (s_g != nullptr) {
-        float g[EPT];
-        load_row<A, VEC, EPT>(s_g, c, g);
-        if (p.gate == MOE_GATE_FULL) {
-          float dg[EPT];
-#pragma unroll
-          for (int e = 0; e < EPT; ++e) dg[e] = d[e] * z[e];
-          store_row<A, VEC, EPT>(static_cast<A*>(p.d_gate) + static_cast<long long>(t) * p.ld_g, c, dg);
-        } else {
-#pragma unroll
-          for (int e = 0; e < EPT; ++e) a_gate[e] += d[e] * z[e];
-        }
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) d[e] *= g[e];
-      }
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) q[0] += d[e] * z[e];
-      group_sum<1>(reinterpret_cast<float(&)[1]>(q[0]), p.tpr, 1 + group, tid, red, parity);
-      // token gate: d is without g, so the sum is dg itself and g times it is sum dz z
-      if (p.gate == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(p.d_gate)[t] = q[0];
-      const float mean = q[0] * tg * inv_h;
-      float dy[EPT];
-      if (post) {
-        load_row<A, VEC, EPT>(static_cast<const A*>(p.w_post), c, w);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-          const float dz = d[e] * tg;
-          a_post[e] += dz * n[e];
-          dy[e] = fy * (dz * (w[e] + p.offset) - n[e] * mean);
+          o[e] = D[e] * y[e] * su;
+          if (post) o[e] *= w_post[e] + p.offset;
+          a_gate[e] += o[e];
+          D[e] *= g[e];
+        }
+        if (p.gate == MOE_GATE_FULL)
+          store_row<A, VEC, EPT>(static_cast<A*>(p.d_gate) + static_cast<long long>(t) * p.ld_g, c, o);
+      }
+      // sum(dz z) over the row is the token's gate times sum(D u)
+      const float mean_y = sum_u * tg * inv_h, s = p.bs * tg;
+      if (post) {
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+          const float dz = s * D[e], n = y[e] * fy;
+          a_post[e] += dz * n;
+          D[e] = fy * (dz * (w_post[e] + p.offset) - n * mean_y);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) dy[e] = d[e] * tg;
+        for (int e = 0; e < EPT; ++e) D[e] *= s;
       }
-      store_row<A, VEC, EPT>(static_cast<A*>(p.h) + static_cast<long long>(t) * p.ld_h, c, dy);
+      store_row<A, VEC, EPT>(static_cast<A*>(p.h) + static_cast<long long>(t) * p.ld_h, c, D);
     }
-    // everyone is done with the slot
-    if (p.tpr == 32)
-      __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.tpr) : "memory");
-    if (tid == 0 && t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
-    if (++slot == p.slots) {
-      slot = 0;
-      phase ^= 1u;
+    if (!ahead) {
+      if (p.tpr == 32)
+        __syncwarp();
+      else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.tpr) : "memory");
+      if (tid == 0 && t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
     }
+    before = slot;
+    slot = next;
+    phase = next_phase;
   }
   if (p.n_part > 0) {
     float* buf = reinterpret_cast<float*>(smem);
@@ -581,15 +673,15 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
 uint32_t row_pitch(int H, int es) { return (static_cast<uint32_t>(H) * es + 15u + 16u) & ~15u; }
 
 // Threads a row, groups and slots: EPT elements a thread; as many groups as
-// fit 1024 threads and the slots' memory, down to one group of one slot.
-void shape_of(NormParams& p, int ept, int rows_r, int rows_a, int es_r, int es_a, int sm) {
+// fit the threads of a CTA and the slots' memory, down to one group of one slot.
+void shape_of(NormParams& p, int ept, int max_threads, int rows_r, int rows_a, int es_r, int es_a, int sm) {
   int tpr = (p.H + ept - 1) / ept;
   tpr = (tpr + 31) / 32 * 32;
   p.tpr = tpr;
   p.pitch_r = row_pitch(p.H, es_r);
   p.pitch_a = row_pitch(p.H, es_a);
   p.slot_bytes = (rows_r * p.pitch_r + rows_a * p.pitch_a + 127u) & ~127u;
-  int groups = kMaxThreads / tpr;
+  int groups = max_threads / tpr;
   if (tpr > 32 && groups > 15) groups = 15;     // one named barrier each
   // no more groups than there are rows for
   const int need = (p.T + sm - 1) / sm;
@@ -601,31 +693,44 @@ void shape_of(NormParams& p, int ept, int rows_r, int rows_a, int es_r, int es_a
   p.slots = slots;
 }
 
-template <typename R, typename A, int VEC, int EPT>
-cudaError_t run(const NormParams& p, bool back, int grid, cudaStream_t s) {
-  static bool done[64] = {false}, done_b[64] = {false};
+template <typename R, typename A, int VEC, int EPT, int MAXT, bool BACK>
+cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
+  static bool done[64] = {false};
+  shape_of(p, EPT, MAXT, rows_r, rows_a, sizeof(R), sizeof(A), sm);
+  const int want = (p.T + p.groups - 1) / p.groups;
+  *grid = want < sm ? want : sm;
   const uint32_t smem = norm_smem(p.slot_bytes, p.slots, p.groups).total;
-  const dim3 g(grid), b(p.tpr * p.groups);
+  auto go = [&](auto k) {
+    const cudaError_t e = set_smem_once(k, 227 * 1024, done);
+    return e != cudaSuccess ? e : launch_pdl(k, dim3(*grid), dim3(p.tpr * p.groups), smem, s, p);
+  };
+  if constexpr (BACK)
+    return go(block_norm_backward_kernel<R, A, VEC, EPT, MAXT>);
+  else
+    return go(block_norm_kernel<R, A, VEC, EPT, MAXT>);
+}
+
+// Elements a thread and threads a CTA.  The backward pass holds three column
+// sums per element: 512 threads have the registers for it (with 1024 it spilled
+// and took three times as long).  Forward, 16 elements from 1024 columns up, so
+// that two or more rows are at work on an SM and one's sums run under another's.
+template <typename R, typename A, int VEC>
+cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
   if (back) {
-    auto k = block_norm_backward_kernel<R, A, VEC, EPT>;
-    const cudaError_t e = set_smem_once(k, 227 * 1024, done_b);
-    return e != cudaSuccess ? e : launch_pdl(k, g, b, smem, s, p);
+    if (p.H <= 8 * 512) return run<R, A, VEC, 8, 512, true>(p, rows_r, rows_a, sm, grid, s);
+    if (p.H <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
+    return run<R, A, VEC, 32, 512, true>(p, rows_r, rows_a, sm, grid, s);
   }
-  auto k = block_norm_kernel<R, A, VEC, EPT>;
-  const cudaError_t e = set_smem_once(k, 227 * 1024, done);
-  return e != cudaSuccess ? e : launch_pdl(k, g, b, smem, s, p);
+  if (p.H <= 1024) return run<R, A, VEC, 8, 1024, false>(p, rows_r, rows_a, sm, grid, s);
+  if (p.H <= 16 * 896) return run<R, A, VEC, 16, 896, false>(p, rows_r, rows_a, sm, grid, s);
+  return run<R, A, VEC, 16, 1024, false>(p, rows_r, rows_a, sm, grid, s);
 }
 
 template <typename R, typename A>
-cudaError_t pick(NormParams& p, bool back, bool vec, int rows_r, int rows_a, int sm, int* grid,
-                 cudaStream_t s) {
-  const int ept = p.H <= 8 * kMaxThreads ? 8 : 16;
-  shape_of(p, ept, rows_r, rows_a, sizeof(R), sizeof(A), sm);
-  const int want = (p.T + p.groups - 1) / p.groups;
-  *grid = want < sm ? want : sm;
-  if (ept == 8)
-    return vec ? run<R, A, 8, 8>(p, back, *grid, s) : run<R, A, 1, 8>(p, back, *grid, s);
-  return vec ? run<R, A, 8, 16>(p, back, *grid, s) : run<R, A, 1, 16>(p, back, *grid, s);
+cudaError_t pick_vec(NormParams& p, bool back, bool vec, int rows_r, int rows_a, int sm, int* grid,
+                     cudaStream_t s) {
+  return vec ? pick<R, A, 8>(p, back, rows_r, rows_a, sm, grid, s)
+             : pick<R, A, 1>(p, back, rows_r, rows_a, sm, grid, s);
 }
 
 }  // namespace
@@ -700,11 +805,11 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
   int grid = 1;
   cudaError_t e;
   if (a.residual_f32 && a.act_f32)
-    e = pick<float, float>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
+    e = pick_vec<float, float>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
   else if (a.residual_f32)
-    e = pick<float, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
+    e = pick_vec<float, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
   else
-    e = pick<__nv_bfloat16, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
+    e = pick_vec<__nv_bfloat16, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
   if (e != cudaSuccess || p.n_part == 0) return e;
   const long long width = static_cast<long long>(p.n_part) * a.H;
   return launch_pdl(column_sum_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(256), 0,
