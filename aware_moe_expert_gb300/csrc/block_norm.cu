@@ -19,8 +19,13 @@
 // Bound: memory.  A group of TPR threads owns a row, EPT elements a thread, and
 // walks over rows with a ring of row slots that bulk copies fill ahead.  Row
 // sums cost a barrier each, so there is one round of them per row: sum(y^2) of
-// the next row is taken with the sums of this one.  Rows of any alignment are
-// copied as the 16-byte granules around them.
+// the next row is taken with the sums of this one.
+// Rows need no alignment: they are copied as the 16-byte granules around them,
+// and a thread's eight columns are the ones of an aligned 16-byte (32-byte for
+// fp32) piece of memory.  A group's rows are a multiple of eight apart, so all of them
+// start at the same place of such a piece, and a thread keeps its columns,
+// weights and column sums.  Only tensors whose rows start at different places
+// from each other take one column at a time.
 // Sums and everything between load and store are fp32; each output is rounded
 // once.
 #include "moe_common.cuh"
@@ -32,13 +37,8 @@ namespace {
 
 constexpr uint32_t kSmemBudget = 200 * 1024;
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T>
 __device__ __forceinline__ T from_f(float v);
 template <>
@@ -46,84 +46,73 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// A thread's EPT elements of a row of H.  VEC = 8: vectors of eight columns,
-// (tid + v TPR) 8 ...; VEC = 1: columns tid + e TPR.
-template <int VEC>
+// How a thread's EPT elements lie in a row of H columns.
+enum Vec {
+  kOne = 1,      // columns tid + e tpr, one at a time
+  kPieces = 8,   // whole pieces of eight columns
+  kSkewed = 9    // pieces of eight columns, the first of which begins `skew` before the row
+};
+
+template <int VEC, int EPT>
 struct Cols {
-  int tid, tpr, H;
+  int tid, tpr, H, skew;
+  uint32_t mask[VEC == kSkewed ? (EPT + 31) / 32 : 1];   // kSkewed: bit e: element e is in the row
+  __device__ __forceinline__ Cols(int tid_, int tpr_, int H_, int skew_)
+      : tid(tid_), tpr(tpr_), H(H_), skew(skew_) {
+    if constexpr (VEC == kSkewed) {
+#pragma unroll
+      for (int i = 0; i < (EPT + 31) / 32; ++i) mask[i] = 0u;
+#pragma unroll
+      for (int e = 0; e < EPT; ++e)
+        if (static_cast<unsigned>(col(e)) < static_cast<unsigned>(H)) mask[e / 32] |= 1u << (e % 32);
+    }
+  }
+  // first column of piece v, and its place from the first piece's start
+  __device__ __forceinline__ int place(int v) const { return (tid + v * tpr) * 8; }
+  __device__ __forceinline__ int first(int v) const { return place(v) - (VEC == kSkewed ? skew : 0); }
   __device__ __forceinline__ int col(int e) const {
-    return VEC == 1 ? tid + e * tpr : (tid + (e / VEC) * tpr) * VEC + e % VEC;
+    return VEC == kOne ? tid + e * tpr : first(e / 8) + e % 8;
+  }
+  __device__ __forceinline__ bool in(int e) const {
+    if constexpr (VEC == kSkewed) return mask[e / 32] >> (e % 32) & 1u;
+    return static_cast<unsigned>(col(e)) < static_cast<unsigned>(H);
+  }
+  // any of piece v is in the row; all of it is
+  __device__ __forceinline__ bool some(int v) const { return first(v) < H; }
+  __device__ __forceinline__ bool whole(int v) const {
+    if constexpr (VEC == kSkewed) return (mask[v / 4] >> (v % 4 * 8) & 255u) == 255u;
+    return some(v);
   }
 };
 
-// Elements past H come back 0 and are not stored.
+// A thread's elements of a row as they are in memory (bf16 two to a register);
+// those outside the row are 0.  `p`: the row's column -skew (kOne: column 0).
 template <typename T, int VEC, int EPT>
-__device__ __forceinline__ void load_row(const T* __restrict__ p, const Cols<VEC>& c,
-                                         float (&v)[EPT]) {
-  if constexpr (VEC == 1) {
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) v[e] = c.col(e) < c.H ? to_f<T>(p[c.col(e)]) : 0.f;
-  } else {
-#pragma unroll
-    for (int e = 0; e < EPT; e += 8) {
-      const int at = c.col(e);
-      if (at < c.H) {
-        if constexpr (sizeof(T) == 2) {
-          const uint4 q = *reinterpret_cast<const uint4*>(p + at);
-          v[e] = bf16lo(q.x); v[e + 1] = bf16hi(q.x);
-          v[e + 2] = bf16lo(q.y); v[e + 3] = bf16hi(q.y);
-          v[e + 4] = bf16lo(q.z); v[e + 5] = bf16hi(q.z);
-          v[e + 6] = bf16lo(q.w); v[e + 7] = bf16hi(q.w);
-        } else {
-          const float4 a = *reinterpret_cast<const float4*>(p + at);
-          const float4 b = *reinterpret_cast<const float4*>(p + at + 4);
-          v[e] = a.x; v[e + 1] = a.y; v[e + 2] = a.z; v[e + 3] = a.w;
-          v[e + 4] = b.x; v[e + 5] = b.y; v[e + 6] = b.z; v[e + 7] = b.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[e + i] = 0.f;
-      }
-    }
-  }
-}
-
-template <typename T, int VEC, int EPT>
-__device__ __forceinline__ void store_row(T* __restrict__ p, const Cols<VEC>& c,
-                                          const float (&v)[EPT]) {
-  if constexpr (VEC == 1) {
-#pragma unroll
-    for (int e = 0; e < EPT; ++e)
-      if (c.col(e) < c.H) p[c.col(e)] = from_f<T>(v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < EPT; e += 8) {
-      const int at = c.col(e);
-      if (at < c.H) {
-        if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<uint4*>(p + at) =
-              make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
-                         pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
-        } else {
-          *reinterpret_cast<float4*>(p + at) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-          *reinterpret_cast<float4*>(p + at + 4) =
-              make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
-        }
-      }
-    }
-  }
-}
-
-// A thread's elements of a row as they are in memory (bf16 two to a register),
-// for what is kept across rows or sums.
-template <typename T, int VEC, int EPT>
-struct Kept;
+struct Row;
 template <int VEC, int EPT>
-struct Kept<float, VEC, EPT> {
+struct Row<float, VEC, EPT> {
   float v[EPT];
-  __device__ __forceinline__ void load(const float* p, const Cols<VEC>& c) {
-    load_row<float, VEC, EPT>(p, c, v);
+  __device__ __forceinline__ void load(const float* p, const Cols<VEC, EPT>& c) {
+    if constexpr (VEC == kOne) {
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) v[e] = c.in(e) ? p[c.col(e)] : 0.f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPT; e += 4) {
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c.some(e / 8)) q = *reinterpret_cast<const float4*>(p + c.place(e / 8) + e % 8);
+        v[e] = q.x;
+        v[e + 1] = q.y;
+        v[e + 2] = q.z;
+        v[e + 3] = q.w;
+      }
+      if constexpr (VEC == kSkewed) {
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) v[e] = c.in(e) ? v[e] : 0.f;
+      }
+    }
   }
+  __device__ __forceinline__ void set(int e, float x) { v[e] = x; }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int e = 0; e < EPT; ++e) v[e] = 0.f;
@@ -131,26 +120,35 @@ struct Kept<float, VEC, EPT> {
   __device__ __forceinline__ float operator[](int e) const { return v[e]; }
 };
 template <int VEC, int EPT>
-struct Kept<__nv_bfloat16, VEC, EPT> {
+struct Row<__nv_bfloat16, VEC, EPT> {
   uint32_t v[EPT / 2];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, const Cols<VEC>& c) {
-    if constexpr (VEC == 1) {
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const Cols<VEC, EPT>& c) {
+    if constexpr (VEC == kOne) {
       const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
       for (int e = 0; e < EPT; e += 2)
-        v[e / 2] = (c.col(e) < c.H ? u[c.col(e)] : 0u) |
-                   (c.col(e + 1) < c.H ? static_cast<uint32_t>(u[c.col(e + 1)]) << 16 : 0u);
+        v[e / 2] = (c.in(e) ? u[c.col(e)] : 0u) |
+                   (c.in(e + 1) ? static_cast<uint32_t>(u[c.col(e + 1)]) << 16 : 0u);
     } else {
 #pragma unroll
       for (int e = 0; e < EPT; e += 8) {
         uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (c.col(e) < c.H) q = *reinterpret_cast<const uint4*>(p + c.col(e));
+        if (c.some(e / 8)) q = *reinterpret_cast<const uint4*>(p + c.place(e / 8));
         v[e / 2] = q.x;
         v[e / 2 + 1] = q.y;
         v[e / 2 + 2] = q.z;
         v[e / 2 + 3] = q.w;
       }
+      if constexpr (VEC == kSkewed) {
+#pragma unroll
+        for (int e = 0; e < EPT; e += 2)
+          v[e / 2] &= (c.in(e) ? 0xffffu : 0u) | (c.in(e + 1) ? 0xffff0000u : 0u);
+      }
     }
+  }
+  __device__ __forceinline__ void set(int e, float x) {    // x: a bf16 value
+    const uint32_t b = __float_as_uint(x) >> 16;
+    v[e / 2] = (e & 1) ? (v[e / 2] & 0xffffu) | (b << 16) : (v[e / 2] & 0xffff0000u) | b;
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -160,6 +158,57 @@ struct Kept<__nv_bfloat16, VEC, EPT> {
     return (e & 1) ? bf16hi(v[e / 2]) : bf16lo(v[e / 2]);
   }
 };
+
+// Columns of a vector [H] that every row shares (any alignment).
+template <typename T, int VEC, int EPT>
+__device__ __forceinline__ void load_cols(const T* __restrict__ p, const Cols<VEC, EPT>& c, float (&v)[EPT]) {
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) v[e] = c.in(e) ? to_f(p[c.col(e)]) : 0.f;
+}
+
+// The first or last piece of a row, part of which lies outside.  A call, so
+// that the other threads branch around it.
+template <typename T>
+__device__ __noinline__ void store_part(T* at, uint32_t mask, float a, float b, float c, float d, float e,
+                                        float f, float g, float h) {
+  if (mask & 1u) at[0] = from_f<T>(a);
+  if (mask & 2u) at[1] = from_f<T>(b);
+  if (mask & 4u) at[2] = from_f<T>(c);
+  if (mask & 8u) at[3] = from_f<T>(d);
+  if (mask & 16u) at[4] = from_f<T>(e);
+  if (mask & 32u) at[5] = from_f<T>(f);
+  if (mask & 64u) at[6] = from_f<T>(g);
+  if (mask & 128u) at[7] = from_f<T>(h);
+}
+
+// `p`: the row's column 0.
+template <typename T, int VEC, int EPT>
+__device__ __forceinline__ void store_row(T* __restrict__ p, const Cols<VEC, EPT>& c, const float (&v)[EPT]) {
+  if constexpr (VEC == kOne) {
+#pragma unroll
+    for (int e = 0; e < EPT; ++e)
+      if (c.in(e)) p[c.col(e)] = from_f<T>(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPT; e += 8) {
+      T* at = p + c.first(e / 8);
+      if (c.whole(e / 8)) {
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4*>(at) =
+              make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                         pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
+        } else {
+          *reinterpret_cast<float4*>(at) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          *reinterpret_cast<float4*>(at + 4) = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+        }
+      } else if constexpr (VEC == kSkewed) {
+        const uint32_t m = c.mask[e / 32] >> (e % 32) & 255u;
+        if (m != 0u)
+          store_part<T>(at, m, v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+      }
+    }
+  }
+}
 
 struct NormParams {
   int T, H;
@@ -186,23 +235,12 @@ struct NormParams {
   int32_t* status;
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
           dst),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
-}
-
-// The 16-byte granules around the `bytes` at p.
-__device__ __forceinline__ uint32_t granules(const void* p, uint32_t bytes, const void** from) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), lo = a & ~static_cast<uintptr_t>(15);
-  *from = reinterpret_cast<const void*>(lo);
-  return static_cast<uint32_t>(((a + bytes + 15) & ~static_cast<uintptr_t>(15)) - lo);
-}
-__device__ __forceinline__ uint32_t skew(const void* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
 }
 
 constexpr int kSumFloats = 8 * 32;    // up to eight sums of up to 32 warps
@@ -251,14 +289,19 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int tpr, int bar, int t
     if (lane % kLanes == 0) buf[value * 32 + warp] = part;
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
     part = 0.f;
+    const float* from = buf + value * 32 + lane % kLanes;
+    const int left = nw - lane % kLanes;
 #pragma unroll
-    for (int w = 0; w < 32; w += kLanes)
-      if (w + lane % kLanes < nw) part += buf[value * 32 + w + lane % kLanes];
+    for (int w = 0; w < 32; w += kLanes) part += w < left ? from[w] : 0.f;
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) part += __shfl_xor_sync(kAll, part, off);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kAll, part, i * (32 / N));
+}
+
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t phase, int32_t* status) {
+  if (!mbar_wait(bar, phase, nullptr)) report(status, MOE_ERR_DEVICE_TIMEOUT);
 }
 
 // Shared memory: [groups][slots] row slots, then the sum buffers, then barriers.
@@ -276,60 +319,72 @@ __host__ __device__ inline NormSmem norm_smem(uint32_t slot_bytes, int slots, in
   return o;
 }
 
-// One group's view of the ring: its rows are first, first + step, ...
-template <typename R, typename A, bool BACK>
+// One group's ring.  A slot holds the rows r, y, [gate], [dr'], [dh] of a token,
+// each as the 16-byte granules around it.  Pieces: column -skew lies at the
+// start of its place; kOne: the granules do.
+template <typename R, typename A, int VEC, bool BACK>
 struct Ring {
   uint8_t* base;
   uint64_t* full;
   const NormParams* p;
-  uint32_t bytes_r, bytes_a;
+  int skew;
 
-  __device__ __forceinline__ void fill_one(uint32_t at, const void* src, uint32_t bytes,
-                                           uint64_t* bar, uint32_t& total, bool issue) const {
-    const void* from;
-    const uint32_t n = granules(src, bytes, &from);
-    total += n;
-    if (issue) bulk_load(at, from, n, bar);
+  template <typename T>
+  __device__ __forceinline__ const T* row(const void* q, int t, long long ld) const {
+    return static_cast<const T*>(q) + static_cast<long long>(t) * ld;
   }
-  __device__ __forceinline__ const R* r_row(int t) const {
-    return static_cast<const R*>(p->r) + static_cast<long long>(t) * p->ld_r;
+  // a row's place in a slot, as Row::load wants it
+  template <typename T>
+  __device__ __forceinline__ const T* place(int slot, uint32_t at, const void* q, int t, long long ld) const {
+    uint32_t off = static_cast<uint32_t>(slot) * p->slot_bytes + at;
+    if (VEC == kOne) off += static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row<T>(q, t, ld)) & 15u);
+    return reinterpret_cast<const T*>(base + off);
   }
-  __device__ __forceinline__ const A* y_row(int t) const {
-    return static_cast<const A*>(p->y) + static_cast<long long>(t) * p->ld_y;
+  template <typename T>
+  __device__ __forceinline__ uint32_t fill_one(uint32_t at, const void* q, int t, long long ld, uint64_t* bar,
+                                               bool issue) const {
+    if (q == nullptr) return 0u;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row<T>(q, t, ld)), lo = a & ~static_cast<uintptr_t>(15);
+    const uint32_t n = static_cast<uint32_t>(
+        ((a + static_cast<uintptr_t>(p->H) * sizeof(T) + 15) & ~static_cast<uintptr_t>(15)) - lo);
+    if (VEC != kOne) at += static_cast<uint32_t>(lo - (a - static_cast<uintptr_t>(skew) * sizeof(T)));
+    if (issue) bulk_load(at, reinterpret_cast<const void*>(lo), n, bar);
+    return n;
   }
-  __device__ __forceinline__ const A* g_row(int t) const {
-    return static_cast<const A*>(p->gate_p) + static_cast<long long>(t) * p->ld_g;
-  }
-  __device__ __forceinline__ const R* dout_row(int t) const {
-    return static_cast<const R*>(p->d_out) + static_cast<long long>(t) * p->ld_dout;
-  }
-  __device__ __forceinline__ const A* dh_row(int t) const {
-    return static_cast<const A*>(p->d_h) + static_cast<long long>(t) * p->ld_dh;
-  }
-  // offsets of the rows inside a slot: r, y, [gate], [d_out], [d_h]
   __device__ __forceinline__ void fill(int slot, int t) const {
     uint64_t* bar = full + slot;
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
       uint32_t at = smem_u32(base) + static_cast<uint32_t>(slot) * p->slot_bytes, total = 0;
       const bool go = pass == 1;
-      fill_one(at, r_row(t), bytes_r, bar, total, go);
+      total += fill_one<R>(at, p->r, t, p->ld_r, bar, go);
       at += p->pitch_r;
-      if (p->y != nullptr) fill_one(at, y_row(t), bytes_a, bar, total, go);
+      total += fill_one<A>(at, p->y, t, p->ld_y, bar, go);
       at += p->pitch_a;
       if (p->gate == MOE_GATE_FULL) {
-        fill_one(at, g_row(t), bytes_a, bar, total, go);
+        total += fill_one<A>(at, p->gate_p, t, p->ld_g, bar, go);
         at += p->pitch_a;
       }
       if (BACK) {
-        if (p->d_out != nullptr) fill_one(at, dout_row(t), bytes_r, bar, total, go);
+        total += fill_one<R>(at, p->d_out, t, p->ld_dout, bar, go);
         at += p->pitch_r;
-        if (p->d_h != nullptr) fill_one(at, dh_row(t), bytes_a, bar, total, go);
+        total += fill_one<A>(at, p->d_h, t, p->ld_dh, bar, go);
       }
       if (!go) mbar_expect_tx(bar, total);
     }
   }
+  __device__ __forceinline__ void wait(int slot, uint32_t phase) const {
+    if (!mbar_try_wait(full + slot, phase)) wait_long(full + slot, phase, p->status);
+  }
 };
+
+// Columns of the first piece before a group's rows: the same for all of them,
+// since the rows are gridDim.x * groups apart (a multiple of eight, or the
+// group has one row).
+template <int VEC>
+__device__ __forceinline__ int skew_of(const NormParams& p, int first) {
+  return VEC == kSkewed ? static_cast<int>((static_cast<long long>(first) * p.ld_r) & 7) : 0;
+}
 
 template <typename R, typename A, int VEC, int EPT, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p) {
@@ -338,46 +393,62 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p)
   const int group = threadIdx.x / p.tpr, tid = threadIdx.x - group * p.tpr;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
   float* red = reinterpret_cast<float*>(smem + L.red) + group * 2 * kSumFloats;
-  Ring<R, A, false> ring;
-  ring.base = smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes;
-  ring.full = bars + group * p.slots;
-  ring.p = &p;
-  ring.bytes_r = static_cast<uint32_t>(p.H * sizeof(R));
-  ring.bytes_a = static_cast<uint32_t>(p.H * sizeof(A));
+  const int step = gridDim.x * p.groups;
+  const int first = blockIdx.x + gridDim.x * group;
+  const Ring<R, A, VEC, false> ring{smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes,
+                                    bars + group * p.slots, &p, skew_of<VEC>(p, first)};
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.groups * p.slots; ++i) mbar_init(bars + i, 1);
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait_and_trigger();
-  const int step = gridDim.x * p.groups;
-  const int first = blockIdx.x + gridDim.x * group;
   if (tid == 0)
     for (int s = 0; s < p.slots; ++s)
       if (first + s * step < p.T) ring.fill(s, first + s * step);
-  const Cols<VEC> c{tid, p.tpr, p.H};
+  const Cols<VEC, EPT> c(tid, p.tpr, p.H, ring.skew);
   const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr;
-  Kept<A, VEC, EPT> w_post, w_pre;
-  w_post.zero();
-  w_pre.zero();
-  if (post) w_post.load(static_cast<const A*>(p.w_post), c);
-  if (pre) w_pre.load(static_cast<const A*>(p.w_pre), c);
+  // the weights of the thread's columns as they are in memory
+  Row<A, VEC, EPT> w1, w2, g;
+  w1.zero();
+  w2.zero();
+  auto take = [&](Row<A, VEC, EPT>& w, const void* q) {
+    if (VEC == kPieces && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+      w.load(static_cast<const A*>(q), c);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < EPT; ++e)
+      if (c.in(e)) w.set(e, to_f(static_cast<const A*>(q)[c.col(e)]));
+  };
+  if (post) take(w1, p.w_post);
+  if (pre) take(w2, p.w_pre);
+  const bool vector_gate = p.gate == MOE_GATE_FULL || p.gate == MOE_GATE_CHANNEL;
+  if (p.gate == MOE_GATE_CHANNEL) {
+    g.zero();
+    take(g, p.gate_p);
+  }
+  const float off1 = post ? p.offset : 1.f;      // without a post-norm: weight 1
   const float inv_h = 1.f / static_cast<float>(p.H);
   const bool ahead = p.slots > 1;     // the next row is there while this one is at work
   int slot = 0, parity = 0;
   uint32_t phase = 0;
-  Kept<A, VEC, EPT> x;                // y of the row
+  Row<A, VEC, EPT> x;                 // y of the row
+  x.zero();
   float sq = 0.f;                     // its sum of squares
   auto take_y = [&](int t, int sl, uint32_t ph) {
-    if (!mbar_wait(ring.full + sl, ph, nullptr)) report(p.status, MOE_ERR_DEVICE_TIMEOUT);
-    const uint8_t* at = ring.base + static_cast<uint32_t>(sl) * p.slot_bytes + p.pitch_r;
-    x.zero();
-    if (p.y != nullptr) x.load(reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.y_row(t)) : 0)), c);
+    ring.wait(sl, ph);
     float q = 0.f;
+    if (p.y != nullptr) {
+      x.load(ring.template place<A>(sl, p.pitch_r, p.y, t, p.ld_y), c);
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) q += x[e] * x[e];
+      for (int e = 0; e < EPT; ++e) q = fmaf(x[e], x[e], q);
+    }
     return q;
   };
+  R* out = static_cast<R*>(p.out) + static_cast<long long>(first) * p.ld_out;
+  A* h = static_cast<A*>(p.h) + static_cast<long long>(first) * p.ld_h;
+  const long long out_step = static_cast<long long>(step) * p.ld_out, h_step = static_cast<long long>(step) * p.ld_h;
   for (int t = first; t < p.T; t += step) {
     if (t == first || !ahead) {
       float q[2] = {take_y(t, slot, phase), 0.f};
@@ -385,36 +456,29 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p)
       sq = q[0];
     }
     float scale = p.bs;
-    if (p.gate == MOE_GATE_TOKEN) scale *= to_f<A>(static_cast<const A*>(p.gate_p)[t]);
+    if (p.gate == MOE_GATE_TOKEN) scale *= to_f(static_cast<const A*>(p.gate_p)[t]);
     if (post) scale *= rsqrtf(sq * inv_h + p.eps);
-    const uint8_t* at = ring.base + static_cast<uint32_t>(slot) * p.slot_bytes;
     float v[EPT];
-    load_row<R, VEC, EPT>(reinterpret_cast<const R*>(at + (VEC == 1 ? skew(ring.r_row(t)) : 0)), c, v);
-    at += p.pitch_r + p.pitch_a;
-    const A* gate = nullptr;
-    if (p.gate == MOE_GATE_FULL)
-      gate = reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.g_row(t)) : 0));
-    else if (p.gate == MOE_GATE_CHANNEL)
-      gate = static_cast<const A*>(p.gate_p);
+    {
+      Row<R, VEC, EPT> r;
+      r.load(ring.template place<R>(slot, 0, p.r, t, p.ld_r), c);
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) v[e] *= p.rs;
-    if (gate != nullptr) {
-      Kept<A, VEC, EPT> g;
-      g.load(gate, c);
+      for (int e = 0; e < EPT; ++e) v[e] = p.rs * r[e];
+    }
+    if (vector_gate) {
+      if (p.gate == MOE_GATE_FULL)
+        g.load(ring.template place<A>(slot, p.pitch_r + p.pitch_a, p.gate_p, t, p.ld_g), c);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] += x[e] * scale * (post ? w_post[e] + p.offset : 1.f) * g[e];
-    } else if (post) {
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] += x[e] * scale * (w_post[e] + p.offset);
+      for (int e = 0; e < EPT; ++e) v[e] = fmaf(x[e] * scale * g[e], w1[e] + off1, v[e]);
     } else {
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] += x[e] * scale;
+      for (int e = 0; e < EPT; ++e) v[e] = fmaf(x[e] * scale, w1[e] + off1, v[e]);
     }
-    if (p.out != nullptr)
-      store_row<R, VEC, EPT>(static_cast<R*>(p.out) + static_cast<long long>(t) * p.ld_out, c, v);
+    if (p.out != nullptr) store_row(out, c, v);
+    out += out_step;
     float q[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) q[0] += v[e] * v[e];
+    for (int e = 0; e < EPT; ++e) q[0] = fmaf(v[e], v[e], q[0]);
     const int next = slot + 1 == p.slots ? 0 : slot + 1;
     const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
     if (ahead && t + step < p.T) q[1] = take_y(t + step, next, next_phase);
@@ -427,31 +491,27 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p)
     if (pre) {
       const float f = rsqrtf(q[0] * inv_h + p.eps);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] *= f * (w_pre[e] + p.offset);
-      store_row<A, VEC, EPT>(static_cast<A*>(p.h) + static_cast<long long>(t) * p.ld_h, c, v);
+      for (int e = 0; e < EPT; ++e) v[e] *= f * (w2[e] + p.offset);
+      store_row(h, c, v);
+      h += h_step;
     }
   }
 }
 
-// Adds a thread's column sums of all groups of the CTA (in group order, through
-// the row slots, which are free by then) and writes the CTA's partial row.
+// A CTA's column sums: the groups' through shared memory (the row slots, which
+// are free by then), added in group order, to the CTA's partial row.
 template <int VEC, int EPT>
-__device__ __forceinline__ void cta_columns(float* buf, float* dst, const Cols<VEC>& c, int group,
+__device__ __forceinline__ void cta_columns(float* buf, float* dst, const Cols<VEC, EPT>& c, int group,
                                             int groups, const float (&v)[EPT]) {
-  for (int g = 0; g < groups; ++g) {
-    __syncthreads();
-    if (g == group) {
+  __syncthreads();
 #pragma unroll
-      for (int e = 0; e < EPT; ++e)
-        if (c.col(e) < c.H) {
-          const int at = c.col(e);
-          const float s = g == 0 ? v[e] : buf[at] + v[e];
-          if (g + 1 == groups)
-            dst[at] = s;
-          else
-            buf[at] = s;
-        }
-    }
+  for (int e = 0; e < EPT; ++e)
+    if (c.in(e)) buf[group * c.H + c.col(e)] = v[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < c.H; i += blockDim.x) {
+    float s = buf[i];
+    for (int g = 1; g < groups; ++g) s += buf[g * c.H + i];
+    dst[i] = s;
   }
 }
 
@@ -462,170 +522,164 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const Norm
   const int group = threadIdx.x / p.tpr, tid = threadIdx.x - group * p.tpr;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
   float* red = reinterpret_cast<float*>(smem + L.red) + group * 2 * kSumFloats;
-  Ring<R, A, true> ring;
-  ring.base = smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes;
-  ring.full = bars + group * p.slots;
-  ring.p = &p;
-  ring.bytes_r = static_cast<uint32_t>(p.H * sizeof(R));
-  ring.bytes_a = static_cast<uint32_t>(p.H * sizeof(A));
+  const int step = gridDim.x * p.groups;
+  const int first = blockIdx.x + gridDim.x * group;
+  const Ring<R, A, VEC, true> ring{smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes,
+                                   bars + group * p.slots, &p, skew_of<VEC>(p, first)};
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.groups * p.slots; ++i) mbar_init(bars + i, 1);
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait_and_trigger();
-  const int step = gridDim.x * p.groups;
-  const int first = blockIdx.x + gridDim.x * group;
   if (tid == 0)
     for (int s = 0; s < p.slots; ++s)
       if (first + s * step < p.T) ring.fill(s, first + s * step);
-  const Cols<VEC> c{tid, p.tpr, p.H};
+  const Cols<VEC, EPT> c(tid, p.tpr, p.H, ring.skew);
   const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr, branch = p.y != nullptr;
+  const bool full = p.gate == MOE_GATE_FULL, vector_gate = full || p.gate == MOE_GATE_CHANNEL;
   const float inv_h = 1.f / static_cast<float>(p.H);
-  float a_post[EPT], a_pre[EPT], a_gate[EPT];   // column sums of dw_post, dw_pre, dg
+  float a_post[EPT], a_pre[EPT], a_gate[EPT];   // column sums of dw_post / bs, dw_pre, dg
+  float w1[EPT], w2[EPT];                       // bs w_post, w_pre
 #pragma unroll
-  for (int e = 0; e < EPT; ++e) a_post[e] = a_pre[e] = a_gate[e] = 0.f;
-  Kept<A, VEC, EPT> w_post, w_pre;
-  w_post.zero();
-  w_pre.zero();
-  if (post) w_post.load(static_cast<const A*>(p.w_post), c);
-  if (pre) w_pre.load(static_cast<const A*>(p.w_pre), c);
+  for (int e = 0; e < EPT; ++e) a_post[e] = a_pre[e] = a_gate[e] = w1[e] = w2[e] = 0.f;
+  if (post) load_cols<A>(static_cast<const A*>(p.w_post), c, w1);
+  if (pre) load_cols<A>(static_cast<const A*>(p.w_pre), c, w2);
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) {
+    w1[e] = (post ? w1[e] + p.offset : 1.f) * p.bs;
+    w2[e] += p.offset;
+  }
+  Row<A, VEC, EPT> g;
+  g.zero();
+  if (p.gate == MOE_GATE_CHANNEL) {
+    float w[EPT];
+    load_cols<A>(static_cast<const A*>(p.gate_p), c, w);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) g.set(e, w[e]);
+  }
   // Rows behind this one's sums: a slot is filled again behind the sums of the
   // next row, so three are needed for sum(y^2) to run a row ahead.
   const bool ahead = p.slots > 2;
-  auto wait = [&](int sl, uint32_t ph) {
-    if (!mbar_wait(ring.full + sl, ph, nullptr)) report(p.status, MOE_ERR_DEVICE_TIMEOUT);
-  };
-  auto y_at = [&](int t, int sl) {
-    return reinterpret_cast<const A*>(ring.base + static_cast<uint32_t>(sl) * p.slot_bytes + p.pitch_r +
-                                      (VEC == 1 ? skew(ring.y_row(t)) : 0));
-  };
   auto squares = [&](int t, int sl) {
-    Kept<A, VEC, EPT> y;
-    y.load(y_at(t, sl), c);
+    Row<A, VEC, EPT> y;
+    y.load(ring.template place<A>(sl, p.pitch_r, p.y, t, p.ld_y), c);
     float q = 0.f;
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) q += y[e] * y[e];
+    for (int e = 0; e < EPT; ++e) q = fmaf(y[e], y[e], q);
     return q;
   };
   int slot = 0, parity = 0, before = 0;
   uint32_t phase = 0;
   float sq = 0.f;                               // sum of squares of the row's y
+  R* out = static_cast<R*>(p.out) + static_cast<long long>(first) * p.ld_out;
+  A* dy = static_cast<A*>(p.h) + static_cast<long long>(first) * p.ld_h;
+  const long long out_step = static_cast<long long>(step) * p.ld_out, dy_step = static_cast<long long>(step) * p.ld_h;
   for (int t = first; t < p.T; t += step) {
     if (t == first || !ahead) {
-      wait(slot, phase);
+      ring.wait(slot, phase);
       float q[2] = {post ? squares(t, slot) : 0.f, 0.f};
       if (post) group_sum<2>(q, p.tpr, 1 + group, tid, red, parity);
       sq = q[0];
     }
     const float fy = post ? rsqrtf(sq * inv_h + p.eps) : 1.f;
     float tg = 1.f;                             // gate of the token
-    if (p.gate == MOE_GATE_TOKEN) tg = to_f<A>(static_cast<const A*>(p.gate_p)[t]);
-    const uint8_t* at = ring.base + static_cast<uint32_t>(slot) * p.slot_bytes;
-    const R* s_r = reinterpret_cast<const R*>(at + (VEC == 1 ? skew(ring.r_row(t)) : 0));
-    at += p.pitch_r + p.pitch_a;
-    const A* s_g = nullptr;
-    if (p.gate == MOE_GATE_FULL) {
-      s_g = reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.g_row(t)) : 0));
+    if (p.gate == MOE_GATE_TOKEN) tg = to_f(static_cast<const A*>(p.gate_p)[t]);
+    uint32_t at = p.pitch_r + p.pitch_a;
+    if (full) {
+      g.load(ring.template place<A>(slot, at, p.gate_p, t, p.ld_g), c);
       at += p.pitch_a;
-    } else if (p.gate == MOE_GATE_CHANNEL) {
-      s_g = static_cast<const A*>(p.gate_p);
     }
-    const R* s_do = reinterpret_cast<const R*>(at + (VEC == 1 ? skew(ring.dout_row(t)) : 0));
-    at += p.pitch_r;
-    const A* s_dh = reinterpret_cast<const A*>(at + (VEC == 1 ? skew(ring.dh_row(t)) : 0));
-
-    // n = y rstd(y) and u = bs g n w_post (without the token's gate), element
-    // by element again in both passes below
-    Kept<A, VEC, EPT> y, g, dh;
-    Kept<R, VEC, EPT> dr, r;
-    y.zero();
+    Row<A, VEC, EPT> dh;
+    Row<R, VEC, EPT> dr;
     dr.zero();
-    r.zero();
     dh.zero();
-    if (branch) y.load(y_at(t, slot), c);
-    if (s_g != nullptr) g.load(s_g, c);
-    if (p.d_out != nullptr) dr.load(s_do, c);
-    if (pre) {
-      r.load(s_r, c);
-      dh.load(s_dh, c);
+    if (p.d_out != nullptr) dr.load(ring.template place<R>(slot, at, p.d_out, t, p.ld_dout), c);
+    if (pre) dh.load(ring.template place<A>(slot, at + p.pitch_r, p.d_h, t, p.ld_dh), c);
+    // n = y rstd(y), u = bs g n w_post (without the token's gate), m~ = r'
+    float n[EPT], m[EPT];
+    {
+      Row<R, VEC, EPT> r;
+      Row<A, VEC, EPT> y;
+      y.zero();
+      r.load(ring.template place<R>(slot, 0, p.r, t, p.ld_r), c);
+      if (branch) y.load(ring.template place<A>(slot, p.pitch_r, p.y, t, p.ld_y), c);
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) {
+        n[e] = y[e] * fy;
+        m[e] = p.rs * r[e];
+      }
     }
-    const float su = p.bs * fy;
-    auto u_of = [&](int e) {
-      float u = y[e] * su;
-      if (post) u *= w_post[e] + p.offset;
-      if (s_g != nullptr) u *= g[e];
-      return u;
-    };
-    // one round of sums for both norms: with m~ = r', d = dh w_pre,
+    // one round of sums for both norms: with d = dh w_pre,
     //   mean(d m) = f^2 sum(d m~) / H,  f = rstd(r')
     //   sum(D u) = sum(dr' u) + f sum(d u) - f mean sum(m~ u)
     float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int e, float u) {
+      m[e] = fmaf(tg, u, m[e]);
+      const float d = dh[e] * w2[e];
+      q[0] = fmaf(m[e], m[e], q[0]);
+      q[1] = fmaf(d, m[e], q[1]);
+      q[2] = fmaf(dr[e], u, q[2]);
+      q[3] = fmaf(d, u, q[3]);
+      q[4] = fmaf(m[e], u, q[4]);
+    };
+    if (vector_gate) {
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      const float u = u_of(e), m = p.rs * r[e] + tg * u, d = dh[e] * (w_pre[e] + p.offset);
-      q[0] += m * m;
-      q[1] += d * m;
-      q[2] += dr[e] * u;
-      q[3] += d * u;
-      q[4] += m * u;
+      for (int e = 0; e < EPT; ++e) add(e, n[e] * w1[e] * g[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) add(e, n[e] * w1[e]);
     }
     const int next = slot + 1 == p.slots ? 0 : slot + 1;
     const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
     if (ahead && t + step < p.T) {
-      wait(next, next_phase);
+      ring.wait(next, next_phase);
       if (post) q[5] = squares(t + step, next);
     }
-    // behind this barrier everyone is done with the row before
+    // behind this barrier everyone is done with the row before, and has this
+    // one in registers
     group_sum<8>(q, p.tpr, 1 + group, tid, red, parity);
-    if (ahead && tid == 0 && t != first && t + (p.slots - 1) * step < p.T)
-      ring.fill(before, t + (p.slots - 1) * step);
+    if (tid == 0) {
+      if (!ahead) {
+        if (t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
+      } else if (t != first && t + (p.slots - 1) * step < p.T) {
+        ring.fill(before, t + (p.slots - 1) * step);
+      }
+    }
     sq = q[5];
     const float f = pre ? rsqrtf(q[0] * inv_h + p.eps) : 0.f, mean_h = q[1] * inv_h * f * f;
-    const float sum_u = q[2] + f * (q[3] - mean_h * q[4]);
+    const float sum_u = q[2] + f * (q[3] - mean_h * q[4]), c2 = f * mean_h;
     if (p.gate == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(p.d_gate)[t] = sum_u;
     float D[EPT], o[EPT];                       // the whole gradient at r'
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
-      const float m = p.rs * r[e] + tg * u_of(e);
-      a_pre[e] += dh[e] * m * f;
-      D[e] = dr[e] + f * (dh[e] * (w_pre[e] + p.offset) - m * mean_h);
+      const float h = dh[e];
+      a_pre[e] = fmaf(h, m[e] * f, a_pre[e]);
+      D[e] = fmaf(-c2, m[e], fmaf(f, h * w2[e], dr[e]));
       o[e] = p.rs * D[e];
     }
-    store_row<R, VEC, EPT>(static_cast<R*>(p.out) + static_cast<long long>(t) * p.ld_out, c, o);
+    store_row(out, c, o);
+    out += out_step;
     if (branch) {
-      if (s_g != nullptr) {
+      if (vector_gate) {
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-          o[e] = D[e] * y[e] * su;
-          if (post) o[e] *= w_post[e] + p.offset;
+          o[e] = D[e] * (n[e] * w1[e]);
           a_gate[e] += o[e];
           D[e] *= g[e];
         }
-        if (p.gate == MOE_GATE_FULL)
-          store_row<A, VEC, EPT>(static_cast<A*>(p.d_gate) + static_cast<long long>(t) * p.ld_g, c, o);
+        if (full) store_row(static_cast<A*>(p.d_gate) + static_cast<long long>(t) * p.ld_g, c, o);
       }
       // sum(dz z) over the row is the token's gate times sum(D u)
-      const float mean_y = sum_u * tg * inv_h, s = p.bs * tg;
-      if (post) {
+      const float c3 = post ? fy * sum_u * tg * inv_h : 0.f;
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) {
-          const float dz = s * D[e], n = y[e] * fy;
-          a_post[e] += dz * n;
-          D[e] = fy * (dz * (w_post[e] + p.offset) - n * mean_y);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) D[e] *= s;
+      for (int e = 0; e < EPT; ++e) {
+        const float dz = tg * D[e];
+        a_post[e] = fmaf(dz, n[e], a_post[e]);
+        D[e] = fmaf(fy, dz * w1[e], -c3 * n[e]);
       }
-      store_row<A, VEC, EPT>(static_cast<A*>(p.h) + static_cast<long long>(t) * p.ld_h, c, D);
-    }
-    if (!ahead) {
-      if (p.tpr == 32)
-        __syncwarp();
-      else
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.tpr) : "memory");
-      if (tid == 0 && t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
+      store_row(dy, c, D);
+      dy += dy_step;
     }
     before = slot;
     slot = next;
@@ -635,47 +689,64 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const Norm
     float* buf = reinterpret_cast<float*>(smem);
     float* dst = p.part + static_cast<size_t>(blockIdx.x) * p.n_part * p.H;
     if (post) {
-      cta_columns<VEC, EPT>(buf, dst, c, group, p.groups, a_post);
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) a_post[e] *= p.bs;
+      cta_columns(buf, dst, c, group, p.groups, a_post);
       dst += p.H;
     }
     if (pre) {
-      cta_columns<VEC, EPT>(buf, dst, c, group, p.groups, a_pre);
+      cta_columns(buf, dst, c, group, p.groups, a_pre);
       dst += p.H;
     }
-    if (p.gate == MOE_GATE_CHANNEL) cta_columns<VEC, EPT>(buf, dst, c, group, p.groups, a_gate);
+    if (p.gate == MOE_GATE_CHANNEL) cta_columns(buf, dst, c, group, p.groups, a_gate);
   }
 }
 
-// Sums the CTAs' partial rows: 32 columns a CTA, eight slices of the parts,
-// each in order, then the slices in order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, int parts,
-                                                         int n_part, int H, float* o0, float* o1,
-                                                         float* o2) {
-  __shared__ float s[8][33];
+// Sums the CTAs' partial rows: 32 columns a CTA, 32 slices of the parts, each in
+// order, then the slices in order.
+constexpr int kSlices = 32;
+__global__ void __launch_bounds__(32 * kSlices) column_sum_kernel(const float* __restrict__ part, int parts,
+                                                                  int n_part, int H, float* o0, float* o1,
+                                                                  float* o2) {
+  __shared__ float s[kSlices][33];
   pdl_wait_and_trigger();
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const long long col = static_cast<long long>(blockIdx.x) * 32 + lane;
   const long long width = static_cast<long long>(n_part) * H;
-  float v = 0.f;
-  if (col < width)
-    for (int i = slice; i < parts; i += 8) v += part[i * width + col];
+  constexpr int kMost = (kNormMaxCtas + kSlices - 1) / kSlices;
+  float w[kMost], v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int r = slice + i * kSlices;
+    w[i] = col < width && r < parts ? part[r * width + col] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) v += w[i];
   s[slice][lane] = v;
   __syncthreads();
-  if (slice == 0 && col < width) {
+  // warp w sums columns w: lane = slice
+  v = s[lane][slice];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][lane];
-    const int which = static_cast<int>(col / H);
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  const long long mine = static_cast<long long>(blockIdx.x) * 32 + slice;
+  if (lane == 0 && mine < width) {
+    const int which = static_cast<int>(mine / H);
     float* o = which == 0 ? o0 : (which == 1 ? o1 : o2);
-    o[col - static_cast<long long>(which) * H] = v;
+    o[mine - static_cast<long long>(which) * H] = v;
   }
 }
 
-uint32_t row_pitch(int H, int es) { return (static_cast<uint32_t>(H) * es + 15u + 16u) & ~15u; }
+// 16 bytes of slack for the granules and 16 for an fp32 piece that begins
+// before them.
+uint32_t row_pitch(int H, int es) { return (static_cast<uint32_t>(H + 7) * es + 15u + 32u) & ~15u; }
+
+// Columns a group's threads span: a skewed row may begin seven into its first piece.
+int span(const NormParams& p, int vec) { return p.H + (vec == kSkewed ? 7 : 0); }
 
 // Threads a row, groups and slots: EPT elements a thread; as many groups as
 // fit the threads of a CTA and the slots' memory, down to one group of one slot.
-void shape_of(NormParams& p, int ept, int max_threads, int rows_r, int rows_a, int es_r, int es_a, int sm) {
-  int tpr = (p.H + ept - 1) / ept;
+void shape_of(NormParams& p, int vec, int ept, int max_threads, int rows_r, int rows_a, int es_r, int es_a, int sm) {
+  int tpr = (span(p, vec) + ept - 1) / ept;
   tpr = (tpr + 31) / 32 * 32;
   p.tpr = tpr;
   p.pitch_r = row_pitch(p.H, es_r);
@@ -696,9 +767,11 @@ void shape_of(NormParams& p, int ept, int max_threads, int rows_r, int rows_a, i
 template <typename R, typename A, int VEC, int EPT, int MAXT, bool BACK>
 cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
   static bool done[64] = {false};
-  shape_of(p, EPT, MAXT, rows_r, rows_a, sizeof(R), sizeof(A), sm);
-  const int want = (p.T + p.groups - 1) / p.groups;
-  *grid = want < sm ? want : sm;
+  shape_of(p, VEC, EPT, MAXT, rows_r, rows_a, sizeof(R), sizeof(A), sm);
+  // a group's rows are grid * groups apart: a multiple of eight if there are several
+  const int want = (p.T + p.groups - 1) / p.groups, most = sm >= 8 ? sm / 8 * 8 : sm;
+  *grid = want <= sm ? want : most;
+  if (want > sm && most % 8 != 0 && VEC == kSkewed) return cudaErrorInvalidConfiguration;
   const uint32_t smem = norm_smem(p.slot_bytes, p.slots, p.groups).total;
   auto go = [&](auto k) {
     const cudaError_t e = set_smem_once(k, 227 * 1024, done);
@@ -711,26 +784,28 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaSt
 }
 
 // Elements a thread and threads a CTA.  The backward pass holds three column
-// sums per element: 512 threads have the registers for it (with 1024 it spilled
-// and took three times as long).  Forward, 16 elements from 1024 columns up, so
-// that two or more rows are at work on an SM and one's sums run under another's.
+// sums per element: 512 threads have the registers for it.
 template <typename R, typename A, int VEC>
 cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
+  const int n = span(p, VEC);
   if (back) {
-    if (p.H <= 8 * 512) return run<R, A, VEC, 8, 512, true>(p, rows_r, rows_a, sm, grid, s);
-    if (p.H <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
-    return run<R, A, VEC, 32, 512, true>(p, rows_r, rows_a, sm, grid, s);
+    if (n <= 8 * 512) return run<R, A, VEC, 8, 512, true>(p, rows_r, rows_a, sm, grid, s);
+    if (n <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
+    return run<R, A, VEC, 40, 512, true>(p, rows_r, rows_a, sm, grid, s);
   }
-  if (p.H <= 1024) return run<R, A, VEC, 8, 1024, false>(p, rows_r, rows_a, sm, grid, s);
-  if (p.H <= 16 * 896) return run<R, A, VEC, 16, 896, false>(p, rows_r, rows_a, sm, grid, s);
-  return run<R, A, VEC, 16, 1024, false>(p, rows_r, rows_a, sm, grid, s);
+  // a row per SM: more threads at it; many rows: two groups at work on an SM
+  if (n <= 1024 || (p.T <= sm && n <= 8 * 1024))
+    return run<R, A, VEC, 8, 1024, false>(p, rows_r, rows_a, sm, grid, s);
+  if (n <= 16 * 896) return run<R, A, VEC, 16, 896, false>(p, rows_r, rows_a, sm, grid, s);
+  return run<R, A, VEC, 24, 768, false>(p, rows_r, rows_a, sm, grid, s);
 }
 
 template <typename R, typename A>
-cudaError_t pick_vec(NormParams& p, bool back, bool vec, int rows_r, int rows_a, int sm, int* grid,
+cudaError_t pick_vec(NormParams& p, bool back, int vec, int rows_r, int rows_a, int sm, int* grid,
                      cudaStream_t s) {
-  return vec ? pick<R, A, 8>(p, back, rows_r, rows_a, sm, grid, s)
-             : pick<R, A, 1>(p, back, rows_r, rows_a, sm, grid, s);
+  if (vec == kPieces) return pick<R, A, kPieces>(p, back, rows_r, rows_a, sm, grid, s);
+  if (vec == kSkewed) return pick<R, A, kSkewed>(p, back, rows_r, rows_a, sm, grid, s);
+  return pick<R, A, kOne>(p, back, rows_r, rows_a, sm, grid, s);
 }
 
 }  // namespace
@@ -775,16 +850,15 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
   p.part = a.part;
   p.status = a.status;
   const int es_r = a.residual_f32 ? 4 : 2, es_a = a.act_f32 ? 4 : 2;
-  auto ok16 = [](const void* q, long long ld, int es) {
-    return q == nullptr || ((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && (ld * es) % 16 == 0);
-  };
   const bool full = a.gate_kind == MOE_GATE_FULL, chan = a.gate_kind == MOE_GATE_CHANNEL;
-  const bool vec = a.H % 8 == 0 && ok16(a.residual, a.ld_residual, es_r) &&
-                   ok16(a.branch, a.ld_branch, es_a) && ok16(a.out, a.ld_out, es_r) &&
-                   ok16(a.h, a.ld_h, es_a) && ok16(a.w_post, 0, es_a) && ok16(a.w_pre, 0, es_a) &&
-                   (!full || (ok16(a.gate, a.ld_gate, es_a) && ok16(a.d_gate, a.ld_gate, es_a))) &&
-                   (!chan || ok16(a.gate, 0, es_a)) && ok16(a.d_out, a.ld_dout, es_r) &&
-                   ok16(a.d_h, a.ld_dh, es_a);
+  // every row of a token starts at the same place of a 16-byte (fp32: 32-byte) piece
+  auto same = [&a](const void* q, long long ld) {
+    return q == nullptr || ((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && (ld - a.ld_residual) % 8 == 0);
+  };
+  const bool alike = same(a.residual, a.ld_residual) && same(a.branch, a.ld_branch) &&
+                   same(a.out, a.ld_out) && same(a.h, a.ld_h) && same(a.d_out, a.ld_dout) &&
+                   same(a.d_h, a.ld_dh) && (!full || (same(a.gate, a.ld_gate) && same(a.d_gate, a.ld_gate)));
+  const int vec = !alike ? kOne : (a.H % 8 == 0 && a.ld_residual % 8 == 0 ? kPieces : kSkewed);
   const int sm = a.sm_count < 1 ? 1 : (a.sm_count < kNormMaxCtas ? a.sm_count : kNormMaxCtas);
   p.n_part = 0;
   float* o[3] = {nullptr, nullptr, nullptr};
@@ -812,7 +886,7 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
     e = pick_vec<__nv_bfloat16, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
   if (e != cudaSuccess || p.n_part == 0) return e;
   const long long width = static_cast<long long>(p.n_part) * a.H;
-  return launch_pdl(column_sum_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(256), 0,
+  return launch_pdl(column_sum_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(32 * kSlices), 0,
                     s, static_cast<const float*>(a.part), grid, p.n_part, a.H, o[0], o[1], o[2]);
 }
 
