@@ -42,10 +42,11 @@ __device__ __forceinline__ float warp_sum_f32(float v) {
   return v;
 }
 
-// Scores for the comparison: expf and one approximate reciprocal (relative
-// error below 4e-7).  The weights that leave the kernel are computed again
-// with the correctly rounded division.
-__device__ __forceinline__ float sigmoid_fast(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
+// Sigmoids for the comparison: __expf and an approximate reciprocal.  Their error
+// is below 1e-6 of a token's largest score (exp(x) is good to 2^-21 + |x| 2^-24
+// of its value, and where |x| is large the score or its complement is small).
+// The weights that leave the kernel are computed again with expf and a division.
+__device__ __forceinline__ float sigmoid_fast(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
 
 // s(l) exp(-m) with m = min(largest selected l, 0): l > 0 only where m = 0.
 __device__ __forceinline__ float sigmoid_over(float l, float m) {
@@ -69,6 +70,7 @@ struct GroupParams {
   int gpl;                // groups per lane (1 unless MANY)
   int per;                // units per lane
   int vec;                // lanes hold aligned multiples of four units: 16-byte loads
+  int inf_bias;           // a selection bias is given: one could be +inf
   int32_t* idx;
   float* w;
   int32_t* k_out;         // nullable
@@ -76,43 +78,21 @@ struct GroupParams {
   int32_t* status;
 };
 
-// Descending compare-exchange; on equal scores the lower unit stays first.
-__device__ __forceinline__ void cas(float& a, int& ia, float& b, int& ib) {
-  const bool sw = b > a || (b == a && ib < ia);
-  const float ta = sw ? b : a, tb = sw ? a : b;
-  const int ja = sw ? ib : ia, jb = sw ? ia : ib;
-  a = ta;
-  b = tb;
-  ia = ja;
-  ib = jb;
-}
-
-// Batcher's odd-even merge sort of a lane's IPL entries (a power of two).
-template <int IPL>
-__device__ __forceinline__ void lane_sort(float (&c)[IPL], int (&u)[IPL]) {
-#pragma unroll
-  for (int p = 1; p < IPL; p <<= 1) {
-#pragma unroll
-    for (int q = p; q >= 1; q >>= 1) {
-#pragma unroll
-      for (int j = q % p; j + q < IPL; j += 2 * q) {
-#pragma unroll
-        for (int i = 0; i < q; ++i)
-          if (i + j + q < IPL && (i + j) / (2 * p) == (i + j + q) / (2 * p))
-            cas(c[i + j], u[i + j], c[i + j + q], u[i + j + q]);
-      }
-    }
-  }
-}
-
 // One warp per token.  G <= 32: a group takes L = floor(32 / G) neighbouring
 // lanes, each with `per` consecutive units, so units ascend with the lanes and
-// a group's two best come from its lanes' sorted heads.  MANY (G > 32): a lane
+// a group's two best come from its lanes' two best.  MANY (G > 32): a lane
 // holds whole groups, at most 16 units.
+// Selection without a sort: the k-th largest of the lanes' best units is a
+// bound that the k best units reach (k maxima of the warp); the units that
+// reach it, a few more than k, are listed and each counts the listed units
+// before it.  Sorting every lane and popping k heads took three times as long
+// at 256 units.  Issue bound: about 400 instructions a token at 256 units, 8 of
+// 8 groups' 4 and k = 8, against 1 KB of logits.
 template <int IPL, bool MANY>
 __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupParams p) {
   __shared__ int32_t s_load[kMaxUnits];
-  __shared__ float s_row[kWarps][kMaxUnits];
+  __shared__ float2 s_list[kWarps][kMaxUnits];        // score, unit
+  __shared__ int32_t s_sel[kWarps][32];
   __shared__ float s_rank[MANY ? kWarps : 1][kMaxUnits];
   pdl_wait_and_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -129,21 +109,29 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
   else
     n = g < p.G ? max(0, min(p.per, p.size - j * p.per)) : 0;
   if (n == 0) u0 = 0;
+  // a NaN bias is reported and takes its unit out, as -inf does
   float b[IPL];
+  bool bad_bias = false;
 #pragma unroll
-  for (int i = 0; i < IPL; ++i)
-    b[i] = i < n && p.sel_bias != nullptr ? __ldg(p.sel_bias + u0 + i) : 0.f;
-  float* row_s = s_row[warp];
+  for (int i = 0; i < IPL; ++i) {
+    b[i] = i < n ? (p.sel_bias != nullptr ? __ldg(p.sel_bias + u0 + i) : 0.f) : -INFINITY;
+    if (b[i] != b[i]) {
+      bad_bias = true;
+      b[i] = -INFINITY;
+    }
+  }
+  if (bad_bias) report(p.status, MOE_ERR_NONFINITE);
+  const unsigned below = (1u << lane) - 1u;
 
   for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
     int k = p.kpt != nullptr ? __ldg(p.kpt + t) : p.k_max;
-    const float* row = p.P + static_cast<size_t>(t) * p.E + u0;
+    const float* row = p.P + static_cast<size_t>(t) * p.E;
     float c[IPL];
     if (p.vec) {
 #pragma unroll
       for (int i = 0; i < IPL; i += 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n) v = __ldg(reinterpret_cast<const float4*>(row + i));
+        if (i < n) v = __ldg(reinterpret_cast<const float4*>(row + u0 + i));
         c[i] = v.x;
         if (i + 1 < IPL) c[i + 1] = v.y;
         if (i + 2 < IPL) c[i + 2] = v.z;
@@ -151,12 +139,12 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < IPL; ++i) c[i] = i < n ? __ldg(row + i) : 0.f;
+      for (int i = 0; i < IPL; ++i) c[i] = i < n ? __ldg(row + u0 + i) : 0.f;
     }
     for (int s = 1; s < p.S; ++s) {
 #pragma unroll
       for (int i = 0; i < IPL; ++i)
-        if (i < n) c[i] += __ldg(row + s * p.slice + i);
+        if (i < n) c[i] += __ldg(row + s * p.slice + u0 + i);
     }
     if (p.bias != nullptr) {
 #pragma unroll
@@ -176,47 +164,45 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
     // NaN and +inf are reported and leave the unit out, like -inf
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < IPL; ++i) {
-      if (i < n) {
-        if (!(c[i] < INFINITY)) {
-          bad = true;
-          c[i] = -INFINITY;
-        }
-        row_s[u0 + i] = c[i];
-      } else {
-        c[i] = -INFINITY;
-      }
+    for (int i = 0; i < IPL; ++i) bad |= !(c[i] < INFINITY);
+    if (__any_sync(kAll, bad)) {
+      if (bad) report(p.status, MOE_ERR_NONFINITE);
+#pragma unroll
+      for (int i = 0; i < IPL; ++i)
+        if (!(c[i] < INFINITY)) c[i] = -INFINITY;
     }
+    // biased scores; -inf (b of the units past n, too) stays -inf
     float mx = 0.f, sum = 1.f;
     if (p.score == MOE_SCORE_SOFTMAX) {
-      mx = c[0];
+      mx = -INFINITY;
 #pragma unroll
-      for (int i = 1; i < IPL; ++i) mx = fmaxf(mx, c[i]);
+      for (int i = 0; i < IPL; ++i)
+        if (i < n) mx = fmaxf(mx, c[i]);
       mx = warp_max_f32(mx);
       const float m0 = mx > -INFINITY ? mx : 0.f;
       float part = 0.f;
 #pragma unroll
       for (int i = 0; i < IPL; ++i) {
-        const float e = expf(c[i] - m0);
+        const float e = i < n ? expf(c[i] - m0) : 0.f;
         part += e;
         c[i] = c[i] > -INFINITY ? e : -INFINITY;
       }
       sum = warp_sum_f32(part);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum > 0.f ? __fdividef(1.f, sum) : 1.f;
 #pragma unroll
-      for (int i = 0; i < IPL; ++i) c[i] = c[i] * inv + b[i];   // -inf stays -inf
+      for (int i = 0; i < IPL; ++i) c[i] = fmaf(c[i], inv, b[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < IPL; ++i) c[i] = c[i] > -INFINITY ? sigmoid_fast(c[i]) + b[i] : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < IPL; ++i) {
-      if (c[i] != c[i]) {     // a NaN bias, or -inf * 0 of a row with nothing left
-        bad |= b[i] != b[i];
-        c[i] = -INFINITY;
+      for (int i = 0; i < IPL; ++i) {
+        const float s = sigmoid_fast(c[i]);
+        c[i] = (c[i] > -INFINITY ? s : -INFINITY) + b[i];
       }
     }
-    if (__any_sync(kAll, bad) && lane == 0) report(p.status, MOE_ERR_NONFINITE);
+    if (p.inf_bias) {      // -inf of a unit that is out, plus a bias of +inf
+#pragma unroll
+      for (int i = 0; i < IPL; ++i)
+        if (c[i] != c[i]) c[i] = -INFINITY;
+    }
 
     if (MANY && p.kept < p.G) {
       float* rank = s_rank[warp];
@@ -243,12 +229,15 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
         }
       }
     }
-    int u[IPL];
+    // the lane's two best
+    float a1 = c[0], a2 = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < IPL; ++i) u[i] = u0 + i;
-    lane_sort<IPL>(c, u);
+    for (int i = 1; i < IPL; ++i) {
+      a2 = fmaxf(a2, fminf(a1, c[i]));
+      a1 = fmaxf(a1, c[i]);
+    }
+    float head = a1;
     if (!MANY && p.kept < p.G) {
-      float a1 = c[0], a2 = IPL > 1 ? c[IPL > 1 ? 1 : 0] : -INFINITY;
       if ((p.L & (p.L - 1)) == 0) {
         for (int off = 1; off < p.L; off <<= 1) {
           const float b1 = __shfl_xor_sync(kAll, a1, off), b2 = __shfl_xor_sync(kAll, a2, off);
@@ -267,36 +256,56 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
       }
       const float rank = a1 + (p.best == 2 && a2 > -INFINITY ? a2 : 0.f);
       int ahead = 0;
+#pragma unroll 8
       for (int o = 0; o < p.G; ++o) {
         const float other = __shfl_sync(kAll, rank, o * p.L);
         ahead += other > rank || (other == rank && o < g);
       }
       if (ahead >= p.kept) {
+        head = -INFINITY;
 #pragma unroll
         for (int i = 0; i < IPL; ++i) c[i] = -INFINITY;
       }
     }
-    // k rounds: the largest head of the warp, lowest lane (= lowest unit) on ties
-    int mine = -1, got = 0;
-    for (; got < k; ++got) {
-      const float m = warp_max_f32(c[0]);
-      if (!(m > -INFINITY)) break;
-      const int who = __ffs(__ballot_sync(kAll, c[0] == m)) - 1;
-      const int unit = __shfl_sync(kAll, u[0], who);
-      if (lane == got) mine = unit;
-      if (lane == who) {
+    // the bound: the k-th largest head, or the largest -inf below it
+    float bound = -INFINITY;
+    for (int r = 0; r < k; ++r) {
+      bound = warp_max_f32(head);
+      if (!(bound > -INFINITY)) break;
+      if (head == bound) head = -INFINITY;
+    }
+    // the units that reach it
+    int listed = 0;
 #pragma unroll
-        for (int i = 0; i + 1 < IPL; ++i) {
-          c[i] = c[i + 1];
-          u[i] = u[i + 1];
-        }
-        c[IPL - 1] = -INFINITY;
-      }
+    for (int i = 0; i < IPL; ++i) {
+      const bool in = c[i] >= bound && c[i] > -INFINITY;
+      const unsigned who = __ballot_sync(kAll, in);
+      if (in) s_list[warp][listed + __popc(who & below)] = make_float2(c[i], __int_as_float(u0 + i));
+      listed += __popc(who);
     }
     __syncwarp();
-    // weights of the selected units, one per lane
+    const int got = min(k, listed);
+    for (int i = lane; i < listed; i += 32) {
+      const float2 mine = s_list[warp][i];
+      const int unit = __float_as_int(mine.y);
+      int ahead = 0;
+#pragma unroll 4
+      for (int o = 0; o < listed; ++o) {
+        const float2 other = s_list[warp][o];
+        ahead += other.x > mine.x || (other.x == mine.x && __float_as_int(other.y) < unit);
+      }
+      if (ahead < got) s_sel[warp][ahead] = unit;
+    }
+    __syncwarp();
+    // weights of the selected units, one per lane, from their logits
     const bool sel = lane < got;
-    const float l = sel ? row_s[mine] : -INFINITY;
+    const int unit = sel ? s_sel[warp][lane] : -1;
+    float l = -INFINITY;
+    if (sel) {
+      l = __ldg(row + unit);
+      for (int s = 1; s < p.S; ++s) l += __ldg(row + s * p.slice + unit);
+      if (p.bias != nullptr) l += __ldg(p.bias + unit / p.n_sub);
+    }
     float wt = 0.f;
     if (p.score == MOE_SCORE_SOFTMAX) {
       const float top = p.renorm ? warp_max_f32(l) : mx;
@@ -311,12 +320,12 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
     }
     if (lane < p.k_max) {
       const size_t o = static_cast<size_t>(t) * p.k_max + lane;
-      p.idx[o] = sel ? mine : -1;
+      p.idx[o] = unit;
       p.w[o] = wt * p.scale;
     }
     if (p.k_out != nullptr && lane == 0) p.k_out[t] = got;
-    if (p.load != nullptr && sel) atomicAdd(&s_load[mine], 1);
-    __syncwarp();   // the row and rank buffers are written again for the next token
+    if (p.load != nullptr && sel) atomicAdd(&s_load[unit], 1);
+    __syncwarp();   // the lists are written again for the next token
   }
   if (p.load != nullptr) {
     __syncthreads();
@@ -461,6 +470,7 @@ cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
   // with every group kept the grouping decides nothing
   if (p.kept == p.G) p.G = p.kept = 1;
   p.sel_bias = a.select_bias;
+  p.inf_bias = a.select_bias != nullptr;
   p.size = p.E / p.G;
   const bool many = p.G > 32;
   p.L = many ? 1 : 32 / p.G;
@@ -473,7 +483,7 @@ cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
   p.load = a.load;
   p.status = a.status;
   const int blocks = (a.T + kWarps - 1) / kWarps;
-  const int grid = blocks < 4 * a.sm_count ? blocks : 4 * a.sm_count;
+  const int grid = blocks < 6 * a.sm_count ? blocks : 6 * a.sm_count;
   if (a.load != nullptr && grid > 1) {
     const cudaError_t e = cudaMemsetAsync(a.load, 0, sizeof(int32_t) * a.E_r, s);
     if (e != cudaSuccess) return e;
