@@ -1,0 +1,181 @@
+"""One feed-forward block of a decoder around the MoE layer, on one GPU.
+
+    residual, h = norm(residual, attention output)    post-norm, residual, pre-norm
+    routed      = group-limited routing of h, then the routed experts
+    shared      = the shared expert, with the adapter of each token's request
+    residual, h = norm(residual, routed + shared)     post-norm, residual, next pre-norm
+
+Every step is a call of the library on the caller's stream; the block owns the
+workspaces and the buffers between the steps.
+
+``python -m aware_moe_expert_gb300.block`` runs a few steps of a small block on
+synthetic inputs and balances its experts.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass, replace
+from typing import Optional
+
+import torch
+
+from . import binding as B
+
+
+@dataclass
+class Adapters:
+    """A pool of low-rank adapters beside the shared expert's two projections
+    (A [n, r, in], B [n, out, r] bf16; ranks int32 [n]; scales fp32 [n])."""
+    gate_up_a: torch.Tensor
+    gate_up_b: torch.Tensor
+    down_a: torch.Tensor
+    down_b: torch.Tensor
+    ranks: torch.Tensor
+    scales: torch.Tensor
+
+
+@dataclass
+class BlockWeights:
+    attn_post_norm: torch.Tensor          # [H]: norm of the attention output
+    pre_norm: torch.Tensor                # [H]: norm of the block's input
+    ffn_post_norm: torch.Tensor           # [H]: norm of the block's output
+    next_pre_norm: torch.Tensor           # [H]: the next block's input norm
+    router: torch.Tensor                  # [E_r, H]
+    w_gate_up: torch.Tensor               # [E_r, 2 I, H]
+    w_down: torch.Tensor                  # [E_r, H, I]
+    shared_gate_up: torch.Tensor          # [2 I_shared, H]
+    shared_down: torch.Tensor             # [H, I_shared]
+    select_bias: torch.Tensor             # fp32 [E_r], moved by balance()
+
+
+class MoeBlock:
+    def __init__(self, layer: B.LayerDesc, groups: B.GroupRoute, weights: BlockWeights,
+                 adapters: Optional[Adapters] = None, *, eps: float = 1e-6,
+                 residual_scale: float = 1.0, branch_scale: float = 1.0, device="cuda"):
+        """layer.T is the largest number of tokens of a step; layer.I_shared is
+        taken from the weights (the shared expert runs here, with adapters)."""
+        self.device = torch.device(device)
+        self.layer, self.weights, self.adapters = layer, weights, adapters
+        self.groups = groups
+        self.groups.select_bias = weights.select_bias
+        self.eps, self.residual_scale, self.branch_scale = eps, residual_scale, branch_scale
+        T, H, k = layer.T, layer.H, layer.k_max
+        self.shared = weights.shared_down.shape[1]
+        new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=self.device)  # noqa: E731
+        i32 = torch.int32
+        self.h, self.act, self.y_shared, self.y = new(T, H), new(T, self.shared), new(T, H), new(T, H)
+        self.logits = new(T, layer.E_r, dtype=torch.float32)
+        self.topk_idx, self.topk_w = new(T, k, dtype=i32), new(T, k, dtype=torch.float32)
+        self.k_used, self.load = new(T, dtype=i32), new(layer.E_r, dtype=i32)
+        self.counts, self.offsets = new(layer.E_r, dtype=i32), new(layer.E_r + 1, dtype=i32)
+        self.sorted_token, self.inv_row = new(T * k, dtype=i32), new(T * k, dtype=i32)
+        self.y_perm = new(T * k, H)
+        self.status = torch.zeros(1, dtype=i32, device=self.device)
+        n = B.moe_workspace_size(layer)
+        if n == 0:
+            raise B.MoeError(2, "moe_workspace_size")
+        self.workspace = new(n, dtype=torch.uint8)
+        n = max(B.moe_lora_workspace_size(self._lora(T, True)),
+                B.moe_lora_workspace_size(self._lora(T, False)))
+        if n == 0:
+            raise B.MoeError(2, "moe_lora_workspace_size")
+        self.lora_workspace = new(n, dtype=torch.uint8)
+
+    def _lora(self, T: int, first: bool) -> B.LoraDesc:
+        a, H = self.adapters, self.layer.H
+        n, r = (0, 8) if a is None else a.gate_up_a.shape[:2] if first else a.down_a.shape[:2]
+        if first:
+            return B.LoraDesc(T=T, K=H, N=2 * self.shared, n_adapters=n, r_max=r, swiglu=True)
+        return B.LoraDesc(T=T, K=self.shared, N=H, n_adapters=n, r_max=r)
+
+    def _norm(self, residual, branch, w_post, w_pre, residual_out, normed, stream):
+        T, H = branch.shape
+        d = B.BlockNormDesc(T=T, H=H, residual_dtype=residual.dtype, eps=self.eps,
+                            residual_scale=self.residual_scale, branch_scale=self.branch_scale,
+                            w_post=w_post, w_pre=w_pre, dev_status=self.status)
+        B.check(B.moe_block_norm(d, residual, branch, None, residual_out, normed, stream),
+                "moe_block_norm")
+
+    def forward(self, residual, attn, k_per_token, adapter_idx=None, stream=None):
+        """residual (bf16 or fp32) and attn (bf16) [T, H], budgets int32 [T],
+        adapter_idx int32 [T] (-1: none).  Updates residual in place and returns
+        the next block's normed input; self.load has the assignments per unit."""
+        T, H = attn.shape
+        if T > self.layer.T:
+            raise ValueError(f"{T} tokens, and buffers for {self.layer.T}")
+        w, a, st, ws = self.weights, self.adapters, self.status, self.workspace
+        d = replace(self.layer, T=T)
+        h = self.h[:T]
+        self._norm(residual, attn, w.attn_post_norm, w.pre_norm, residual, h, stream)
+        idx, tw, k_used = self.topk_idx[:T], self.topk_w[:T], self.k_used[:T]
+        B.check(B.moe_route_groups(d, self.groups, h, w.router, None, k_per_token,
+                                   self.logits[:T], idx, tw, k_used, self.load, st, ws, stream),
+                "moe_route_groups")
+        B.check(B.moe_permute(d, idx, k_used, self.counts, self.offsets, self.sorted_token,
+                              self.inv_row, st, ws, stream), "moe_permute")
+        B.check(B.moe_grouped_ffn(d, h, self.sorted_token, self.offsets, w.w_gate_up, w.w_down,
+                                  self.y_perm, st, ws, stream), "moe_grouped_ffn")
+        act, y_shared = self.act[:T], self.y_shared[:T]
+        pool = lambda x, y: (x, y, a.ranks, a.scales, adapter_idx)  # noqa: E731
+        none = (None,) * 5
+        B.check(B.moe_lora_project(self._lora(T, True), h, w.shared_gate_up,
+                                   *(none if a is None else pool(a.gate_up_a, a.gate_up_b)), act,
+                                   st, self.lora_workspace, stream), "moe_lora_project")
+        B.check(B.moe_lora_project(self._lora(T, False), act, w.shared_down,
+                                   *(none if a is None else pool(a.down_a, a.down_b)), y_shared,
+                                   st, self.lora_workspace, stream), "moe_lora_project")
+        y = self.y[:T]
+        B.check(B.moe_combine(d, self.y_perm, y_shared, self.inv_row, tw, k_used, y, st, stream),
+                "moe_combine")
+        out = torch.empty_like(y)
+        self._norm(residual, y, w.ffn_post_norm, w.next_pre_norm, residual, out, stream)
+        return out
+
+    def balance(self, rate: float = 0.001):
+        """Moves the selection bias towards equal loads by `rate` a step."""
+        load = self.load.float()
+        self.weights.select_bias += rate * torch.sign(load.mean() - load)
+
+    def device_status(self, stream=None) -> int:
+        return B.moe_get_device_status(self.status, stream)
+
+
+def synthetic(T=64, H=256, experts=32, I=128, shared=256, n_adapters=6, rank=16, seed=0,  # noqa: E741
+              device="cuda"):
+    """A small block with random weights: (block, residual, attn, k, adapter_idx)."""
+    g = torch.Generator(device=device).manual_seed(seed)
+    bf = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=device) * std).bfloat16()  # noqa: E731
+    norm = lambda: (1 + 0.1 * torch.randn(H, generator=g, device=device)).bfloat16()  # noqa: E731
+    w = BlockWeights(norm(), norm(), norm(), norm(), bf(experts, H, std=H ** -0.5),
+                     bf(experts, 2 * I, H, std=H ** -0.5), bf(experts, H, I, std=I ** -0.5),
+                     bf(2 * shared, H, std=H ** -0.5), bf(H, shared, std=shared ** -0.5),
+                     torch.zeros(experts, device=device))
+    pool = Adapters(bf(n_adapters, rank, H, std=H ** -0.5),
+                    bf(n_adapters, 2 * shared, rank, std=0.5 * rank ** -0.5),
+                    bf(n_adapters, rank, shared, std=shared ** -0.5),
+                    bf(n_adapters, H, rank, std=0.5 * rank ** -0.5),
+                    torch.randint(rank // 2, rank + 1, (n_adapters,), generator=g, device=device,
+                                  dtype=torch.int32),
+                    0.5 + torch.rand(n_adapters, generator=g, device=device))
+    layer = B.LayerDesc(T=T, H=H, n_experts=experts, n_sub=1, I_sub=I, k_max=6, score="sigmoid",
+                        renorm=True, route_scale=2.5)
+    block = MoeBlock(layer, B.GroupRoute(n_groups=8, groups_kept=4, group_best=2), w, pool,
+                     device=device)
+    k = torch.randint(3, 7, (T,), generator=g, device=device, dtype=torch.int32)
+    adapter = torch.randint(-1, n_adapters, (T,), generator=g, device=device, dtype=torch.int32)
+    return block, bf(T, H, std=2.0).float(), bf(T, H, std=0.5), k, adapter
+
+
+def main():
+    block, residual, attn, k, adapter = synthetic(T=512)
+    for step in range(200):
+        h = block.forward(residual.clone(), attn, k, adapter)
+        load = block.load.float()
+        if step % 50 == 0 or step == 199:
+            print(f"step {step}: heaviest expert at {float(load.max() / load.mean()):.2f} of the "
+                  f"mean load, |h| {float(h.float().abs().mean()):.3f}")
+        block.balance()
+    print("device status:", B.moe_status_string(block.device_status()))
+
+
+if __name__ == "__main__":
+    main()
