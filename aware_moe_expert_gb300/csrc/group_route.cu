@@ -74,7 +74,8 @@ struct GroupParams {
   int32_t* idx;
   float* w;
   int32_t* k_out;         // nullable
-  int32_t* load;          // nullable; zeroed before the launch unless the grid is one CTA
+  int32_t* load;          // nullable
+  int zeroed;             // more than one CTA adds to load: a launch before this one clears it
   int32_t* status;
 };
 
@@ -94,7 +95,10 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
   __shared__ float2 s_list[kWarps][kMaxUnits];        // score, unit
   __shared__ int32_t s_sel[kWarps][32];
   __shared__ float s_rank[MANY ? kWarps : 1][kMaxUnits];
-  pdl_wait_and_trigger();
+  // With `zeroed` the kernel before this one clears `load`, after it has itself
+  // waited for everything before: only `load` is waited for, at the end.
+  if (!p.zeroed) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (p.load != nullptr) {
     for (int i = threadIdx.x; i < p.E; i += blockDim.x) s_load[i] = 0;
@@ -329,6 +333,7 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
   }
   if (p.load != nullptr) {
     __syncthreads();
+    if (p.zeroed) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = threadIdx.x; i < p.E; i += blockDim.x) {
       const int v = s_load[i];
       if (gridDim.x == 1)
@@ -337,6 +342,11 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
         atomicAdd(p.load + i, v);
     }
   }
+}
+
+__global__ void __launch_bounds__(kMaxUnits) zero_load_kernel(int32_t* load, int E) {
+  pdl_wait_and_trigger();
+  if (static_cast<int>(threadIdx.x) < E) load[threadIdx.x] = 0;
 }
 
 struct RouteBackParams {
@@ -484,8 +494,9 @@ cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
   p.status = a.status;
   const int blocks = (a.T + kWarps - 1) / kWarps;
   const int grid = blocks < 6 * a.sm_count ? blocks : 6 * a.sm_count;
-  if (a.load != nullptr && grid > 1) {
-    const cudaError_t e = cudaMemsetAsync(a.load, 0, sizeof(int32_t) * a.E_r, s);
+  p.zeroed = a.load != nullptr && grid > 1;
+  if (p.zeroed) {
+    const cudaError_t e = launch_pdl(zero_load_kernel, dim3(1), dim3(kMaxUnits), 0, s, a.load, a.E_r);
     if (e != cudaSuccess) return e;
   }
   const dim3 g(grid), b(kWarps * 32);
