@@ -117,7 +117,7 @@ struct Row<float, VEC, EPT> {
 #pragma unroll
     for (int e = 0; e < EPT; ++e) v[e] = 0.f;
   }
-  __device__ __forceinline__ float operator[](int e) const { return v[e]; }
+  __device__ __forceinline__ float2 pair(int i) const { return make_float2(v[2 * i], v[2 * i + 1]); }
 };
 template <int VEC, int EPT>
 struct Row<__nv_bfloat16, VEC, EPT> {
@@ -154,16 +154,24 @@ struct Row<__nv_bfloat16, VEC, EPT> {
 #pragma unroll
     for (int e = 0; e < EPT / 2; ++e) v[e] = 0u;
   }
-  __device__ __forceinline__ float operator[](int e) const {
-    return (e & 1) ? bf16hi(v[e / 2]) : bf16lo(v[e / 2]);
-  }
+  __device__ __forceinline__ float2 pair(int i) const { return make_float2(bf16lo(v[i]), bf16hi(v[i])); }
 };
+
+// Two elements at a time: the SM's packed fp32 instructions halve the
+// arithmetic's share of the issue slots, which bound the backward pass.
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // Columns of a vector [H] that every row shares (any alignment).
 template <typename T, int VEC, int EPT>
-__device__ __forceinline__ void load_cols(const T* __restrict__ p, const Cols<VEC, EPT>& c, float (&v)[EPT]) {
+__device__ __forceinline__ void load_cols(const T* __restrict__ p, const Cols<VEC, EPT>& c,
+                                          float2 (&v)[EPT / 2]) {
 #pragma unroll
-  for (int e = 0; e < EPT; ++e) v[e] = c.in(e) ? to_f(p[c.col(e)]) : 0.f;
+  for (int i = 0; i < EPT / 2; ++i)
+    v[i] = make_float2(c.in(2 * i) ? to_f(p[c.col(2 * i)]) : 0.f,
+                       c.in(2 * i + 1) ? to_f(p[c.col(2 * i + 1)]) : 0.f);
 }
 
 // The first or last piece of a row, part of which lies outside.  A call, so
@@ -183,28 +191,30 @@ __device__ __noinline__ void store_part(T* at, uint32_t mask, float a, float b, 
 
 // `p`: the row's column 0.
 template <typename T, int VEC, int EPT>
-__device__ __forceinline__ void store_row(T* __restrict__ p, const Cols<VEC, EPT>& c, const float (&v)[EPT]) {
+__device__ __forceinline__ void store_row(T* __restrict__ p, const Cols<VEC, EPT>& c,
+                                          const float2 (&v)[EPT / 2]) {
   if constexpr (VEC == kOne) {
 #pragma unroll
-    for (int e = 0; e < EPT; ++e)
-      if (c.in(e)) p[c.col(e)] = from_f<T>(v[e]);
+    for (int i = 0; i < EPT / 2; ++i) {
+      if (c.in(2 * i)) p[c.col(2 * i)] = from_f<T>(v[i].x);
+      if (c.in(2 * i + 1)) p[c.col(2 * i + 1)] = from_f<T>(v[i].y);
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < EPT; e += 8) {
       T* at = p + c.first(e / 8);
+      const float2 &a = v[e / 2], &b = v[e / 2 + 1], &d = v[e / 2 + 2], &f = v[e / 2 + 3];
       if (c.whole(e / 8)) {
         if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<uint4*>(at) =
-              make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
-                         pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
+          *reinterpret_cast<uint4*>(at) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y),
+                                                     pack_bf16x2(d.x, d.y), pack_bf16x2(f.x, f.y));
         } else {
-          *reinterpret_cast<float4*>(at) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-          *reinterpret_cast<float4*>(at + 4) = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+          *reinterpret_cast<float4*>(at) = make_float4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<float4*>(at + 4) = make_float4(d.x, d.y, f.x, f.y);
         }
       } else if constexpr (VEC == kSkewed) {
         const uint32_t m = c.mask[e / 32] >> (e % 32) & 255u;
-        if (m != 0u)
-          store_part<T>(at, m, v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+        if (m != 0u) store_part<T>(at, m, a.x, a.y, b.x, b.y, d.x, d.y, f.x, f.y);
       }
     }
   }
@@ -308,13 +318,14 @@ __device__ __noinline__ void wait_long(uint64_t* bar, uint32_t phase, int32_t* s
 struct NormSmem {
   uint32_t red, bars, total;
 };
+// Two barriers a slot: full, and (forward) empty.
 __host__ __device__ inline NormSmem norm_smem(uint32_t slot_bytes, int slots, int groups) {
   NormSmem o;
   uint32_t b = slot_bytes * static_cast<uint32_t>(slots) * static_cast<uint32_t>(groups);
   o.red = b;
   b += static_cast<uint32_t>(groups) * 2 * kSumFloats * 4;
   o.bars = b;
-  b += static_cast<uint32_t>(groups * slots) * 8;
+  b += static_cast<uint32_t>(groups * slots) * 16;
   o.total = b;
   return o;
 }
@@ -322,59 +333,118 @@ __host__ __device__ inline NormSmem norm_smem(uint32_t slot_bytes, int slots, in
 // One group's ring.  A slot holds the rows r, y, [gate], [dr'], [dh] of a token,
 // each as the 16-byte granules around it.  Pieces: column -skew lies at the
 // start of its place; kOne: the granules do.
-template <typename R, typename A, int VEC, bool BACK>
+// Filling a slot is a chain of address arithmetic, and a thread of the group
+// that did it alone held up the group's next sums for longer than the sums
+// took.  Forward, a warp of its own does it, a lane for each group (Producer);
+// backward, whose registers leave no room for one, the group's first warp, a
+// lane for each tensor (Filler).
+template <typename R, typename A, int VEC>
 struct Ring {
   uint8_t* base;
   uint64_t* full;
   const NormParams* p;
-  int skew;
 
-  template <typename T>
-  __device__ __forceinline__ const T* row(const void* q, int t, long long ld) const {
-    return static_cast<const T*>(q) + static_cast<long long>(t) * ld;
-  }
+  __device__ __forceinline__ Ring(const NormParams* q, uint8_t* smem, uint64_t* bars, int group)
+      : base(smem + static_cast<uint32_t>(group * q->slots) * q->slot_bytes),
+        full(bars + group * q->slots),
+        p(q) {}
   // a row's place in a slot, as Row::load wants it
   template <typename T>
-  __device__ __forceinline__ const T* place(int slot, uint32_t at, const void* q, int t, long long ld) const {
-    uint32_t off = static_cast<uint32_t>(slot) * p->slot_bytes + at;
-    if (VEC == kOne) off += static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row<T>(q, t, ld)) & 15u);
+  __device__ __forceinline__ const T* place(int slot, uint32_t off, const void* q, int t, long long ld) const {
+    off += static_cast<uint32_t>(slot) * p->slot_bytes;
+    if (VEC == kOne)
+      off += static_cast<uint32_t>(
+          reinterpret_cast<uintptr_t>(static_cast<const T*>(q) + static_cast<long long>(t) * ld) & 15u);
     return reinterpret_cast<const T*>(base + off);
-  }
-  template <typename T>
-  __device__ __forceinline__ uint32_t fill_one(uint32_t at, const void* q, int t, long long ld, uint64_t* bar,
-                                               bool issue) const {
-    if (q == nullptr) return 0u;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(row<T>(q, t, ld)), lo = a & ~static_cast<uintptr_t>(15);
-    const uint32_t n = static_cast<uint32_t>(
-        ((a + static_cast<uintptr_t>(p->H) * sizeof(T) + 15) & ~static_cast<uintptr_t>(15)) - lo);
-    if (VEC != kOne) at += static_cast<uint32_t>(lo - (a - static_cast<uintptr_t>(skew) * sizeof(T)));
-    if (issue) bulk_load(at, reinterpret_cast<const void*>(lo), n, bar);
-    return n;
-  }
-  __device__ __forceinline__ void fill(int slot, int t) const {
-    uint64_t* bar = full + slot;
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      uint32_t at = smem_u32(base) + static_cast<uint32_t>(slot) * p->slot_bytes, total = 0;
-      const bool go = pass == 1;
-      total += fill_one<R>(at, p->r, t, p->ld_r, bar, go);
-      at += p->pitch_r;
-      total += fill_one<A>(at, p->y, t, p->ld_y, bar, go);
-      at += p->pitch_a;
-      if (p->gate == MOE_GATE_FULL) {
-        total += fill_one<A>(at, p->gate_p, t, p->ld_g, bar, go);
-        at += p->pitch_a;
-      }
-      if (BACK) {
-        total += fill_one<R>(at, p->d_out, t, p->ld_dout, bar, go);
-        at += p->pitch_r;
-        total += fill_one<A>(at, p->d_h, t, p->ld_dh, bar, go);
-      }
-      if (!go) mbar_expect_tx(bar, total);
-    }
   }
   __device__ __forceinline__ void wait(int slot, uint32_t phase) const {
     if (!mbar_try_wait(full + slot, phase)) wait_long(full + slot, phase, p->status);
+  }
+};
+
+// The rows of one tensor that a group copies.
+template <int VEC>
+struct RowStream {
+  uintptr_t next = 0;           // the next row
+  long long stride = 0;
+  uint32_t bytes = 0, at = 0, before = 0;
+
+  template <typename T>
+  __device__ __forceinline__ void take(const NormParams& p, const void* q, long long ld, uint32_t place,
+                                       int skew, int first, int step) {
+    if (q == nullptr) return;
+    next = reinterpret_cast<uintptr_t>(q) + static_cast<long long>(first) * ld * static_cast<long long>(sizeof(T));
+    stride = static_cast<long long>(step) * ld * static_cast<long long>(sizeof(T));
+    bytes = static_cast<uint32_t>(p.H) * sizeof(T);
+    at = place;
+    before = VEC == kOne ? 0u : static_cast<uint32_t>(skew) * sizeof(T);
+  }
+  __device__ __forceinline__ uintptr_t from() const { return next & ~static_cast<uintptr_t>(15); }
+  __device__ __forceinline__ uint32_t size() const {
+    return bytes != 0u ? static_cast<uint32_t>(((next + bytes + 15) & ~static_cast<uintptr_t>(15)) - from()) : 0u;
+  }
+  __device__ __forceinline__ void copy(uint32_t slot, uint64_t* full) {
+    if (bytes == 0u) return;
+    const uint32_t skip = VEC == kOne ? 0u : static_cast<uint32_t>(from() - (next - before));
+    bulk_load(slot + at + skip, reinterpret_cast<const void*>(from()), size(), full);
+    next += stride;
+  }
+};
+
+// A lane of the forward pass's producer warp: every row of its group, a slot as
+// soon as it is free.
+template <typename R, typename A, int VEC>
+__device__ __forceinline__ void produce(const Ring<R, A, VEC>& ring, uint64_t* empty, int skew, int first,
+                                        int step) {
+  const NormParams& p = *ring.p;
+  RowStream<VEC> r, y, g;
+  r.template take<R>(p, p.r, p.ld_r, 0u, skew, first, step);
+  y.template take<A>(p, p.y, p.ld_y, p.pitch_r, skew, first, step);
+  if (p.gate == MOE_GATE_FULL)
+    g.template take<A>(p, p.gate_p, p.ld_g, p.pitch_r + p.pitch_a, skew, first, step);
+  uint32_t phase = 1;
+  int slot = 0;
+  for (int t = first; t < p.T; t += step) {
+    if (!mbar_wait(empty + slot, phase, nullptr)) {
+      report(p.status, MOE_ERR_DEVICE_TIMEOUT);
+      return;
+    }
+    const uint32_t to = smem_u32(ring.base) + static_cast<uint32_t>(slot) * p.slot_bytes;
+    mbar_expect_tx(ring.full + slot, r.size() + y.size() + g.size());
+    r.copy(to, ring.full + slot);
+    y.copy(to, ring.full + slot);
+    g.copy(to, ring.full + slot);
+    if (++slot == p.slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+}
+
+// The backward pass's: lane i of the group's first warp has tensor i.
+template <typename R, typename A, int VEC>
+struct Filler {
+  RowStream<VEC> s;
+  int left;                     // rows still to copy
+
+  __device__ __forceinline__ Filler(const NormParams& p, int skew, int first, int step, int lane)
+      : left(first < p.T ? (p.T - 1 - first) / step + 1 : 0) {
+    const bool gate = p.gate == MOE_GATE_FULL;
+    const uint32_t o_gate = p.pitch_r + p.pitch_a, o_do = o_gate + (gate ? p.pitch_a : 0u);
+    if (lane == 0) s.template take<R>(p, p.r, p.ld_r, 0u, skew, first, step);
+    if (lane == 1) s.template take<A>(p, p.y, p.ld_y, p.pitch_r, skew, first, step);
+    if (lane == 2 && gate) s.template take<A>(p, p.gate_p, p.ld_g, o_gate, skew, first, step);
+    if (lane == 3) s.template take<R>(p, p.d_out, p.ld_dout, o_do, skew, first, step);
+    if (lane == 4) s.template take<A>(p, p.d_h, p.ld_dh, o_do + p.pitch_r, skew, first, step);
+  }
+  // the group's next row into `slot`
+  __device__ __forceinline__ void fill(const Ring<R, A, VEC>& ring, int slot, int lane) {
+    if (left <= 0) return;
+    --left;
+    const uint32_t total = __reduce_add_sync(0xffffffffu, s.size());
+    if (lane == 0) mbar_expect_tx(ring.full + slot, total);
+    __syncwarp();
+    s.copy(smem_u32(ring.base) + static_cast<uint32_t>(slot) * ring.p->slot_bytes, ring.full + slot);
   }
 };
 
@@ -386,27 +456,32 @@ __device__ __forceinline__ int skew_of(const NormParams& p, int first) {
   return VEC == kSkewed ? static_cast<int>((static_cast<long long>(first) * p.ld_r) & 7) : 0;
 }
 
+// MAXT threads in groups, and the producer warp.
 template <typename R, typename A, int VEC, int EPT, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(MAXT + 32, 1) block_norm_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const NormSmem L = norm_smem(p.slot_bytes, p.slots, p.groups);
-  const int group = threadIdx.x / p.tpr, tid = threadIdx.x - group * p.tpr;
+  const bool producer = threadIdx.x >= p.tpr * p.groups;
+  const int group = producer ? threadIdx.x & 31 : threadIdx.x / p.tpr;
+  const int tid = threadIdx.x - group * p.tpr;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
   float* red = reinterpret_cast<float*>(smem + L.red) + group * 2 * kSumFloats;
   const int step = gridDim.x * p.groups;
   const int first = blockIdx.x + gridDim.x * group;
-  const Ring<R, A, VEC, false> ring{smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes,
-                                    bars + group * p.slots, &p, skew_of<VEC>(p, first)};
+  const Ring<R, A, VEC> ring(&p, smem, bars, group);
+  uint64_t* empty = bars + (p.groups + group) * p.slots;
+  const int skew = skew_of<VEC>(p, first);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.groups * p.slots; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 2 * p.groups * p.slots; ++i) mbar_init(bars + i, 1);
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait_and_trigger();
-  if (tid == 0)
-    for (int s = 0; s < p.slots; ++s)
-      if (first + s * step < p.T) ring.fill(s, first + s * step);
-  const Cols<VEC, EPT> c(tid, p.tpr, p.H, ring.skew);
+  if (producer) {
+    if (group < p.groups) produce(ring, empty, skew, first, step);
+    return;
+  }
+  const Cols<VEC, EPT> c(tid, p.tpr, p.H, skew);
   const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr;
   // the weights of the thread's columns as they are in memory
   Row<A, VEC, EPT> w1, w2, g;
@@ -441,8 +516,10 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p)
     float q = 0.f;
     if (p.y != nullptr) {
       x.load(ring.template place<A>(sl, p.pitch_r, p.y, t, p.ld_y), c);
+      float2 a = two(0.f);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) q = fmaf(x[e], x[e], q);
+      for (int i = 0; i < EPT / 2; ++i) a = fma(x.pair(i), x.pair(i), a);
+      q = a.x + a.y;
     }
     return q;
   };
@@ -458,40 +535,43 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p)
     float scale = p.bs;
     if (p.gate == MOE_GATE_TOKEN) scale *= to_f(static_cast<const A*>(p.gate_p)[t]);
     if (post) scale *= rsqrtf(sq * inv_h + p.eps);
-    float v[EPT];
+    float2 v[EPT / 2];
     {
       Row<R, VEC, EPT> r;
       r.load(ring.template place<R>(slot, 0, p.r, t, p.ld_r), c);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] = p.rs * r[e];
+      for (int i = 0; i < EPT / 2; ++i) v[i] = mul(two(p.rs), r.pair(i));
     }
     if (vector_gate) {
       if (p.gate == MOE_GATE_FULL)
         g.load(ring.template place<A>(slot, p.pitch_r + p.pitch_a, p.gate_p, t, p.ld_g), c);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] = fmaf(x[e] * scale * g[e], w1[e] + off1, v[e]);
+      for (int i = 0; i < EPT / 2; ++i)
+        v[i] = fma(mul(mul(x.pair(i), two(scale)), g.pair(i)), add(w1.pair(i), two(off1)), v[i]);
     } else {
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] = fmaf(x[e] * scale, w1[e] + off1, v[e]);
+      for (int i = 0; i < EPT / 2; ++i)
+        v[i] = fma(mul(x.pair(i), two(scale)), add(w1.pair(i), two(off1)), v[i]);
     }
     if (p.out != nullptr) store_row(out, c, v);
     out += out_step;
-    float q[2] = {0.f, 0.f};
+    float2 vv = two(0.f);
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) q[0] = fmaf(v[e], v[e], q[0]);
+    for (int i = 0; i < EPT / 2; ++i) vv = fma(v[i], v[i], vv);
+    float q[2] = {vv.x + vv.y, 0.f};
     const int next = slot + 1 == p.slots ? 0 : slot + 1;
     const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
     if (ahead && t + step < p.T) q[1] = take_y(t + step, next, next_phase);
     // behind this barrier every thread has its part of the slot
     group_sum<2>(q, p.tpr, 1 + group, tid, red, parity);
-    if (tid == 0 && t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
+    if (tid == 0) mbar_arrive(empty + slot);
     slot = next;
     phase = next_phase;
     sq = q[1];
     if (pre) {
       const float f = rsqrtf(q[0] * inv_h + p.eps);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) v[e] *= f * (w2[e] + p.offset);
+      for (int i = 0; i < EPT / 2; ++i) v[i] = mul(mul(v[i], two(f)), add(w2.pair(i), two(p.offset)));
       store_row(h, c, v);
       h += h_step;
     }
@@ -502,11 +582,13 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const NormParams p)
 // are free by then), added in group order, to the CTA's partial row.
 template <int VEC, int EPT>
 __device__ __forceinline__ void cta_columns(float* buf, float* dst, const Cols<VEC, EPT>& c, int group,
-                                            int groups, const float (&v)[EPT]) {
+                                            int groups, const float2 (&v)[EPT / 2]) {
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < EPT; ++e)
-    if (c.in(e)) buf[group * c.H + c.col(e)] = v[e];
+  for (int i = 0; i < EPT / 2; ++i) {
+    if (c.in(2 * i)) buf[group * c.H + c.col(2 * i)] = v[i].x;
+    if (c.in(2 * i + 1)) buf[group * c.H + c.col(2 * i + 1)] = v[i].y;
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < c.H; i += blockDim.x) {
     float s = buf[i];
@@ -524,52 +606,54 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const Norm
   float* red = reinterpret_cast<float*>(smem + L.red) + group * 2 * kSumFloats;
   const int step = gridDim.x * p.groups;
   const int first = blockIdx.x + gridDim.x * group;
-  const Ring<R, A, VEC, true> ring{smem + static_cast<uint32_t>(group * p.slots) * p.slot_bytes,
-                                   bars + group * p.slots, &p, skew_of<VEC>(p, first)};
+  const Ring<R, A, VEC> ring(&p, smem, bars, group);
+  const int skew = skew_of<VEC>(p, first);
+  Filler<R, A, VEC> filler(p, skew, first, step, tid);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.groups * p.slots; ++i) mbar_init(bars + i, 1);
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait_and_trigger();
-  if (tid == 0)
-    for (int s = 0; s < p.slots; ++s)
-      if (first + s * step < p.T) ring.fill(s, first + s * step);
-  const Cols<VEC, EPT> c(tid, p.tpr, p.H, ring.skew);
+  if (tid < 32)
+    for (int i = 0; i < p.slots; ++i) filler.fill(ring, i, tid);
+  const Cols<VEC, EPT> c(tid, p.tpr, p.H, skew);
   const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr, branch = p.y != nullptr;
   const bool full = p.gate == MOE_GATE_FULL, vector_gate = full || p.gate == MOE_GATE_CHANNEL;
   const float inv_h = 1.f / static_cast<float>(p.H);
-  float a_post[EPT], a_pre[EPT], a_gate[EPT];   // column sums of dw_post / bs, dw_pre, dg
-  float w1[EPT], w2[EPT];                       // bs w_post, w_pre
+  constexpr int P = EPT / 2;
+  float2 a_post[P], a_pre[P], a_gate[P];        // column sums of dw_post / bs, dw_pre, dg
+  float2 w1[P], w2[P];                          // bs w_post, w_pre
 #pragma unroll
-  for (int e = 0; e < EPT; ++e) a_post[e] = a_pre[e] = a_gate[e] = w1[e] = w2[e] = 0.f;
+  for (int i = 0; i < P; ++i) a_post[i] = a_pre[i] = a_gate[i] = w1[i] = w2[i] = two(0.f);
   if (post) load_cols<A>(static_cast<const A*>(p.w_post), c, w1);
   if (pre) load_cols<A>(static_cast<const A*>(p.w_pre), c, w2);
 #pragma unroll
-  for (int e = 0; e < EPT; ++e) {
-    w1[e] = (post ? w1[e] + p.offset : 1.f) * p.bs;
-    w2[e] += p.offset;
+  for (int i = 0; i < P; ++i) {
+    w1[i] = post ? mul(add(w1[i], two(p.offset)), two(p.bs)) : two(p.bs);
+    w2[i] = add(w2[i], two(p.offset));
   }
   Row<A, VEC, EPT> g;
   g.zero();
   if (p.gate == MOE_GATE_CHANNEL) {
-    float w[EPT];
+    float2 w[P];
     load_cols<A>(static_cast<const A*>(p.gate_p), c, w);
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) g.set(e, w[e]);
+    for (int i = 0; i < P; ++i) {
+      g.set(2 * i, w[i].x);
+      g.set(2 * i + 1, w[i].y);
+    }
   }
-  // Rows behind this one's sums: a slot is filled again behind the sums of the
-  // next row, so three are needed for sum(y^2) to run a row ahead.
-  const bool ahead = p.slots > 2;
+  const bool ahead = p.slots > 1;
   auto squares = [&](int t, int sl) {
     Row<A, VEC, EPT> y;
     y.load(ring.template place<A>(sl, p.pitch_r, p.y, t, p.ld_y), c);
-    float q = 0.f;
+    float2 q = two(0.f);
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) q = fmaf(y[e], y[e], q);
-    return q;
+    for (int i = 0; i < P; ++i) q = fma(y.pair(i), y.pair(i), q);
+    return q.x + q.y;
   };
-  int slot = 0, parity = 0, before = 0;
+  int slot = 0, parity = 0;
   uint32_t phase = 0;
   float sq = 0.f;                               // sum of squares of the row's y
   R* out = static_cast<R*>(p.out) + static_cast<long long>(first) * p.ld_out;
@@ -597,7 +681,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const Norm
     if (p.d_out != nullptr) dr.load(ring.template place<R>(slot, at, p.d_out, t, p.ld_dout), c);
     if (pre) dh.load(ring.template place<A>(slot, at + p.pitch_r, p.d_h, t, p.ld_dh), c);
     // n = y rstd(y), u = bs g n w_post (without the token's gate), m~ = r'
-    float n[EPT], m[EPT];
+    float2 n[P], m[P];
     {
       Row<R, VEC, EPT> r;
       Row<A, VEC, EPT> y;
@@ -605,83 +689,77 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const Norm
       r.load(ring.template place<R>(slot, 0, p.r, t, p.ld_r), c);
       if (branch) y.load(ring.template place<A>(slot, p.pitch_r, p.y, t, p.ld_y), c);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        n[e] = y[e] * fy;
-        m[e] = p.rs * r[e];
+      for (int i = 0; i < P; ++i) {
+        n[i] = mul(y.pair(i), two(fy));
+        m[i] = mul(r.pair(i), two(p.rs));
       }
     }
     // one round of sums for both norms: with d = dh w_pre,
     //   mean(d m) = f^2 sum(d m~) / H,  f = rstd(r')
     //   sum(D u) = sum(dr' u) + f sum(d u) - f mean sum(m~ u)
-    float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    auto add = [&](int e, float u) {
-      m[e] = fmaf(tg, u, m[e]);
-      const float d = dh[e] * w2[e];
-      q[0] = fmaf(m[e], m[e], q[0]);
-      q[1] = fmaf(d, m[e], q[1]);
-      q[2] = fmaf(dr[e], u, q[2]);
-      q[3] = fmaf(d, u, q[3]);
-      q[4] = fmaf(m[e], u, q[4]);
+    float2 s[5] = {two(0.f), two(0.f), two(0.f), two(0.f), two(0.f)};
+    auto gather = [&](int i, float2 u) {
+      m[i] = fma(two(tg), u, m[i]);
+      const float2 d = mul(dh.pair(i), w2[i]);
+      s[0] = fma(m[i], m[i], s[0]);
+      s[1] = fma(d, m[i], s[1]);
+      s[2] = fma(dr.pair(i), u, s[2]);
+      s[3] = fma(d, u, s[3]);
+      s[4] = fma(m[i], u, s[4]);
     };
     if (vector_gate) {
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) add(e, n[e] * w1[e] * g[e]);
+      for (int i = 0; i < P; ++i) gather(i, mul(mul(n[i], w1[i]), g.pair(i)));
     } else {
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) add(e, n[e] * w1[e]);
+      for (int i = 0; i < P; ++i) gather(i, mul(n[i], w1[i]));
     }
+    float q[8] = {s[0].x + s[0].y, s[1].x + s[1].y, s[2].x + s[2].y, s[3].x + s[3].y,
+                  s[4].x + s[4].y, 0.f, 0.f, 0.f};
     const int next = slot + 1 == p.slots ? 0 : slot + 1;
     const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
     if (ahead && t + step < p.T) {
       ring.wait(next, next_phase);
       if (post) q[5] = squares(t + step, next);
     }
-    // behind this barrier everyone is done with the row before, and has this
-    // one in registers
+    // behind this barrier everyone has the row in registers
     group_sum<8>(q, p.tpr, 1 + group, tid, red, parity);
-    if (tid == 0) {
-      if (!ahead) {
-        if (t + p.slots * step < p.T) ring.fill(slot, t + p.slots * step);
-      } else if (t != first && t + (p.slots - 1) * step < p.T) {
-        ring.fill(before, t + (p.slots - 1) * step);
-      }
-    }
+    if (tid < 32) filler.fill(ring, slot, tid);
     sq = q[5];
     const float f = pre ? rsqrtf(q[0] * inv_h + p.eps) : 0.f, mean_h = q[1] * inv_h * f * f;
     const float sum_u = q[2] + f * (q[3] - mean_h * q[4]), c2 = f * mean_h;
     if (p.gate == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(p.d_gate)[t] = sum_u;
-    float D[EPT], o[EPT];                       // the whole gradient at r'
+    float2 D[P], o[P];                          // the whole gradient at r'
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      const float h = dh[e];
-      a_pre[e] = fmaf(h, m[e] * f, a_pre[e]);
-      D[e] = fmaf(-c2, m[e], fmaf(f, h * w2[e], dr[e]));
-      o[e] = p.rs * D[e];
+    for (int i = 0; i < P; ++i) {
+      const float2 h = dh.pair(i);
+      a_pre[i] = fma(h, mul(m[i], two(f)), a_pre[i]);
+      D[i] = fma(m[i], two(-c2), fma(mul(h, w2[i]), two(f), dr.pair(i)));
+      o[i] = mul(D[i], two(p.rs));
     }
     store_row(out, c, o);
     out += out_step;
     if (branch) {
       if (vector_gate) {
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) {
-          o[e] = D[e] * (n[e] * w1[e]);
-          a_gate[e] += o[e];
-          D[e] *= g[e];
+        for (int i = 0; i < P; ++i) {
+          o[i] = mul(D[i], mul(n[i], w1[i]));
+          a_gate[i] = add(a_gate[i], o[i]);
+          D[i] = mul(D[i], g.pair(i));
         }
         if (full) store_row(static_cast<A*>(p.d_gate) + static_cast<long long>(t) * p.ld_g, c, o);
       }
       // sum(dz z) over the row is the token's gate times sum(D u)
       const float c3 = post ? fy * sum_u * tg * inv_h : 0.f;
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        const float dz = tg * D[e];
-        a_post[e] = fmaf(dz, n[e], a_post[e]);
-        D[e] = fmaf(fy, dz * w1[e], -c3 * n[e]);
+      for (int i = 0; i < P; ++i) {
+        const float2 dz = mul(D[i], two(tg));
+        a_post[i] = fma(dz, n[i], a_post[i]);
+        D[i] = fma(mul(dz, w1[i]), two(fy), mul(n[i], two(-c3)));
       }
       store_row(dy, c, D);
       dy += dy_step;
     }
-    before = slot;
     slot = next;
     phase = next_phase;
   }
@@ -690,7 +768,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const Norm
     float* dst = p.part + static_cast<size_t>(blockIdx.x) * p.n_part * p.H;
     if (post) {
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) a_post[e] *= p.bs;
+      for (int i = 0; i < P; ++i) a_post[i] = mul(a_post[i], two(p.bs));
       cta_columns(buf, dst, c, group, p.groups, a_post);
       dst += p.H;
     }
@@ -775,7 +853,7 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaSt
   const uint32_t smem = norm_smem(p.slot_bytes, p.slots, p.groups).total;
   auto go = [&](auto k) {
     const cudaError_t e = set_smem_once(k, 227 * 1024, done);
-    return e != cudaSuccess ? e : launch_pdl(k, dim3(*grid), dim3(p.tpr * p.groups), smem, s, p);
+    return e != cudaSuccess ? e : launch_pdl(k, dim3(*grid), dim3(p.tpr * p.groups + (BACK ? 0 : 32)), smem, s, p);
   };
   if constexpr (BACK)
     return go(block_norm_backward_kernel<R, A, VEC, EPT, MAXT>);
@@ -783,8 +861,9 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaSt
     return go(block_norm_kernel<R, A, VEC, EPT, MAXT>);
 }
 
-// Elements a thread and threads a CTA.  The backward pass holds three column
-// sums per element: 512 threads have the registers for it.
+// Elements a thread and threads a CTA: eight elements as long as the threads
+// reach.  The backward pass holds three column sums per element: 512 threads
+// have the registers for it (1024 spilled and took twice as long).
 template <typename R, typename A, int VEC>
 cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
   const int n = span(p, VEC);
@@ -793,11 +872,8 @@ cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* 
     if (n <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
     return run<R, A, VEC, 40, 512, true>(p, rows_r, rows_a, sm, grid, s);
   }
-  // a row per SM: more threads at it; many rows: two groups at work on an SM
-  if (n <= 1024 || (p.T <= sm && n <= 8 * 1024))
-    return run<R, A, VEC, 8, 1024, false>(p, rows_r, rows_a, sm, grid, s);
-  if (n <= 16 * 896) return run<R, A, VEC, 16, 896, false>(p, rows_r, rows_a, sm, grid, s);
-  return run<R, A, VEC, 24, 768, false>(p, rows_r, rows_a, sm, grid, s);
+  if (n <= 8 * 992) return run<R, A, VEC, 8, 992, false>(p, rows_r, rows_a, sm, grid, s);
+  return run<R, A, VEC, 24, 736, false>(p, rows_r, rows_a, sm, grid, s);
 }
 
 template <typename R, typename A>
