@@ -57,6 +57,7 @@ template <int VEC, int EPT>
 struct Cols {
   int tid, tpr, H, skew;
   uint32_t mask[VEC == kSkewed ? (EPT + 31) / 32 : 1];   // kSkewed: bit e: element e is in the row
+  uint32_t half[VEC == kSkewed ? EPT / 2 : 1];           // and the same over two bf16
   __device__ __forceinline__ Cols(int tid_, int tpr_, int H_, int skew_)
       : tid(tid_), tpr(tpr_), H(H_), skew(skew_) {
     if constexpr (VEC == kSkewed) {
@@ -65,6 +66,8 @@ struct Cols {
 #pragma unroll
       for (int e = 0; e < EPT; ++e)
         if (static_cast<unsigned>(col(e)) < static_cast<unsigned>(H)) mask[e / 32] |= 1u << (e % 32);
+#pragma unroll
+      for (int e = 0; e < EPT; e += 2) half[e / 2] = (in(e) ? 0xffffu : 0u) | (in(e + 1) ? 0xffff0000u : 0u);
     }
   }
   // first column of piece v, and its place from the first piece's start
@@ -141,8 +144,7 @@ struct Row<__nv_bfloat16, VEC, EPT> {
       }
       if constexpr (VEC == kSkewed) {
 #pragma unroll
-        for (int e = 0; e < EPT; e += 2)
-          v[e / 2] &= (c.in(e) ? 0xffffu : 0u) | (c.in(e + 1) ? 0xffff0000u : 0u);
+        for (int i = 0; i < EPT / 2; ++i) v[i] &= c.half[i];
       }
     }
   }
@@ -174,21 +176,6 @@ __device__ __forceinline__ void load_cols(const T* __restrict__ p, const Cols<VE
                        c.in(2 * i + 1) ? to_f(p[c.col(2 * i + 1)]) : 0.f);
 }
 
-// The first or last piece of a row, part of which lies outside.  A call, so
-// that the other threads branch around it.
-template <typename T>
-__device__ __noinline__ void store_part(T* at, uint32_t mask, float a, float b, float c, float d, float e,
-                                        float f, float g, float h) {
-  if (mask & 1u) at[0] = from_f<T>(a);
-  if (mask & 2u) at[1] = from_f<T>(b);
-  if (mask & 4u) at[2] = from_f<T>(c);
-  if (mask & 8u) at[3] = from_f<T>(d);
-  if (mask & 16u) at[4] = from_f<T>(e);
-  if (mask & 32u) at[5] = from_f<T>(f);
-  if (mask & 64u) at[6] = from_f<T>(g);
-  if (mask & 128u) at[7] = from_f<T>(h);
-}
-
 // `p`: the row's column 0.
 template <typename T, int VEC, int EPT>
 __device__ __forceinline__ void store_row(T* __restrict__ p, const Cols<VEC, EPT>& c,
@@ -213,8 +200,15 @@ __device__ __forceinline__ void store_row(T* __restrict__ p, const Cols<VEC, EPT
           *reinterpret_cast<float4*>(at + 4) = make_float4(d.x, d.y, f.x, f.y);
         }
       } else if constexpr (VEC == kSkewed) {
-        const uint32_t m = c.mask[e / 32] >> (e % 32) & 255u;
-        if (m != 0u) store_part<T>(at, m, a.x, a.y, b.x, b.y, d.x, d.y, f.x, f.y);
+        // the row's first or last piece
+        if (c.in(e)) at[0] = from_f<T>(a.x);
+        if (c.in(e + 1)) at[1] = from_f<T>(a.y);
+        if (c.in(e + 2)) at[2] = from_f<T>(b.x);
+        if (c.in(e + 3)) at[3] = from_f<T>(b.y);
+        if (c.in(e + 4)) at[4] = from_f<T>(d.x);
+        if (c.in(e + 5)) at[5] = from_f<T>(d.y);
+        if (c.in(e + 6)) at[6] = from_f<T>(f.x);
+        if (c.in(e + 7)) at[7] = from_f<T>(f.y);
       }
     }
   }
@@ -434,6 +428,7 @@ struct Filler {
     if (lane == 0) s.template take<R>(p, p.r, p.ld_r, 0u, skew, first, step);
     if (lane == 1) s.template take<A>(p, p.y, p.ld_y, p.pitch_r, skew, first, step);
     if (lane == 2 && gate) s.template take<A>(p, p.gate_p, p.ld_g, o_gate, skew, first, step);
+    // (forward: null)
     if (lane == 3) s.template take<R>(p, p.d_out, p.ld_dout, o_do, skew, first, step);
     if (lane == 4) s.template take<A>(p, p.d_h, p.ld_dh, o_do + p.pitch_r, skew, first, step);
   }
@@ -456,9 +451,10 @@ __device__ __forceinline__ int skew_of(const NormParams& p, int first) {
   return VEC == kSkewed ? static_cast<int>((static_cast<long long>(first) * p.ld_r) & 7) : 0;
 }
 
-// MAXT threads in groups, and the producer warp.
-template <typename R, typename A, int VEC, int EPT, int MAXT>
-__global__ void __launch_bounds__(MAXT + 32, 1) block_norm_kernel(const NormParams p) {
+// MAXT threads in groups, and the producer warp.  SELF: groups of one warp fill
+// their own slots (31 of them kept one producer warp too busy).
+template <typename R, typename A, int VEC, int EPT, int MAXT, bool SELF>
+__global__ void __launch_bounds__(MAXT + (SELF ? 0 : 32), 1) block_norm_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const NormSmem L = norm_smem(p.slot_bytes, p.slots, p.groups);
   const bool producer = threadIdx.x >= p.tpr * p.groups;
@@ -477,7 +473,10 @@ __global__ void __launch_bounds__(MAXT + 32, 1) block_norm_kernel(const NormPara
   }
   __syncthreads();
   pdl_wait_and_trigger();
-  if (producer) {
+  Filler<R, A, VEC> filler(p, skew, first, step, SELF ? tid : 32);
+  if (SELF) {
+    for (int i = 0; i < p.slots; ++i) filler.fill(ring, i, tid);
+  } else if (producer) {
     if (group < p.groups) produce(ring, empty, skew, first, step);
     return;
   }
@@ -564,7 +563,10 @@ __global__ void __launch_bounds__(MAXT + 32, 1) block_norm_kernel(const NormPara
     if (ahead && t + step < p.T) q[1] = take_y(t + step, next, next_phase);
     // behind this barrier every thread has its part of the slot
     group_sum<2>(q, p.tpr, 1 + group, tid, red, parity);
-    if (tid == 0) mbar_arrive(empty + slot);
+    if (SELF)
+      filler.fill(ring, slot, tid);
+    else if (tid == 0)
+      mbar_arrive(empty + slot);
     slot = next;
     phase = next_phase;
     sq = q[1];
@@ -842,7 +844,7 @@ void shape_of(NormParams& p, int vec, int ept, int max_threads, int rows_r, int 
   p.slots = slots;
 }
 
-template <typename R, typename A, int VEC, int EPT, int MAXT, bool BACK>
+template <typename R, typename A, int VEC, int EPT, int MAXT, bool BACK, bool SELF = false>
 cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
   static bool done[64] = {false};
   shape_of(p, VEC, EPT, MAXT, rows_r, rows_a, sizeof(R), sizeof(A), sm);
@@ -853,12 +855,12 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaSt
   const uint32_t smem = norm_smem(p.slot_bytes, p.slots, p.groups).total;
   auto go = [&](auto k) {
     const cudaError_t e = set_smem_once(k, 227 * 1024, done);
-    return e != cudaSuccess ? e : launch_pdl(k, dim3(*grid), dim3(p.tpr * p.groups + (BACK ? 0 : 32)), smem, s, p);
+    return e != cudaSuccess ? e : launch_pdl(k, dim3(*grid), dim3(p.tpr * p.groups + (BACK || SELF ? 0 : 32)), smem, s, p);
   };
   if constexpr (BACK)
     return go(block_norm_backward_kernel<R, A, VEC, EPT, MAXT>);
   else
-    return go(block_norm_kernel<R, A, VEC, EPT, MAXT>);
+    return go(block_norm_kernel<R, A, VEC, EPT, MAXT, SELF>);
 }
 
 // Elements a thread and threads a CTA: eight elements as long as the threads
@@ -872,6 +874,7 @@ cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* 
     if (n <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
     return run<R, A, VEC, 40, 512, true>(p, rows_r, rows_a, sm, grid, s);
   }
+  if (n <= 8 * 32) return run<R, A, VEC, 8, 512, false, true>(p, rows_r, rows_a, sm, grid, s);
   if (n <= 8 * 992) return run<R, A, VEC, 8, 992, false>(p, rows_r, rows_a, sm, grid, s);
   return run<R, A, VEC, 24, 736, false>(p, rows_r, rows_a, sm, grid, s);
 }
