@@ -16,8 +16,9 @@
 //   few tokens   lora_swap_kernel: W's rows are the MMA's M, the weight stream
 //                is the bound
 //   many tokens  lora_pair_kernel: CTA pairs, the tensor cores are the bound
-// v is rounded to bf16, being an MMA operand: 2^-9 of the adapter's term, below
-// the rounding of y unless that term outgrows y.
+// v is kept in fp32; as an MMA operand it is two bf16, v = hi + lo, which take
+// the adapter's k-steps twice (one bf16 of v put 2^-9 of the adapter's term into
+// y, beside its own 2^-9, and y lost up to a third of its accuracy).
 // The zeros only hide what is finite.  So that no token's result depends on
 // another's adapter, a factor that is Inf or NaN counts as 0 and is reported:
 // the pair kernel's warps look at the factors as they place them; the swapped
@@ -46,7 +47,7 @@ struct LoraParams {   // what the kernels share
   const int32_t* ranks;
   const float* scales;
   const int32_t* adapter;
-  __nv_bfloat16* v;                     // [T, r_max]
+  float* v;                             // [T, r_max]
   __nv_bfloat16* y;
   long long ldy;
   int T, K, N, outs, n, r_max, swiglu;
@@ -174,15 +175,38 @@ __device__ __forceinline__ uint4 clean8(uint4 q, int cols, bool& bad) {
   return q;
 }
 
+// Eight fp32 as two bf16 each: v = hi + lo to 2^-17 of v.
+__device__ __forceinline__ void split8(const float4& a, const float4& b, uint4& hi, uint4& lo) {
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t* h = &hi.x;
+  uint32_t* l = &lo.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    const float d0 = v[2 * i] - bf16lo(h[i]), d1 = v[2 * i + 1] - bf16hi(h[i]);
+    // Inf and NaN are in hi
+    l[i] = pack_bf16x2(fabsf(d0) < INFINITY ? d0 : 0.f, fabsf(d1) < INFINITY ? d1 : 0.f);
+  }
+}
+
 // A worker's part of one k-block of four groups [4 j, 4 j + 4) of adapter
-// columns: the 16-byte chunk c of every sixteenth factor row and token row.
-// The loads are issued a block ahead of the stores, the factors even before
-// the kernel that computes v has finished.
+// columns: the 16-byte chunk c of every sixteenth factor row and token row, in
+// the 128-byte swizzle that the MMA descriptors expect.
 template <int VROWS>
 struct Block {
-  uint4 b[8], v[VROWS / 16];
+  static constexpr int kV = VROWS / 16;
+  uint4 b[8];
   int a, col, cols;
 
+  // the chunk's place among the groups
+  __device__ __forceinline__ void place(int e, const uint32_t* s_grp, int j, int groups) {
+    const int gi = 4 * j + ((e & 7) >> 1), half = (e & 1) * 8;
+    const bool live = gi < groups;
+    const uint32_t g = live ? s_grp[gi] : 0u;
+    a = live ? grp_adapter(g) : -2;
+    col = grp_first(g) + half;
+    cols = live ? grp_cols(g) - half : 0;
+  }
   // factor row i is row map(i) of W (none if negative)
   template <typename Map>
   __device__ __forceinline__ void load_b(const LoraParams& p, int e, const uint32_t* s_grp, int j,
@@ -198,43 +222,51 @@ struct Block {
             p.b + (static_cast<long long>(a) * p.N + wr) * p.r_max + col));
     }
   }
-  __device__ __forceinline__ void load_v(const LoraParams& p, int e, const int* s_ad, int t0) {
-#pragma unroll
-    for (int i = 0; i < VROWS / 16; ++i) {
-      const int r = (e >> 3) + 16 * i;
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (cols > 0 && s_ad[r] == a)
-        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.v + static_cast<long long>(t0 + r) * p.r_max + col));
-    }
-  }
-  // the chunk's place among the groups only, without the factors
-  __device__ __forceinline__ void place(int e, const uint32_t* s_grp, int j, int groups) {
-    const int gi = 4 * j + ((e & 7) >> 1), half = (e & 1) * 8;
-    const bool live = gi < groups;
-    const uint32_t g = live ? s_grp[gi] : 0u;
-    a = live ? grp_adapter(g) : -2;
-    col = grp_first(g) + half;
-    cols = live ? grp_cols(g) - half : 0;
-  }
-  __device__ __forceinline__ void store_v(int e, uint8_t* s_v) {
+  __device__ __forceinline__ static uint32_t chunk(int e) {
     const int c = e & 7, r0 = e >> 3;
-    const uint32_t at = static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
-#pragma unroll
-    for (int i = 0; i < VROWS / 16; ++i) *reinterpret_cast<uint4*>(s_v + at + i * 2048) = v[i];
-    fence_proxy_async_smem();
+    return static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
   }
-  // in the 128-byte swizzle that the MMA descriptors expect
-  __device__ __forceinline__ void store(const LoraParams& p, int e, uint8_t* s_b, uint8_t* s_v) {
-    const int c = e & 7, r0 = e >> 3;
-    const uint32_t at = static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+  __device__ __forceinline__ void store_b(const LoraParams& p, int e, uint8_t* s_b) {
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<uint4*>(s_b + at + i * 2048) = clean8(b[i], cols, bad);
-#pragma unroll
-    for (int i = 0; i < VROWS / 16; ++i) *reinterpret_cast<uint4*>(s_v + at + i * 2048) = v[i];
+      *reinterpret_cast<uint4*>(s_b + chunk(e) + i * 2048) = clean8(b[i], cols, bad);
     if (bad) report(p.status, MOE_ERR_NONFINITE);
-    fence_proxy_async_smem();
+  }
+  // token rows [16 i0, 16 i0 + 16 N) of the tile that begins at token t0
+  template <int N>
+  __device__ __forceinline__ void load_v(const LoraParams& p, int e, const int* s_ad, int t0, int i0,
+                                         uint4 (&hi)[N], uint4 (&lo)[N]) {
+    float4 x[N], y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = (e >> 3) + 16 * (i0 + i);
+      x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (cols > 0 && s_ad[r] == a) {
+        const float4* v =
+            reinterpret_cast<const float4*>(p.v + static_cast<long long>(t0 + r) * p.r_max + col);
+        x[i] = __ldcg(v);
+        y[i] = __ldcg(v + 1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) split8(x[i], y[i], hi[i], lo[i]);
+  }
+  template <int N>
+  __device__ __forceinline__ static void store_v(int e, int i0, uint8_t* s_v, const uint4 (&w)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(s_v + chunk(e) + (i0 + i) * 2048) = w[i];
+  }
+  // the whole v tile, hi and behind it lo
+  __device__ __forceinline__ void put_v(const LoraParams& p, int e, const int* s_ad, int t0, uint8_t* s_v) {
+    constexpr int N = kV < 8 ? kV : 8;
+#pragma unroll
+    for (int i0 = 0; i0 < kV; i0 += N) {
+      uint4 hi[N], lo[N];
+      load_v<N>(p, e, s_ad, t0, i0, hi, lo);
+      store_v<N>(e, i0, s_v, hi);
+      store_v<N>(e, i0, s_v + VROWS * 128, lo);
+    }
   }
 };
 
@@ -301,7 +333,7 @@ __global__ void __launch_bounds__(kDotThreads, 2)
 #pragma unroll
     for (int w = 0; w < kDotThreads / 32; ++w) sum += s_part[w][threadIdx.x];
     const int i = i0 + threadIdx.x;
-    p.v[static_cast<long long>(t) * p.r_max + i] = __float2bfloat16_rn(i < rank ? sum * scale : 0.f);
+    p.v[static_cast<long long>(t) * p.r_max + i] = i < rank ? sum * scale : 0.f;
   }
 }
 
@@ -326,9 +358,10 @@ template <int NT, bool SHRINK>
 struct SwapCfg {
   static constexpr uint32_t kStage = kTile + NT * 128;
   static constexpr int kStages = NT >= 256 ? (SHRINK ? 4 : 3) : (NT >= 128 ? 5 : 6);
-  static constexpr int kVSlots = SHRINK ? 0 : (NT >= 128 ? 2 : 4);  // v tiles of adapter k-blocks
+  static constexpr int kVSlots = SHRINK ? 0 : (NT >= 128 ? 1 : (NT >= 64 ? 2 : 4));
+  static constexpr uint32_t kVBytes = 2 * NT * 128;               // v tile of an adapter k-block: hi, lo
   static constexpr uint32_t kOffV = kStages * kStage;
-  static constexpr uint32_t kOffBar = kOffV + kVSlots * NT * 128;
+  static constexpr uint32_t kOffBar = kOffV + kVSlots * kVBytes;
   static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 3 + 2 * 4) * 8;
   static constexpr uint32_t kOffAd = kOffMisc + 64;
   static constexpr uint32_t kOffGrp = kOffAd + NT * 4;
@@ -383,8 +416,7 @@ __device__ __forceinline__ void finish(const LoraParams& p, const float* part, c
     for (int n = 0; n < count; ++n) {
       const float v = sum(n, row);
       if (ad[n] == a)
-        p.v[static_cast<long long>(first + n) * p.r_max + col] =
-            __float2bfloat16_rn(i < grp_cols(gr) ? v * sc : 0.f);
+        p.v[static_cast<long long>(first + n) * p.r_max + col] = i < grp_cols(gr) ? v * sc : 0.f;
     }
   } else if (p.swiglu) {
     const int o = blk * 64 + (row & 63);
@@ -442,17 +474,21 @@ __device__ __forceinline__ void look_over(const LoraParams& p, uint8_t* smem, co
   const int blocks = (groups + 3) / 4;
   for (int j = rank, i = 0; j < blocks; j += S, ++i) {
     f.load_b(p, e, s_grp, j, groups, [&](int r) { return tile_row(p, blk, r); });
-    f.load_v(p, e, s_ad, t0);
-    f.store(p, e, smem, smem + C::kOffV);
+    f.store_b(p, e, smem);
+    f.put_v(p, e, s_ad, t0, smem + C::kOffV);
+    fence_proxy_async_smem();
     tc_fence_before();
     workers_sync();
     if (e == 0) {
       tc_fence_after();
-      const uint64_t ad = sdesc_sw128(smem_u32(smem)), bd = sdesc_sw128(smem_u32(smem + C::kOffV));
-#pragma unroll
-      for (int k = 0; k < kBK / 16; ++k)
-        umma_bf16(tmem + C::kCols, ad + 2u * k, bd + 2u * k, idesc_bf16_f32(kRows, NT),
+      const uint64_t ad = sdesc_sw128(smem_u32(smem)), hi = sdesc_sw128(smem_u32(smem + C::kOffV)),
+                     lo = sdesc_sw128(smem_u32(smem + C::kOffV + NT * 128));
+      const int n = min(4, groups - 4 * j);
+      for (int k = 0; k < n; ++k) {
+        umma_bf16(tmem + C::kCols, ad + 2u * k, hi + 2u * k, idesc_bf16_f32(kRows, NT),
                   (i | k) != 0 ? 1u : 0u);
+        umma_bf16(tmem + C::kCols, ad + 2u * k, lo + 2u * k, idesc_bf16_f32(kRows, NT), 1u);
+      }
       umma_commit(redo);
     }
     int ok = 1;
@@ -633,11 +669,14 @@ __global__ void __launch_bounds__(192, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_u32(smem + stage * C::kStage);
-            const uint64_t bd = sdesc_sw128(smem_u32(smem + C::kOffV + sl * NT * 128));
+            const uint64_t hi = sdesc_sw128(smem_u32(smem + C::kOffV + sl * C::kVBytes));
+            const uint64_t lo = sdesc_sw128(smem_u32(smem + C::kOffV + sl * C::kVBytes + NT * 128));
             const int n = min(4, total - 4 * j);
-            for (int k = 0; k < n; ++k)     // a group is one k-step
-              umma_bf16(tmem + C::kCols, sdesc_sw32(sa + k * kRows * kGroup * 2), bd + 2u * k, idesc,
-                        (i | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < n; ++k) {   // a group is one k-step for hi and one for lo
+              const uint64_t ad = sdesc_sw32(sa + k * kRows * kGroup * 2);
+              umma_bf16(tmem + C::kCols, ad, hi + 2u * k, idesc, (i | k) != 0 ? 1u : 0u);
+              umma_bf16(tmem + C::kCols, ad, lo + 2u * k, idesc, 1u);
+            }
             umma_commit(&empty[stage]);
             umma_commit(&vempty[sl]);
             if (++stage == C::kStages) {
@@ -662,8 +701,6 @@ __global__ void __launch_bounds__(192, 1)
         const int blocks = (groups + 3) / 4;
         asm volatile("griddepcontrol.wait;" ::: "memory");
         Block<NT> f;
-        f.place(e, s_grp, rank, groups);
-        f.load_v(p, e, s_ad, t0);
         for (int j = rank, i = 0; j < blocks; j += S, ++i) {
           const int sl = i % C::kVSlots;
           int ok = 1;
@@ -673,11 +710,11 @@ __global__ void __launch_bounds__(192, 1)
             if (lane == 0) fail(s_abort, p.status);
             break;
           }
-          f.store_v(e, smem + C::kOffV + sl * NT * 128);
+          f.place(e, s_grp, j, groups);
+          f.put_v(p, e, s_ad, t0, smem + C::kOffV + sl * C::kVBytes);
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&vfull[sl]);
-          f.place(e, s_grp, j + S, groups);
-          f.load_v(p, e, s_ad, t0);
         }
       }
     }
@@ -1076,8 +1113,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       f.load_b(p, e, s_grp, 0, groups, map);
       if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
       waited = true;
-      f.load_v(p, e, s_ad + row0, mt * 256 + row0);
-      for (int j = 0; run && j <= blocks; ++j) {
+      // every block goes into the slot twice: with v's hi and, the factors left
+      // in place, with its lo; the post after the last ends the tile
+      uint4 hi[kRows / 16], lo[kRows / 16];
+      for (int i = 0; run && i <= 2 * blocks; ++i) {
+        const int j = i >> 1;
+        const bool end = j == blocks, second = (i & 1) != 0;
+        if (!end && !second) f.load_v(p, e, s_ad + row0, mt * 256 + row0, 0, hi, lo);
         int ok = 1;
         if (lane == 0) ok = mbar_wait(lempty, lp ^ 1u, s_abort) ? 1 : 0;
         run = __shfl_sync(0xffffffffu, ok, 0) != 0;
@@ -1085,15 +1127,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (lane == 0) fail(s_abort, p.status);
           break;
         }
-        if (j < blocks) f.store(p, e, smem + C::kOffSlot + kTile, smem + C::kOffSlot);
-        if (e == 0) *s_more = j < blocks ? 1 : 0;
+        if (!end) {
+          if (!second) f.store_b(p, e, smem + C::kOffSlot + kTile);
+          f.store_v(e, 0, smem + C::kOffSlot, second ? lo : hi);
+          fence_proxy_async_smem();
+        }
+        if (e == 0) *s_more = end ? 0 : 1;
         __syncwarp();
         if (lane == 0) arrive_release_cluster(lfull_l);
         lp ^= 1u;
-        if (j + 1 < blocks) {
-          f.load_b(p, e, s_grp, j + 1, groups, map);
-          f.load_v(p, e, s_ad + row0, mt * 256 + row0);
-        }
+        if (!end && second && j + 1 < blocks) f.load_b(p, e, s_grp, j + 1, groups, map);
       }
     }
     // the last commit on this CTA's lempty has arrived
@@ -1262,7 +1305,7 @@ cudaError_t run_pair(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t lora_workspace_bytes(int T, int r_max) { return static_cast<size_t>(T) * r_max * 2; }
+size_t lora_workspace_bytes(int T, int r_max) { return static_cast<size_t>(T) * r_max * 4; }
 
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   LoraParams p{};
@@ -1270,7 +1313,7 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   p.ranks = g.ranks;
   p.scales = g.scales;
   p.adapter = g.adapter;
-  p.v = static_cast<__nv_bfloat16*>(g.ws);
+  p.v = static_cast<float*>(g.ws);
   p.y = static_cast<__nv_bfloat16*>(g.y);
   p.ldy = g.ldy;
   p.T = g.T;

@@ -501,8 +501,8 @@ moe_status moe_block_norm_backward(const moe_norm_desc* desc, const void* residu
  * A projection that all requests share, with a low-rank adapter per request:
  *     y_t = x_t W^T + scale_a (x_t A_a^T) B_a^T,      a = adapter_idx[t], or none (-1)
  * and with `swiglu` SiLU(y[0, N/2)) * y[N/2, N) (the gate|up projection of a
- * shared expert).  Sums in fp32; the low-rank intermediate is rounded to bf16
- * as a tensor-core operand, y once at the end.  An element of B in use that is
+ * shared expert).  Sums and the low-rank intermediate in fp32 (the latter to
+ * 2^-17 as a pair of tensor-core operands), y rounded once.  An element of B in use that is
  * Inf or NaN counts as 0 and is reported (MOE_ERR_NONFINITE); whatever is in one
  * adapter or one token's x, the other tokens' results are what they are without.
  */
