@@ -795,15 +795,18 @@ __global__ void __launch_bounds__(192, 1)
 // the tile's K columns are done.
 constexpr int kPairN = 256;
 constexpr int kPairStages = 5;
+constexpr int kPairSlots = 3;                                     // groups of adapter columns under way
 constexpr int kPairThreads = 192 + kWorkers;
 constexpr uint32_t kPairTmem = 2 * kPairN;
 
 struct PairCfg {
   static constexpr uint32_t kStage = 2 * kTile;                   // 128 token rows, 128 W rows
+  static constexpr uint32_t kGroupTile = kRows * kGroup * 2;
+  static constexpr uint32_t kSlot = 3 * kGroupTile;               // v's hi and lo, the factors
   static constexpr uint32_t kOffSlot = kPairStages * kStage;
-  static constexpr uint32_t kOffOut = kOffSlot + kStage;
+  static constexpr uint32_t kOffOut = kOffSlot + kPairSlots * kSlot;
   static constexpr uint32_t kOffBar = kOffOut + 4 * kStageRowsBytes;
-  static constexpr uint32_t kOffMisc = kOffBar + (2 * kPairStages + 7) * 8;
+  static constexpr uint32_t kOffMisc = kOffBar + (2 * kPairStages + 2 * kPairSlots + 5) * 8;
   static constexpr uint32_t kOffAd = kOffMisc + 64;
   static constexpr uint32_t kOffGrp = kOffAd + kMaxTileTokens * 4;
   static constexpr uint32_t kUsed = kOffGrp + kMaxTileTokens * 8 * 4;
@@ -834,6 +837,14 @@ __device__ __forceinline__ void arrive_release_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// A worker's factor row and token row of one group of adapter columns.
+struct PairRow {
+  uint4 b0, b1;
+  float4 v[4];
+  int cols, first;
+  bool own;
+};
+
 __global__ void __launch_bounds__(kPairThreads, 1)
     lora_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmY, const LoraParams p) {
@@ -844,14 +855,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);   // leader
   uint64_t* empty = full + kPairStages;
   uint64_t* lfull = empty + kPairStages;   // leader: eight warps of the pair
-  uint64_t* lempty = lfull + 1;
-  uint64_t* tfull = lfull + 2;
+  uint64_t* lempty = lfull + kPairSlots;
+  uint64_t* tfull = lempty + kPairSlots;
   uint64_t* tempty = tfull + 2;            // leader
   uint64_t* done = tempty + 2;             // leader
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* s_more = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-  int* s_sum = reinterpret_cast<int*>(smem + C::kOffMisc + 16);
+  int* s_sum = reinterpret_cast<int*>(smem + C::kOffMisc + 32);
   int* s_ad = reinterpret_cast<int*>(smem + C::kOffAd);
   uint32_t* s_grp = reinterpret_cast<uint32_t*>(smem + C::kOffGrp);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -862,8 +873,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(lfull, 8);
-    mbar_init(lempty, 1);
+    for (int s = 0; s < kPairSlots; ++s) {
+      mbar_init(&lfull[s], 8);
+      mbar_init(&lempty[s], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 8);
@@ -942,11 +955,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (leader && lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(256, kPairN);
-      int stage = 0, acc = 0;
+      int stage = 0, acc = 0, slot = 0;
       uint32_t phase = 0, aphase = 0, lp = 0;
-      bool ok = true;
-      const uint64_t la = sdesc_sw128(smem_u32(smem + C::kOffSlot));
-      const uint64_t lb = sdesc_sw128(smem_u32(smem + C::kOffSlot + kTile));
+      bool ok = true, more = false;
+      // one group of the tile's adapter columns; the slot that ends them holds none
+      auto take = [&](uint32_t d) {
+        if (!mbar_wait_cluster(&lfull[slot], lp, s_abort)) {
+          ok = false;
+          return;
+        }
+        more = s_more[slot] != 0;
+        if (more) {
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + C::kOffSlot + slot * C::kSlot);
+          const uint64_t b = sdesc_sw32(at + 2 * C::kGroupTile);
+          umma_bf16_pair(d, sdesc_sw32(at), b, idesc, 1u);
+          umma_bf16_pair(d, sdesc_sw32(at + C::kGroupTile), b, idesc, 1u);
+        }
+        umma_commit_pair(&lempty[slot], 0x3);
+        if (++slot == kPairSlots) {
+          slot = 0;
+          lp ^= 1u;
+        }
+      };
       for (int w = cid; ok && w < total; w += ncl) {
         if (!mbar_wait(&tempty[acc], aphase ^ 1u, s_abort)) {
           ok = false;
@@ -954,7 +985,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(acc * kPairN);
-        for (int kb = 0; kb < KB; ++kb) {
+        more = true;
+        for (int kb = 0; ok && kb < KB; ++kb) {
           if (!mbar_wait(&full[stage], phase, s_abort)) {
             ok = false;
             break;
@@ -970,22 +1002,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             stage = 0;
             phase ^= 1u;
           }
+          if (more && 2 * kb >= KB) take(d);
         }
-        // the tile's adapter blocks; the slot that ends them holds none
-        for (bool more = true; ok && more;) {
-          if (!mbar_wait_cluster(lfull, lp, s_abort)) {
-            ok = false;
-            break;
-          }
-          more = *s_more != 0;
-          if (more) {
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) umma_bf16_pair(d, la + 2u * k, lb + 2u * k, idesc, 1u);
-          }
-          umma_commit_pair(lempty, 0x3);
-          lp ^= 1u;
-        }
+        while (ok && more) take(d);
         if (!ok) break;
         umma_commit_pair(&tfull[acc], 0x3);
         if (++acc == 2) {
@@ -1092,9 +1111,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t lfull_l = mapa_shared(smem_u32(lfull), 0);
     bool waited = p.wait_first != 0;
     uint32_t lp = 0;
-    int built = -1, groups = 0;
-    Block<kRows> f;
+    int built = -1, groups = 0, slot = 0;
     bool run = true;   // after a wait that gave up: keep the workers' barriers, touch nothing
+    // where row e's two chunks of 16 bytes lie under the 32-byte swizzle
+    const uint32_t c0 = static_cast<uint32_t>(e) * 32u + ((static_cast<uint32_t>(e) & 4u) << 2);
     for (int w = cid; w < total; w += ncl) {
       const int mt = w / n_tiles, nt = w - mt * n_tiles;
       if (mt != built) {
@@ -1103,44 +1123,87 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         built = mt;
       }
       const int half = p.swiglu ? 64 : kRows;
-      const int o0 = nt * per_n + static_cast<int>(rank) * half;
-      auto map = [&](int i) {
-        const int o = o0 + (i < half ? i : i - half);
-        return o < p.outs ? (i < half ? o : p.outs + o) : -1;
+      const int o = nt * per_n + static_cast<int>(rank) * half + (e < half ? e : e - half);
+      const int wr = o < p.outs ? (e < half ? o : p.outs + o) : -1;
+      const int t = mt * 256 + static_cast<int>(rank) * 128 + e;
+      const int mine = s_ad[static_cast<int>(rank) * 128 + e];   // -1 past the last token
+      const __nv_bfloat16* brow = p.b + static_cast<long long>(wr) * p.r_max;
+      const float* vrow = p.v + static_cast<long long>(t) * p.r_max;
+      // this thread's factor row and token row of a group, two groups ahead
+      PairRow ahead[2];
+      auto load_b = [&](PairRow& f, int j) {
+        const uint32_t g = j < groups ? s_grp[j] : 0u;
+        f.cols = j < groups ? grp_cols(g) : 0;
+        f.first = grp_first(g);
+        f.own = j < groups && grp_adapter(g) == mine;
+        f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
+        if (f.cols > 0 && wr >= 0) {
+          const uint4* b = reinterpret_cast<const uint4*>(
+              brow + static_cast<long long>(grp_adapter(g)) * p.N * p.r_max + f.first);
+          f.b0 = __ldg(b);
+          if (f.cols > 8) f.b1 = __ldg(b + 1);
+        }
       };
-      const int blocks = (groups + 3) / 4;
-      const int row0 = static_cast<int>(rank) * 128;
-      f.load_b(p, e, s_grp, 0, groups, map);
+      auto load_v = [&](PairRow& f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f.v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (f.own && 8 * (i / 2) < f.cols)
+            f.v[i] = __ldcg(reinterpret_cast<const float4*>(vrow + f.first) + i);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_b(ahead[i], i);
       if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
       waited = true;
-      // every block goes into the slot twice: with v's hi and, the factors left
-      // in place, with its lo; the post after the last ends the tile
-      uint4 hi[kRows / 16], lo[kRows / 16];
-      for (int i = 0; run && i <= 2 * blocks; ++i) {
-        const int j = i >> 1;
-        const bool end = j == blocks, second = (i & 1) != 0;
-        if (!end && !second) f.load_v(p, e, s_ad + row0, mt * 256 + row0, 0, hi, lo);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_v(ahead[i]);
+      // the post after the last group ends the tile
+#pragma unroll 2
+      for (int j = 0; run && j <= groups; ++j) {
+        PairRow& f = ahead[j & 1];
         int ok = 1;
-        if (lane == 0) ok = mbar_wait(lempty, lp ^ 1u, s_abort) ? 1 : 0;
+        if (lane == 0) ok = mbar_wait(&lempty[slot], lp ^ 1u, s_abort) ? 1 : 0;
         run = __shfl_sync(0xffffffffu, ok, 0) != 0;
         if (!run) {
           if (lane == 0) fail(s_abort, p.status);
           break;
         }
-        if (!end) {
-          if (!second) f.store_b(p, e, smem + C::kOffSlot + kTile);
-          f.store_v(e, 0, smem + C::kOffSlot, second ? lo : hi);
+        if (j < groups) {
+          uint8_t* at = smem + C::kOffSlot + slot * C::kSlot + c0;
+          uint8_t* at1 = smem + C::kOffSlot + slot * C::kSlot + (c0 ^ 16u);
+          bool bad = false;
+          *reinterpret_cast<uint4*>(at + 2 * C::kGroupTile) = clean8(f.b0, f.cols, bad);
+          *reinterpret_cast<uint4*>(at1 + 2 * C::kGroupTile) = clean8(f.b1, f.cols - 8, bad);
+          if (bad) report(p.status, MOE_ERR_NONFINITE);
+          uint4 hi, lo;
+          split8(f.v[0], f.v[1], hi, lo);
+          *reinterpret_cast<uint4*>(at) = hi;
+          *reinterpret_cast<uint4*>(at + C::kGroupTile) = lo;
+          split8(f.v[2], f.v[3], hi, lo);
+          *reinterpret_cast<uint4*>(at1) = hi;
+          *reinterpret_cast<uint4*>(at1 + C::kGroupTile) = lo;
           fence_proxy_async_smem();
         }
-        if (e == 0) *s_more = end ? 0 : 1;
+        if (e == 0) s_more[slot] = j < groups ? 1 : 0;
         __syncwarp();
-        if (lane == 0) arrive_release_cluster(lfull_l);
-        lp ^= 1u;
-        if (!end && second && j + 1 < blocks) f.load_b(p, e, s_grp, j + 1, groups, map);
+        if (lane == 0) arrive_release_cluster(lfull_l + 8u * static_cast<uint32_t>(slot));
+        if (++slot == kPairSlots) {
+          slot = 0;
+          lp ^= 1u;
+        }
+        load_b(f, j + 2);
+        load_v(f);
       }
     }
-    // the last commit on this CTA's lempty has arrived
-    if (run && lane == 0 && !mbar_wait(lempty, lp ^ 1u, nullptr)) fail(s_abort, p.status);
+    // the last commits on this CTA's lempty have arrived
+    for (int i = 0; run && i < kPairSlots; ++i) {
+      if (lane == 0 && !mbar_wait(&lempty[slot], lp ^ 1u, nullptr)) fail(s_abort, p.status);
+      if (++slot == kPairSlots) {
+        slot = 0;
+        lp ^= 1u;
+      }
+    }
     __syncwarp();
   }
 
