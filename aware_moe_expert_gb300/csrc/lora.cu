@@ -358,11 +358,15 @@ template <int NT, bool SHRINK>
 struct SwapCfg {
   static constexpr uint32_t kStage = kTile + NT * 128;
   static constexpr int kStages = NT >= 256 ? (SHRINK ? 4 : 3) : (NT >= 128 ? 5 : 6);
-  static constexpr int kVSlots = SHRINK ? 0 : (NT >= 128 ? 1 : (NT >= 64 ? 2 : 4));
-  static constexpr uint32_t kVBytes = 2 * NT * 128;               // v tile of an adapter k-block: hi, lo
+  static constexpr int kG = NT <= 64 ? 4 : 1;                     // groups of adapter columns a v slot holds
+  static constexpr int kVSlots = SHRINK ? 0 : (NT == 64 ? 2 : 4);
+  static constexpr uint32_t kVTile = NT * kGroup * 2;
+  static constexpr uint32_t kVBytes = 2 * kG * kVTile;            // v of each group: hi, lo
+  static constexpr int kAhead = NT == 128 ? 4 : (NT == 256 ? 2 : 1);  // slots' worth in a worker's registers
   static constexpr uint32_t kOffV = kStages * kStage;
   static constexpr uint32_t kOffBar = kOffV + kVSlots * kVBytes;
-  static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 3 + 2 * 4) * 8;
+  static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 3 + 2 * kVSlots) * 8;
+  static_assert(SHRINK || kVSlots * kVBytes >= 2 * NT * 128, "look_over has a whole block there");
   static constexpr uint32_t kOffAd = kOffMisc + 64;
   static constexpr uint32_t kOffGrp = kOffAd + NT * 4;
   static constexpr uint32_t kUsed = kOffGrp + NT * 8 * 4;
@@ -371,6 +375,49 @@ struct SwapCfg {
   static_assert(NT * kRows * 4 <= kOffV, "the partial sums reuse the ring");
   static constexpr uint32_t kCols = NT < 32 ? 32 : NT;            // loads read 32 columns
   static constexpr uint32_t kTmem = SHRINK ? kCols : 2 * kCols;   // projection: the adapters' sums, too
+};
+
+// A worker's part of v of G groups for NT tokens: a chunk of eight columns of one
+// of the groups, of every (64 / G)th token.
+template <int NT, int G>
+struct VRows {
+  static constexpr int kStep = 64 / G, kN = NT < kStep ? 1 : NT / kStep;
+  float4 v[kN][2];
+
+  __device__ __forceinline__ void load(const LoraParams& p, const int* s_ad, const uint32_t* s_grp,
+                                       int gi, int groups, int t0, int e) {
+    const int half = e & 1, r0 = e / (2 * G);
+    gi += (e >> 1) % G;
+    const uint32_t g = gi < groups ? s_grp[gi] : 0u;
+    const bool live = gi < groups && grp_cols(g) > 8 * half;
+    const int a = grp_adapter(g), col = grp_first(g) + 8 * half;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int r = r0 + kStep * i;
+      v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (live && r < NT && s_ad[r] == a) {
+        const float4* from =
+            reinterpret_cast<const float4*>(p.v + static_cast<long long>(t0 + r) * p.r_max + col);
+        v[i][0] = __ldcg(from);
+        v[i][1] = __ldcg(from + 1);
+      }
+    }
+  }
+  // each group's tile of 16 columns in the 32-byte swizzle, hi and behind it lo
+  __device__ __forceinline__ void store(uint8_t* to, int e) const {
+    const int half = e & 1, r0 = e / (2 * G);
+    to += (e >> 1) % G * (NT * kGroup * 4);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int r = r0 + kStep * i;
+      if (r >= NT) break;
+      uint4 hi, lo;
+      split8(v[i][0], v[i][1], hi, lo);
+      uint8_t* at = to + r * 32 + ((half ^ ((r >> 2) & 1)) << 4);
+      *reinterpret_cast<uint4*>(at) = hi;
+      *reinterpret_cast<uint4*>(at + NT * kGroup * 2) = lo;
+    }
+  }
 };
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
@@ -412,12 +459,10 @@ __device__ __forceinline__ void finish(const LoraParams& p, const float* part, c
     const int i = row % kGroup, a = grp_adapter(gr), col = grp_first(gr) + i;
     const float sc = __ldg(p.scales + a);
     if (col >= p.r_max) return;
-#pragma unroll 4
-    for (int n = 0; n < count; ++n) {
-      const float v = sum(n, row);
+    for (int n = 0; n < count; ++n)
       if (ad[n] == a)
-        p.v[static_cast<long long>(first + n) * p.r_max + col] = i < grp_cols(gr) ? v * sc : 0.f;
-    }
+        p.v[static_cast<long long>(first + n) * p.r_max + col] =
+            i < grp_cols(gr) ? sum(n, row) * sc : 0.f;
   } else if (p.swiglu) {
     const int o = blk * 64 + (row & 63);
     if (o >= p.outs) return;
@@ -512,8 +557,8 @@ __global__ void __launch_bounds__(192, 1)
   uint64_t* tfull = empty + C::kStages;    // the accumulators are complete
   uint64_t* tbl = tfull + 1;               // the groups are listed
   uint64_t* vfull = tfull + 2;             // a v tile is in its slot
-  uint64_t* vempty = vfull + 4;
-  uint64_t* redo = vempty + 4;
+  uint64_t* vempty = vfull + C::kVSlots;
+  uint64_t* redo = vempty + C::kVSlots;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   int* s_total = reinterpret_cast<int*>(smem + C::kOffMisc + 12);
@@ -534,7 +579,7 @@ __global__ void __launch_bounds__(192, 1)
     mbar_init(tfull, 1);
     mbar_init(tbl, 4);
     mbar_init(redo, 1);
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < C::kVSlots; ++s) {
       mbar_init(&vfull[s], 4);
       mbar_init(&vempty[s], 1);
     }
@@ -660,25 +705,35 @@ __global__ void __launch_bounds__(192, 1)
         if (!SHRINK && ok && p.n > 0) {
           ok = mbar_wait(tbl, 0u, s_abort);
           const int total = ok ? *s_total : 0, blocks = (total + 3) / 4;
-          for (int j = rank, i = 0; ok && j < blocks; j += S, ++i) {
-            const int sl = i % C::kVSlots;
-            if (!mbar_wait(&full[stage], phase, s_abort) ||
-                !mbar_wait(&vfull[sl], (i / C::kVSlots) & 1, s_abort)) {
+          int sl = 0;
+          uint32_t vphase = 0;
+          for (int j = rank; ok && j < blocks; j += S) {
+            if (!mbar_wait(&full[stage], phase, s_abort)) {
               ok = false;
               break;
             }
-            tc_fence_after();
             const uint32_t sa = smem_u32(smem + stage * C::kStage);
-            const uint64_t hi = sdesc_sw128(smem_u32(smem + C::kOffV + sl * C::kVBytes));
-            const uint64_t lo = sdesc_sw128(smem_u32(smem + C::kOffV + sl * C::kVBytes + NT * 128));
             const int n = min(4, total - 4 * j);
-            for (int k = 0; k < n; ++k) {   // a group is one k-step for hi and one for lo
-              const uint64_t ad = sdesc_sw32(sa + k * kRows * kGroup * 2);
-              umma_bf16(tmem + C::kCols, ad, hi + 2u * k, idesc, (i | k) != 0 ? 1u : 0u);
-              umma_bf16(tmem + C::kCols, ad, lo + 2u * k, idesc, 1u);
+            for (int k = 0; k < n; k += C::kG) {
+              if (!mbar_wait(&vfull[sl], vphase, s_abort)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              uint32_t sv = smem_u32(smem + C::kOffV + sl * C::kVBytes);
+              for (int g = k; g < k + C::kG && g < n; ++g, sv += 2 * C::kVTile) {
+                // a group is one k-step for hi and one for lo
+                const uint64_t ad = sdesc_sw32(sa + g * kRows * kGroup * 2);
+                umma_bf16(tmem + C::kCols, ad, sdesc_sw32(sv), idesc, j != rank || g != 0 ? 1u : 0u);
+                umma_bf16(tmem + C::kCols, ad, sdesc_sw32(sv + C::kVTile), idesc, 1u);
+              }
+              umma_commit(&vempty[sl]);
+              if (++sl == C::kVSlots) {
+                sl = 0;
+                vphase ^= 1u;
+              }
             }
             umma_commit(&empty[stage]);
-            umma_commit(&vempty[sl]);
             if (++stage == C::kStages) {
               stage = 0;
               phase ^= 1u;
@@ -698,23 +753,37 @@ __global__ void __launch_bounds__(192, 1)
         if (e == 0) *s_total = groups;
         __syncwarp();
         if (lane == 0) mbar_arrive(tbl);
-        const int blocks = (groups + 3) / 4;
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        Block<NT> f;
-        for (int j = rank, i = 0; j < blocks; j += S, ++i) {
-          const int sl = i % C::kVSlots;
-          int ok = 1;
-          if (lane == 0) ok = mbar_wait(&vempty[sl], ((i / C::kVSlots) & 1) ^ 1, s_abort) ? 1 : 0;
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
-            if (lane == 0) fail(s_abort, p.status);
-            break;
+        // a thread's values of the next slots are on their way while it waits for one
+        constexpr int kAhead = C::kAhead, kG = C::kG;
+        VRows<NT, kG> ahead[kAhead];
+        auto group_of = [&](int i) { return 4 * (rank + S * (i * kG >> 2)) + (i * kG & 3); };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ahead[i].load(p, s_ad, s_grp, group_of(i), groups, t0, e);
+        int sl = 0;
+        uint32_t vphase = 0;
+        bool run = true;
+        for (int i0 = 0; run && group_of(i0) < groups; i0 += kAhead) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            if (!run || group_of(i0 + i) >= groups) break;
+            int ok = 1;
+            if (lane == 0) ok = mbar_wait(&vempty[sl], vphase ^ 1u, s_abort) ? 1 : 0;
+            run = __shfl_sync(0xffffffffu, ok, 0) != 0;
+            if (!run) {
+              if (lane == 0) fail(s_abort, p.status);
+              break;
+            }
+            ahead[i].store(smem + C::kOffV + sl * C::kVBytes, e);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfull[sl]);
+            if (++sl == C::kVSlots) {
+              sl = 0;
+              vphase ^= 1u;
+            }
+            ahead[i].load(p, s_ad, s_grp, group_of(i0 + i + kAhead), groups, t0, e);
           }
-          f.place(e, s_grp, j, groups);
-          f.put_v(p, e, s_ad, t0, smem + C::kOffV + sl * C::kVBytes);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&vfull[sl]);
         }
       }
     }
@@ -736,6 +805,14 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll 1
       for (int n0 = 0; n0 < NT && t0 + n0 < p.T; n0 += 32) {
         uint32_t v[32];
+        unsigned wanted = 0xffffffffu;
+        if (SHRINK) {      // a warp has two groups: only their adapters' tokens
+          const int g = 2 * q, n = n0 + lane, a = n < NT ? s_ad[n] : -1;
+          const uint32_t* grp = s_grp + blk * 8;
+          wanted = __ballot_sync(0xffffffffu, a >= 0 && ((g < ng && a == grp_adapter(grp[g])) ||
+                                                         (g + 1 < ng && a == grp_adapter(grp[g + 1]))));
+          if (wanted == 0u) continue;
+        }
         tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + n0, v);
         if (!SHRINK && 4 * rank < groups) {      // this CTA had adapter k-blocks
           uint32_t w[32];
@@ -749,7 +826,7 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int n = n0 + i, owner = n >> lg;
-          if (n < NT && t0 + n < p.T)
+          if (n < NT && t0 + n < p.T && (wanted >> i & 1u))
             st_cluster_f32(mapa_shared(mine + static_cast<uint32_t>((n & (per - 1)) * kRows * 4),
                                        static_cast<uint32_t>(owner)),
                            __uint_as_float(v[i]));
@@ -1284,7 +1361,7 @@ int tile_tokens(int T) {
 }
 
 // Up to here (tokens x r_max) v is a dot product per token and rank.
-constexpr long long kDotMax = 8192;
+constexpr long long kDotMax = 16384;
 
 template <int NT, bool SHRINK>
 cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t s) {
