@@ -357,12 +357,11 @@ __global__ void __launch_bounds__(kDotThreads, 2)
 template <int NT, bool SHRINK>
 struct SwapCfg {
   static constexpr uint32_t kStage = kTile + NT * 128;
-  static constexpr int kStages = NT >= 256 ? (SHRINK ? 4 : 3) : (NT >= 128 ? 5 : 6);
-  static constexpr int kG = NT <= 64 ? 4 : 1;                     // groups of adapter columns a v slot holds
-  static constexpr int kVSlots = SHRINK ? 0 : (NT == 64 ? 2 : 4);
+  static constexpr int kStages = NT >= 256 ? (SHRINK ? 4 : 3) : (NT >= 128 ? (SHRINK ? 5 : 4) : 6);
+  static constexpr int kG = NT <= 128 ? 4 : 2;                    // groups of adapter columns a v slot holds
+  static constexpr int kVSlots = SHRINK ? 0 : (NT >= 64 ? 2 : 4);
   static constexpr uint32_t kVTile = NT * kGroup * 2;
   static constexpr uint32_t kVBytes = 2 * kG * kVTile;            // v of each group: hi, lo
-  static constexpr int kAhead = NT == 128 ? 4 : (NT == 256 ? 2 : 1);  // slots' worth in a worker's registers
   static constexpr uint32_t kOffV = kStages * kStage;
   static constexpr uint32_t kOffBar = kOffV + kVSlots * kVBytes;
   static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 3 + 2 * kVSlots) * 8;
@@ -383,6 +382,7 @@ template <int NT, int G>
 struct VRows {
   static constexpr int kStep = 64 / G, kN = NT < kStep ? 1 : NT / kStep;
   float4 v[kN][2];
+  unsigned own;           // bit i: the i-th of them has this adapter
 
   __device__ __forceinline__ void load(const LoraParams& p, const int* s_ad, const uint32_t* s_grp,
                                        int gi, int groups, int t0, int e) {
@@ -391,11 +391,12 @@ struct VRows {
     const uint32_t g = gi < groups ? s_grp[gi] : 0u;
     const bool live = gi < groups && grp_cols(g) > 8 * half;
     const int a = grp_adapter(g), col = grp_first(g) + 8 * half;
+    own = 0u;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int r = r0 + kStep * i;
-      v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (live && r < NT && s_ad[r] == a) {
+        own |= 1u << i;
         const float4* from =
             reinterpret_cast<const float4*>(p.v + static_cast<long long>(t0 + r) * p.r_max + col);
         v[i][0] = __ldcg(from);
@@ -411,8 +412,8 @@ struct VRows {
     for (int i = 0; i < kN; ++i) {
       const int r = r0 + kStep * i;
       if (r >= NT) break;
-      uint4 hi, lo;
-      split8(v[i][0], v[i][1], hi, lo);
+      uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+      if (own >> i & 1u) split8(v[i][0], v[i][1], hi, lo);
       uint8_t* at = to + r * 32 + ((half ^ ((r >> 2) & 1)) << 4);
       *reinterpret_cast<uint4*>(at) = hi;
       *reinterpret_cast<uint4*>(at + NT * kGroup * 2) = lo;
@@ -754,36 +755,29 @@ __global__ void __launch_bounds__(192, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(tbl);
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        // a thread's values of the next slots are on their way while it waits for one
-        constexpr int kAhead = C::kAhead, kG = C::kG;
-        VRows<NT, kG> ahead[kAhead];
+        // a thread's values of the next slot are on their way while it waits for it
+        constexpr int kG = C::kG;
+        VRows<NT, kG> next;
         auto group_of = [&](int i) { return 4 * (rank + S * (i * kG >> 2)) + (i * kG & 3); };
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) ahead[i].load(p, s_ad, s_grp, group_of(i), groups, t0, e);
+        next.load(p, s_ad, s_grp, group_of(0), groups, t0, e);
         int sl = 0;
         uint32_t vphase = 0;
-        bool run = true;
-        for (int i0 = 0; run && group_of(i0) < groups; i0 += kAhead) {
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            if (!run || group_of(i0 + i) >= groups) break;
-            int ok = 1;
-            if (lane == 0) ok = mbar_wait(&vempty[sl], vphase ^ 1u, s_abort) ? 1 : 0;
-            run = __shfl_sync(0xffffffffu, ok, 0) != 0;
-            if (!run) {
-              if (lane == 0) fail(s_abort, p.status);
-              break;
-            }
-            ahead[i].store(smem + C::kOffV + sl * C::kVBytes, e);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&vfull[sl]);
-            if (++sl == C::kVSlots) {
-              sl = 0;
-              vphase ^= 1u;
-            }
-            ahead[i].load(p, s_ad, s_grp, group_of(i0 + i + kAhead), groups, t0, e);
+        for (int i = 0; group_of(i) < groups; ++i) {
+          int ok = 1;
+          if (lane == 0) ok = mbar_wait(&vempty[sl], vphase ^ 1u, s_abort) ? 1 : 0;
+          if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            if (lane == 0) fail(s_abort, p.status);
+            break;
           }
+          next.store(smem + C::kOffV + sl * C::kVBytes, e);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vfull[sl]);
+          if (++sl == C::kVSlots) {
+            sl = 0;
+            vphase ^= 1u;
+          }
+          next.load(p, s_ad, s_grp, group_of(i + 1), groups, t0, e);
         }
       }
     }
@@ -892,7 +886,7 @@ struct PairCfg {
 };
 
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = 0;
   while (true) {
     for (int i = 0; i < 64; ++i) {
       uint32_t ok;
@@ -906,6 +900,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
       if (ok) return true;
     }
     if (abort != nullptr && *abort) return false;
+    if (t0 == 0) t0 = globaltimer();
     if (globaltimer() - t0 > kWaitLimitNs) return false;
   }
 }
