@@ -637,25 +637,21 @@ void tmap_store(const TmapKey& k, const CUtensorMap& m) {
 }
 }  // namespace
 
-bool encode_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, long long ld,
-                      int box_rows, int box_cols) {
-  auto fn = encode_fn();
-  if (fn == nullptr || rows <= 0) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_cols == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // bf16 [rows, cols] row-major, box = 64 columns x box_rows rows, 128-B swizzle.
 bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
   const TmapKey key{base, rows, cols, box_rows, 2};
   if (rows > 0 && tmap_lookup(key, m)) return true;
-  if (!encode_tmap_bf16(m, base, rows, cols, cols, box_rows)) return false;
+  auto fn = encode_fn();
+  if (fn == nullptr || rows <= 0) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return false;
   tmap_store(key, *m);
   return true;
 }

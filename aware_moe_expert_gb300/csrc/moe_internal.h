@@ -305,10 +305,6 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s);
 // bf16 [rows, cols] row-major tensor map: box of 64 columns x box_rows rows,
 // 128-byte swizzle, zero fill out of bounds.
 bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);
-// The same with ld elements between rows (a multiple of 8), encoded anew on
-// every call; box of 64 columns (128-byte swizzle) or 16 (32-byte swizzle).
-bool encode_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, long long ld,
-                      int box_rows, int box_cols = 64);
 bool gemm_supports_f32_router(int E_r);
 // Output columns per tile and K splits of the tensor-core router GEMM for T
 // tokens: small batches take 64-column tiles, and K is split until about 128
