@@ -42,15 +42,24 @@ __device__ __forceinline__ float warp_sum_f32(float v) {
   return v;
 }
 
-// Sigmoids for the comparison: __expf and an approximate reciprocal.  Their error
-// is below 1e-6 of a token's largest score (exp(x) is good to 2^-21 + |x| 2^-24
-// of its value, and where |x| is large the score or its complement is small).
-// The weights that leave the kernel are computed again with expf and a division.
-__device__ __forceinline__ float sigmoid_fast(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+// Sigmoid for the comparison, 1 / (1 + 2^(-l log2 e)) with the approximate
+// exponential and reciprocal: each is good to 2^-22 of its value, the rounded
+// product in the exponent adds |l| 2^-24.  The weights that leave the kernel are
+// computed again with expf and a division.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
-// s(l) exp(-m) with m = min(largest selected l, 0): l > 0 only where m = 0.
+// s(l) exp(-m) with m = min(largest selected l, 0), the same in every lane:
+// l > 0 only where m = 0.
 __device__ __forceinline__ float sigmoid_over(float l, float m) {
-  return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
+  const float e = expf(-fabsf(l));
+  float top = l > 0.f ? 1.f : e;
+  if (m < 0.f) top = expf(l - m);
+  return top / (1.f + e);
 }
 
 struct GroupParams {
@@ -70,7 +79,6 @@ struct GroupParams {
   int gpl;                // groups per lane (1 unless MANY)
   int per;                // units per lane
   int vec;                // lanes hold aligned multiples of four units: 16-byte loads
-  int inf_bias;           // a selection bias is given: one could be +inf
   int32_t* idx;
   float* w;
   int32_t* k_out;         // nullable
@@ -125,7 +133,6 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
     }
   }
   if (bad_bias) report(p.status, MOE_ERR_NONFINITE);
-  const unsigned below = (1u << lane) - 1u;
 
   for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
     int k = p.kpt != nullptr ? __ldg(p.kpt + t) : p.k_max;
@@ -166,16 +173,24 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
       k = min(max(k, 0), p.k_max);
     }
     // NaN and +inf are reported and leave the unit out, like -inf
-    bool bad = false;
+    bool odd = false;
 #pragma unroll
-    for (int i = 0; i < IPL; ++i) bad |= !(c[i] < INFINITY);
-    if (__any_sync(kAll, bad)) {
+    for (int i = 0; i < IPL; ++i) odd |= !(fabsf(c[i]) < INFINITY);
+    const bool masked = __any_sync(kAll, odd);
+    unsigned out = 0u;               // bit i: unit i is out
+    if (masked) {
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < IPL; ++i) {
+        if (!(c[i] < INFINITY)) {
+          bad = true;
+          c[i] = -INFINITY;
+        }
+        if (c[i] == -INFINITY) out |= 1u << i;
+      }
       if (bad) report(p.status, MOE_ERR_NONFINITE);
-#pragma unroll
-      for (int i = 0; i < IPL; ++i)
-        if (!(c[i] < INFINITY)) c[i] = -INFINITY;
     }
-    // biased scores; -inf (b of the units past n, too) stays -inf
+    // biased scores; the units past n are out by their b
     float mx = 0.f, sum = 1.f;
     if (p.score == MOE_SCORE_SOFTMAX) {
       mx = -INFINITY;
@@ -187,9 +202,8 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
       float part = 0.f;
 #pragma unroll
       for (int i = 0; i < IPL; ++i) {
-        const float e = i < n ? expf(c[i] - m0) : 0.f;
-        part += e;
-        c[i] = c[i] > -INFINITY ? e : -INFINITY;
+        c[i] = i < n ? expf(c[i] - m0) : 0.f;
+        part += c[i];
       }
       sum = warp_sum_f32(part);
       const float inv = sum > 0.f ? __fdividef(1.f, sum) : 1.f;
@@ -197,15 +211,12 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
       for (int i = 0; i < IPL; ++i) c[i] = fmaf(c[i], inv, b[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < IPL; ++i) {
-        const float s = sigmoid_fast(c[i]);
-        c[i] = (c[i] > -INFINITY ? s : -INFINITY) + b[i];
-      }
+      for (int i = 0; i < IPL; ++i) c[i] = sigmoid_fast(c[i]) + b[i];
     }
-    if (p.inf_bias) {      // -inf of a unit that is out, plus a bias of +inf
+    if (masked) {
 #pragma unroll
       for (int i = 0; i < IPL; ++i)
-        if (c[i] != c[i]) c[i] = -INFINITY;
+        if (out >> i & 1u) c[i] = -INFINITY;
     }
 
     if (MANY && p.kept < p.G) {
@@ -278,15 +289,23 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
       if (!(bound > -INFINITY)) break;
       if (head == bound) head = -INFINITY;
     }
-    // the units that reach it
+    // the units that reach it, in any order
+    const float least = bound > -INFINITY ? bound : -3.402823466e38f;
     int listed = 0;
 #pragma unroll
-    for (int i = 0; i < IPL; ++i) {
-      const bool in = c[i] >= bound && c[i] > -INFINITY;
-      const unsigned who = __ballot_sync(kAll, in);
-      if (in) s_list[warp][listed + __popc(who & below)] = make_float2(c[i], __int_as_float(u0 + i));
-      listed += __popc(who);
+    for (int i = 0; i < IPL; ++i) listed += c[i] >= least;
+    int to = listed;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(kAll, to, off);
+      if (lane >= off) to += o;
     }
+    const int mine_n = listed;
+    listed = __shfl_sync(kAll, to, 31);
+    to -= mine_n;
+#pragma unroll
+    for (int i = 0; i < IPL; ++i)
+      if (c[i] >= least) s_list[warp][to++] = make_float2(c[i], __int_as_float(u0 + i));
     __syncwarp();
     const int got = min(k, listed);
     for (int i = lane; i < listed; i += 32) {
@@ -480,7 +499,6 @@ cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
   // with every group kept the grouping decides nothing
   if (p.kept == p.G) p.G = p.kept = 1;
   p.sel_bias = a.select_bias;
-  p.inf_bias = a.select_bias != nullptr;
   p.size = p.E / p.G;
   const bool many = p.G > 32;
   p.L = many ? 1 : 32 / p.G;
@@ -493,7 +511,7 @@ cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
   p.load = a.load;
   p.status = a.status;
   const int blocks = (a.T + kWarps - 1) / kWarps;
-  const int grid = blocks < 6 * a.sm_count ? blocks : 6 * a.sm_count;
+  const int grid = blocks < 4 * a.sm_count ? blocks : 4 * a.sm_count;
   p.zeroed = a.load != nullptr && grid > 1;
   if (p.zeroed) {
     const cudaError_t e = launch_pdl(zero_load_kernel, dim3(1), dim3(kMaxUnits), 0, s, a.load, a.E_r);
