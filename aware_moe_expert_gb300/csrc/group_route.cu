@@ -19,6 +19,8 @@
 // neither the other logits nor their sum.  A renormalised sigmoid takes the
 // common factor exp(m), m = min(max selected l, 0), out of every s.  Neither can
 // divide by a sum that underflowed.
+#include <cuda_fp16.h>
+
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -27,6 +29,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;            // tokens of a CTA at a time
+constexpr int kMaxWarps = 16;        // the same where that makes more CTAs than SMs
 constexpr int kMaxUnits = 256;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -35,6 +38,14 @@ __device__ __forceinline__ float warp_max_f32(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
+
+__device__ __forceinline__ float warp_min_f32(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 
 __device__ __forceinline__ float warp_sum_f32(float v) {
 #pragma unroll
@@ -91,18 +102,20 @@ struct GroupParams {
 // lanes, each with `per` consecutive units, so units ascend with the lanes and
 // a group's two best come from its lanes' two best.  MANY (G > 32): a lane
 // holds whole groups, at most 16 units.
-// Selection without a sort: the k-th largest of the lanes' best units is a
-// bound that the k best units reach (k maxima of the warp); the units that
-// reach it, a few more than k, are listed and each counts the listed units
-// before it.  Sorting every lane and popping k heads took three times as long
-// at 256 units.  Issue bound: about 400 instructions a token at 256 units, 8 of
-// 8 groups' 4 and k = 8, against 1 KB of logits.
+// Selection without a sort: k of the lanes' best units reach a bound, so the k
+// best units do; the units that reach it, a few more than k, are listed and each
+// counts the listed units before it.  The bound is found by counting in fp16,
+// two lanes' heads at a time (k rounds of a warp maximum took 2 us more).
+// Bound: issue slots and, before them, the chain through a token: 32 warps a SM
+// keep both apart.  16384 tokens of 256 units in 8 groups, 4 kept, k = 8, with
+// load counts: 15.4 us, 1.2 TB/s (sorting every lane and popping k heads: 24.7);
+// one token 3.5 us, which is the launch and one chain.
 template <int IPL, bool MANY>
-__global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupParams p) {
+__global__ void __launch_bounds__(kMaxWarps * 32) group_route_kernel(const GroupParams p) {
   __shared__ int32_t s_load[kMaxUnits];
-  __shared__ float2 s_list[kWarps][kMaxUnits];        // score, unit
-  __shared__ int32_t s_sel[kWarps][32];
-  __shared__ float s_rank[MANY ? kWarps : 1][kMaxUnits];
+  __shared__ float2 s_list[kMaxWarps][kMaxUnits];     // score, unit
+  __shared__ int32_t s_sel[kMaxWarps][32];
+  __shared__ __align__(16) __half s_head[kMaxWarps][32];
   // With `zeroed` the kernel before this one clears `load`, after it has itself
   // waited for everything before: only `load` is waited for, at the end.
   if (!p.zeroed) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -134,7 +147,8 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
   }
   if (bad_bias) report(p.status, MOE_ERR_NONFINITE);
 
-  for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
+  const int warps = blockDim.x >> 5;
+  for (int t = blockIdx.x * warps + warp; t < p.T; t += gridDim.x * warps) {
     int k = p.kpt != nullptr ? __ldg(p.kpt + t) : p.k_max;
     const float* row = p.P + static_cast<size_t>(t) * p.E;
     float c[IPL];
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
     }
 
     if (MANY && p.kept < p.G) {
-      float* rank = s_rank[warp];
+      float* rank = reinterpret_cast<float*>(s_list[warp]);
       for (int q = 0; q < p.gpl; ++q) {
         float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -243,6 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
             if (i / p.size == q) c[i] = -INFINITY;
         }
       }
+      __syncwarp();
     }
     // the lane's two best
     float a1 = c[0], a2 = -INFINITY;
@@ -282,13 +297,23 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const GroupPar
         for (int i = 0; i < IPL; ++i) c[i] = -INFINITY;
       }
     }
-    // the bound: the k-th largest head, or the largest -inf below it
-    float bound = -INFINITY;
-    for (int r = 0; r < k; ++r) {
-      bound = warp_max_f32(head);
-      if (!(bound > -INFINITY)) break;
-      if (head == bound) head = -INFINITY;
+    // the bound: the least head of the lanes with fewer than k larger ones, where
+    // larger is larger as fp16 (never more lanes than the k best leave out)
+    __half* heads = s_head[warp];
+    heads[lane] = __float2half_rn(head);
+    __syncwarp();
+    const __half2 own = __half2half2(heads[lane]);
+    __half2 larger = __float2half2_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(heads)[i];
+      larger = __hadd2(larger, __hgt2(as_half2(v.x), own));
+      larger = __hadd2(larger, __hgt2(as_half2(v.y), own));
+      larger = __hadd2(larger, __hgt2(as_half2(v.z), own));
+      larger = __hadd2(larger, __hgt2(as_half2(v.w), own));
     }
+    const float before = __low2float(larger) + __high2float(larger);
+    const float bound = warp_min_f32(before < static_cast<float>(k) ? head : INFINITY);
     // the units that reach it, in any order
     const float least = bound > -INFINITY ? bound : -3.402823466e38f;
     int listed = 0;
@@ -379,14 +404,18 @@ struct RouteBackParams {
   int32_t* status;
 };
 
-// One warp per token: lane j takes slot j; the row leaves through shared
-// memory, whole.
-__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const RouteBackParams p) {
+// One warp per token: lane j takes slot j.  The softmax that is not renormalised
+// has a row of gradients: its logits are in registers, NV a lane, read once.
+// The others (NV = 0) have k: their row leaves through shared memory, whole.
+// Bound: latency, of which occupancy hides most (40 registers for the others: 5.2
+// us, 48: 6.1).  16384 tokens of 128 units, k = 8: 4.9 us dense (3.6 TB/s), 5.1
+// renormalised; from 64 to 256 units a row in eight registers a lane: 7.0.
+template <int NV>
+__global__ void __launch_bounds__(kWarps * 32, NV == 0 ? 6 : 4) route_backward_kernel(const RouteBackParams p) {
   __shared__ __align__(16) float s_row[kWarps][kMaxUnits];
   pdl_wait_and_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* d = s_row[warp];
-  const bool dense = p.score == MOE_SCORE_SOFTMAX && !p.renorm;
   for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
     const float* row = p.logits + static_cast<size_t>(t) * p.E;
     float* out = p.d_logits + static_cast<size_t>(t) * p.E;
@@ -397,45 +426,63 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
       u = p.idx[o];
       gw = p.d_w[o];
     }
-    const unsigned same = __match_any_sync(kAll, u);
-    if (u >= p.E || u < -1 || (u >= 0 && same != (1u << lane))) {
-      report(p.status, MOE_ERR_BAD_INDEX);
-      if (u >= p.E || u < -1 || (same & ((1u << lane) - 1u)) != 0u) u = -1;
+    float v[NV + 1];
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        v[j] = lane + 32 * j < p.E ? __ldg(row + lane + 32 * j) : -INFINITY;
     }
-    float l = u >= 0 ? __ldg(row + u) : -INFINITY;
-    bool bad = !(l < INFINITY);
-    if (bad) l = -INFINITY;
-    const bool sel = u >= 0 && l > -INFINITY;
-    if (!sel) gw = 0.f;
     for (int i = lane; i < p.E; i += 32) d[i] = 0.f;
     __syncwarp();
-    if (dense) {
-      float mx = -INFINITY;
-      for (int i = lane; i < p.E; i += 32) {
-        const float v = __ldg(row + i);
-        bad |= !(v < INFINITY);
-        if (v < INFINITY) mx = fmaxf(mx, v);
+    // a unit listed twice has two slots for its mark
+    int* mark = reinterpret_cast<int*>(d);
+    bool wrong = u >= p.E || u < -1;
+    if (wrong) u = -1;
+    if (u >= 0) mark[u] = lane;
+    __syncwarp();
+    if (u >= 0 && mark[u] != lane) wrong = true;
+    if (__any_sync(kAll, wrong)) {
+      if (wrong) report(p.status, MOE_ERR_BAD_INDEX);
+      if ((__match_any_sync(kAll, u) & ((1u << lane) - 1u)) != 0u) u = -1;   // the first slot stays
+    }
+    __syncwarp();
+    bool bad = false;
+    if constexpr (NV > 0) {
+      if (u >= 0) d[u] = gw * p.scale;
+      float mx = -INFINITY, sum = 0.f, dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!(v[j] < INFINITY)) {
+          bad = true;
+          v[j] = -INFINITY;
+        }
+        mx = fmaxf(mx, v[j]);
       }
       mx = warp_max_f32(mx);
-      if (sel) d[u] = gw * p.scale;
       __syncwarp();
-      float sum = 0.f, dot = 0.f;
-      for (int i = lane; i < p.E; i += 32) {
-        const float v = __ldg(row + i);
-        const float e = v < INFINITY && mx > -INFINITY ? expf(v - mx) : 0.f;
-        sum += e;
-        dot += e * d[i];
+      if (!(mx > -INFINITY)) mx = 0.f;
+      float dv[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        // a unit that is out has no part, whatever a slot says
+        dv[j] = v[j] > -INFINITY ? d[lane + 32 * j] : 0.f;
+        v[j] = expf(v[j] - mx);
+        sum += v[j];
+        dot += v[j] * dv[j];
       }
       sum = warp_sum_f32(sum);
       dot = warp_sum_f32(dot);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       dot *= inv;
-      for (int i = lane; i < p.E; i += 32) {
-        const float v = __ldg(row + i);
-        const float e = v < INFINITY && mx > -INFINITY ? expf(v - mx) * inv : 0.f;
-        out[i] = e * (d[i] - dot);
-      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (lane + 32 * j < p.E) out[lane + 32 * j] = v[j] * inv * (dv[j] - dot);
     } else {
+      float l = u >= 0 ? __ldg(row + u) : -INFINITY;
+      bad = !(l < INFINITY);
+      if (bad) l = -INFINITY;
+      const bool sel = u >= 0 && l > -INFINITY;
+      if (!sel) gw = 0.f;
       float dl;
       if (p.score == MOE_SCORE_SOFTMAX) {
         const float top = warp_max_f32(l);
@@ -456,7 +503,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
         }
         dl = p.scale * wt * ms * (gw - dot);
       }
-      if (sel) d[u] = dl;
+      if (u >= 0) d[u] = sel ? dl : 0.f;
       __syncwarp();
       if (p.vec) {
         for (int i = lane; i < p.E / 4; i += 32)
@@ -510,14 +557,19 @@ cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
   p.k_out = a.k_out;
   p.load = a.load;
   p.status = a.status;
-  const int blocks = (a.T + kWarps - 1) / kWarps;
-  const int grid = blocks < 4 * a.sm_count ? blocks : 4 * a.sm_count;
+  // 16 warps where there are more tokens than eight a SM: half as many CTAs add
+  // to the same load counts (256 units, with 8 and 16: 600 tokens 4.8, 5.2 us;
+  // 2400 5.6, 5.4; 4096 8.5, 7.0; 16384 17.2, 15.4).  32 warps a SM: 24 took
+  // 18.1 us where 32 took 17.7 and 40 took 18.0.
+  const int warps = a.T > kWarps * a.sm_count ? kMaxWarps : kWarps;
+  const int blocks = (a.T + warps - 1) / warps, most = 4 * kWarps / warps * a.sm_count;
+  const int grid = blocks < most ? blocks : most;
   p.zeroed = a.load != nullptr && grid > 1;
   if (p.zeroed) {
     const cudaError_t e = launch_pdl(zero_load_kernel, dim3(1), dim3(kMaxUnits), 0, s, a.load, a.E_r);
     if (e != cudaSuccess) return e;
   }
-  const dim3 g(grid), b(kWarps * 32);
+  const dim3 g(grid), b(warps * 32);
   if (many) return launch_pdl(group_route_kernel<16, true>, g, b, 0, s, p);
   if (p.per <= 1) return launch_pdl(group_route_kernel<1, false>, g, b, 0, s, p);
   if (p.per <= 2) return launch_pdl(group_route_kernel<2, false>, g, b, 0, s, p);
@@ -543,7 +595,10 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
   p.status = a.status;
   const int blocks = (a.T + kWarps - 1) / kWarps;
   const int grid = blocks < 8 * a.sm_count ? blocks : 8 * a.sm_count;
-  return launch_pdl(route_backward_kernel, dim3(grid), dim3(kWarps * 32), 0, s, p);
+  const dim3 g(grid), b(kWarps * 32);
+  if (a.score != MOE_SCORE_SOFTMAX || a.renorm) return launch_pdl(route_backward_kernel<0>, g, b, 0, s, p);
+  if (a.E_r <= 128) return launch_pdl(route_backward_kernel<4>, g, b, 0, s, p);
+  return launch_pdl(route_backward_kernel<kMaxUnits / 32>, g, b, 0, s, p);
 }
 
 }  // namespace moe
