@@ -408,8 +408,8 @@ struct RouteBackParams {
 // has a row of gradients: its logits are in registers, NV a lane, read once.
 // The others (NV = 0) have k: their row leaves through shared memory, whole.
 // Bound: latency, of which occupancy hides most (40 registers for the others: 5.2
-// us, 48: 6.1).  16384 tokens of 128 units, k = 8: 4.9 us dense (3.6 TB/s), 5.1
-// renormalised; from 64 to 256 units a row in eight registers a lane: 7.0.
+// us, 48: 6.1).  16384 tokens of 128 units, k = 8: 4.9 us dense (3.6 TB/s; with a
+// row in eight registers a lane whatever its length 7.0), 5.1 renormalised.
 template <int NV>
 __global__ void __launch_bounds__(kWarps * 32, NV == 0 ? 6 : 4) route_backward_kernel(const RouteBackParams p) {
   __shared__ __align__(16) float s_row[kWarps][kMaxUnits];
