@@ -157,6 +157,11 @@ __device__ __forceinline__ int build_groups(const LoraParams& p, int t0, int e, 
 // Eight bf16 of a factor: those past `cols` and those that are not finite are 0.
 __device__ __forceinline__ uint4 clean8(uint4 q, int cols, bool& bad) {
   uint32_t* w = &q.x;
+  // an exponent of all ones carries into its half's top bit
+  uint32_t carry = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) carry |= (w[i] & 0x7f807f80u) + 0x00800080u;
+  if (cols >= 8 && (carry & 0x80008000u) == 0u) return q;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t lo = w[i] & 0xffffu, hi = w[i] >> 16;
@@ -1184,6 +1189,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     bool waited = p.wait_first != 0;
     uint32_t lp = 0;
     int built = -1, groups = 0, slot = 0;
+    unsigned dirty = (1u << kPairSlots) - 1u;   // slots whose row of v is not zero
     bool run = true;   // after a wait that gave up: keep the workers' barriers, touch nothing
     // where row e's two chunks of 16 bytes lie under the 32-byte swizzle
     const uint32_t c0 = static_cast<uint32_t>(e) * 32u + ((static_cast<uint32_t>(e) & 4u) << 2);
@@ -1201,8 +1207,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int mine = s_ad[static_cast<int>(rank) * 128 + e];   // -1 past the last token
       const __nv_bfloat16* brow = p.b + static_cast<long long>(wr) * p.r_max;
       const float* vrow = p.v + static_cast<long long>(t) * p.r_max;
-      // this thread's factor row and token row of a group, two groups ahead
-      PairRow ahead[2];
+      // this thread's factor row and token row of the next groups: as many as
+      // there are slots, all on their way together, because what makes a slot's
+      // contents visible waits for every load before it
+      PairRow ahead[kPairSlots];
       auto load_b = [&](PairRow& f, int j) {
         const uint32_t g = j < groups ? s_grp[j] : 0u;
         f.cols = j < groups ? grp_cols(g) : 0;
@@ -1217,55 +1225,71 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       };
       auto load_v = [&](PairRow& f) {
+        if (!f.own) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f.v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (f.own && 8 * (i / 2) < f.cols)
-            f.v[i] = __ldcg(reinterpret_cast<const float4*>(vrow + f.first) + i);
-        }
+        for (int i = 0; i < 4; ++i)
+          f.v[i] = 8 * (i / 2) < f.cols ? __ldcg(reinterpret_cast<const float4*>(vrow + f.first) + i)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
       };
 #pragma unroll
-      for (int i = 0; i < 2; ++i) load_b(ahead[i], i);
+      for (int i = 0; i < kPairSlots; ++i) load_b(ahead[i], i);
       if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
       waited = true;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) load_v(ahead[i]);
+      for (int i = 0; i < kPairSlots; ++i) load_v(ahead[i]);
       // the post after the last group ends the tile
-#pragma unroll 2
-      for (int j = 0; run && j <= groups; ++j) {
-        PairRow& f = ahead[j & 1];
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(&lempty[slot], lp ^ 1u, s_abort) ? 1 : 0;
-        run = __shfl_sync(0xffffffffu, ok, 0) != 0;
-        if (!run) {
-          if (lane == 0) fail(s_abort, p.status);
-          break;
+      for (int j0 = 0; run && j0 <= groups; j0 += kPairSlots) {
+        const int n = min(kPairSlots, groups + 1 - j0), first = slot;
+#pragma unroll
+        for (int i = 0; i < kPairSlots; ++i) {
+          if (!run || i >= n) break;
+          const PairRow& f = ahead[i];
+          int ok = 1;
+          if (lane == 0) ok = mbar_wait(&lempty[slot], lp ^ 1u, s_abort) ? 1 : 0;
+          run = __shfl_sync(0xffffffffu, ok, 0) != 0;
+          if (!run) {
+            if (lane == 0) fail(s_abort, p.status);
+            break;
+          }
+          if (j0 + i < groups) {
+            uint8_t* at = smem + C::kOffSlot + slot * C::kSlot + c0;
+            uint8_t* at1 = smem + C::kOffSlot + slot * C::kSlot + (c0 ^ 16u);
+            bool bad = false;
+            *reinterpret_cast<uint4*>(at + 2 * C::kGroupTile) = clean8(f.b0, f.cols, bad);
+            *reinterpret_cast<uint4*>(at1 + 2 * C::kGroupTile) = clean8(f.b1, f.cols - 8, bad);
+            if (bad) report(p.status, MOE_ERR_NONFINITE);
+            if (f.own || (dirty >> slot & 1u)) {
+              uint4 hi0 = make_uint4(0u, 0u, 0u, 0u), lo0 = hi0, hi1 = hi0, lo1 = hi0;
+              if (f.own) {
+                split8(f.v[0], f.v[1], hi0, lo0);
+                split8(f.v[2], f.v[3], hi1, lo1);
+              }
+              *reinterpret_cast<uint4*>(at) = hi0;
+              *reinterpret_cast<uint4*>(at + C::kGroupTile) = lo0;
+              *reinterpret_cast<uint4*>(at1) = hi1;
+              *reinterpret_cast<uint4*>(at1 + C::kGroupTile) = lo1;
+              dirty = f.own ? dirty | 1u << slot : dirty & ~(1u << slot);
+            }
+          }
+          if (e == 0) s_more[slot] = j0 + i < groups ? 1 : 0;
+          if (++slot == kPairSlots) {
+            slot = 0;
+            lp ^= 1u;
+          }
         }
-        if (j < groups) {
-          uint8_t* at = smem + C::kOffSlot + slot * C::kSlot + c0;
-          uint8_t* at1 = smem + C::kOffSlot + slot * C::kSlot + (c0 ^ 16u);
-          bool bad = false;
-          *reinterpret_cast<uint4*>(at + 2 * C::kGroupTile) = clean8(f.b0, f.cols, bad);
-          *reinterpret_cast<uint4*>(at1 + 2 * C::kGroupTile) = clean8(f.b1, f.cols - 8, bad);
-          if (bad) report(p.status, MOE_ERR_NONFINITE);
-          uint4 hi, lo;
-          split8(f.v[0], f.v[1], hi, lo);
-          *reinterpret_cast<uint4*>(at) = hi;
-          *reinterpret_cast<uint4*>(at + C::kGroupTile) = lo;
-          split8(f.v[2], f.v[3], hi, lo);
-          *reinterpret_cast<uint4*>(at1) = hi;
-          *reinterpret_cast<uint4*>(at1 + C::kGroupTile) = lo;
-          fence_proxy_async_smem();
-        }
-        if (e == 0) s_more[slot] = j < groups ? 1 : 0;
+        if (!run) break;
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_release_cluster(lfull_l + 8u * static_cast<uint32_t>(slot));
-        if (++slot == kPairSlots) {
-          slot = 0;
-          lp ^= 1u;
+        if (lane == 0) {
+          for (int i = 0; i < n; ++i) {
+            const int at = first + i < kPairSlots ? first + i : first + i - kPairSlots;
+            arrive_release_cluster(lfull_l + 8u * static_cast<uint32_t>(at));
+          }
         }
-        load_b(f, j + 2);
-        load_v(f);
+#pragma unroll
+        for (int i = 0; i < kPairSlots; ++i) load_b(ahead[i], j0 + kPairSlots + i);
+#pragma unroll
+        for (int i = 0; i < kPairSlots; ++i) load_v(ahead[i]);
       }
     }
     // the last commits on this CTA's lempty have arrived
