@@ -575,8 +575,6 @@ __global__ void __launch_bounds__(192, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = gridDim.x, rank = blockIdx.x;
   const int t0 = blockIdx.z * NT;
-  const int per = NT / S;                  // tokens of this CTA: a power of two
-  const int lg = 31 - __clz(per);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -615,16 +613,27 @@ __global__ void __launch_bounds__(192, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *s_tmem;
   const int KB = (p.K + kBK - 1) / kBK;
-  const int kb0 = static_cast<int>(static_cast<long long>(KB) * rank / S);
-  const int kb1 = static_cast<int>(static_cast<long long>(KB) * (rank + 1) / S);
-  // SHRINK: blocks of eight groups, gridDim.y apart
-  const int passes_end = SHRINK ? (*s_total + 7) / 8 : static_cast<int>(blockIdx.y) + 1;
+  // SHRINK: blocks of eight groups.  How many there are is known here only: K is
+  // split over as many of the cluster's CTAs as leave every block one turn.
+  int split = S, unit = blockIdx.y, units = 1, turns_end = 1;
+  if (SHRINK) {
+    turns_end = (*s_total + 7) / 8;
+    while (split > 1 && turns_end * split > S * static_cast<int>(gridDim.y)) split >>= 1;
+    unit = static_cast<int>(blockIdx.y) * (S / split) + rank / split;
+    units = static_cast<int>(gridDim.y) * (S / split);
+  }
+  const int part_of = rank & (split - 1);  // this CTA's part of K, and of the tokens
+  const int per = NT / split;              // tokens of this CTA: a power of two
+  const int kb0 = static_cast<int>(static_cast<long long>(KB) * part_of / split);
+  const int kb1 = static_cast<int>(static_cast<long long>(KB) * (part_of + 1) / split);
   int stage = 0;
   uint32_t phase = 0, pass_parity = 0;
-  for (int blk = blockIdx.y; blk < passes_end; blk += gridDim.y) {
+  for (int turn = 0; turn < turns_end; turn += units) {
+    const int blk = turn + unit;
     const int ng = SHRINK ? min(8, *s_total - blk * 8) : 0;
+    const bool idle = SHRINK && ng <= 0;
     if (warp == 0) {
-      if (lane == 0) {
+      if (lane == 0 && !idle) {
         const uint32_t bytes = (SHRINK ? static_cast<uint32_t>(ng) * kGroup * kBK * 2 : kTile) + NT * 128;
         bool ok = *s_abort == 0;
         for (int kb = kb0; ok && kb < kb1; ++kb) {
@@ -688,7 +697,7 @@ __global__ void __launch_bounds__(192, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (lane == 0 && !idle) {
         constexpr uint32_t idesc = idesc_bf16_f32(kRows, NT);
         bool ok = *s_abort == 0;
         for (int kb = kb0; ok && kb < kb1; ++kb) {
@@ -786,7 +795,7 @@ __global__ void __launch_bounds__(192, 1)
         }
       }
     }
-    if (warp >= 2) {
+    if (warp >= 2 && !idle) {
       int ok = 1;
       if (lane == 0) ok = mbar_wait(tfull, pass_parity, s_abort) ? 1 : 0;
       if (lane == 0 && !ok) fail(s_abort, p.status);
@@ -794,13 +803,15 @@ __global__ void __launch_bounds__(192, 1)
       if (!SHRINK && 4 * rank < groups) look_over<NT>(p, smem, s_ad, s_grp, s_sum, redo, s_abort, tmem,
                                                       blk, t0, rank, S, groups, threadIdx.x - 64);
     }
-    pass_parity ^= 1u;
+    if (!idle) pass_parity ^= 1u;
     __syncwarp();
     if (S > 1) cluster_sync_all();   // every ring of the cluster is free
-    if (warp >= 2) {
+    // 1 << lg tokens a CTA sums; at: the place of the first CTA of this one's part of
+    // the cluster (constants for SHRINK, whose split the compiler cannot tell)
+    auto push = [&](int lg, int at) {
       tc_fence_after();
       const int q = warp & 3;
-      const uint32_t mine = smem_u32(part) + static_cast<uint32_t>((rank * per * kRows + q * 32 + lane) * 4);
+      const uint32_t mine = smem_u32(part) + static_cast<uint32_t>((part_of * per * kRows + q * 32 + lane) * 4);
 #pragma unroll 1
       for (int n0 = 0; n0 < NT && t0 + n0 < p.T; n0 += 32) {
         uint32_t v[32];
@@ -824,25 +835,36 @@ __global__ void __launch_bounds__(192, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const int n = n0 + i, owner = n >> lg;
+          const int n = n0 + i;
           if (n < NT && t0 + n < p.T && (wanted >> i & 1u))
-            st_cluster_f32(mapa_shared(mine + static_cast<uint32_t>((n & (per - 1)) * kRows * 4),
-                                       static_cast<uint32_t>(owner)),
+            st_cluster_f32(mapa_shared(mine + static_cast<uint32_t>((n & ((1 << lg) - 1)) * kRows * 4),
+                                       static_cast<uint32_t>(at + (n >> lg))),
                            __uint_as_float(v[i]));
         }
       }
       tc_fence_before();
+    };
+    if (warp >= 2 && !idle) {
+      constexpr int kLg = NT == 256 ? 8 : NT == 128 ? 7 : NT == 64 ? 6 : NT == 32 ? 5 : 4;
+      if (!SHRINK || split == S)
+        push(31 - __clz(NT / S), 0);
+      else if (split == 4)
+        push(kLg - 2, rank & ~3);
+      else if (split == 2)
+        push(kLg - 1, rank & ~1);
+      else
+        push(kLg, rank);
     }
     __syncwarp();
     if (S > 1)
       cluster_sync_all();
     else
       __syncthreads();
-    if (warp >= 2) {
-      const int lr = (warp & 3) * 32 + lane, first = t0 + rank * per, count = min(per, p.T - first);
-      const int* ad = s_ad + rank * per;
+    if (warp >= 2 && !idle) {
+      const int lr = (warp & 3) * 32 + lane, first = t0 + part_of * per, count = min(per, p.T - first);
+      const int* ad = s_ad + part_of * per;
       const uint32_t* grp = s_grp + (SHRINK ? blk * 8 : 0);
-      switch (S) {
+      switch (split) {
         case 1: finish<SHRINK, 1>(p, part, ad, grp, ng, first, count, per, blk, lr); break;
         case 2: finish<SHRINK, 2>(p, part, ad, grp, ng, first, count, per, blk, lr); break;
         case 4: finish<SHRINK, 4>(p, part, ad, grp, ng, first, count, per, blk, lr); break;
