@@ -26,6 +26,8 @@
 // computes a tile's again with looked-over factors if one is not finite.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "gemm_common.cuh"
@@ -443,6 +445,34 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
   return d;
 }
 
+// SHRINK: what row `row` of a tile of eight groups is, a column of v of one
+// adapter; the lanes of a warp have two groups.
+struct ShrinkRow {
+  int a, col, a0, a1;
+  bool live, use;
+  float scale;
+  __device__ __forceinline__ ShrinkRow(const LoraParams& p, const uint32_t* grp, int ng, int row) {
+    const int g = row / kGroup;
+    const uint32_t gr = g < ng ? grp[g] : 0u;
+    a = g < ng ? grp_adapter(gr) : -2;
+    col = grp_first(gr) + row % kGroup;
+    live = g < ng && col < p.r_max;
+    use = row % kGroup < grp_cols(gr);  // past the rank v is 0
+    scale = g < ng ? __ldg(p.scales + a) : 0.f;
+    a0 = __shfl_sync(0xffffffffu, a, 0);
+    a1 = __shfl_sync(0xffffffffu, a, 16);
+  }
+  // by the whole warp, `ad` the adapter of the lane's token: the tokens whose
+  // adapter the calling lane's group belongs to
+  __device__ __forceinline__ unsigned tokens(int ad) const {
+    const unsigned m0 = __ballot_sync(0xffffffffu, ad == a0), m1 = __ballot_sync(0xffffffffu, ad == a1);
+    return !live ? 0u : (a == a0 ? m0 : m1);
+  }
+  __device__ __forceinline__ void put(const LoraParams& p, int t, float v) const {
+    p.v[static_cast<long long>(t) * p.r_max + col] = use ? v * scale : 0.f;
+  }
+};
+
 // Sums the S partial rows of this CTA's tokens, in rank order, and stores them;
 // a thread has row `row` of the tile.
 template <bool SHRINK, int S>
@@ -459,16 +489,23 @@ __device__ __forceinline__ void finish(const LoraParams& p, const float* part, c
     return v;
   };
   if (SHRINK) {
-    const int g = row / kGroup;
-    if (g >= ng) return;
-    const uint32_t gr = grp[g];
-    const int i = row % kGroup, a = grp_adapter(gr), col = grp_first(gr) + i;
-    const float sc = __ldg(p.scales + a);
-    if (col >= p.r_max) return;
-    for (int n = 0; n < count; ++n)
-      if (ad[n] == a)
-        p.v[static_cast<long long>(first + n) * p.r_max + col] =
-            i < grp_cols(gr) ? sum(n, row) * sc : 0.f;
+    const ShrinkRow m(p, grp, ng, row);
+    for (int n0 = 0; n0 < count; n0 += 32) {
+      unsigned mine = m.tokens(n0 + (row & 31) < count ? ad[n0 + (row & 31)] : -1);
+      while (mine != 0u) {              // up to four tokens' loads at a time
+        int n[4];
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          n[k] = mine != 0u ? n0 + __ffs(mine) - 1 : -1;
+          mine &= mine - 1u;
+          v[k] = n[k] >= 0 ? sum(n[k], row) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (n[k] >= 0) m.put(p, first + n[k], v[k]);
+      }
+    }
   } else if (p.swiglu) {
     const int o = blk * 64 + (row & 63);
     if (o >= p.outs) return;
@@ -805,7 +842,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     if (!idle) pass_parity ^= 1u;
     __syncwarp();
-    if (S > 1) cluster_sync_all();   // every ring of the cluster is free
+    if (split > 1) cluster_sync_all();   // every ring of the cluster is free
     // 1 << lg tokens a CTA sums; at: the place of the first CTA of this one's part of
     // the cluster (constants for SHRINK, whose split the compiler cannot tell)
     auto push = [&](int lg, int at) {
@@ -844,23 +881,42 @@ __global__ void __launch_bounds__(192, 1)
       }
       tc_fence_before();
     };
+    // SHRINK with all of K here: the sums are v
+    auto direct = [&]() {
+      tc_fence_after();
+      const int q = warp & 3;
+      const ShrinkRow m(p, s_grp + blk * 8, ng, q * 32 + lane);
+#pragma unroll 1
+      for (int n0 = 0; n0 < NT && t0 + n0 < p.T; n0 += 32) {
+        const unsigned mine = m.tokens(n0 + lane < NT ? s_ad[n0 + lane] : -1);
+        const unsigned any = __reduce_or_sync(0xffffffffu, mine);
+        if (any == 0u) continue;
+        uint32_t v[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + n0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if ((any >> i & 1u) && (mine >> i & 1u)) m.put(p, t0 + n0 + i, __uint_as_float(v[i]));
+      }
+      tc_fence_before();
+    };
     if (warp >= 2 && !idle) {
       constexpr int kLg = NT == 256 ? 8 : NT == 128 ? 7 : NT == 64 ? 6 : NT == 32 ? 5 : 4;
-      if (!SHRINK || split == S)
+      if (SHRINK && split == 1)
+        direct();
+      else if (!SHRINK || split == S)
         push(31 - __clz(NT / S), 0);
       else if (split == 4)
         push(kLg - 2, rank & ~3);
-      else if (split == 2)
-        push(kLg - 1, rank & ~1);
       else
-        push(kLg, rank);
+        push(kLg - 1, rank & ~1);
     }
     __syncwarp();
-    if (S > 1)
+    if (split > 1)
       cluster_sync_all();
     else
       __syncthreads();
-    if (warp >= 2 && !idle) {
+    if (warp >= 2 && !idle && !(SHRINK && split == 1)) {
       const int lr = (warp & 3) * 32 + lane, first = t0 + part_of * per, count = min(per, p.T - first);
       const int* ad = s_ad + part_of * per;
       const uint32_t* grp = s_grp + (SHRINK ? blk * 8 : 0);
@@ -1362,31 +1418,76 @@ cudaError_t launch_cluster(K kern, dim3 grid, int threads, int smem, int cluster
 //   the bytes into an SM (120 GB/s each measured with all SMs at it),
 //   the MMA (0.33 us for 128 x 256 x 64 in one CTA; less falls slower than N)
 // plus what a CTA does before and after its loop, which grows with its tokens
-// and, for the cluster's exchange of partial sums, with them again.
+// and, for the cluster's exchange of partial sums, with them again.  How many
+// adapters meet in a tile is known on the device only: the estimate is the
+// geometric mean of none and of as many as there can be, each of whose groups
+// of columns costs a slot (0.15 us at 16 tokens to 0.6 at 256, over the splits).
 struct Shape {
   int nt, splits;      // nt = 0: CTA pairs
 };
 
-Shape pick_shape(int T, int K, int outs, int rows_per_tile, int sm) {
+// CTAs that run at a time in clusters of S, a CTA a SM: the parts of the chip
+// that a cluster must fit into are no multiples of it (152 SMs: 144 of four,
+// 120 of eight; 128 CTAs in clusters of eight took two rounds, 14 us where
+// fours took 9.5).  Asked once.
+int cluster_room(int S, int sm) {
+  static std::atomic<int> known[64][4];
+  if (S == 1) return sm;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm;
+  std::atomic<int>& k = known[dev][S == 2 ? 1 : (S == 4 ? 2 : 3)];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    using C = SwapCfg<256, true>;
+    auto kern = lora_swap_kernel<256, true>;
+    static bool done[64] = {false};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (set_smem_once(kern, static_cast<int>(C::kSmem), done) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return sm / S * S;
+    }
+    n *= S;
+    k.store(n, std::memory_order_relaxed);
+  }
+  return n < sm ? n : sm;
+}
+
+Shape pick_shape(int T, int K, int outs, int rows_per_tile, int adapters, int r_max, int sm) {
   const double KB = (K + kBK - 1) / kBK;
   Shape best{0, 1};
   const double pair_tiles = static_cast<double>((T + 255) / 256) * ((outs + 2 * rows_per_tile - 1) / (2 * rows_per_tile));
   const double pairs = sm > 1 ? sm / 2 : 1;
-  double least = std::ceil(pair_tiles / pairs) * KB * 0.33 + 6.0;
+  const double groups = r_max / 32.0 + 0.5;          // of an adapter, ranks being mixed
+  auto both = [](double us, double more) { return std::sqrt(us * (us + more)); };
+  const double pair_rounds = std::ceil(pair_tiles / pairs);
+  double least = both(pair_rounds * KB * 0.33 + 6.0, pair_rounds * 0.5 * groups * std::min(adapters, 256));
   const int rows = (outs + rows_per_tile - 1) / rows_per_tile;
   for (int nt = 16; nt <= 256; nt *= 2) {
     const int tt = (T + nt - 1) / nt;
     if (tt > 64) continue;
     for (int S = 1; S <= 8 && S <= KB; S *= 2) {
       const double ctas = static_cast<double>(rows) * tt * S;
-      const double rounds = std::ceil(ctas / sm), busy = ctas < sm ? ctas : sm;
+      const int room = cluster_room(S, sm);
+      const double rounds = std::ceil(ctas / room), busy = ctas < room ? ctas : room;
       const double hbm = 16384.0 * busy / tt / 7.0e6, in = (16384.0 + 128.0 * nt) / 1.2e5;
       const double mma = 0.12 + nt * 0.0008;
       const double block = hbm > in ? (hbm > mma ? hbm : mma) : (in > mma ? in : mma);
       const double us = rounds * (std::ceil(KB / S) * block + 3.0 + nt * 0.01 +
                                   (S > 1 ? 0.8 + nt * 0.015 : 0.0));
-      if (us < least) {
-        least = us;
+      const double est = both(us, rounds * (0.12 + nt * 0.0018) * groups * std::min(adapters, nt) / S);
+      if (est < least) {
+        least = est;
         best = Shape{nt, S};
       }
     }
@@ -1401,8 +1502,10 @@ int tile_tokens(int T) {
   return nt;
 }
 
-// Up to here (tokens x r_max) v is a dot product per token and rank.
-constexpr long long kDotMax = 16384;
+// Up to tokens x r_max x (K + 5000) v is a dot product per token and rank: every
+// row of A is read from L2 for each of its tokens, the tensor cores' kernel reads
+// it once a tile and takes 8 us for the least.
+constexpr double kDotMost = 1e8;
 
 // bf16 [rows, cols] with ld elements between rows (a multiple of 8): boxes of
 // box_rows x 64 columns (128-byte swizzle) or x 16 (32-byte swizzle).  Encoded
@@ -1449,14 +1552,21 @@ cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t
   const int tt = (g.T + NT - 1) / NT;
   int rows;                               // blocks of 128 rows
   if (SHRINK) {
-    // how many blocks a tile has is known on the device only: K is split as
-    // far as the tiles leave SMs, and the blocks take what is left
+    // how many blocks a tile has is known on the device only: the widest
+    // clusters that leave not too many SMs without one, and the blocks share
+    // them out between K and themselves
     const long long adapters = g.n_adapters < NT ? g.n_adapters : NT;
     const long long most = (adapters * ((g.r_max + kGroup - 1) / kGroup) + 7) / 8;
-    while (S < 8 && S * 2 <= KB && static_cast<long long>(tt) * S * 2 <= g.sm_count) S *= 2;
-    const long long room = g.sm_count / (static_cast<long long>(tt) * S);
-    rows = static_cast<int>(most < room ? most : room);
-    if (rows < 1) rows = 1;
+    auto rows_at = [&](int c) {
+      return std::min(most, std::max<long long>(1, cluster_room(c, g.sm_count) / (static_cast<long long>(tt) * c)));
+    };
+    long long used = 0;
+    for (int c = 1; c <= 8 && c <= KB; c *= 2) {
+      if (static_cast<long long>(tt) * c > cluster_room(c, g.sm_count)) break;
+      used = std::max(used, tt * c * rows_at(c));
+      if (5 * tt * c * rows_at(c) >= 3 * used) S = c;
+    }
+    rows = static_cast<int>(rows_at(S));
   } else {
     const int per = g.swiglu ? 64 : kRows;
     rows = (p.outs + per - 1) / per;
@@ -1532,11 +1642,11 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   p.status = g.status;
   p.wait_first = g.n_adapters == 0 ? 1 : 0;
   if (g.T == 0) return cudaSuccess;
-  const Shape shape = pick_shape(g.T, g.K, p.outs, g.swiglu ? 64 : kRows, g.sm_count);
+  const Shape shape = pick_shape(g.T, g.K, p.outs, g.swiglu ? 64 : kRows, g.n_adapters, g.r_max, g.sm_count);
   const bool pair = shape.nt == 0;
   if (g.n_adapters > 0) {
     cudaError_t e;
-    if (static_cast<long long>(g.T) * g.r_max <= kDotMax)
+    if (static_cast<double>(g.T) * g.r_max * (g.K + 5000.0) <= kDotMost)
       e = launch_pdl(lora_dot_kernel, dim3(g.r_max / kDotRanks, g.T), dim3(kDotThreads), 0, s, p,
                      static_cast<const __nv_bfloat16*>(g.x), static_cast<const __nv_bfloat16*>(g.a),
                      g.ldx);
