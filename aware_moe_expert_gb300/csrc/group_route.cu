@@ -31,6 +31,7 @@ namespace {
 constexpr int kWarps = 8;            // tokens of a CTA at a time
 constexpr int kMaxWarps = 16;        // the same where that makes more CTAs than SMs
 constexpr int kMaxUnits = 256;
+constexpr int kMostGroups = kMaxUnits / 32;   // groups of a lane where it has several
 constexpr unsigned kAll = 0xffffffffu;
 
 __device__ __forceinline__ float warp_max_f32(float v) {
@@ -239,23 +240,58 @@ __global__ void __launch_bounds__(kMaxWarps * 32) group_route_kernel(const Group
         float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
-          if (i < n && i / p.size == q) {
+          if (i < n && static_cast<unsigned>(i - q * p.size) < static_cast<unsigned>(p.size)) {
             a2 = fmaxf(a2, fminf(a1, c[i]));
             a1 = fmaxf(a1, c[i]);
           }
         if (g + q < p.G) rank[g + q] = a1 + (p.best == 2 && a2 > -INFINITY ? a2 : 0.f);
       }
       __syncwarp();
-      for (int q = 0; q < p.gpl; ++q) {
-        if (g + q >= p.G) break;
-        const float mine = rank[g + q];
-        int ahead = 0;
-        for (int o = 0; o < p.G; ++o) ahead += rank[o] > mine || (rank[o] == mine && o < g + q);
-        if (ahead >= p.kept) {
+      // Groups ahead of each of the lane's: counted in fp16, two at a time.  Larger
+      // as fp16 is larger, so the groups with fewer than `kept` such ahead are
+      // the ones that stay and those that tie with the last of them; the ties, if
+      // there are more than `kept`, are counted exactly.
+      __half* coarse = reinterpret_cast<__half*>(rank + kMaxUnits);
+      for (int o = lane; o < 256; o += 32) coarse[o] = __float2half_rn(o < p.G ? rank[o] : -INFINITY);
+      __syncwarp();
+      __half2 own[kMostGroups], ahead[kMostGroups];
 #pragma unroll
-          for (int i = 0; i < IPL; ++i)
-            if (i / p.size == q) c[i] = -INFINITY;
+      for (int q = 0; q < kMostGroups; ++q) {
+        own[q] = __half2half2(coarse[min(g + q, 255)]);
+        ahead[q] = __float2half2_rn(0.f);
+      }
+      for (int o = 0; o < p.G; o += 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(coarse + o);
+#pragma unroll
+        for (int q = 0; q < kMostGroups; ++q) {
+          if (q >= p.gpl) break;
+          ahead[q] = __hadd2(ahead[q], __hadd2(__hgt2(as_half2(v.x), own[q]), __hgt2(as_half2(v.y), own[q])));
+          ahead[q] = __hadd2(ahead[q], __hadd2(__hgt2(as_half2(v.z), own[q]), __hgt2(as_half2(v.w), own[q])));
         }
+      }
+      int stay = 0;
+      unsigned in = 0u;
+#pragma unroll
+      for (int q = 0; q < kMostGroups; ++q) {
+        const bool mine = q < p.gpl && g + q < p.G &&
+                          __low2float(ahead[q]) + __high2float(ahead[q]) < static_cast<float>(p.kept);
+        stay += __popc(__ballot_sync(kAll, mine));
+        if (mine) in |= 1u << q;
+      }
+      if (stay > p.kept) {
+        for (int q = 0; q < p.gpl; ++q) {
+          if (!(in >> q & 1u)) continue;
+          const float mine = rank[g + q];
+          int before = 0;
+          for (int o = 0; o < p.G; ++o) before += rank[o] > mine || (rank[o] == mine && o < g + q);
+          if (before >= p.kept) in &= ~(1u << q);
+        }
+      }
+      for (int q = 0; q < p.gpl; ++q) {
+        if (in >> q & 1u) continue;
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+          if (static_cast<unsigned>(i - q * p.size) < static_cast<unsigned>(p.size)) c[i] = -INFINITY;
       }
       __syncwarp();
     }
