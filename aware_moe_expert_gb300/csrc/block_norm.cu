@@ -452,7 +452,11 @@ __device__ __forceinline__ int skew_of(const NormParams& p, int first) {
 }
 
 // MAXT threads in groups, and the producer warp.  SELF: groups of one warp fill
-// their own slots (31 of them kept one producer warp too busy).
+// their own slots (31 of them kept one producer warp too busy: 16384 x 256 took 12
+// us, 9 without).
+// Measured: 16384 x 7168 bf16 with both norms 161 us, 5.8 TB/s, 0.86 of a copy;
+// two block sums a row (one between the norms) are what is left of it.  16384 x
+// 4096, fp32 residual and a full gate 143 us.  One row of 7168: 3.3 us.
 template <typename R, typename A, int VEC, int EPT, int MAXT, bool SELF>
 __global__ void __launch_bounds__(MAXT + (SELF ? 0 : 32), 1) block_norm_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -599,6 +603,10 @@ __device__ __forceinline__ void cta_columns(float* buf, float* dst, const Cols<V
   }
 }
 
+// Bound: issue slots (about 570 warp instructions a row and warp at eight elements
+// a thread) under the 16 warps whose registers hold the column sums.  8192 x 2048
+// bf16 with a gate per token: 52 us with the column sums' launch, 3.9 TB/s; 7168
+// columns 255 us: one row at a time, 16 elements a thread, and spills.
 template <typename R, typename A, int VEC, int EPT, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -864,15 +872,18 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaSt
 }
 
 // Elements a thread and threads a CTA: eight elements as long as the threads
-// reach.  The backward pass holds three column sums per element: 512 threads
-// have the registers for it (1024 spilled and took twice as long).
+// reach (16384 x 7168: 161 us, 16 elements in 896 threads 167).  The backward
+// pass holds three column sums per element: 512 threads have the registers for
+// it (8192 x 2048: 52 us, 1024 threads spill and take 86).
 template <typename R, typename A, int VEC>
 cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
   const int n = span(p, VEC);
-  if (back) {
-    if (n <= 8 * 512) return run<R, A, VEC, 8, 512, true>(p, rows_r, rows_a, sm, grid, s);
-    if (n <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
-    return run<R, A, VEC, 40, 512, true>(p, rows_r, rows_a, sm, grid, s);
+  if constexpr (VEC != kSkewed) {
+    if (back) {
+      if (n <= 8 * 512) return run<R, A, VEC, 8, 512, true>(p, rows_r, rows_a, sm, grid, s);
+      if (n <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
+      return run<R, A, VEC, 40, 512, true>(p, rows_r, rows_a, sm, grid, s);
+    }
   }
   if (n <= 8 * 32) return run<R, A, VEC, 8, 512, false, true>(p, rows_r, rows_a, sm, grid, s);
   if (n <= 8 * 992) return run<R, A, VEC, 8, 992, false>(p, rows_r, rows_a, sm, grid, s);
@@ -937,7 +948,12 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
   const bool alike = same(a.residual, a.ld_residual) && same(a.branch, a.ld_branch) &&
                    same(a.out, a.ld_out) && same(a.h, a.ld_h) && same(a.d_out, a.ld_dout) &&
                    same(a.d_h, a.ld_dh) && (!full || (same(a.gate, a.ld_gate) && same(a.d_gate, a.ld_gate)));
-  const int vec = !alike ? kOne : (a.H % 8 == 0 && a.ld_residual % 8 == 0 ? kPieces : kSkewed);
+  // pieces where every row starts at the same place of one (forward, 16384 x 7168:
+  // 161 us, one column at a time 254); if that is not its start, the masks pay
+  // forward only (16384 x 2001: 63 and 70; backward 8192 x 2001: 71 and 70, fp32
+  // 81 and 73)
+  const bool whole = a.H % 8 == 0 && a.ld_residual % 8 == 0;
+  const int vec = !alike || (a.back && !whole) ? kOne : (whole ? kPieces : kSkewed);
   const int sm = a.sm_count < 1 ? 1 : (a.sm_count < kNormMaxCtas ? a.sm_count : kNormMaxCtas);
   p.n_part = 0;
   float* o[3] = {nullptr, nullptr, nullptr};

@@ -11,8 +11,8 @@
 // the adapters extend the reduction axis: of a tile of tokens, the distinct
 // adapters' columns of B, in groups of 16, follow the K columns of W,
 //   y[t, :] = [x_t | v_t in its adapter's columns, 0 elsewhere] [W | B_a0 | B_a1 ...]^T
-// so a tile's adapters cost ceil(sum of their ranks / 64) more k-blocks of the
-// same MMA loop, whatever the tokens' order; no token is sorted or copied.
+// so a group costs two more k-steps of the same MMA loop (v is two operands),
+// whatever the tokens' order; no token is sorted or copied.
 //   few tokens   lora_swap_kernel: W's rows are the MMA's M, the weight stream
 //                is the bound
 //   many tokens  lora_pair_kernel: CTA pairs, the tensor cores are the bound
@@ -283,6 +283,8 @@ struct Block {
 // left out (nothing reads its v).  The chain of dependent loads is two long:
 // the adapter's index, then its rank, scale and rows together (rows past the
 // rank exist in the pool and are not used).
+// Bound: A's rows, read from L2 once per token: 1024 tokens, K 7168, r 16 in about
+// 30 us, 9 TB/s; below 64 tokens the chain, 4-5 us.
 constexpr int kDotThreads = 256;
 constexpr int kDotRanks = 8;
 constexpr int kDotVecs = 2;      // 16-byte vectors of a row a thread has in flight
@@ -361,6 +363,12 @@ __global__ void __launch_bounds__(kDotThreads, 2)
 // 2-3 us, and v with its chain of loads came late.
 // Warps: 0 TMA, 1 MMA, 2-5 v tiles, sums and stores: a thread has the row of
 // its TMEM lane.
+// Bound: W's stream.  K 7168, N 4096: one token 13.6 us without adapters (4.3 TB/s
+// of W; the rest is the way to its first bytes and the exchange of the sums),
+// 14.5 with one of rank 16, v's kernel under it; 64 tokens 15.4 without, 23.0 with
+// 48 adapters of up to rank 32, whose v comes 4-5 us late and whose groups' slots
+// take the rest.  SHRINK, K 7168, r 64, 1024 tokens: 92 us with an adapter each,
+// 33 in requests of 64 (with a projection to 128 outputs behind it).
 template <int NT, bool SHRINK>
 struct SwapCfg {
   static constexpr uint32_t kStage = kTile + NT * 128;
@@ -944,9 +952,13 @@ __global__ void __launch_bounds__(192, 1)
 // 256 tokens x 256 rows of W a tile (tcgen05 cta_group::2: each CTA holds 128
 // token rows and half of the weight rows), persistent, accumulators double
 // buffered in TMEM so that a tile's stores run under the next tile's MMAs.
-// Warps: 0 TMA, 1 MMA (leader), 2-5 stores, 6-9 adapter k-blocks.  The
-// adapters' warps run ahead: a tile's first block is in its slot long before
-// the tile's K columns are done.
+// Warps: 0 TMA, 1 MMA (leader), 2-5 stores, 6-9 adapters' groups.  The last run
+// ahead, and the MMA warp takes a group after each k-block of a tile's second
+// half, so that their slots' round trips lie under the K columns; always there,
+// whatever is ready, so that the order of the sums does not change.
+// Bound: the tensor cores.  16384 tokens, K 7168, N 4096: 608 us without adapters
+// (1.58 PFLOP/s, power capped), 672 with 32 of up to rank 64, of which v is 45.
+// 1024 tokens with an adapter each: 43 and 162, a group's slot 0.5 us.
 constexpr int kPairN = 256;
 constexpr int kPairStages = 5;
 constexpr int kPairSlots = 3;                                     // groups of adapter columns under way
