@@ -603,7 +603,7 @@ __device__ __forceinline__ void cta_columns(float* buf, float* dst, const Cols<V
   }
 }
 
-// Bound: issue slots (about 570 warp instructions a row and warp at eight elements
+// Bound: issue slots (about 510 warp instructions a row and warp at eight elements
 // a thread) under the 16 warps whose registers hold the column sums.  8192 x 2048
 // bf16 with a gate per token: 52 us with the column sums' launch, 3.9 TB/s; 7168
 // columns 255 us: one row at a time, 16 elements a thread, and spills.
