@@ -97,6 +97,13 @@ def test_ranks(T, r):
     _check(_make(T, 256, 192, 6, r, r), _spread(T, 6, r, request=max(1, T // 9)))
 
 
+@pytest.mark.parametrize("N,ldy", [(2048, 0), (2050, 0), (2049, 0), (2049, 2052), (2049, 2056)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_tokens_rows_at_any_alignment(N, ldy, swiglu):
+    N = 2 * N if swiglu else N
+    _check(_make(3001, 512, N, 5, 24, N + ldy), _spread(3001, 5, ldy, request=300), swiglu, ldy=ldy)
+
+
 @pytest.mark.parametrize("T", [64, 256, 700])
 def test_every_token_its_own_adapter(T):
     _check(_make(T, 128, 192, 300, 16, T), (np.arange(T) * 7 % 300).astype(np.int32))
