@@ -1526,10 +1526,15 @@ Shape pick_shape(int T, int K, int outs, int rows_per_tile, int adapters, int r_
   return best;
 }
 
-// Tokens per tile where the factors of A are the rows.
-int tile_tokens(int T) {
+// Tokens per tile where the factors of A are the rows.  A tile's sums take as
+// long as its loads where there are few blocks of eight groups, so half a tile
+// is faster up to three (691 tokens, K 5048, 6 adapters, r 32: 18 and 23 us);
+// with more, x is read again for each (512 tokens, K 7168, 48 adapters: 98 and 85).
+int tile_tokens(int T, int adapters, int r_max) {
+  const int groups = std::min(adapters, 256) * ((r_max + kGroup - 1) / kGroup);
+  const int most = groups <= 3 * 8 ? 128 : 256;
   int nt = 16;
-  while (nt < T && nt < 256) nt *= 2;
+  while (nt < T && nt < most) nt *= 2;
   return nt;
 }
 
@@ -1611,7 +1616,7 @@ cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t
 }
 
 cudaError_t run_shrink(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
-  switch (tile_tokens(g.T)) {
+  switch (tile_tokens(g.T, g.n_adapters, g.r_max)) {
     case 16: return run_swap<16, true>(g, p, 1, s);
     case 32: return run_swap<32, true>(g, p, 1, s);
     case 64: return run_swap<64, true>(g, p, 1, s);
