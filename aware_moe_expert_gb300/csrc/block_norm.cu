@@ -293,10 +293,21 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int tpr, int bar, int t
     if (lane % kLanes == 0) buf[value * 32 + warp] = part;
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
     part = 0.f;
-    const float* from = buf + value * 32 + lane % kLanes;
-    const int left = nw - lane % kLanes;
+    // four warps' sums a load where few lanes share a value, which takes a `red`
+    // that was cleared (backward, 8192 x 2048: 49 us, 51 one at a time; forward,
+    // 16384 x 7168: 155 and 148)
+    const float* from = buf + value * 32;
+    const int l = lane % kLanes;
 #pragma unroll
-    for (int w = 0; w < 32; w += kLanes) part += w < left ? from[w] : 0.f;
+    for (int w = 0; w < 32; w += N == 8 ? 4 * kLanes : kLanes) {
+      if (w >= nw) break;
+      if constexpr (N == 8) {
+        const float4 q = *reinterpret_cast<const float4*>(from + w + 4 * l);
+        part += (q.x + q.y) + (q.z + q.w);
+      } else {
+        part += w < nw - l ? from[w + l] : 0.f;
+      }
+    }
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) part += __shfl_xor_sync(kAll, part, off);
   }
@@ -454,9 +465,9 @@ __device__ __forceinline__ int skew_of(const NormParams& p, int first) {
 // MAXT threads in groups, and the producer warp.  SELF: groups of one warp fill
 // their own slots (31 of them kept one producer warp too busy: 16384 x 256 took 12
 // us, 9 without).
-// Measured: 16384 x 7168 bf16 with both norms 161 us, 5.8 TB/s, 0.86 of a copy;
+// Measured: 16384 x 7168 bf16 with both norms 148 us, 6.4 TB/s, 0.94 of a copy;
 // two block sums a row (one between the norms) are what is left of it.  16384 x
-// 4096, fp32 residual and a full gate 143 us.  One row of 7168: 3.3 us.
+// 4096, fp32 residual and a full gate 143 us (before its sums' last step).  One row of 7168: 3.3 us.
 template <typename R, typename A, int VEC, int EPT, int MAXT, bool SELF>
 __global__ void __launch_bounds__(MAXT + (SELF ? 0 : 32), 1) block_norm_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -605,8 +616,8 @@ __device__ __forceinline__ void cta_columns(float* buf, float* dst, const Cols<V
 
 // Bound: issue slots (about 510 warp instructions a row and warp at eight elements
 // a thread) under the 16 warps whose registers hold the column sums.  8192 x 2048
-// bf16 with a gate per token: 52 us with the column sums' launch, 3.9 TB/s; 7168
-// columns 255 us: one row at a time, 16 elements a thread, and spills.
+// bf16 with a gate per token: 50 us with the column sums' launch, 4.0 TB/s; 7168
+// columns 245 us: one row at a time, 16 elements a thread, and spills.
 template <typename R, typename A, int VEC, int EPT, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -619,6 +630,9 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_backward_kernel(const Norm
   const Ring<R, A, VEC> ring(&p, smem, bars, group);
   const int skew = skew_of<VEC>(p, first);
   Filler<R, A, VEC> filler(p, skew, first, step, tid);
+  // group_sum reads the sums of warps that do not exist
+  for (int i = threadIdx.x; i < p.groups * 2 * kSumFloats; i += blockDim.x)
+    reinterpret_cast<float*>(smem + L.red)[i] = 0.f;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.groups * p.slots; ++i) mbar_init(bars + i, 1);
     fence_barrier_init();
@@ -872,9 +886,9 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaSt
 }
 
 // Elements a thread and threads a CTA: eight elements as long as the threads
-// reach (16384 x 7168: 161 us, 16 elements in 896 threads 167).  The backward
+// reach (16384 x 7168: 148 us, 16 elements in 896 threads 205).  The backward
 // pass holds three column sums per element: 512 threads have the registers for
-// it (8192 x 2048: 52 us, 1024 threads spill and take 86).
+// it (8192 x 2048: 50 us, 1024 threads spill and take 86).
 template <typename R, typename A, int VEC>
 cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
   const int n = span(p, VEC);
@@ -949,8 +963,8 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
                    same(a.out, a.ld_out) && same(a.h, a.ld_h) && same(a.d_out, a.ld_dout) &&
                    same(a.d_h, a.ld_dh) && (!full || (same(a.gate, a.ld_gate) && same(a.d_gate, a.ld_gate)));
   // pieces where every row starts at the same place of one (forward, 16384 x 7168:
-  // 161 us, one column at a time 254); if that is not its start, the masks pay
-  // forward only (16384 x 2001: 63 and 70; backward 8192 x 2001: 71 and 70, fp32
+  // 148 us, one column at a time 252); if that is not its start, the masks pay
+  // forward only (16384 x 2001: 62 and 70; backward 8192 x 2001: 71 and 70, fp32
   // 81 and 73)
   const bool whole = a.H % 8 == 0 && a.ld_residual % 8 == 0;
   const int vec = !alike || (a.back && !whole) ? kOne : (whole ? kPieces : kSkewed);

@@ -1532,7 +1532,7 @@ Shape pick_shape(int T, int K, int outs, int rows_per_tile, int adapters, int r_
 // with more, x is read again for each (512 tokens, K 7168, 48 adapters: 98 and 85).
 int tile_tokens(int T, int adapters, int r_max) {
   const int groups = std::min(adapters, 256) * ((r_max + kGroup - 1) / kGroup);
-  const int most = groups <= 3 * 8 ? 128 : 256;
+  const int most = groups <= 3 * 8 && T <= 128 * 65535 ? 128 : 256;   // 65535: a grid's z
   int nt = 16;
   while (nt < T && nt < most) nt *= 2;
   return nt;
