@@ -13,6 +13,7 @@ synthetic inputs and balances its experts.
 """
 from __future__ import annotations
 
+import ctypes
 from dataclasses import dataclass, replace
 from typing import Optional
 
@@ -47,6 +48,19 @@ class BlockWeights:
     select_bias: torch.Tensor             # fp32 [E_r], moved by balance()
 
 
+def _workspace_bytes(layer: B.LayerDesc) -> int:
+    """Bytes of workspace that do for a step of any number of tokens up to layer.T.
+    A step of fewer tokens can need more than one of layer.T does: it takes other
+    kernels and splits its reductions further."""
+    d, size = layer.c(), B.lib().moe_workspace_size
+    n = 0
+    for d.T in range(layer.T + 1):
+        n = max(n, size(ctypes.byref(d)))
+    if n == 0:
+        raise B.MoeError(2, "moe_workspace_size")
+    return n
+
+
 class MoeBlock:
     def __init__(self, layer: B.LayerDesc, groups: B.GroupRoute, weights: BlockWeights,
                  adapters: Optional[Adapters] = None, *, eps: float = 1e-6,
@@ -70,10 +84,7 @@ class MoeBlock:
         self.sorted_token, self.inv_row = new(T * k, dtype=i32), new(T * k, dtype=i32)
         self.y_perm = new(T * k, H)
         self.status = torch.zeros(1, dtype=i32, device=self.device)
-        n = B.moe_workspace_size(layer)
-        if n == 0:
-            raise B.MoeError(2, "moe_workspace_size")
-        self.workspace = new(n, dtype=torch.uint8)
+        self.workspace = new(_workspace_bytes(layer), dtype=torch.uint8)
         n = max(B.moe_lora_workspace_size(self._lora(T, True)),
                 B.moe_lora_workspace_size(self._lora(T, False)))
         if n == 0:

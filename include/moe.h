@@ -94,7 +94,8 @@ typedef struct {
   uint32_t debug_flags;           /* MOE_DEBUG_* bits, tests only                 */
 } moe_layer_desc;
 
-/* Bytes of workspace every call below needs for this desc (0 on a bad desc). */
+/* Bytes of workspace every call below needs for this desc (0 on a bad desc).  Not
+ * monotonic in T: fewer tokens can need more. */
 size_t moe_workspace_size(const moe_layer_desc* desc);
 
 /* Steps 1-3 of the layer: router logits, per-token top-k_t, gate weights.
