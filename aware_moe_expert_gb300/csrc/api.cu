@@ -1285,6 +1285,25 @@ moe_status moe_block_norm(const moe_norm_desc* desc, const void* residual, const
   return cuda_status(moe::launch_block_norm(a, static_cast<cudaStream_t>(stream)));
 }
 
+// For tests, which need no GPU for it: CTAs, row groups, slots and bytes of shared
+// memory of a call with this desc on a GPU of `sm` SMs.
+int moe_block_norm_plan(const moe_norm_desc* desc, int back, int aligned, int sm, int32_t* plan) {
+  if (desc == nullptr || desc->T < 1 || plan == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  const uintptr_t at = 4096;     // looked at, not read
+  moe::BlockNormArgs a{};
+  MOE_TRY(norm_args(desc, reinterpret_cast<void*>(aligned ? at : at + 4), reinterpret_cast<void*>(at),
+                    desc->gate_kind != MOE_GATE_NONE ? reinterpret_cast<void*>(at) : nullptr, back != 0, &a));
+  a.back = back != 0;
+  a.sm_count = sm;
+  moe::NormPlan n{};
+  MOE_TRY(cuda_status(moe::launch_block_norm(a, nullptr, &n)));
+  plan[0] = n.grid;
+  plan[1] = n.groups;
+  plan[2] = n.slots;
+  plan[3] = static_cast<int32_t>(n.smem);
+  return MOE_OK;
+}
+
 size_t moe_block_norm_workspace_size(const moe_norm_desc* desc) {
   if (validate_norm(desc) != MOE_OK) return 0;
   return align_up(moe::block_norm_part_bytes(desc->T, desc->H, 3));

@@ -35,7 +35,8 @@ namespace moe {
 
 namespace {
 
-constexpr uint32_t kSmemBudget = 200 * 1024;
+constexpr uint32_t kSmemBudget = 200 * 1024;   // row slots
+constexpr uint32_t kSmemMost = 227 * 1024;     // and with the sum buffers and barriers
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -862,22 +863,35 @@ void shape_of(NormParams& p, int vec, int ept, int max_threads, int rows_r, int 
   while (groups > 1 && groups * 2 * p.slot_bytes > kSmemBudget) --groups;
   int slots = static_cast<int>(kSmemBudget / (groups * p.slot_bytes));
   slots = slots > 4 ? 4 : (slots < 1 ? 1 : slots);
+  // the sum buffers count, too: 2 KB a group (138 to 389 columns, fp32, 14 to 16
+  // groups); a third or fourth slot goes before a group does
+  while (norm_smem(p.slot_bytes, slots, groups).total > kSmemMost) {
+    if (slots > 2 || groups == 1)
+      --slots;
+    else
+      --groups;
+  }
   p.groups = groups;
   p.slots = slots;
 }
 
 template <typename R, typename A, int VEC, int EPT, int MAXT, bool BACK, bool SELF = false>
-cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
+cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, NormPlan* plan, cudaStream_t s) {
   static bool done[64] = {false};
   shape_of(p, VEC, EPT, MAXT, rows_r, rows_a, sizeof(R), sizeof(A), sm);
   // a group's rows are grid * groups apart: a multiple of eight if there are several
   const int want = (p.T + p.groups - 1) / p.groups, most = sm >= 8 ? sm / 8 * 8 : sm;
-  *grid = want <= sm ? want : most;
+  plan->grid = want <= sm ? want : most;
   if (want > sm && most % 8 != 0 && VEC == kSkewed) return cudaErrorInvalidConfiguration;
-  const uint32_t smem = norm_smem(p.slot_bytes, p.slots, p.groups).total;
+  plan->groups = p.groups;
+  plan->slots = p.slots;
+  plan->smem = norm_smem(p.slot_bytes, p.slots, p.groups).total;
+  if (plan->only) return cudaSuccess;
   auto go = [&](auto k) {
-    const cudaError_t e = set_smem_once(k, 227 * 1024, done);
-    return e != cudaSuccess ? e : launch_pdl(k, dim3(*grid), dim3(p.tpr * p.groups + (BACK || SELF ? 0 : 32)), smem, s, p);
+    const cudaError_t e = set_smem_once(k, static_cast<int>(kSmemMost), done);
+    return e != cudaSuccess ? e
+                            : launch_pdl(k, dim3(plan->grid), dim3(p.tpr * p.groups + (BACK || SELF ? 0 : 32)),
+                                         plan->smem, s, p);
   };
   if constexpr (BACK)
     return go(block_norm_backward_kernel<R, A, VEC, EPT, MAXT>);
@@ -890,26 +904,26 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, int* grid, cudaSt
 // pass holds three column sums per element: 512 threads have the registers for
 // it (8192 x 2048: 50 us, 1024 threads spill and take 86).
 template <typename R, typename A, int VEC>
-cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, int* grid, cudaStream_t s) {
+cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, NormPlan* plan, cudaStream_t s) {
   const int n = span(p, VEC);
   if constexpr (VEC != kSkewed) {
     if (back) {
-      if (n <= 8 * 512) return run<R, A, VEC, 8, 512, true>(p, rows_r, rows_a, sm, grid, s);
-      if (n <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, grid, s);
-      return run<R, A, VEC, 40, 512, true>(p, rows_r, rows_a, sm, grid, s);
+      if (n <= 8 * 512) return run<R, A, VEC, 8, 512, true>(p, rows_r, rows_a, sm, plan, s);
+      if (n <= 16 * 512) return run<R, A, VEC, 16, 512, true>(p, rows_r, rows_a, sm, plan, s);
+      return run<R, A, VEC, 40, 512, true>(p, rows_r, rows_a, sm, plan, s);
     }
   }
-  if (n <= 8 * 32) return run<R, A, VEC, 8, 512, false, true>(p, rows_r, rows_a, sm, grid, s);
-  if (n <= 8 * 992) return run<R, A, VEC, 8, 992, false>(p, rows_r, rows_a, sm, grid, s);
-  return run<R, A, VEC, 24, 736, false>(p, rows_r, rows_a, sm, grid, s);
+  if (n <= 8 * 32) return run<R, A, VEC, 8, 512, false, true>(p, rows_r, rows_a, sm, plan, s);
+  if (n <= 8 * 992) return run<R, A, VEC, 8, 992, false>(p, rows_r, rows_a, sm, plan, s);
+  return run<R, A, VEC, 24, 736, false>(p, rows_r, rows_a, sm, plan, s);
 }
 
 template <typename R, typename A>
-cudaError_t pick_vec(NormParams& p, bool back, int vec, int rows_r, int rows_a, int sm, int* grid,
-                     cudaStream_t s) {
-  if (vec == kPieces) return pick<R, A, kPieces>(p, back, rows_r, rows_a, sm, grid, s);
-  if (vec == kSkewed) return pick<R, A, kSkewed>(p, back, rows_r, rows_a, sm, grid, s);
-  return pick<R, A, kOne>(p, back, rows_r, rows_a, sm, grid, s);
+cudaError_t pick_vec(NormParams& p, bool back, int vec, int rows_r, int rows_a, int sm,
+                     NormPlan* plan, cudaStream_t s) {
+  if (vec == kPieces) return pick<R, A, kPieces>(p, back, rows_r, rows_a, sm, plan, s);
+  if (vec == kSkewed) return pick<R, A, kSkewed>(p, back, rows_r, rows_a, sm, plan, s);
+  return pick<R, A, kOne>(p, back, rows_r, rows_a, sm, plan, s);
 }
 
 }  // namespace
@@ -925,7 +939,7 @@ size_t block_norm_part_bytes(int T, int H, int n_part) {
   return ctas * n_part * static_cast<size_t>(H) * 4;
 }
 
-cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
+cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s, NormPlan* plan_only) {
   NormParams p{};
   p.T = a.T;
   p.H = a.H;
@@ -985,18 +999,20 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
     return cudaSuccess;
   }
   const int rows_r = a.back ? 2 : 1, rows_a = (a.back ? 2 : 1) + (full ? 1 : 0);
-  int grid = 1;
+  NormPlan own{};
+  NormPlan* plan = plan_only != nullptr ? plan_only : &own;
+  plan->only = plan_only != nullptr;
   cudaError_t e;
   if (a.residual_f32 && a.act_f32)
-    e = pick_vec<float, float>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
+    e = pick_vec<float, float>(p, a.back, vec, rows_r, rows_a, sm, plan, s);
   else if (a.residual_f32)
-    e = pick_vec<float, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
+    e = pick_vec<float, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, plan, s);
   else
-    e = pick_vec<__nv_bfloat16, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, &grid, s);
-  if (e != cudaSuccess || p.n_part == 0) return e;
+    e = pick_vec<__nv_bfloat16, __nv_bfloat16>(p, a.back, vec, rows_r, rows_a, sm, plan, s);
+  if (e != cudaSuccess || p.n_part == 0 || plan->only) return e;
   const long long width = static_cast<long long>(p.n_part) * a.H;
   return launch_pdl(column_sum_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(32 * kSlices), 0,
-                    s, static_cast<const float*>(a.part), grid, p.n_part, a.H, o[0], o[1], o[2]);
+                    s, static_cast<const float*>(a.part), plan->grid, p.n_part, a.H, o[0], o[1], o[2]);
 }
 
 }  // namespace moe

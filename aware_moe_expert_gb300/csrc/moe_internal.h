@@ -281,7 +281,13 @@ struct BlockNormArgs {
 // Whether one row of every tensor fits the shared memory of a CTA together.
 bool block_norm_fits(int H, bool residual_f32, bool act_f32, bool full_gate, bool back);
 size_t block_norm_part_bytes(int T, int H, int n_part);
-cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s);
+// How a call is launched; with `only`, the plan alone.
+struct NormPlan {
+  int grid, groups, slots;     // CTAs, rows of a CTA at a time, row slots of each
+  uint32_t smem;               // dynamic shared memory of a CTA
+  bool only;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s, NormPlan* plan_only = nullptr);
 
 // ---- lora.cu: a shared projection with an adapter per request
 struct LoraArgs {
