@@ -13,6 +13,7 @@ synthetic inputs and balances its experts.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass, replace
 from typing import Optional
@@ -61,6 +62,15 @@ def _workspace_bytes(layer: B.LayerDesc) -> int:
     return n
 
 
+def _on(stream):
+    """The given stream (a torch stream or a handle) as the current one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
 class MoeBlock:
     def __init__(self, layer: B.LayerDesc, groups: B.GroupRoute, weights: BlockWeights,
                  adapters: Optional[Adapters] = None, *, eps: float = 1e-6,
@@ -98,53 +108,60 @@ class MoeBlock:
             return B.LoraDesc(T=T, K=H, N=2 * self.shared, n_adapters=n, r_max=r, swiglu=True)
         return B.LoraDesc(T=T, K=self.shared, N=H, n_adapters=n, r_max=r)
 
-    def _norm(self, residual, branch, w_post, w_pre, residual_out, normed, stream):
+    def _norm(self, residual, branch, w_post, w_pre, residual_out, normed):
         T, H = branch.shape
         d = B.BlockNormDesc(T=T, H=H, residual_dtype=residual.dtype, eps=self.eps,
                             residual_scale=self.residual_scale, branch_scale=self.branch_scale,
                             w_post=w_post, w_pre=w_pre, dev_status=self.status)
-        B.check(B.moe_block_norm(d, residual, branch, None, residual_out, normed, stream),
-                "moe_block_norm")
+        B.check(B.moe_block_norm(d, residual, branch, None, residual_out, normed), "moe_block_norm")
 
     def forward(self, residual, attn, k_per_token, adapter_idx=None, stream=None):
         """residual (bf16 or fp32) and attn (bf16) [T, H], budgets int32 [T],
         adapter_idx int32 [T] (-1: none).  Updates residual in place and returns
-        the next block's normed input; self.load has the assignments per unit."""
+        the next block's normed input; self.load has the assignments per unit.
+        All of it is work of `stream` (default: the current one), on which the
+        inputs have to be ready; the result belongs to that stream."""
+        with _on(stream):
+            return self._forward(residual, attn, k_per_token, adapter_idx)
+
+    def _forward(self, residual, attn, k_per_token, adapter_idx):
         T, H = attn.shape
         if T > self.layer.T:
             raise ValueError(f"{T} tokens, and buffers for {self.layer.T}")
         w, a, st, ws = self.weights, self.adapters, self.status, self.workspace
         d = replace(self.layer, T=T)
         h = self.h[:T]
-        self._norm(residual, attn, w.attn_post_norm, w.pre_norm, residual, h, stream)
+        self._norm(residual, attn, w.attn_post_norm, w.pre_norm, residual, h)
         idx, tw, k_used = self.topk_idx[:T], self.topk_w[:T], self.k_used[:T]
         B.check(B.moe_route_groups(d, self.groups, h, w.router, None, k_per_token,
-                                   self.logits[:T], idx, tw, k_used, self.load, st, ws, stream),
+                                   self.logits[:T], idx, tw, k_used, self.load, st, ws),
                 "moe_route_groups")
         B.check(B.moe_permute(d, idx, k_used, self.counts, self.offsets, self.sorted_token,
-                              self.inv_row, st, ws, stream), "moe_permute")
+                              self.inv_row, st, ws), "moe_permute")
         B.check(B.moe_grouped_ffn(d, h, self.sorted_token, self.offsets, w.w_gate_up, w.w_down,
-                                  self.y_perm, st, ws, stream), "moe_grouped_ffn")
+                                  self.y_perm, st, ws), "moe_grouped_ffn")
         act, y_shared = self.act[:T], self.y_shared[:T]
         pool = lambda x, y: (x, y, a.ranks, a.scales, adapter_idx)  # noqa: E731
         none = (None,) * 5
         B.check(B.moe_lora_project(self._lora(T, True), h, w.shared_gate_up,
                                    *(none if a is None else pool(a.gate_up_a, a.gate_up_b)), act,
-                                   st, self.lora_workspace, stream), "moe_lora_project")
+                                   st, self.lora_workspace), "moe_lora_project")
         B.check(B.moe_lora_project(self._lora(T, False), act, w.shared_down,
                                    *(none if a is None else pool(a.down_a, a.down_b)), y_shared,
-                                   st, self.lora_workspace, stream), "moe_lora_project")
+                                   st, self.lora_workspace), "moe_lora_project")
         y = self.y[:T]
-        B.check(B.moe_combine(d, self.y_perm, y_shared, self.inv_row, tw, k_used, y, st, stream),
+        B.check(B.moe_combine(d, self.y_perm, y_shared, self.inv_row, tw, k_used, y, st),
                 "moe_combine")
         out = torch.empty_like(y)
-        self._norm(residual, y, w.ffn_post_norm, w.next_pre_norm, residual, out, stream)
+        self._norm(residual, y, w.ffn_post_norm, w.next_pre_norm, residual, out)
         return out
 
-    def balance(self, rate: float = 0.001):
-        """Moves the selection bias towards equal loads by `rate` a step."""
-        load = self.load.float()
-        self.weights.select_bias += rate * torch.sign(load.mean() - load)
+    def balance(self, rate: float = 0.001, stream=None):
+        """Moves the selection bias towards equal loads by `rate` a step, on the
+        stream that the steps run on (default: the current one)."""
+        with _on(stream):
+            load = self.load.float()
+            self.weights.select_bias += rate * torch.sign(load.mean() - load)
 
     def device_status(self, stream=None) -> int:
         return B.moe_get_device_status(self.status, stream)

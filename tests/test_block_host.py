@@ -42,3 +42,64 @@ def test_the_workspace_does_for_a_step_of_any_size(T, H, experts, I, k):  # noqa
         assert B.moe_workspace_size(d) <= block.workspace.numel(), t
         for first in (True, False):
             assert B.moe_lora_workspace_size(block._lora(t, first)) <= block.lora_workspace.numel()
+
+
+class _Calls:
+    """Records the library's calls, and which stream is current, in their place."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.calls = "current", []
+        me = self
+
+        class On:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                self.before, me.current = me.current, self.stream
+
+            def __exit__(self, *_):
+                me.current = self.before
+
+        monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
+        for name in ("moe_block_norm", "moe_route_groups", "moe_permute", "moe_grouped_ffn",
+                     "moe_lora_project", "moe_combine"):
+            monkeypatch.setattr(B, name, self._fake(name))
+        for name in ("empty_like", "sign"):
+            monkeypatch.setattr(torch, name, self._through(name, getattr(torch, name)))
+
+    def _on(self, stream):
+        return self.current if stream is None else stream
+
+    def _fake(self, name):
+        def call(*args):
+            params = getattr(B.lib(), name).argtypes
+            stream = args[-1] if len(args) == len(params) else None
+            self.calls.append((name, args, self._on(stream)))
+            return 0
+        return call
+
+    def _through(self, name, real):
+        def call(*args, **kw):
+            self.calls.append((name, args, self.current))
+            return real(*args, **kw)
+        return call
+
+
+def _step(T, H=256):
+    return (torch.zeros(T, H), torch.zeros(T, H, dtype=torch.bfloat16),
+            torch.ones(T, dtype=torch.int32), torch.zeros(T, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("stream,current", [(None, "current"), ("side", "side"),
+                                            (4096, ("external", 4096))])
+def test_a_step_and_its_balancing_are_work_of_one_stream(monkeypatch, stream, current):
+    block, calls = _block(), _Calls(monkeypatch)
+    block.forward(*_step(20), stream=stream)
+    assert len(calls.calls) == 9         # eight of the library and the result's memory
+    block.balance(0.01, stream=stream)
+    names = [c[0] for c in calls.calls]
+    assert names.count("empty_like") == 1 and names[-1] == "sign"
+    assert [c[2] for c in calls.calls] == [current] * 10
+    assert calls.current == "current"
