@@ -79,8 +79,8 @@ class MoeBlock:
         taken from the weights (the shared expert runs here, with adapters)."""
         self.device = torch.device(device)
         self.layer, self.weights, self.adapters = layer, weights, adapters
-        self.groups = groups
-        self.groups.select_bias = weights.select_bias
+        # this block's bias in a copy: blocks may be built from one GroupRoute
+        self.groups = replace(groups, select_bias=weights.select_bias)
         self.eps, self.residual_scale, self.branch_scale = eps, residual_scale, branch_scale
         T, H, k = layer.T, layer.H, layer.k_max
         self.shared = weights.shared_down.shape[1]

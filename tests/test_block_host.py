@@ -103,3 +103,15 @@ def test_a_step_and_its_balancing_are_work_of_one_stream(monkeypatch, stream, cu
     assert names.count("empty_like") == 1 and names[-1] == "sign"
     assert [c[2] for c in calls.calls] == [current] * 10
     assert calls.current == "current"
+
+
+def test_blocks_of_one_group_route_keep_their_own_bias(monkeypatch):
+    groups = B.GroupRoute(n_groups=8, groups_kept=4, group_best=2)
+    blocks = [_block(groups=groups) for _ in range(2)]
+    assert groups.select_bias is None
+    calls = _Calls(monkeypatch)
+    for block in blocks:
+        block.forward(*_step(5))
+    used = [c[1][1].select_bias for c in calls.calls if c[0] == "moe_route_groups"]
+    assert [b.data_ptr() for b in used] == [b.weights.select_bias.data_ptr() for b in blocks]
+    assert used[0].data_ptr() != used[1].data_ptr()
