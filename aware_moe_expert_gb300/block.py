@@ -49,6 +49,9 @@ class BlockWeights:
     select_bias: torch.Tensor             # fp32 [E_r], moved by balance()
 
 
+MAX_RANK = 128       # of a pool, the largest r_max
+
+
 def _workspace_bytes(layer: B.LayerDesc) -> int:
     """Bytes of workspace that do for a step of any number of tokens up to layer.T.
     A step of fewer tokens can need more than one of layer.T does: it takes other
@@ -95,8 +98,9 @@ class MoeBlock:
         self.y_perm = new(T * k, H)
         self.status = torch.zeros(1, dtype=i32, device=self.device)
         self.workspace = new(_workspace_bytes(layer), dtype=torch.uint8)
-        n = max(B.moe_lora_workspace_size(self._lora(T, True)),
-                B.moe_lora_workspace_size(self._lora(T, False)))
+        # for a pool of any rank: self.adapters may be replaced between steps
+        n = min(B.moe_lora_workspace_size(replace(self._lora(T, first), r_max=MAX_RANK))
+                for first in (True, False))
         if n == 0:
             raise B.MoeError(2, "moe_lora_workspace_size")
         self.lora_workspace = new(n, dtype=torch.uint8)

@@ -115,3 +115,12 @@ def test_blocks_of_one_group_route_keep_their_own_bias(monkeypatch):
     used = [c[1][1].select_bias for c in calls.calls if c[0] == "moe_route_groups"]
     assert [b.data_ptr() for b in used] == [b.weights.select_bias.data_ptr() for b in blocks]
     assert used[0].data_ptr() != used[1].data_ptr()
+
+
+@pytest.mark.parametrize("rank", [24, 128])
+def test_a_pool_of_larger_rank_may_take_the_place_of_another(rank):
+    for block in (_block(rank=16), _block(rank=8)):
+        block.adapters = _block(rank=rank).adapters
+        for first in (True, False):
+            n = B.moe_lora_workspace_size(block._lora(block.layer.T, first))
+            assert 0 < n <= block.lora_workspace.numel()
