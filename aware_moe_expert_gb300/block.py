@@ -133,6 +133,7 @@ class MoeBlock:
         if T > self.layer.T:
             raise ValueError(f"{T} tokens, and buffers for {self.layer.T}")
         w, a, st, ws = self.weights, self.adapters, self.status, self.workspace
+        self.groups.select_bias = w.select_bias      # which may have been replaced
         d = replace(self.layer, T=T)
         h = self.h[:T]
         self._norm(residual, attn, w.attn_post_norm, w.pre_norm, residual, h)

@@ -124,3 +124,12 @@ def test_a_pool_of_larger_rank_may_take_the_place_of_another(rank):
         for first in (True, False):
             n = B.moe_lora_workspace_size(block._lora(block.layer.T, first))
             assert 0 < n <= block.lora_workspace.numel()
+
+
+def test_a_replaced_selection_bias_is_the_one_that_routes(monkeypatch):
+    block = _block()
+    block.weights.select_bias = torch.ones(32)
+    calls = _Calls(monkeypatch)
+    block.forward(*_step(5))
+    used = [c[1][1].select_bias for c in calls.calls if c[0] == "moe_route_groups"]
+    assert used[0].data_ptr() == block.weights.select_bias.data_ptr()
