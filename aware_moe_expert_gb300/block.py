@@ -105,8 +105,8 @@ class MoeBlock:
             raise B.MoeError(2, "moe_lora_workspace_size")
         self.lora_workspace = new(n, dtype=torch.uint8)
 
-    def _lora(self, T: int, first: bool) -> B.LoraDesc:
-        a, H = self.adapters, self.layer.H
+    def _lora(self, T: int, first: bool, pool: bool = True) -> B.LoraDesc:
+        a, H = self.adapters if pool else None, self.layer.H
         n, r = (0, 8) if a is None else a.gate_up_a.shape[:2] if first else a.down_a.shape[:2]
         if first:
             return B.LoraDesc(T=T, K=H, N=2 * self.shared, n_adapters=n, r_max=r, swiglu=True)
@@ -121,7 +121,7 @@ class MoeBlock:
 
     def forward(self, residual, attn, k_per_token, adapter_idx=None, stream=None):
         """residual (bf16 or fp32) and attn (bf16) [T, H], budgets int32 [T],
-        adapter_idx int32 [T] (-1: none).  Updates residual in place and returns
+        adapter_idx int32 [T] (-1: none; without it no token has one).  Updates residual in place and returns
         the next block's normed input; self.load has the assignments per unit.
         All of it is work of `stream` (default: the current one), on which the
         inputs have to be ready; the result belongs to that stream."""
@@ -132,7 +132,8 @@ class MoeBlock:
         T, H = attn.shape
         if T > self.layer.T:
             raise ValueError(f"{T} tokens, and buffers for {self.layer.T}")
-        w, a, st, ws = self.weights, self.adapters, self.status, self.workspace
+        w, st, ws = self.weights, self.status, self.workspace
+        a = None if adapter_idx is None else self.adapters
         self.groups.select_bias = w.select_bias      # which may have been replaced
         d = replace(self.layer, T=T)
         h = self.h[:T]
@@ -148,10 +149,10 @@ class MoeBlock:
         act, y_shared = self.act[:T], self.y_shared[:T]
         pool = lambda x, y: (x, y, a.ranks, a.scales, adapter_idx)  # noqa: E731
         none = (None,) * 5
-        B.check(B.moe_lora_project(self._lora(T, True), h, w.shared_gate_up,
+        B.check(B.moe_lora_project(self._lora(T, True, a is not None), h, w.shared_gate_up,
                                    *(none if a is None else pool(a.gate_up_a, a.gate_up_b)), act,
                                    st, self.lora_workspace), "moe_lora_project")
-        B.check(B.moe_lora_project(self._lora(T, False), act, w.shared_down,
+        B.check(B.moe_lora_project(self._lora(T, False, a is not None), act, w.shared_down,
                                    *(none if a is None else pool(a.down_a, a.down_b)), y_shared,
                                    st, self.lora_workspace), "moe_lora_project")
         y = self.y[:T]

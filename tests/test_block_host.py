@@ -133,3 +133,11 @@ def test_a_replaced_selection_bias_is_the_one_that_routes(monkeypatch):
     block.forward(*_step(5))
     used = [c[1][1].select_bias for c in calls.calls if c[0] == "moe_route_groups"]
     assert used[0].data_ptr() == block.weights.select_bias.data_ptr()
+
+
+def test_a_step_without_adapter_indexes_uses_no_pool(monkeypatch):
+    block, calls = _block(), _Calls(monkeypatch)
+    block.forward(*_step(5)[:3])
+    used = [c[1] for c in calls.calls if c[0] == "moe_lora_project"]
+    assert [a[0].n_adapters for a in used] == [0, 0]
+    assert all(x is None for a in used for x in a[3:8])

@@ -56,3 +56,11 @@ def test_a_step_of_fewer_tokens_that_needs_more_workspace():
     b = K.synthetic(T=341, seed=13)[0].forward(residual[:341].clone(), attn[:341], k[:341],
                                                adapter[:341])
     assert block.device_status() == 0 and torch.equal(a, b)
+
+
+def test_a_step_without_adapter_indexes():
+    block, residual, attn, k, _ = K.synthetic(T=40, seed=14)
+    a = block.forward(residual.clone(), attn, k)
+    block.adapters = None
+    b = block.forward(residual.clone(), attn, k)
+    assert block.device_status() == 0 and torch.equal(a, b)
