@@ -74,6 +74,23 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _want(name, t, shape, dtypes, device, strided=False):
+    """The library reads addresses: what is not this tensor is refused here."""
+    ok = (isinstance(t, torch.Tensor) and tuple(t.shape) == tuple(shape) and t.dtype in dtypes
+          and t.device.type == device.type)
+    if ok and strided:      # rows may lie apart
+        ok = t.stride(-1) == 1 and (t.shape[0] < 2 or t.stride(0) >= t.shape[1])
+    elif ok:
+        ok = t.is_contiguous()
+    if not ok:
+        kind = "rows" if strided else "contiguous"
+        names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise ValueError(f"{name}: {kind} {names} {list(shape)} on {device.type} wanted")
+
+
+BF16, F32, I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+
+
 class MoeBlock:
     def __init__(self, layer: B.LayerDesc, groups: B.GroupRoute, weights: BlockWeights,
                  adapters: Optional[Adapters] = None, *, eps: float = 1e-6,
@@ -81,12 +98,19 @@ class MoeBlock:
         """layer.T is the largest number of tokens of a step; layer.I_shared is
         taken from the weights (the shared expert runs here, with adapters)."""
         self.device = torch.device(device)
-        self.layer, self.weights, self.adapters = layer, weights, adapters
+        self.layer, self.weights = layer, weights
         # this block's bias in a copy: blocks may be built from one GroupRoute
         self.groups = replace(groups, select_bias=weights.select_bias)
         self.eps, self.residual_scale, self.branch_scale = eps, residual_scale, branch_scale
         T, H, k = layer.T, layer.H, layer.k_max
         self.shared = weights.shared_down.shape[1]
+        E, I = layer.E_r, layer.I_sub  # noqa: E741
+        for name, shape in dict(attn_post_norm=(H,), pre_norm=(H,), ffn_post_norm=(H,),
+                                next_pre_norm=(H,), router=(E, H), w_gate_up=(E, 2 * I, H),
+                                w_down=(E, H, I), shared_gate_up=(2 * self.shared, H),
+                                shared_down=(H, self.shared)).items():
+            _want(name, getattr(weights, name), shape, BF16, self.device)
+        self.adapters = adapters
         new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=self.device)  # noqa: E731
         i32 = torch.int32
         self.h, self.act, self.y_shared, self.y = new(T, H), new(T, self.shared), new(T, H), new(T, H)
@@ -105,6 +129,22 @@ class MoeBlock:
             raise B.MoeError(2, "moe_lora_workspace_size")
         self.lora_workspace = new(n, dtype=torch.uint8)
 
+    @property
+    def adapters(self) -> Optional[Adapters]:
+        return self._adapters
+
+    @adapters.setter
+    def adapters(self, a: Optional[Adapters]):
+        if a is not None:
+            H, n = self.layer.H, a.ranks.shape[0]
+            r, r2 = a.gate_up_a.shape[1], a.down_a.shape[1]
+            for name, shape in dict(gate_up_a=(n, r, H), gate_up_b=(n, 2 * self.shared, r),
+                                    down_a=(n, r2, self.shared), down_b=(n, H, r2)).items():
+                _want(name, getattr(a, name), shape, BF16, self.device)
+            _want("ranks", a.ranks, (n,), I32, self.device)
+            _want("scales", a.scales, (n,), F32, self.device)
+        self._adapters = a
+
     def _lora(self, T: int, first: bool, pool: bool = True) -> B.LoraDesc:
         a, H = self.adapters if pool else None, self.layer.H
         n, r = (0, 8) if a is None else a.gate_up_a.shape[:2] if first else a.down_a.shape[:2]
@@ -114,13 +154,15 @@ class MoeBlock:
 
     def _norm(self, residual, branch, w_post, w_pre, residual_out, normed):
         T, H = branch.shape
+        ld, ld_branch = (residual.stride(0), branch.stride(0)) if T > 1 else (0, 0)
         d = B.BlockNormDesc(T=T, H=H, residual_dtype=residual.dtype, eps=self.eps,
+                            ld_residual=ld, ld_out=ld, ld_branch=ld_branch,
                             residual_scale=self.residual_scale, branch_scale=self.branch_scale,
                             w_post=w_post, w_pre=w_pre, dev_status=self.status)
         B.check(B.moe_block_norm(d, residual, branch, None, residual_out, normed), "moe_block_norm")
 
     def forward(self, residual, attn, k_per_token, adapter_idx=None, stream=None):
-        """residual (bf16 or fp32) and attn (bf16) [T, H], budgets int32 [T],
+        """residual (bf16 or fp32) and attn (bf16) [T, H], rows at any stride, budgets int32 [T],
         adapter_idx int32 [T] (-1: none; without it no token has one).  Updates residual in place and returns
         the next block's normed input; self.load has the assignments per unit.
         All of it is work of `stream` (default: the current one), on which the
@@ -129,9 +171,15 @@ class MoeBlock:
             return self._forward(residual, attn, k_per_token, adapter_idx)
 
     def _forward(self, residual, attn, k_per_token, adapter_idx):
-        T, H = attn.shape
+        T, dev = attn.shape[0], self.device
         if T > self.layer.T:
             raise ValueError(f"{T} tokens, and buffers for {self.layer.T}")
+        _want("attn", attn, (T, self.layer.H), BF16, dev, strided=True)
+        _want("residual", residual, (T, self.layer.H), BF16 + F32, dev, strided=True)
+        _want("k_per_token", k_per_token, (T,), I32, dev)
+        if adapter_idx is not None:
+            _want("adapter_idx", adapter_idx, (T,), I32, dev)
+        _want("select_bias", self.weights.select_bias, (self.layer.E_r,), F32, dev)
         w, st, ws = self.weights, self.status, self.workspace
         a = None if adapter_idx is None else self.adapters
         self.groups.select_bias = w.select_bias      # which may have been replaced

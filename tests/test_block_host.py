@@ -141,3 +141,45 @@ def test_a_step_without_adapter_indexes_uses_no_pool(monkeypatch):
     used = [c[1] for c in calls.calls if c[0] == "moe_lora_project"]
     assert [a[0].n_adapters for a in used] == [0, 0]
     assert all(x is None for a in used for x in a[3:8])
+
+
+@pytest.mark.parametrize("bad", [
+    dict(attn=torch.zeros(20, 256)), dict(attn=torch.zeros(20, 128, dtype=torch.bfloat16)),
+    dict(attn=torch.zeros(256, 20, dtype=torch.bfloat16).t()),
+    dict(attn=torch.zeros(1, 256, dtype=torch.bfloat16).expand(20, 256)),
+    dict(attn=torch.zeros(65, 256, dtype=torch.bfloat16)),
+    dict(residual=torch.zeros(20, 256, dtype=torch.float16)), dict(residual=torch.zeros(19, 256)),
+    dict(residual=torch.zeros(20, 512)[:, ::2]),
+    dict(k=torch.ones(20, dtype=torch.int64)), dict(k=torch.ones(19, dtype=torch.int32)),
+    dict(k=torch.ones(40, dtype=torch.int32)[::2]),
+    dict(adapter=torch.ones(20, dtype=torch.int64)), dict(adapter=torch.ones(4, dtype=torch.int32))])
+def test_a_step_refuses_what_the_library_would_misread(monkeypatch, bad):
+    block, calls = _block(), _Calls(monkeypatch)
+    step = dict(zip(("residual", "attn", "k", "adapter"), _step(20)))
+    step.update(bad)
+    with pytest.raises(ValueError):
+        block.forward(*step.values())
+    assert not calls.calls
+
+
+def test_rows_at_a_stride_are_handed_on_with_it(monkeypatch):
+    block, calls = _block(), _Calls(monkeypatch)
+    _, _, k, adapter = _step(20)
+    block.forward(torch.zeros(20, 300)[:, :256], torch.zeros(20, 264, dtype=torch.bfloat16)[:, :256],
+                  k, adapter)
+    first, last = [c[1][0] for c in calls.calls if c[0] == "moe_block_norm"]
+    assert (first.ld_residual, first.ld_out, first.ld_branch) == (300, 300, 264)
+    assert (last.ld_residual, last.ld_out, last.ld_branch) == (300, 300, 256)
+
+
+def test_weights_and_pools_of_another_shape_are_refused():
+    block = _block()
+    for other in (_block(n_adapters=5), _block(shared=128)):
+        pool = dataclasses.replace(block.adapters, down_a=other.adapters.down_a)
+        with pytest.raises(ValueError):
+            block.adapters = pool
+    with pytest.raises(ValueError):
+        block.adapters = dataclasses.replace(block.adapters, ranks=block.adapters.ranks.long())
+    w = dataclasses.replace(block.weights, w_down=block.weights.w_down.transpose(1, 2))
+    with pytest.raises(ValueError):
+        K.MoeBlock(block.layer, B.GroupRoute(), w, device="cpu")

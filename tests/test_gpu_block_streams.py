@@ -64,3 +64,19 @@ def test_a_step_without_adapter_indexes():
     block.adapters = None
     b = block.forward(residual.clone(), attn, k)
     assert block.device_status() == 0 and torch.equal(a, b)
+
+
+def test_rows_at_a_stride_and_no_tokens():
+    block, residual, attn, k, adapter = K.synthetic(T=40, seed=15)
+    want_r = residual.clone()
+    want = block.forward(want_r, attn, k, adapter)
+    wide = torch.full((40, 300), 7.0, device="cuda")
+    wide[:, :256] = residual
+    apart = torch.zeros(40, 264, device="cuda", dtype=torch.bfloat16)
+    apart[:, :256] = attn
+    got = block.forward(wide[:, :256], apart[:, :256], k, adapter)
+    # another order of a row's sums: the layer's tolerance
+    assert (got.float() - want.float()).abs().max() <= 1e-2 + 1e-2 * want.float().abs().max()
+    assert torch.allclose(wide[:, :256], want_r, rtol=1e-2, atol=1e-2) and (wide[:, 256:] == 7).all()
+    assert block.forward(residual[:0], attn[:0], k[:0], adapter[:0]).shape == (0, 256)
+    assert (block.load == 0).all() and block.device_status() == 0
