@@ -848,6 +848,7 @@ moe_status norm_args(const moe_norm_desc* d, const void* residual, const void* b
   if (gate != nullptr && d->gate_kind == MOE_GATE_NONE) return MOE_ERR_INVALID_ARGUMENT;
   MOE_TRY(check_norm_ptr(d->w_post, false, d->act_type));
   MOE_TRY(check_norm_ptr(d->w_pre, false, d->act_type));
+  if (d->dev_status != nullptr) MOE_TRY(check_ptrs4({d->dev_status}));
   auto ld = [d](int64_t v) { return static_cast<long long>(v != 0 ? v : d->H); };
   a->T = d->T;
   a->H = d->H;

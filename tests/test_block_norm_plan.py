@@ -55,3 +55,10 @@ def test_every_width_fits_a_cta(lib, res, act, gate, back, sm):
     full, size = gate == "full", {BF16: 2, F32: 4}
     rows, a_row = 2 + 2 * back + full, (1 + back) * size[res] + (1 + back + full) * size[act]
     assert all(a_row * (h + 7) + 47 * rows + 128 > 200 * 1024 for h in refused)
+
+
+def test_a_misaligned_status_word_is_refused(lib):
+    at = 1 << 20         # aligned, not dereferenced
+    d = B.BlockNormDesc(T=4, H=64, w_pre=at, dev_status=at + 2)
+    assert B.moe_block_norm(d, at, at, None, at, at, 0) == 1
+    assert B.moe_block_norm_backward(d, at, at, None, at, at, at, at, None, None, at, at, 0) == 1
