@@ -34,6 +34,12 @@ constexpr int kMaxUnits = 256;
 constexpr int kMostGroups = kMaxUnits / 32;   // groups of a lane where it has several
 constexpr unsigned kAll = 0xffffffffu;
 
+// A token's list of units (score, unit).  Its space also holds the ranks of more
+// than 32 groups, which are read by 16 bytes.
+struct alignas(16) UnitList {
+  float2 v[kMaxUnits];
+};
+
 __device__ __forceinline__ float warp_max_f32(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -114,7 +120,7 @@ struct GroupParams {
 template <int IPL, bool MANY>
 __global__ void __launch_bounds__(kMaxWarps * 32) group_route_kernel(const GroupParams p) {
   __shared__ int32_t s_load[kMaxUnits];
-  __shared__ float2 s_list[kMaxWarps][kMaxUnits];     // score, unit
+  __shared__ UnitList s_list[kMaxWarps];
   __shared__ int32_t s_sel[kMaxWarps][32];
   __shared__ __align__(16) __half s_head[kMaxWarps][32];
   // With `zeroed` the kernel before this one clears `load`, after it has itself
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) group_route_kernel(const Group
     }
 
     if (MANY && p.kept < p.G) {
-      float* rank = reinterpret_cast<float*>(s_list[warp]);
+      float* rank = reinterpret_cast<float*>(s_list[warp].v);
       for (int q = 0; q < p.gpl; ++q) {
         float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -366,16 +372,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32) group_route_kernel(const Group
     to -= mine_n;
 #pragma unroll
     for (int i = 0; i < IPL; ++i)
-      if (c[i] >= least) s_list[warp][to++] = make_float2(c[i], __int_as_float(u0 + i));
+      if (c[i] >= least) s_list[warp].v[to++] = make_float2(c[i], __int_as_float(u0 + i));
     __syncwarp();
     const int got = min(k, listed);
     for (int i = lane; i < listed; i += 32) {
-      const float2 mine = s_list[warp][i];
+      const float2 mine = s_list[warp].v[i];
       const int unit = __float_as_int(mine.y);
       int ahead = 0;
 #pragma unroll 4
       for (int o = 0; o < listed; ++o) {
-        const float2 other = s_list[warp][o];
+        const float2 other = s_list[warp].v[o];
         ahead += other.x > mine.x || (other.x == mine.x && __float_as_int(other.y) < unit);
       }
       if (ahead < got) s_sel[warp][ahead] = unit;
