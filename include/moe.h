@@ -392,8 +392,8 @@ moe_status moe_layer_forward_cg(const moe_layer_desc* desc, const moe_cg_router*
  * softmax and counts in no group.  NaN and +inf do the same and are reported
  * (MOE_ERR_NONFINITE), and so is a NaN bias; a bias of -inf takes a unit out of
  * the selection.  A token with fewer than k_t units left gets those.
- * Scores are compared in fp32, each within (1 + |L| / 16) 1e-6 of the token's
- * largest.
+ * Scores are compared in fp32: a sigmoid within 1e-6 of its value (0 below 2^-126),
+ * a softmax within 2e-6 of the token's largest.
  */
 typedef struct {
   int32_t n_groups;           /* groups of E_r / n_groups consecutive units; divides E_r  */
