@@ -17,8 +17,8 @@
 //                is the bound
 //   many tokens  lora_pair_kernel: CTA pairs, the tensor cores are the bound
 // v is kept in fp32; as an MMA operand it is two bf16, v = hi + lo, which take
-// the adapter's k-steps twice (one bf16 of v put 2^-9 of the adapter's term into
-// y, beside its own 2^-9, and y lost up to a third of its accuracy).
+// the adapter's k-steps twice (one bf16 of v put up to 2^-8 of the adapter's
+// term into y, beside its own rounding, and y lost up to a third of its accuracy).
 // The zeros only hide what is finite.  So that no token's result depends on
 // another's adapter, a factor that is Inf or NaN counts as 0 and is reported:
 // the pair kernel's warps look at the factors as they place them; the swapped
@@ -453,8 +453,10 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
   return d;
 }
 
-// SiLU to 2^-20 of its value (|g| < 87; beyond, on the left, 0), which bf16 does not
-// see (4392 tokens, K 808, 1472 outputs, one adapter: 40 us; exact division 66).
+// SiLU within (4 + 1.2 |g|) 2^-23 of its value where g > -87 (the bounds of __expf and
+// __fdividef; 2^-16 at the end, 2^-20 from -4 up), 0 where it is below 2^-119.  y is
+// rounded to 2^-8 of its value (4392 tokens, K 808, 1472 outputs, one adapter: 40 us; exact
+// division 66).
 __device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 // SHRINK: what row `row` of a tile of eight groups is, a column of v of one
