@@ -1350,6 +1350,25 @@ size_t moe_lora_workspace_size(const moe_lora_desc* desc) {
   return align_up(moe::lora_workspace_bytes(desc->T, desc->r_max) + 1);
 }
 
+// For tests: the LoraPlan of a call with this desc.
+int moe_lora_plan(const moe_lora_desc* desc, int32_t* plan) {
+  MOE_TRY(validate_lora(desc));
+  if (desc->T < 1 || plan == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  moe::LoraArgs g{};
+  g.T = desc->T;
+  g.K = desc->K;
+  g.N = desc->N;
+  g.n_adapters = desc->n_adapters;
+  g.r_max = desc->r_max;
+  g.swiglu = desc->swiglu;
+  g.sm_count = sm_count() > 0 ? sm_count() : 152;
+  const moe::LoraPlan p = moe::lora_plan(g);
+  plan[0] = p.tile;
+  plan[1] = p.splits;
+  plan[2] = p.v_tile;
+  return MOE_OK;
+}
+
 moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void* w,
                             const void* lora_a, const void* lora_b, const int32_t* ranks,
                             const float* scales, const int32_t* adapter_idx, void* y,

@@ -1617,8 +1617,8 @@ cudaError_t run_swap(const LoraArgs& g, const LoraParams& p, int S, cudaStream_t
   return launch_cluster(kern, dim3(S, rows, tt), 192, static_cast<int>(C::kSmem), S, s, tw, tx, tb, p);
 }
 
-cudaError_t run_shrink(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
-  switch (tile_tokens(g.T, g.n_adapters, g.r_max)) {
+cudaError_t run_shrink(const LoraArgs& g, const LoraParams& p, int tile, cudaStream_t s) {
+  switch (tile) {
     case 16: return run_swap<16, true>(g, p, 1, s);
     case 32: return run_swap<32, true>(g, p, 1, s);
     case 64: return run_swap<64, true>(g, p, 1, s);
@@ -1662,6 +1662,13 @@ cudaError_t run_pair(const LoraArgs& g, const LoraParams& p, cudaStream_t s) {
 
 size_t lora_workspace_bytes(int T, int r_max) { return static_cast<size_t>(T) * r_max * 4; }
 
+LoraPlan lora_plan(const LoraArgs& g) {
+  const Shape shape = pick_shape(g.T, g.K, g.swiglu ? g.N / 2 : g.N, g.swiglu ? 64 : kRows, g.n_adapters, g.r_max,
+                                 g.sm_count);
+  const bool dots = static_cast<double>(g.T) * g.r_max * (g.K + 5000.0) <= kDotMost;
+  return LoraPlan{shape.nt, shape.splits, dots ? 0 : tile_tokens(g.T, g.n_adapters, g.r_max)};
+}
+
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   LoraParams p{};
   p.b = static_cast<const __nv_bfloat16*>(g.b);
@@ -1681,19 +1688,18 @@ cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s) {
   p.status = g.status;
   p.wait_first = g.n_adapters == 0 ? 1 : 0;
   if (g.T == 0) return cudaSuccess;
-  const Shape shape = pick_shape(g.T, g.K, p.outs, g.swiglu ? 64 : kRows, g.n_adapters, g.r_max, g.sm_count);
-  const bool pair = shape.nt == 0;
+  const LoraPlan plan = lora_plan(g);
   if (g.n_adapters > 0) {
     cudaError_t e;
-    if (static_cast<double>(g.T) * g.r_max * (g.K + 5000.0) <= kDotMost)
+    if (plan.v_tile == 0)
       e = launch_pdl(lora_dot_kernel, dim3(g.r_max / kDotRanks, g.T), dim3(kDotThreads), 0, s, p,
                      static_cast<const __nv_bfloat16*>(g.x), static_cast<const __nv_bfloat16*>(g.a),
                      g.ldx);
     else
-      e = run_shrink(g, p, s);
+      e = run_shrink(g, p, plan.v_tile, s);
     if (e != cudaSuccess) return e;
   }
-  if (!pair) return run_project(g, p, shape, s);
+  if (plan.tile != 0) return run_project(g, p, Shape{plan.tile, plan.splits}, s);
   const uintptr_t at = reinterpret_cast<uintptr_t>(g.y);
   p.vec_y = (at & 15u) == 0 && g.ldy % 8 == 0 ? 16 : ((at & 3u) == 0 && g.ldy % 2 == 0 ? 4 : 2);
   return run_pair(g, p, s);

@@ -305,6 +305,12 @@ struct LoraArgs {
   int32_t* status;
   int sm_count;
 };
+// The kernels of a call: tokens of a tile of the projection (0: CTA pairs), the CTAs
+// that split its K, and tokens of a tile of v (0: dot products).
+struct LoraPlan {
+  int tile, splits, v_tile;
+};
+LoraPlan lora_plan(const LoraArgs& g);
 size_t lora_workspace_bytes(int T, int r_max);
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s);
 
