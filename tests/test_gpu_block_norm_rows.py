@@ -59,7 +59,7 @@ def _off_the_grid(monkeypatch, names=("y",)):
 # pieces, pieces that begin before the row, one column at a time; one slot and several
 FORWARD = [
     (20000, 64, BF16, BF16, "full"), (20000, 101, BF16, BF16, "channel"), (17000, 256, F32, BF16, "none"),
-    (16000, 250, F32, F32, "token"), (9000, 512, BF16, BF16, "full"), (5000, 1001, F32, BF16, "channel"),
+    (16000, 250, F32, F32, "token"), (14000, 512, BF16, BF16, "full"), (5000, 1001, F32, BF16, "channel"),
     (4000, 2048, F32, F32, "full"), (3000, 2001, BF16, BF16, "none"), (1000, 7168, BF16, BF16, "token"),
     (1000, 7929, BF16, BF16, "full"), (900, 8192, BF16, BF16, "full"), (700, 8193, F32, BF16, "channel"),
     (700, 12288, F32, F32, "none"), (600, 16384, F32, F32, "channel"), (600, 16383, F32, F32, "none"),
