@@ -567,6 +567,20 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+bool encode_tmap(CUtensorMap* m, const void* base, int elem, long long rows, int cols, long long ld, int box_rows,
+                 int box_cols) {
+  auto fn = encode_fn();
+  if (fn == nullptr || rows <= 0) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(elem)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_cols * elem == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Encoded tensor maps, keyed by everything that goes into them, so that a
 // call on tensors seen before skips the encoding (host time of the small
 // decode calls); host memory only.  64 sets of 4 ways: a key goes to the set
@@ -637,44 +651,22 @@ void tmap_store(const TmapKey& k, const CUtensorMap& m) {
 }
 }  // namespace
 
-// bf16 [rows, cols] row-major, box = 64 columns x box_rows rows, 128-B swizzle.
-bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
-  const TmapKey key{base, rows, cols, box_rows, 2};
-  if (rows > 0 && tmap_lookup(key, m)) return true;
-  auto fn = encode_fn();
-  if (fn == nullptr || rows <= 0) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return false;
+static bool make_tmap(CUtensorMap* m, const TmapKey& key, int box_cols) {
+  if (key.rows > 0 && tmap_lookup(key, m)) return true;
+  if (!encode_tmap(m, key.base, key.elem, key.rows, key.cols, key.cols, key.box_rows, box_cols)) return false;
   tmap_store(key, *m);
   return true;
 }
 
+// bf16 [rows, cols] row-major, box = 64 columns x box_rows rows, 128-B swizzle.
+bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
+  return make_tmap(m, TmapKey{base, rows, cols, box_rows, 2}, 64);
+}
+
 // fp32 [rows, cols] row-major, boxes of 32 columns (128 bytes) x box_rows.
 bool make_tmap_f32(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {
-  const TmapKey key{base, rows, cols, box_rows, 4};
-  if (rows > 0 && tmap_lookup(key, m)) return true;
-  auto fn = encode_fn();
-  if (fn == nullptr || rows <= 0 || cols % 32 != 0 ||
-      (reinterpret_cast<uintptr_t>(base) & 15u) != 0)
-    return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 4};
-  cuuint32_t box[2] = {32u, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return false;
-  tmap_store(key, *m);
-  return true;
+  if (cols % 32 != 0 || (reinterpret_cast<uintptr_t>(base) & 15u) != 0) return false;
+  return make_tmap(m, TmapKey{base, rows, cols, box_rows, 4}, 32);
 }
 
 bool gemm_supports_f32_router(int E_r) { return E_r == 64 || E_r == 128 || E_r == 256; }

@@ -24,8 +24,6 @@
 // the pair kernel's warps look at the factors as they place them; the swapped
 // kernel, which lets the TMA place them, keeps the adapters' sums apart and
 // computes a tile's again with looked-over factors if one is not finite.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -1545,29 +1543,10 @@ int tile_tokens(int T, int adapters, int r_max) {
 // it once a tile and takes 8 us for the least.
 constexpr double kDotMost = 1e8;
 
-// bf16 [rows, cols] with ld elements between rows (a multiple of 8): boxes of
-// box_rows x 64 columns (128-byte swizzle) or x 16 (32-byte swizzle).  Encoded
-// anew on every call: x, y and their strides are the caller's.
-bool encode_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, long long ld,
-                      int box_rows, int box_cols = 64) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                                           cudaEnableDefault, &q);
-    return e == cudaSuccess && q == cudaDriverEntryPointSuccess
-               ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
-               : nullptr;
-  }();
-  if (fn == nullptr || rows <= 0) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_cols == kGroup ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// bf16, encoded anew on every call: x, y and their strides are the caller's.
+bool encode_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, long long ld, int box_rows,
+                      int box_cols = 64) {
+  return encode_tmap(m, base, 2, rows, cols, ld, box_rows, box_cols);
 }
 
 template <int NT, bool SHRINK>

@@ -37,8 +37,14 @@ __device__ __forceinline__ void pdl_wait_and_trigger() {
 }
 
 // Host: launch with programmatic stream serialization, so the launch of this
-// grid overlaps the tail of the previous one (every kernel here calls
-// pdl_wait_and_trigger() before touching global memory written upstream).
+// grid overlaps the tail of the previous one.  A kernel calls
+// pdl_wait_and_trigger() before touching global memory written upstream, or runs
+// right behind a launch of the same call whose threads all wait before they
+// trigger: then everything before that launch is complete, and the kernel waits
+// only for what that launch writes (group_route_kernel behind zero_load_kernel,
+// the projections of lora.cu behind the kernel that computes v).  Either way all
+// of a kernel's CTAs have waited by the time it completes, so that one kernel's
+// completion implies every earlier one's.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t s, Args&&... args) {

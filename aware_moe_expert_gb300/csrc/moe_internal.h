@@ -314,6 +314,12 @@ LoraPlan lora_plan(const LoraArgs& g);
 size_t lora_workspace_bytes(int T, int r_max);
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s);
 
+// Tensor map of a row-major [rows, cols] array of bf16 (elem 2) or fp32 (4) with ld
+// elements between rows: boxes of box_rows x box_cols, 32 or 128 bytes wide, swizzled
+// over as many.  Encodes at every call; make_tmap_bf16 keeps maps it has made.
+bool encode_tmap(CUtensorMap* m, const void* base, int elem, long long rows, int cols, long long ld, int box_rows,
+                 int box_cols);
+
 // bf16 [rows, cols] row-major tensor map: box of 64 columns x box_rows rows,
 // 128-byte swizzle, zero fill out of bounds.
 bool make_tmap_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);
