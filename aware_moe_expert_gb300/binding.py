@@ -232,6 +232,12 @@ def desc_for(wl, T=None, expert_bias=None, w_shared_gate_up=None, w_shared_down=
                      debug_flags=debug_flags)
 
 
+def _c(desc):
+    """The ctypes form of a descriptor, which a caller may have built itself
+    once (desc.c()) to skip the conversion on every call."""
+    return desc if isinstance(desc, ctypes.Structure) else desc.c()
+
+
 def moe_workspace_size(desc: LayerDesc) -> int:
     d = desc.c()
     return int(lib().moe_workspace_size(ctypes.byref(d)))
@@ -239,7 +245,7 @@ def moe_workspace_size(desc: LayerDesc) -> int:
 
 def moe_route(desc, x, router_w, logits_in, k_per_token, logits_out, topk_idx, topk_w,
               dev_status, workspace, stream=None) -> int:
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_route(ctypes.byref(d), _ptr(x), _ptr(router_w), _ptr(logits_in),
                            _ptr(k_per_token), _ptr(logits_out), _ptr(topk_idx), _ptr(topk_w),
                            _ptr(dev_status), _ptr(workspace), _stream(stream))
@@ -247,7 +253,7 @@ def moe_route(desc, x, router_w, logits_in, k_per_token, logits_out, topk_idx, t
 
 def moe_permute(desc, topk_idx, k_per_token, counts, offsets, sorted_token, inv_row, dev_status,
                 workspace, stream=None) -> int:
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_permute(ctypes.byref(d), _ptr(topk_idx), _ptr(k_per_token), _ptr(counts),
                              _ptr(offsets), _ptr(sorted_token), _ptr(inv_row), _ptr(dev_status),
                              _ptr(workspace), _stream(stream))
@@ -257,7 +263,7 @@ def moe_permute_static(desc, topk_idx, k_per_token, counts, offsets, sorted_toke
                        dev_status, stream=None) -> int:
     """moe_permute with its scratch in the library's own device array (no
     workspace argument, nothing allocated)."""
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_permute_static(ctypes.byref(d), _ptr(topk_idx), _ptr(k_per_token),
                                     _ptr(counts), _ptr(offsets), _ptr(sorted_token),
                                     _ptr(inv_row), _ptr(dev_status), _stream(stream))
@@ -265,35 +271,35 @@ def moe_permute_static(desc, topk_idx, k_per_token, counts, offsets, sorted_toke
 
 def moe_gate_up(desc, x, sorted_token, offsets, w_gate_up, act, dev_status, workspace,
                 stream=None) -> int:
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_gate_up(ctypes.byref(d), _ptr(x), _ptr(sorted_token), _ptr(offsets),
                              _ptr(w_gate_up), _ptr(act), _ptr(dev_status), _ptr(workspace),
                              _stream(stream))
 
 
 def moe_down(desc, act, offsets, w_down, y_perm, dev_status, workspace, stream=None) -> int:
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_down(ctypes.byref(d), _ptr(act), _ptr(offsets), _ptr(w_down), _ptr(y_perm),
                           _ptr(dev_status), _ptr(workspace), _stream(stream))
 
 
 def moe_grouped_ffn(desc, x, sorted_token, offsets, w_gate_up, w_down, y_perm, dev_status,
                     workspace, stream=None) -> int:
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_grouped_ffn(ctypes.byref(d), _ptr(x), _ptr(sorted_token), _ptr(offsets),
                                  _ptr(w_gate_up), _ptr(w_down), _ptr(y_perm), _ptr(dev_status),
                                  _ptr(workspace), _stream(stream))
 
 
 def moe_shared_ffn(desc, x, y_shared, dev_status, workspace, stream=None) -> int:
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_shared_ffn(ctypes.byref(d), _ptr(x), _ptr(y_shared), _ptr(dev_status),
                                 _ptr(workspace), _stream(stream))
 
 
 def moe_combine(desc, y_perm, y_shared, inv_row, topk_w, k_per_token, out, dev_status,
                 stream=None) -> int:
-    d = desc.c()
+    d = _c(desc)
     return lib().moe_combine(ctypes.byref(d), _ptr(y_perm), _ptr(y_shared), _ptr(inv_row),
                              _ptr(topk_w), _ptr(k_per_token), _ptr(out), _ptr(dev_status),
                              _stream(stream))
@@ -468,12 +474,6 @@ class GroupRoute:
     def c(self) -> MoeGroupRoute:
         return MoeGroupRoute(int(self.n_groups), int(self.groups_kept), int(self.group_best),
                              _ptr(self.select_bias))
-
-
-def _c(desc):
-    """The ctypes form of a descriptor, which a caller may have built itself
-    once (desc.c()) to skip the conversion on every call."""
-    return desc if isinstance(desc, ctypes.Structure) else desc.c()
 
 
 def moe_route_groups(desc, groups, x, router_w, logits_in, k_per_token, logits_out, topk_idx,

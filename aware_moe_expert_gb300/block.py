@@ -76,13 +76,14 @@ def _on(stream):
 
 def _want(name, t, shape, dtypes, device, strided=False):
     """The library reads addresses: what is not this tensor is refused here."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and t.is_cuda == (device.type == "cuda")):
+        return
     ok = (isinstance(t, torch.Tensor) and tuple(t.shape) == tuple(shape) and t.dtype in dtypes
           and t.device.type == device.type)
     if ok and strided:      # rows may lie apart
         ok = t.stride(-1) == 1 and (t.shape[0] < 2 or t.stride(0) >= t.shape[1])
-    elif ok:
-        ok = t.is_contiguous()
-    if not ok:
+    if not ok or not strided:
         kind = "rows" if strided else "contiguous"
         names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{name}: {kind} {names} {list(shape)} on {device.type} wanted")
@@ -183,7 +184,8 @@ class MoeBlock:
         w, st, ws = self.weights, self.status, self.workspace
         a = None if adapter_idx is None else self.adapters
         self.groups.select_bias = w.select_bias      # which may have been replaced
-        d = replace(self.layer, T=T)
+        d = self.layer.c()
+        d.T = T
         h = self.h[:T]
         self._norm(residual, attn, w.attn_post_norm, w.pre_norm, residual, h)
         idx, tw, k_used = self.topk_idx[:T], self.topk_w[:T], self.k_used[:T]

@@ -468,7 +468,7 @@ __device__ __forceinline__ int skew_of(const NormParams& p, int first) {
 // us, 9 without).
 // Measured: 16384 x 7168 bf16 with both norms 148 us, 6.4 TB/s, 0.94 of a copy;
 // two block sums a row (one between the norms) are what is left of it.  16384 x
-// 4096, fp32 residual and a full gate 143 us (before its sums' last step).  One row of 7168: 3.3 us.
+// 4096, fp32 residual and a full gate 136 us.  One row of 7168: 3.3 us.
 template <typename R, typename A, int VEC, int EPT, int MAXT, bool SELF>
 __global__ void __launch_bounds__(MAXT + (SELF ? 0 : 32), 1) block_norm_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -902,7 +902,11 @@ cudaError_t run(NormParams& p, int rows_r, int rows_a, int sm, NormPlan* plan, c
 // Elements a thread and threads a CTA: eight elements as long as the threads
 // reach (16384 x 7168: 148 us, 16 elements in 896 threads 205).  The backward
 // pass holds three column sums per element: 512 threads have the registers for
-// it (8192 x 2048: 50 us, 1024 threads spill and take 86).
+// it (8192 x 2048: 50 us, 1024 threads spill and take 86).  Wider rows spill on both
+// sides of these rules.  Forward, 16384 x 8192, 8192 x 12288 and 4096 x 16384: 239, 231
+// and 130 us; 16 elements in 992 threads as far as they reach 414 and 211, 40 in 512
+// threads 405, 324 and 195.  Backward, 8192 x 7168 and 8192: 245 and 260 us with 16
+// elements; above, 40: 4096 x 8200 fp32 362, 4096 x 16384 629 (32 elements 383 and 516).
 template <typename R, typename A, int VEC>
 cudaError_t pick(NormParams& p, bool back, int rows_r, int rows_a, int sm, NormPlan* plan, cudaStream_t s) {
   const int n = span(p, VEC);

@@ -126,7 +126,7 @@ struct GroupParams {
 // two lanes' heads at a time (k rounds of a warp maximum took 2 us more).
 // Bound: issue slots and, before them, the chain through a token: 32 warps a SM
 // keep both apart.  16384 tokens of 256 units in 8 groups, 4 kept, k = 8, with
-// load counts: 15.4 us, 1.2 TB/s (sorting every lane and popping k heads: 24.7);
+// load counts: 15.6 us, 1.2 TB/s (sorting every lane and popping k heads: 24.7);
 // one token 3.5 us, which is the launch and one chain.
 template <int IPL, bool MANY>
 __global__ void __launch_bounds__(kMaxWarps * 32) group_route_kernel(const GroupParams p) {
@@ -617,9 +617,9 @@ cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
   p.load = a.load;
   p.status = a.status;
   // 16 warps where there are more tokens than eight a SM: half as many CTAs add
-  // to the same load counts (256 units, with 8 and 16: 600 tokens 4.8, 5.2 us;
-  // 2400 5.6, 5.4; 4096 8.5, 7.0; 16384 17.2, 15.4).  32 warps a SM: 24 took
-  // 18.1 us where 32 took 17.7 and 40 took 18.0.
+  // to the same load counts (256 units, with 8 and 16: 600 tokens 4.5, 4.9 us;
+  // 2400 5.4, 5.2; 4096 8.5, 7.1; 16384 17.7, 15.8).  32 warps a SM: 16384 tokens
+  // take 15.9 us, 19.6 with 16 and 20.2 with 48.
   const int warps = a.T > kWarps * a.sm_count ? kMaxWarps : kWarps;
   const int blocks = (a.T + warps - 1) / warps, most = 4 * kWarps / warps * a.sm_count;
   const int grid = blocks < most ? blocks : most;

@@ -1453,6 +1453,10 @@ cudaError_t launch_cluster(K kern, dim3 grid, int threads, int smem, int cluster
 // adapters meet in a tile is known on the device only: the estimate is the
 // geometric mean of none and of as many as there can be, each of whose groups
 // of columns costs a slot (0.15 us at 16 tokens to 0.6 at 256, over the splits).
+// Swapped against pairs, K 7168, N 4096, 48 adapters of r 32 a token each, then in
+// requests of 64, then none: 512 tokens 85, 41, 39 and 142, 53, 46 us; 1024 148, 75, 63
+// and 162, 72, 47; 2048 279, 129, 120 and 298, 109, 84.  The estimate takes the
+// swapped kernel up to 512, pairs from 768.
 struct Shape {
   int nt, splits;      // nt = 0: CTA pairs
 };
