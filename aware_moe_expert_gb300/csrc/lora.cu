@@ -1230,31 +1230,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           for (int i = 0; i < 16; ++i)
             pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
         }
-        const int col = nt * per_n + ci * 32;
-        if (p.vec_y == 16) {
-          if ((ci & 1) == 0) {
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-          }
+        const int col = nt * per_n + ci * 32, col0 = col - (ci & 1) * 32;
+        if (p.vec_y == 16 && (ci & 1) == 0) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+        }
+        // the map clips rows, and columns in pieces of 16 bytes only: what lies behind
+        // an end inside such a piece would be written
+        if (p.vec_y == 16 && ((p.outs & 7) == 0 || col0 + 64 <= p.outs)) {
           stage_row_32(sbuf, lane, (ci & 1) * 4, pk);
           if ((ci & 1) != 0) {
             fence_proxy_async_smem();
             __syncwarp();
-            // rows past T and columns past the outputs are clipped by the map
             if (lane == 0) {
-              if (row0 < p.T && col - 32 < p.outs) tma_store_2d(&tmY, sbuf, col - 32, row0);
+              if (row0 < p.T && col0 < p.outs) tma_store_2d(&tmY, sbuf, col0, row0);
               bulk_commit();
             }
           }
         } else {
-          // rows the map cannot describe: through the buffer, so that a warp
-          // stores 64 neighbouring columns of a row at a time
+          // rows the map cannot describe, and their ends: through the buffer, so that
+          // a warp stores 64 neighbouring columns of a row at a time
           stage_row_32(sbuf, lane, (ci & 1) * 4, pk);
           if ((ci & 1) != 0) {
             __syncwarp();
-            const int c0 = col - 32 + lane, c2 = col - 32 + 2 * lane;
+            const int c0 = col0 + lane, c2 = col0 + 2 * lane;
             const int rows = min(32, p.T - row0);
-            if (p.vec_y == 4) {
+            if (p.vec_y >= 4) {
               const uint8_t* from = sbuf + ((lane & 3) << 2);
               if (c2 + 1 < p.outs) {
 #pragma unroll 4

@@ -2,6 +2,8 @@
 import numpy as np
 import pytest
 import torch
+from test_gpu_lora import _check, _make, _spread
+from test_gpu_lora_variants import plan
 
 from aware_moe_expert_gb300 import binding as B
 
@@ -37,3 +39,17 @@ def test_silu_of_large_gates(T, N):
     low, high = (torch.tensor(v).bfloat16().double().numpy() for v in (ref - err, ref + err))
     assert (((low <= got) & (got <= high)) | ((g < -87) & (got == 0))).all()
     assert (g < -87).any() and (g > 87).any()
+
+
+@pytest.mark.parametrize("outs", [2041, 2042, 2047, 2048, 2049, 2050, 2055])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_columns_behind_the_outputs_keep_what_they_hold(outs, swiglu):
+    """CTA pairs into rows that lie 16 bytes aligned apart: nothing behind their ends is
+    written, whatever part of a 16-byte piece the last output leaves."""
+    T, K, N, n, r = 3001, 64, 2 * outs if swiglu else outs, 5, 16
+    assert plan(T, K, N, n, r, swiglu)[0] == 0
+    for ldy in ((outs + 7) // 8 * 8, (outs + 7) // 8 * 8 + 8, outs + 1):
+        v = _make(T, K, N, n, r, outs)
+        y = _check(v, _spread(T, n, outs, request=300), swiglu, ldy=ldy)
+        base = torch.as_strided(y, (T, ldy), (ldy, 1))
+        assert (base[:, outs:] == 99).all()
