@@ -284,31 +284,31 @@ def _handle(c, s):
 
     def pack(w):
         codes, scales, factor = w
-        desc = B.W4Desc(count=codes.shape[0], rows=codes.shape[1], K=2 * codes.shape[2],
+        desc = B.QuantDesc(count=codes.shape[0], rows=codes.shape[1], K=2 * codes.shape[2],
                         code=c["code"], group=c["group"])
-        packed = new(B.moe_w4_size(desc), dtype=torch.uint8)
-        B.check(B.moe_w4_pack(desc, codes, scales, factor, packed, h["status"]))
+        packed = new(B.moe_quant_size(desc), dtype=torch.uint8)
+        B.check(B.moe_quant_pack(desc, codes, scales, factor, packed, h["status"]))
         return packed
 
     h = dict(B=B, status=torch.zeros(1, dtype=I32, device=DEV))
     if c["op"] == "project":
-        desc = B.W4Project(T=c["T"], K=c["K"], N=c["N"], code=c["code"], group=c["group"],
+        desc = B.QuantProject(T=c["T"], K=c["K"], N=c["N"], code=c["code"], group=c["group"],
                            swiglu=c["swiglu"])
         h.update(desc=desc.c(), w=pack(s["w"]),
                  y=new(c["T"], c["N"] // 2 if c["swiglu"] else c["N"], dtype=BF16),
-                 workspace=new(B.moe_w4_project_workspace_size(desc), dtype=torch.uint8))
+                 workspace=new(B.moe_quant_project_workspace_size(desc), dtype=torch.uint8))
         return h
     layer = c["op"] == "layer"
     desc = B.LayerDesc(T=c["T"], H=c["H"], n_experts=c["E"], n_sub=1, I_sub=c["I"], k_max=c["k"],
                        score=c.get("score", "softmax"), renorm=c.get("renorm", False),
                        I_shared=c.get("shared", 0))
     shared = layer and c["shared"]
-    h["weights"] = B.W4Weights(code=c["code"], group=c["group"], gate_up=pack(s["gate_up"]),
+    h["weights"] = B.QuantWeights(code=c["code"], group=c["group"], gate_up=pack(s["gate_up"]),
                                down=pack(s["down"]),
                                shared_gate_up=pack(s["shared_gate_up"]) if shared else None,
                                shared_down=pack(s["shared_down"]) if shared else None)
     h.update(desc=desc.c(), w=h["weights"].c(), groups=None,
-             workspace=new(B.moe_w4_workspace_size(desc), dtype=torch.uint8))
+             workspace=new(B.moe_quant_workspace_size(desc), dtype=torch.uint8))
     if layer:
         h["out"] = new(c["T"], c["H"], dtype=BF16)
         if c["groups"]:
@@ -322,14 +322,14 @@ def _handle(c, s):
 def _own_project(state):
     h = state["handle"]
     B = h["B"]
-    B.check(B.moe_w4_project(h["desc"], state["x"], h["w"], h["y"], h["status"], h["workspace"]))
+    B.check(B.moe_quant_project(h["desc"], state["x"], h["w"], h["y"], h["status"], h["workspace"]))
     return h["y"]
 
 
 def _own_layer(state):
     h = state["handle"]
     B = h["B"]
-    B.check(B.moe_layer_forward_w4(h["desc"], h["groups"], h["w"], state["x"], state["router"],
+    B.check(B.moe_layer_forward_quant(h["desc"], h["groups"], h["w"], state["x"], state["router"],
                                    state["k"], None, h["out"], h["status"], h["workspace"]))
     return h["out"]
 
@@ -337,7 +337,7 @@ def _own_layer(state):
 def _own_experts(state):
     h = state["handle"]
     B = h["B"]
-    B.check(B.moe_grouped_ffn_w4(h["desc"], h["w"], state["x"], state["token"], state["offsets"],
+    B.check(B.moe_grouped_ffn_quant(h["desc"], h["w"], state["x"], state["token"], state["offsets"],
                                  h["y"], h["status"], h["workspace"]))
     return h["y"]
 
