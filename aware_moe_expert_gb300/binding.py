@@ -35,7 +35,10 @@ EXPORTS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_gate_up", "moe
            "moe_cost_lookup", "moe_tier_schedule", "moe_layer_forward_paths",
            "moe_layer_forward_host", "moe_route_groups", "moe_route_backward",
            "moe_layer_forward_groups", "moe_block_norm", "moe_block_norm_backward",
-           "moe_block_norm_workspace_size", "moe_lora_project", "moe_lora_workspace_size")
+           "moe_block_norm_workspace_size", "moe_lora_project", "moe_lora_workspace_size",
+           "moe_quant_size", "moe_quant_pack", "moe_quant_quantize", "moe_quant_unpack",
+           "moe_quant_project", "moe_quant_project_workspace_size", "moe_quant_workspace_size",
+           "moe_grouped_ffn_quant", "moe_shared_ffn_quant", "moe_layer_forward_quant")
 
 
 class MoeLayerDesc(ctypes.Structure):
@@ -89,6 +92,23 @@ class MoeLoraDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("n_adapters", ctypes.c_int32), ("r_max", ctypes.c_int32),
                 ("swiglu", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class MoeQuantDesc(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("rows", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("code", ctypes.c_int), ("group", ctypes.c_int32)]
+
+
+class MoeQuantProjectDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("code", ctypes.c_int), ("group", ctypes.c_int32), ("swiglu", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class MoeQuantWeights(ctypes.Structure):
+    _fields_ = [("code", ctypes.c_int), ("group", ctypes.c_int32), ("gate_up", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("shared_gate_up", ctypes.c_void_p),
+                ("shared_down", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -155,6 +175,24 @@ def lib() -> ctypes.CDLL:
             "moe_lora_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(MoeLoraDesc)]),
             "moe_lora_project": (ctypes.c_int, [ctypes.POINTER(MoeLoraDesc), vp, vp, vp, vp, vp,
                                                 vp, i32p, vp, i32p, vp, vp]),
+            "moe_quant_size": (ctypes.c_size_t, [ctypes.POINTER(MoeQuantDesc)]),
+            "moe_quant_pack": (ctypes.c_int, [ctypes.POINTER(MoeQuantDesc), vp, vp, vp, vp, i32p,
+                                              vp]),
+            "moe_quant_quantize": (ctypes.c_int, [ctypes.POINTER(MoeQuantDesc), vp, vp, i32p,
+                                                  vp]),
+            "moe_quant_unpack": (ctypes.c_int, [ctypes.POINTER(MoeQuantDesc), vp, vp, vp]),
+            "moe_quant_project_workspace_size": (ctypes.c_size_t,
+                                                 [ctypes.POINTER(MoeQuantProjectDesc)]),
+            "moe_quant_project": (ctypes.c_int, [ctypes.POINTER(MoeQuantProjectDesc), vp, vp, vp,
+                                                 i32p, vp, vp]),
+            "moe_quant_workspace_size": (ctypes.c_size_t, [D]),
+            "moe_grouped_ffn_quant": (ctypes.c_int, [D, ctypes.POINTER(MoeQuantWeights), vp, i32p,
+                                                     i32p, vp, i32p, vp, vp]),
+            "moe_shared_ffn_quant": (ctypes.c_int, [D, ctypes.POINTER(MoeQuantWeights), vp, vp,
+                                                    i32p, vp, vp]),
+            "moe_layer_forward_quant": (ctypes.c_int, [D, ctypes.POINTER(MoeGroupRoute),
+                                                       ctypes.POINTER(MoeQuantWeights), vp, vp,
+                                                       i32p, i32p, vp, i32p, vp, vp]),
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         }
         for name, (res, args) in sig.items():
@@ -575,6 +613,107 @@ def moe_lora_project(desc, x, w, lora_a, lora_b, ranks, scales, adapter_idx, y, 
     return lib().moe_lora_project(_c(desc), _ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b),
                                   _ptr(ranks), _ptr(scales), _ptr(adapter_idx), _ptr(y),
                                   _ptr(dev_status), _ptr(workspace), _stream(stream))
+
+
+_QUANT = {"e2m1": 0, "int4": 1}
+
+
+@dataclass
+class QuantDesc:
+    """Python mirror of moe_quant_desc: `count` matrices [rows, K] of 4-bit weights."""
+    count: int
+    rows: int
+    K: int
+    code: str = "e2m1"                       # "e2m1" | "int4"
+    group: int = 16                          # 16 | 32
+
+    def c(self) -> MoeQuantDesc:
+        return MoeQuantDesc(int(self.count), int(self.rows), int(self.K), _QUANT[self.code],
+                            int(self.group))
+
+
+def moe_quant_size(desc) -> int:
+    return int(lib().moe_quant_size(_c(desc)))
+
+
+def moe_quant_pack(desc, codes, scales, factors, packed, dev_status, stream=None) -> int:
+    return lib().moe_quant_pack(_c(desc), _ptr(codes), _ptr(scales), _ptr(factors), _ptr(packed),
+                                _ptr(dev_status), _stream(stream))
+
+
+def moe_quant_quantize(desc, w, packed, dev_status, stream=None) -> int:
+    return lib().moe_quant_quantize(_c(desc), _ptr(w), _ptr(packed), _ptr(dev_status),
+                                    _stream(stream))
+
+
+def moe_quant_unpack(desc, packed, w, stream=None) -> int:
+    return lib().moe_quant_unpack(_c(desc), _ptr(packed), _ptr(w), _stream(stream))
+
+
+@dataclass
+class QuantProject:
+    """Python mirror of moe_quant_project_desc."""
+    T: int
+    K: int
+    N: int
+    code: str = "e2m1"
+    group: int = 16
+    swiglu: bool = False
+    ldx: int = 0
+    ldy: int = 0
+
+    def c(self) -> MoeQuantProjectDesc:
+        return MoeQuantProjectDesc(int(self.T), int(self.K), int(self.N), _QUANT[self.code],
+                                   int(self.group), int(bool(self.swiglu)), int(self.ldx),
+                                   int(self.ldy))
+
+
+def moe_quant_project_workspace_size(desc) -> int:
+    return int(lib().moe_quant_project_workspace_size(_c(desc)))
+
+
+def moe_quant_project(desc, x, w, y, dev_status, workspace, stream=None) -> int:
+    return lib().moe_quant_project(_c(desc), _ptr(x), _ptr(w), _ptr(y), _ptr(dev_status),
+                                   _ptr(workspace), _stream(stream))
+
+
+@dataclass
+class QuantWeights:
+    """Python mirror of moe_quant_weights; the packed tensors are kept alive by reference."""
+    code: str
+    group: int
+    gate_up: Optional[torch.Tensor] = None
+    down: Optional[torch.Tensor] = None
+    shared_gate_up: Optional[torch.Tensor] = None
+    shared_down: Optional[torch.Tensor] = None
+
+    def c(self) -> MoeQuantWeights:
+        return MoeQuantWeights(_QUANT[self.code], int(self.group), _ptr(self.gate_up),
+                               _ptr(self.down), _ptr(self.shared_gate_up), _ptr(self.shared_down))
+
+
+def moe_quant_workspace_size(desc) -> int:
+    return int(lib().moe_quant_workspace_size(_c(desc)))
+
+
+def moe_grouped_ffn_quant(desc, weights, x, sorted_token, offsets, y_perm, dev_status, workspace,
+                          stream=None) -> int:
+    return lib().moe_grouped_ffn_quant(_c(desc), _c(weights), _ptr(x), _ptr(sorted_token),
+                                       _ptr(offsets), _ptr(y_perm), _ptr(dev_status),
+                                       _ptr(workspace), _stream(stream))
+
+
+def moe_shared_ffn_quant(desc, weights, x, y_shared, dev_status, workspace, stream=None) -> int:
+    return lib().moe_shared_ffn_quant(_c(desc), _c(weights), _ptr(x), _ptr(y_shared),
+                                      _ptr(dev_status), _ptr(workspace), _stream(stream))
+
+
+def moe_layer_forward_quant(desc, groups, weights, x, router_w, k_per_token, load, out, dev_status,
+                            workspace, stream=None) -> int:
+    return lib().moe_layer_forward_quant(_c(desc), None if groups is None else _c(groups),
+                                         _c(weights), _ptr(x), _ptr(router_w), _ptr(k_per_token),
+                                         _ptr(load), _ptr(out), _ptr(dev_status), _ptr(workspace),
+                                         _stream(stream))
 
 
 def moe_get_device_status(dev_status, stream=None) -> int:

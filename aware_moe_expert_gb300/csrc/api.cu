@@ -890,6 +890,112 @@ moe_status validate_lora(const moe_lora_desc* d) {
   return MOE_OK;
 }
 
+// ---------------------------------------------------------------- 4-bit weights
+
+bool quant_kind_ok(int code, int group) {
+  return (code == MOE_QUANT_E2M1 || code == MOE_QUANT_INT) && (group == 16 || group == 32);
+}
+
+// Bounds that keep every index of the kernels in 32 bits and offsets in 64.
+bool quant_dims_ok(long long count, long long rows, long long K) {
+  return count <= (1 << 20) && rows <= (1 << 20) && K <= (1 << 20);
+}
+
+moe_status validate_quant(const moe_quant_desc* d) {
+  if (d == nullptr || d->count < 1 || d->rows < 1 || d->K < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->code != MOE_QUANT_E2M1 && d->code != MOE_QUANT_INT) return MOE_ERR_INVALID_ARGUMENT;
+  if (!quant_kind_ok(d->code, d->group) || d->K % 8 != 0 || !quant_dims_ok(d->count, d->rows, d->K))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+moe_status validate_quant_project(const moe_quant_project_desc* d) {
+  if (d == nullptr || d->T < 0 || d->K < 1 || d->N < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->code != MOE_QUANT_E2M1 && d->code != MOE_QUANT_INT) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->ldx != 0 && d->ldx < d->K) return MOE_ERR_INVALID_ARGUMENT;
+  if (d->ldy != 0 && d->ldy < (d->swiglu ? d->N / 2 : d->N)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!quant_kind_ok(d->code, d->group) || d->K % 8 != 0 || d->ldx % 8 != 0 ||
+      !quant_dims_ok(1, d->N, d->K) || d->T > (1 << 23) || (d->swiglu && d->N % 2 != 0))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+// The layer's desc without its bf16 shared weights, which packed ones replace.
+moe_status validate_quant_layer(const moe_layer_desc* d) {
+  if (d == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  moe_layer_desc c = *d;
+  c.I_shared = 0;
+  MOE_TRY(validate(&c));
+  if (d->I_shared < 0) return MOE_ERR_INVALID_ARGUMENT;
+  return d->I_shared % 64 != 0 || d->I_shared > (1 << 20) ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
+moe_status validate_quant_weights(const moe_layer_desc* d, const moe_quant_weights* w, bool routed,
+                                  bool shared) {
+  if (w == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (w->code != MOE_QUANT_E2M1 && w->code != MOE_QUANT_INT) return MOE_ERR_INVALID_ARGUMENT;
+  if (!quant_kind_ok(w->code, w->group)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (routed) MOE_TRY(check_ptrs({w->gate_up, w->down}));
+  if (shared && d->I_shared > 0) MOE_TRY(check_ptrs({w->shared_gate_up, w->shared_down}));
+  return MOE_OK;
+}
+
+// Behind the layer's own workspace: fp32 outputs of the experts and the shared expert.
+struct QuantLayout {
+  size_t y, ysh, total;
+};
+QuantLayout quant_layout_of(const moe_layer_desc& d) {
+  QuantLayout q;
+  size_t o = layout_of(d).total;
+  q.y = o;
+  o = align_up(o + static_cast<size_t>(d.T) * d.k_max * d.H * 4);
+  q.ysh = o;
+  o = align_up(o + (d.I_shared > 0 ? static_cast<size_t>(d.T) * d.H * 4 : 0));
+  q.total = o;
+  return q;
+}
+
+moe_status do_quant_ffn(const moe_layer_desc* d, const moe_quant_weights* w, bool shared,
+                        const void* x, const int32_t* sorted_token, const int32_t* offsets,
+                        void* y, bool f32, int32_t* status, void* ws, cudaStream_t s) {
+  const Layout l = layout_of(*d);
+  const int I = shared ? d->I_shared : d->I_sub;
+  const long long rows = shared ? d->T : static_cast<long long>(d->T) * d->k_max;
+  moe::QuantGemmArgs a{};
+  a.x = x;
+  a.ldx = d->H;
+  a.x_rows = d->T;
+  a.token = sorted_token;
+  a.offsets = offsets;
+  a.n_groups = shared ? 1 : E_r_of(d);
+  a.dense_rows = d->T;
+  a.w = shared ? w->shared_gate_up : w->gate_up;
+  a.code = w->code;
+  a.group = w->group;
+  a.n = I;
+  a.K = d->H;
+  a.swiglu = 1;
+  a.out = at<void>(ws, shared ? l.act_sh : l.act);
+  a.ldo = I;
+  a.out_rows = rows;
+  a.status = status;
+  a.sm_count = sm_count();
+  MOE_TRY(cuda_status(moe::launch_quant_gemm(a, s)));
+  moe::QuantGemmArgs b = a;
+  b.x = a.out;
+  b.ldx = I;
+  b.x_rows = static_cast<int>(rows);
+  b.token = nullptr;
+  b.w = shared ? w->shared_down : w->down;
+  b.n = d->H;
+  b.K = I;
+  b.swiglu = 0;
+  b.out = y;
+  b.ldo = d->H;
+  b.out_f32 = f32;
+  return cuda_status(moe::launch_quant_gemm(b, s));
+}
+
 }  // namespace
 
 namespace moe {
@@ -1404,6 +1510,178 @@ moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void
   g.status = dev_status;
   g.sm_count = sm_count();
   return cuda_status(moe::launch_lora_project(g, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_quant_size(const moe_quant_desc* desc) {
+  if (validate_quant(desc) != MOE_OK) return 0;
+  return align_up(moe::quant_bytes(desc->count, desc->rows, desc->K, desc->group));
+}
+
+static moe::QuantPackArgs quant_pack_args(const moe_quant_desc* d) {
+  moe::QuantPackArgs a{};
+  a.count = d->count;
+  a.rows = d->rows;
+  a.K = d->K;
+  a.code = d->code;
+  a.group = d->group;
+  return a;
+}
+
+moe_status moe_quant_pack(const moe_quant_desc* desc, const void* codes, const void* scales,
+                          const float* factors, void* packed, int32_t* dev_status, void* stream) {
+  MOE_TRY(validate_quant(desc));
+  if (codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  MOE_TRY(check_ptrs({packed}));
+  MOE_TRY(check_ptrs4({factors, dev_status}));
+  moe::QuantPackArgs a = quant_pack_args(desc);
+  a.codes = codes;
+  a.scales = scales;
+  a.factors = factors;
+  a.packed = packed;
+  a.status = dev_status;
+  return cuda_status(moe::launch_quant_pack(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_quant_quantize(const moe_quant_desc* desc, const void* w, void* packed,
+                              int32_t* dev_status, void* stream) {
+  MOE_TRY(validate_quant(desc));
+  MOE_TRY(check_ptrs({w, packed}));
+  MOE_TRY(check_ptrs4({dev_status}));
+  moe::QuantPackArgs a = quant_pack_args(desc);
+  a.w = w;
+  a.packed = packed;
+  a.status = dev_status;
+  return cuda_status(moe::launch_quant_pack(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_quant_unpack(const moe_quant_desc* desc, const void* packed, void* w,
+                            void* stream) {
+  MOE_TRY(validate_quant(desc));
+  MOE_TRY(check_ptrs({packed, w}));
+  moe::QuantPackArgs a = quant_pack_args(desc);
+  a.packed = const_cast<void*>(packed);
+  a.w_out = w;
+  return cuda_status(moe::launch_quant_unpack(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_quant_project_workspace_size(const moe_quant_project_desc* desc) {
+  return validate_quant_project(desc) != MOE_OK ? 0 : kAlign;
+}
+
+moe_status moe_quant_project(const moe_quant_project_desc* desc, const void* x, const void* w,
+                             void* y, int32_t* dev_status, void* workspace, void* stream) {
+  MOE_TRY(validate_quant_project(desc));
+  if (desc->T == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({x, w}));
+  if (y == nullptr || (reinterpret_cast<uintptr_t>(y) & 1u) != 0) return MOE_ERR_INVALID_ARGUMENT;
+  MOE_TRY(check_ptrs4({dev_status}));
+  MOE_TRY(check_ws(workspace));
+  moe::QuantGemmArgs a{};
+  a.x = x;
+  a.ldx = desc->ldx != 0 ? desc->ldx : desc->K;
+  a.x_rows = desc->T;
+  a.n_groups = 1;
+  a.dense_rows = desc->T;
+  a.w = w;
+  a.code = desc->code;
+  a.group = desc->group;
+  a.n = desc->swiglu ? desc->N / 2 : desc->N;
+  a.K = desc->K;
+  a.swiglu = desc->swiglu;
+  a.out = y;
+  a.ldo = desc->ldy != 0 ? desc->ldy : a.n;
+  a.out_rows = desc->T;
+  a.status = dev_status;
+  a.sm_count = sm_count();
+  return cuda_status(moe::launch_quant_gemm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_quant_workspace_size(const moe_layer_desc* desc) {
+  if (validate_quant_layer(desc) != MOE_OK) return 0;
+  return quant_layout_of(*desc).total;
+}
+
+moe_status moe_grouped_ffn_quant(const moe_layer_desc* desc, const moe_quant_weights* weights,
+                                 const void* x, const int32_t* sorted_token,
+                                 const int32_t* offsets, void* y_perm, int32_t* dev_status,
+                                 void* workspace, void* stream) {
+  MOE_TRY(validate_quant_layer(desc));
+  MOE_TRY(validate_quant_weights(desc, weights, desc->T > 0, false));
+  if (desc->T == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({x, y_perm}));
+  MOE_TRY(check_ptrs4({sorted_token, offsets, dev_status}));
+  MOE_TRY(check_ws(workspace));
+  return do_quant_ffn(desc, weights, false, x, sorted_token, offsets, y_perm, false, dev_status,
+                      workspace, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_shared_ffn_quant(const moe_layer_desc* desc, const moe_quant_weights* weights,
+                                const void* x, void* y_shared, int32_t* dev_status,
+                                void* workspace, void* stream) {
+  MOE_TRY(validate_quant_layer(desc));
+  if (desc->I_shared <= 0) return MOE_ERR_INVALID_ARGUMENT;
+  MOE_TRY(validate_quant_weights(desc, weights, false, desc->T > 0));
+  if (desc->T == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({x, y_shared}));
+  MOE_TRY(check_ptrs4({dev_status}));
+  MOE_TRY(check_ws(workspace));
+  return do_quant_ffn(desc, weights, true, x, nullptr, nullptr, y_shared, false, dev_status,
+                      workspace, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_layer_forward_quant(const moe_layer_desc* desc, const moe_group_route* groups,
+                                   const moe_quant_weights* weights, const void* x,
+                                   const void* router_w, const int32_t* k_per_token,
+                                   int32_t* load, void* out, int32_t* dev_status,
+                                   void* workspace, void* stream) {
+  MOE_TRY(validate_quant_layer(desc));
+  moe_layer_desc d = *desc;      // the routing steps' desc: no bf16 shared expert
+  d.I_shared = 0;
+  if (groups != nullptr) MOE_TRY(validate_groups(&d, groups));
+  if (load != nullptr) {
+    if (groups == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    MOE_TRY(check_ptrs4({load}));
+  }
+  MOE_TRY(validate_quant_weights(desc, weights, d.T > 0, d.T > 0));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d.T == 0)
+    return load == nullptr
+               ? MOE_OK
+               : cuda_status(cudaMemsetAsync(load, 0, sizeof(int32_t) * E_r_of(desc), s));
+  MOE_TRY(check_ptrs({x, router_w, out}));
+  MOE_TRY(check_ptrs4({k_per_token, dev_status}));
+  MOE_TRY(check_ws(workspace));
+  const Layout l = layout_of(*desc);
+  const QuantLayout q = quant_layout_of(*desc);
+  int32_t* topk_idx = at<int32_t>(workspace, l.topk_idx);
+  float* topk_w = at<float>(workspace, l.topk_w);
+  int32_t* counts = at<int32_t>(workspace, l.counts);
+  int32_t* offsets = at<int32_t>(workspace, l.offsets);
+  int32_t* sorted_token = at<int32_t>(workspace, l.sorted_token);
+  int32_t* inv_row = at<int32_t>(workspace, l.inv_row);
+  const int32_t* k_used = k_per_token;
+  bool bitmap_done = false;
+  if (groups != nullptr) {
+    int32_t* k_left = at<int32_t>(workspace, l.fold_k);
+    MOE_TRY(do_route_groups(desc, groups, x, router_w, nullptr, k_per_token, nullptr, topk_idx,
+                            topk_w, k_left, load, dev_status, workspace, s));
+    k_used = k_left;
+  } else {
+    MOE_TRY(do_route(desc, x, router_w, nullptr, k_per_token, nullptr, topk_idx, topk_w,
+                     dev_status, workspace, s, &bitmap_done));
+  }
+  MOE_TRY(do_permute(desc, topk_idx, k_used, counts, offsets, sorted_token, inv_row, dev_status,
+                     workspace, s, bitmap_done));
+  float* ysh = desc->I_shared > 0 ? at<float>(workspace, q.ysh) : nullptr;
+  if (ysh != nullptr)
+    MOE_TRY(do_quant_ffn(desc, weights, true, x, nullptr, nullptr, ysh, true, dev_status,
+                         workspace, s));
+  float* y = at<float>(workspace, q.y);
+  MOE_TRY(do_quant_ffn(desc, weights, false, x, sorted_token, offsets, y, true, dev_status,
+                       workspace, s));
+  return cuda_status(moe::launch_combine_f32(y, ysh, inv_row, topk_w, k_used, d.T, d.H, d.k_max,
+                                             static_cast<int>(static_cast<long long>(d.T) * d.k_max),
+                                             out, dev_status, s));
 }
 
 moe_status moe_get_device_status(const int32_t* dev_status, void* stream) {

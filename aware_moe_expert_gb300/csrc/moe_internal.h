@@ -314,6 +314,43 @@ LoraPlan lora_plan(const LoraArgs& g);
 size_t lora_workspace_bytes(int T, int r_max);
 cudaError_t launch_lora_project(const LoraArgs& g, cudaStream_t s);
 
+// ---- quant_pack.cu: packing of 4-bit weights (layout: quant.cuh)
+struct QuantPackArgs {
+  const void* codes;           // [count, rows, K / 2]; null: quantise w (pack only)
+  const void* scales;          // e4m3 [count, rows, ceil(K / group)]
+  const float* factors;        // [count]
+  const void* w;               // bf16 [count, rows, K]
+  void* w_out;                 // unpack: bf16 [count, rows, K]
+  void* packed;
+  int count, rows, K, code, group;
+  int32_t* status;
+};
+size_t quant_bytes(int count, int rows, int K, int group);
+cudaError_t launch_quant_pack(const QuantPackArgs& a, cudaStream_t s);
+cudaError_t launch_quant_unpack(const QuantPackArgs& a, cudaStream_t s);
+
+// ---- quant_gemm.cu: products of bf16 rows with packed 4-bit weights
+struct QuantGemmArgs {
+  const void* x;               // bf16 [x_rows, K], ldx elements between rows
+  long long ldx;
+  int x_rows;
+  const int32_t* token;        // row r of the product is x row token[r]; null: row r
+  const int32_t* offsets;      // [n_groups + 1] device: rows of each group; null: one group of
+  int n_groups, dense_rows;    //   dense_rows
+  const void* w;               // packed: a matrix (SwiGLU: gate, then up) of n rows per group
+  int code, group, n, K, swiglu;
+  void* out;                   // bf16 or fp32 [out_rows, n], ldo elements between rows
+  long long ldo, out_rows;
+  int out_f32;
+  int32_t* status;
+  int sm_count;
+};
+cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s);
+// The weighted sum of fp32 rows y (and fp32 y_shared, nullable), like launch_combine's.
+cudaError_t launch_combine_f32(const float* y, const float* y_shared, const int32_t* inv_row,
+                               const float* topk_w, const int32_t* k_per_token, int T, int H,
+                               int k_max, int n_rows, void* out, int32_t* status, cudaStream_t s);
+
 // Tensor map of a row-major [rows, cols] array of bf16 (elem 2) or fp32 (4) with ld
 // elements between rows: boxes of box_rows x box_cols, 32 or 128 bytes wide, swizzled
 // over as many.  Encodes at every call; make_tmap_bf16 keeps maps it has made.

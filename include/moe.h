@@ -532,6 +532,99 @@ moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void
                             const float* scales, const int32_t* adapter_idx, void* y,
                             int32_t* dev_status, void* workspace, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Weights of 4 bits.  A matrix [rows, K] has a code for every weight, a scale
+ * for every `group` consecutive inputs of a row and one factor:
+ *     W[n, k] = factor * scale[n, k / group] * value(code[n, k])
+ * with e2m1 codes (bit 3 the sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6) or integers
+ * (code - 8, codes 0..15); scales e4m3 and not negative, the factor fp32.  A
+ * checkpoint with e8m0 scales has them as e4m3 and a factor where a matrix spans
+ * up to 18 powers of two, one with groups of 64 or 128 by repeating scales.
+ * Products take the codes times their scale (exact in bf16), sum in fp32 and
+ * multiply the sums by the factor: no weight is rounded.
+ * moe_quant_pack lays weights out once; only the packed form is used after.
+ */
+typedef enum { MOE_QUANT_E2M1 = 0, MOE_QUANT_INT = 1 } moe_quant_code;
+
+typedef struct {
+  int32_t count, rows, K;     /* matrices, outputs and inputs of each; K % 8 == 0        */
+  moe_quant_code code;
+  int32_t group;              /* 16 or 32                                                */
+} moe_quant_desc;
+
+/* Bytes of `count` packed matrices (0 on a bad desc). */
+size_t moe_quant_size(const moe_quant_desc* desc);
+
+/*   codes    uint8 [count, rows, K / 2]: two a byte, the even input in the low half
+ *   scales   e4m3 [count, rows, ceil(K / group)]; a negative or NaN one is reported
+ *            (MOE_ERR_NONFINITE) and its weights are 0
+ *   factors  fp32 [count]; one that is not finite is reported
+ *   packed   moe_quant_size bytes, 16-byte aligned */
+moe_status moe_quant_pack(const moe_quant_desc* desc, const void* codes, const void* scales,
+                          const float* factors, void* packed, int32_t* dev_status, void* stream);
+
+/* Quantises bf16 w [count, rows, K]: a matrix's largest weight gets the largest
+ * scale and code, a group's scale is the nearest e4m3 to its largest weight over the
+ * largest code (6 or 7), a weight gets the nearest code (ties: the even one; integers -8..7).  Weights that
+ * are not finite count as 0 and are reported (MOE_ERR_NONFINITE). */
+moe_status moe_quant_quantize(const moe_quant_desc* desc, const void* w, void* packed,
+                              int32_t* dev_status, void* stream);
+
+/* The packed weights as bf16 w [count, rows, K], rounded once from fp32. */
+moe_status moe_quant_unpack(const moe_quant_desc* desc, const void* packed, void* w,
+                            void* stream);
+
+/* y_t = x_t W^T, with `swiglu` SiLU(x_t W_0^T) * (x_t W_1^T) of two matrices of N / 2
+ * outputs; sums in fp32, y rounded once. */
+typedef struct {
+  int32_t T, K, N;            /* tokens, inputs, outputs (before SwiGLU); K % 8 == 0     */
+  moe_quant_code code;
+  int32_t group;
+  int32_t swiglu;             /* 1: w is packed as 2 matrices of N / 2 rows, else as 1 of N */
+  int64_t ldx, ldy;           /* elements between rows; 0 = contiguous; ldx % 8 == 0     */
+} moe_quant_project_desc;
+
+/* Bytes of workspace moe_quant_project needs (0 on a bad desc). */
+size_t moe_quant_project_workspace_size(const moe_quant_project_desc* desc);
+
+/*   x bf16 [T, K], w packed, y bf16 [T, N] ([T, N / 2] with swiglu, any 2-byte alignment) */
+moe_status moe_quant_project(const moe_quant_project_desc* desc, const void* x, const void* w,
+                             void* y, int32_t* dev_status, void* workspace, void* stream);
+
+/* A layer's experts (and shared expert) packed; all with one code and group. */
+typedef struct {
+  moe_quant_code code;
+  int32_t group;
+  const void* gate_up;        /* count 2 * E_r (gate, then up of a unit), rows I_sub, K H */
+  const void* down;           /* count E_r, rows H, K I_sub                               */
+  const void* shared_gate_up; /* nullable: count 2, rows I_shared, K H                    */
+  const void* shared_down;    /* nullable: count 1, rows H, K I_shared                    */
+} moe_quant_weights;
+
+/* Workspace bytes for the calls below (0 on a bad desc).  Of desc they use the shape,
+ * the routing and I_shared; not w_shared_gate_up, w_shared_down and path. */
+size_t moe_quant_workspace_size(const moe_layer_desc* desc);
+
+/* moe_grouped_ffn on packed weights. */
+moe_status moe_grouped_ffn_quant(const moe_layer_desc* desc, const moe_quant_weights* weights,
+                                 const void* x, const int32_t* sorted_token,
+                                 const int32_t* offsets, void* y_perm, int32_t* dev_status,
+                                 void* workspace, void* stream);
+
+/* moe_shared_ffn on packed weights: y_shared bf16 [T, H]. */
+moe_status moe_shared_ffn_quant(const moe_layer_desc* desc, const moe_quant_weights* weights,
+                                const void* x, void* y_shared, int32_t* dev_status,
+                                void* workspace, void* stream);
+
+/* The whole layer on packed weights: moe_layer_forward's router (groups null) or
+ * moe_layer_forward_groups' (load nullable; null without groups).  The experts'
+ * outputs stay fp32 up to the weighted sum. */
+moe_status moe_layer_forward_quant(const moe_layer_desc* desc, const moe_group_route* groups,
+                                   const moe_quant_weights* weights, const void* x,
+                                   const void* router_w, const int32_t* k_per_token,
+                                   int32_t* load, void* out, int32_t* dev_status,
+                                   void* workspace, void* stream);
+
 /* Synchronises `stream`, then returns the code stored in *dev_status
  * (MOE_OK if zero), or MOE_ERR_CUDA if the synchronisation itself failed. */
 moe_status moe_get_device_status(const int32_t* dev_status, void* stream);
