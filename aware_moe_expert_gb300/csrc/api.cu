@@ -978,10 +978,12 @@ moe_status do_quant_ffn(const moe_layer_desc* d, const moe_quant_weights* w, boo
   a.out = at<void>(ws, shared ? l.act_sh : l.act);
   a.ldo = I;
   a.out_rows = rows;
+  a.early = shared;
   a.status = status;
   a.sm_count = sm_count();
   MOE_TRY(cuda_status(moe::launch_quant_gemm(a, s)));
   moe::QuantGemmArgs b = a;
+  b.early = 1;
   b.x = a.out;
   b.ldx = I;
   b.x_rows = static_cast<int>(rows);
@@ -1591,6 +1593,7 @@ moe_status moe_quant_project(const moe_quant_project_desc* desc, const void* x, 
   a.out = y;
   a.ldo = desc->ldy != 0 ? desc->ldy : a.n;
   a.out_rows = desc->T;
+  a.early = 1;
   a.status = dev_status;
   a.sm_count = sm_count();
   return cuda_status(moe::launch_quant_gemm(a, static_cast<cudaStream_t>(stream)));

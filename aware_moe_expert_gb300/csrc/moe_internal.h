@@ -342,6 +342,7 @@ struct QuantGemmArgs {
   void* out;                   // bf16 or fp32 [out_rows, n], ldo elements between rows
   long long ldo, out_rows;
   int out_f32;
+  int early;                   // offsets were written before the launch that this one follows
   int32_t* status;
   int sm_count;
 };

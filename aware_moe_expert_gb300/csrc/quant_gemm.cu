@@ -1,8 +1,27 @@
-// Products of bf16 rows with packed 4-bit weights, dense or grouped by expert:
-// y_r = x_r W^T, or with SwiGLU silu(x_r G^T) * (x_r U^T) of two matrices.
+// Products of bf16 rows with packed 4-bit weights, dense or grouped by expert, on
+// the tensor cores: y_r = x_r W^T, or with SwiGLU silu(x_r G^T) * (x_r U^T).
 //
-// The simplest form: a warp per output feature and eight rows, whole words of
-// eight weights per lane, fp32 sums.
+// 128 rows of weights are the M side of tcgen05.mma, a chunk of up to NT tokens the
+// N side, so every weight is expanded once per chunk.  The expanded weights never
+// see shared memory: a thread reads one row's 64 bytes of codes for 128 inputs
+// (four 16-byte loads), expands them in registers (quant.cuh) and stores them as
+// the A operand in TMEM; only the tokens come from shared memory.  Expanding into
+// shared memory instead would write and read 2 bytes a weight there, four times the
+// codes' own traffic and more than an SM's 128 bytes a clock carry at the rate HBM
+// delivers codes.
+//
+// An item is two 128-row tiles (of one matrix, or the gate and up rows of the same
+// 128 features) x one chunk of a group's tokens, the whole of K: both tiles share
+// the chunk's tokens, halving their traffic.
+// Roles of the warps, one CTA an SM, items dealt round robin:
+//   0       bulk copies of weight records and TMA loads of token rows into a ring
+//   1       TMEM, MMA issue
+//   2-5     epilogue (TMEM lane quarter = warp % 4)
+//   6-13    expansion: four warps a tile
+//   14-17   GATHER: copy the token rows that an index names, instead of TMA
+// Every wait is bounded.
+#include <algorithm>
+
 #include "gemm_common.cuh"
 #include "moe_internal.h"
 #include "quant.cuh"
@@ -10,116 +29,548 @@
 namespace moe {
 namespace {
 
-constexpr int kRowsAtOnce = 8;
-constexpr int kRowThreads = 256;
+constexpr int kExpandWarps = 8;
+constexpr int kBaseThreads = (6 + kExpandWarps) * 32;
+constexpr int kGatherThreads = 128;
+constexpr uint32_t kMaxRecord = quant_record(16);
+constexpr uint32_t kWStage = 2 * kMaxRecord;      // both tiles' records of 128 inputs
+constexpr int kABufs = 2;                         // TMEM buffers of expanded weights
+constexpr uint32_t kACols = 128;                  // columns of one: 2 tiles x 128 bf16 inputs
 
-struct RowsParams {
-  const __nv_bfloat16* x;
-  const int32_t* token;
-  const int32_t* offsets;
+template <int NT, bool SPLIT>
+struct TileCfg {
+  static constexpr int kStages = NT == 128 ? 4 : (SPLIT ? 4 : 6);
+  static constexpr uint32_t kTok = NT * kQK * 2;  // a stage's tokens: two blocks of 64 inputs
+  static constexpr uint32_t kOffW = kStages * kTok;
+  static constexpr uint32_t kOffPart = kOffW + kStages * kWStage;
+  static constexpr uint32_t kPart = SPLIT ? NT * 256 * 4 : 0;
+  static constexpr uint32_t kOffBar = kOffPart + kPart;
+  static constexpr int kDBufs = NT == 128 ? 1 : 2;
+  static constexpr int kBars = 3 * kStages + 2 * kABufs + 2 * kDBufs + 1;
+  static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+  static constexpr uint32_t kOffPrefix = kOffMisc + 16;
+  static constexpr uint32_t kOffOffs = kOffPrefix + (kMaxGroups + 1) * 4;
+  static constexpr uint32_t kSmem = kOffOffs + (kMaxGroups + 1) * 4 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kABufs * kACols + kDBufs * 2 * NT <= 512, "TMEM columns");
+};
+
+struct TileParams {
   const uint8_t* w;
   const float* factor;
+  const uint4* x;              // GATHER
+  const int32_t* token;
+  const int32_t* offsets;
   void* out;
   long long ldx, ldo, out_rows;
   size_t matrix;
-  int dense_rows, x_rows, n, K, kb;
+  uint32_t record;
+  int n_groups, dense_rows, x_rows, n, K, kb, rt, blocks, code, group, swiglu, f32, early, splits;
   int32_t* status;
 };
 
-template <int CODE, int GROUP, bool SWIGLU, bool F32>
-__global__ void __launch_bounds__(kRowThreads) quant_rows_kernel(const RowsParams p) {
-  pdl_wait_and_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = blockIdx.x * (kRowThreads / 32) + warp;
-  const int g = blockIdx.y;
-  const int first = p.offsets != nullptr ? p.offsets[g] : 0;
-  const int last = p.offsets != nullptr ? p.offsets[g + 1] : p.dense_rows;
-  if (first < 0 || last < first || last > p.out_rows) {
-    if (threadIdx.x == 0) report(p.status, MOE_ERR_BAD_INDEX);
-    return;
-  }
-  if (n >= p.n) return;
-  constexpr int M = SWIGLU ? 2 : 1;
-  constexpr uint32_t kRec = quant_record(GROUP);
-  const uint8_t* rec0 = p.w + p.matrix * (static_cast<size_t>(g) * M) +
-                        static_cast<size_t>(n / kQRows) * p.kb * kRec;
-  const int r = n % kQRows;
-  for (int t0 = first; t0 < last; t0 += kRowsAtOnce) {
-    float acc[M][kRowsAtOnce] = {};
-    const __nv_bfloat16* row[kRowsAtOnce];
-    for (int i = 0; i < kRowsAtOnce; ++i) {
-      int t = min(t0 + i, last - 1);
-      if (p.token != nullptr) {
-        t = p.token[t];
-        if (t < 0 || t >= p.x_rows) {
-          report(p.status, MOE_ERR_BAD_INDEX);
-          t = 0;
-        }
-      }
-      row[i] = p.x + t * p.ldx;
-    }
-    for (int v = lane; v < p.kb * 16; v += 32) {
-      const int k = (v % 16) * 8, kk = v * 8;
-      if (kk >= p.K) break;
-      float w[M][8];
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T: lane = row of A, a column two consecutive bf16 inputs.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// One row's 128 expanded weights to TMEM columns d .. d + 63, and the row's scales
+// (sc: a byte for every 16 inputs).
+template <int CODE>
+__device__ __forceinline__ void expand_row(const uint4 (&c)[4], uint2 sc, uint32_t d) {
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const uint8_t* rec = rec0 + p.matrix * m + static_cast<size_t>(v / 16) * kRec;
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[32];
+    const uint32_t s4 = h == 0 ? sc.x : sc.y;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {                    // word 2 h + i: 32 inputs
+      const QuantScale<CODE> q[2] = {QuantScale<CODE>((s4 >> (16 * i)) & 0xFFu),
+                                     QuantScale<CODE>((s4 >> (16 * i + 8)) & 0xFFu)};
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t w = h == 0 ? (i == 0 ? c[p].x : c[p].y) : (i == 0 ? c[p].z : c[p].w);
         uint32_t e[4];
-        quant_expand<CODE>(
-            *reinterpret_cast<const uint32_t*>(rec + quant_piece(r, (k % 32) / 8) + 4 * (k / 32)),
-            QuantScale<CODE>(rec[kQCodeBytes + r * (kQK / GROUP) + k / GROUP]), e);
+        quant_expand<CODE>(w, q[p >> 1], e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[m][2 * i] = bf16lo(e[i]);
-          w[m][2 * i + 1] = bf16hi(e[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kRowsAtOnce; ++i) {
-        const uint4 q = *reinterpret_cast<const uint4*>(row[i] + kk);
-        const uint32_t xv[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[m][i] = fmaf(w[m][2 * j], bf16lo(xv[j]), acc[m][i]);
-            acc[m][i] = fmaf(w[m][2 * j + 1], bf16hi(xv[j]), acc[m][i]);
-          }
+        for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
       }
     }
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const float f = p.factor[g * M + m] * quant_unit<CODE>();
-#pragma unroll
-      for (int i = 0; i < kRowsAtOnce; ++i) {
-        for (int o = 16; o > 0; o >>= 1) acc[m][i] += __shfl_xor_sync(0xffffffffu, acc[m][i], o);
-        acc[m][i] *= f;
-      }
-    }
-    for (int i = 0; i < kRowsAtOnce; ++i) {
-      if (lane != i || t0 + i >= last) continue;
-      float y = 0.f;
-#pragma unroll
-      for (int j = 0; j < kRowsAtOnce; ++j)
-        if (j == i) y = SWIGLU ? silu_f(acc[0][j]) * acc[M - 1][j] : acc[0][j];
-      const size_t at = static_cast<size_t>(t0 + i) * p.ldo + n;
-      if (F32)
-        static_cast<float*>(p.out)[at] = y;
-      else
-        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-    }
+    tmem_st32(d + 32u * h, v);
   }
 }
 
-template <int CODE, int GROUP>
-cudaError_t launch_code(const QuantGemmArgs& a, const RowsParams& p, cudaStream_t s) {
-  const dim3 grid((p.n + kRowThreads / 32 - 1) / (kRowThreads / 32), a.n_groups);
-  if (a.swiglu)
-    return launch_pdl(quant_rows_kernel<CODE, GROUP, true, false>, grid, dim3(kRowThreads), 0, s, p);
-  return a.out_f32
-             ? launch_pdl(quant_rows_kernel<CODE, GROUP, false, true>, grid, dim3(kRowThreads), 0, s, p)
-             : launch_pdl(quant_rows_kernel<CODE, GROUP, false, false>, grid, dim3(kRowThreads), 0, s, p);
+template <int NT, bool GATHER, bool SPLIT>
+__global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBaseThreads, 1)
+    quant_tile_kernel(const __grid_constant__ CUtensorMap tm16,
+                      const __grid_constant__ CUtensorMap tm64, const TileParams p) {
+  using Cfg = TileCfg<NT, SPLIT>;
+  constexpr int kStages = Cfg::kStages, kDBufs = Cfg::kDBufs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBar);
+  uint64_t* bfull = wfull + kStages;
+  uint64_t* empty = bfull + kStages;
+  uint64_t* afull = empty + kStages;
+  uint64_t* aempty = afull + kABufs;
+  uint64_t* dfull = aempty + kABufs;
+  uint64_t* dempty = dfull + kDBufs;
+  uint64_t* mma_done = dempty + kDBufs;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  int* s_total = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 8);
+  int* s_prefix = reinterpret_cast<int*>(smem + Cfg::kOffPrefix);
+  int* s_offs = reinterpret_cast<int*>(smem + Cfg::kOffOffs);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&bfull[s], GATHER ? kGatherThreads : 1);
+      mbar_init(&empty[s], kExpandWarps + 1);
+    }
+    for (int i = 0; i < kABufs; ++i) {
+      mbar_init(&afull[i], kExpandWarps);
+      mbar_init(&aempty[i], 1);
+    }
+    for (int i = 0; i < kDBufs; ++i) {
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dempty[i], 4);
+    }
+    mbar_init(mma_done, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0 && !GATHER) {
+    tma_prefetch_desc(&tm16);
+    tma_prefetch_desc(&tm64);
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  // `early`: the offsets were written before the launch that this one follows, so
+  // only the token rows have to be waited for (the producer does, behind its first
+  // weights)
+  if (!p.early) pdl_wait_and_trigger();
+  if (warp == 2)
+    build_tile_table<NT>(p.offsets, p.n_groups, p.dense_rows, p.out_rows, s_prefix, s_offs, s_total,
+                         p.status, lane);
+  tc_fence_before();
+  if constexpr (SPLIT)
+    cluster_sync_all();        // also: the peers run, so their shared memory may be written
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem, tmem_d = tmem + kABufs * kACols;
+  const int total = *s_total * p.blocks;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? total : static_cast<int>(gridDim.x);   // a cluster has one item
+  const int kb0 = SPLIT ? p.kb * rank / p.splits : 0;
+  const int kb1 = SPLIT ? p.kb * (rank + 1) / p.splits : p.kb;
+  // item w: chunk w / blocks; tiles of row block w % blocks
+  auto tiles_of = [&](int b) { return p.swiglu ? 2 : min(2, p.rt - 2 * b); };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, parity = 0, bparity = 0, issued = 0, bissued = 0;
+      bool ok = true, waited = !p.early;
+      auto tokens = [&](int st, uint32_t ph, int kb, const Tile& t) {
+        if (GATHER) return;
+        bissued |= 1u << st;
+        bparity = (bparity & ~(1u << st)) | (ph << st);
+        const int nb = (t.rows + 15) / 16;
+        const bool wide = nb > 2;
+        const int boxes = wide ? (t.rows + 63) / 64 : nb;
+        const int box = wide ? 64 : 16;
+        mbar_expect_tx(&bfull[st], static_cast<uint32_t>(2 * boxes * box * 128));
+        for (int j = 0; j < 2; ++j)
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(smem + st * Cfg::kTok + j * (NT * 128) + i * box * 128, wide ? &tm64 : &tm16,
+                        &bfull[st], kb * kQK + j * 64, t.row0 + i * box);
+      };
+      for (int w = first; w < total && ok; w += step) {
+        const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+        const int nt = tiles_of(t.nt);
+        const uint8_t* src0 = p.w + p.matrix * (static_cast<size_t>(t.g) * (p.swiglu ? 2 : 1)) +
+                              static_cast<size_t>(p.swiglu ? t.nt : 2 * t.nt) * p.kb * p.record;
+        const size_t next = p.swiglu ? p.matrix : static_cast<size_t>(p.kb) * p.record;
+        int behind = kb0;                             // tokens loaded up to here
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!waited && kb - kb0 == kStages) {
+            pdl_wait_and_trigger();
+            waited = true;
+          }
+          if (waited)
+            for (; behind < kb; ++behind) {
+              // the first kStages weights of the CTA: all of phase 0
+              const int st = (stage + kStages - (kb - behind)) % kStages;
+              tokens(st, 0u, behind, t);
+            }
+          if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&wfull[stage], p.record * nt);
+          for (int i = 0; i < nt; ++i)
+            bulk_load(smem + Cfg::kOffW + stage * kWStage + i * kMaxRecord,
+                      src0 + next * i + static_cast<size_t>(kb) * p.record, p.record, &wfull[stage]);
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (waited) {
+            tokens(stage, phase, kb, t);
+            behind = kb + 1;
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!waited) {
+          pdl_wait_and_trigger();
+          waited = true;
+        }
+        if (ok)
+          for (; behind < kb1; ++behind) tokens((stage + kStages - (kb1 - behind)) % kStages, 0u, behind, t);
+      }
+      if (!waited) pdl_wait_and_trigger();
+      if (!ok) fail(s_abort, p.status);
+      // nothing may be in flight into this shared memory when the CTA ends
+      for (int s = 0; s < kStages; ++s) {
+        if ((issued >> s) & 1u) mbar_wait(&wfull[s], (parity >> s) & 1u, nullptr);
+        if ((bissued >> s) & 1u) mbar_wait(&bfull[s], (bparity >> s) & 1u, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (p.early) pdl_wait_and_trigger();
+    if (lane == 0) {
+      int stage = 0, ab = 0, db = 0;
+      uint32_t phase = 0, aphase = 0, dphase = 0;
+      bool ok = true;
+      for (int w = first; w < total && ok; w += step) {
+        const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+        const int nt = tiles_of(t.nt);
+        const uint32_t idesc = idesc_bf16_f32(128, (t.rows + 15) / 16 * 16);
+        if (!mbar_wait(&dempty[db], dphase ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tmem_d + static_cast<uint32_t>(db * 2 * NT);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&bfull[stage], phase, s_abort) || !mbar_wait(&afull[ab], aphase, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sb = smem_u32(smem + stage * Cfg::kTok);
+          const uint64_t b[2] = {sdesc_sw128(sb), sdesc_sw128(sb + NT * 128)};
+          for (int i = 0; i < nt; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_bf16_ts(d + static_cast<uint32_t>(i * NT),
+                           tmem + static_cast<uint32_t>(ab * kACols + i * 64 + k * 8),
+                           b[k >> 2] + 2u * (k & 3), idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+          umma_commit(&empty[stage]);
+          umma_commit(&aempty[ab]);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++ab == kABufs) {
+            ab = 0;
+            aphase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&dfull[db]);
+        if (++db == kDBufs) {
+          db = 0;
+          dphase ^= 1u;
+        }
+      }
+      if (!ok) fail(s_abort, p.status);
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0u, nullptr);
+    }
+    __syncwarp();
+  } else if (warp >= 6 && warp < 6 + kExpandWarps) {
+    if (p.early) pdl_wait_and_trigger();
+    const int tile = (warp - 6) >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int stage = 0, ab = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = true;
+    for (int w = first; w < total && ok; w += step) {
+      const bool mine = tile < tiles_of(w % p.blocks);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&wfull[stage], phase, s_abort));
+        if (!ok) break;
+        uint4 c[4];
+        uint2 sc = make_uint2(0u, 0u);
+        if (mine) {
+          const uint8_t* rec = smem + Cfg::kOffW + stage * kWStage + tile * kMaxRecord;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(rec + quant_piece(r, i));
+          if (p.group == 16) {
+            sc = *reinterpret_cast<const uint2*>(rec + kQCodeBytes + r * 8);
+          } else {       // a byte for every 32 inputs, twice
+            const uint32_t s = *reinterpret_cast<const uint32_t*>(rec + kQCodeBytes + r * 4);
+            sc = make_uint2(__byte_perm(s, 0u, 0x1100), __byte_perm(s, 0u, 0x3322));
+          }
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&aempty[ab], aphase ^ 1u, s_abort));
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (mine) {
+          tc_fence_after();
+          const uint32_t d = tmem + lanes + static_cast<uint32_t>(ab * kACols + tile * 64);
+          if (p.code == MOE_QUANT_INT)
+            expand_row<MOE_QUANT_INT>(c, sc, d);
+          else
+            expand_row<MOE_QUANT_E2M1>(c, sc, d);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&afull[ab]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++ab == kABufs) {
+          ab = 0;
+          aphase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) fail(s_abort, p.status);
+  } else if (GATHER && warp >= 6 + kExpandWarps) {
+    // Thread g copies the 16-byte piece g % 8 of token rows g / 8 + 16 i of both
+    // 64-input blocks of a stage; a piece lands at piece ^ (row % 8) of its 128-byte
+    // row.  Pieces past K are zero (their weights are, but zero times NaN is not).
+    // A stage's copies are one cp.async group, reported kLag groups later.
+    constexpr int kLag = kStages - 2, kPer = NT / 16;
+    const int g = threadIdx.x - kBaseThreads, piece = g & 7, rg = g >> 3;
+    int stage = 0, astage = 0, pending = 0;
+    uint32_t phase = 0;
+    bool ok = true, bad = false;
+    for (int w = first; w < total && ok; w += step) {
+      const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+      const uint4* src[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int row = rg + 16 * i;
+        int tok = -1;
+        if (row < t.rows) {
+          tok = __ldg(p.token + t.row0 + row);
+          if (tok < 0 || tok >= p.x_rows) {
+            bad = true;
+            tok = -1;
+          }
+        }
+        src[i] = tok >= 0 ? p.x + static_cast<size_t>(tok) * (p.ldx / 8) + piece : nullptr;
+      }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sb = smem_u32(smem + stage * Cfg::kTok);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool in = kb * kQK + j * 64 + piece * 8 < p.K;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int row = rg + 16 * i;
+            if (row < t.rows)       // a token out of range reads as zeros
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               sb + j * (NT * 128) + row * 128 + ((piece ^ (row & 7)) << 4)),
+                           "l"(in && src[i] != nullptr ? src[i] + kb * (kQK / 8) + j * 8 : p.x),
+                           "r"(in && src[i] != nullptr ? 16u : 0u)
+                           : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++pending > kLag) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+          fence_proxy_async_smem();
+          mbar_arrive(&bfull[astage]);
+          if (++astage == kStages) astage = 0;
+          --pending;
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    if (ok) {
+      for (; pending > 0; --pending) {
+        mbar_arrive(&bfull[astage]);
+        if (++astage == kStages) astage = 0;
+      }
+    } else if (lane == 0) {
+      fail(s_abort, p.status);
+    }
+    if (bad) report(p.status, MOE_ERR_BAD_INDEX);
+  } else if (warp >= 2 && warp < 6) {
+    if (p.early) pdl_wait_and_trigger();
+    const int q = warp & 3, r = q * 32 + lane;
+    int db = 0;
+    uint32_t dphase = 0;
+    bool ok = true;
+    for (int w = first; w < total; w += step) {
+      const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+      const int nt = tiles_of(t.nt);
+      const float u = p.code == MOE_QUANT_E2M1 ? quant_unit<MOE_QUANT_E2M1>() : 1.f;
+      const float f0 = __ldg(p.factor + (p.swiglu ? 2 * t.g : t.g)) * u;
+      const float f1 = p.swiglu ? __ldg(p.factor + 2 * t.g + 1) * u : f0;
+      ok = __all_sync(0xffffffffu, mbar_wait(&dfull[db], dphase, s_abort));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem_d + (static_cast<uint32_t>(q * 32) << 16) +
+                         static_cast<uint32_t>(db * 2 * NT);
+      if constexpr (SPLIT) {
+        // column c is summed by the CTA c % splits: its slot [rank][c / splits][256 rows]
+        const uint32_t part = smem_u32(smem + Cfg::kOffPart);
+        const int per = (t.rows + 15) / 16 * 16 / p.splits;
+        for (int i = 0; i < nt; ++i)
+          for (int c0 = 0; c0 < t.rows; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(d + static_cast<uint32_t>(i * NT + c0), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const int col = c0 + c, to = col % p.splits;
+              st_cluster_f32(mapa_shared(part, static_cast<uint32_t>(to)) +
+                                 static_cast<uint32_t>(((rank * per + col / p.splits) * 256 + i * 128 + r) * 4),
+                             __uint_as_float(v[c]) * (i == 0 ? f0 : f1));
+            }
+          }
+      } else if (p.swiglu) {
+        const int col = t.nt * 128 + r;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(t.row0) * p.ldo + col;
+        for (int c0 = 0; c0 < t.rows; c0 += 16) {
+          uint32_t a[16], b[16];
+          tmem_ld16(d + static_cast<uint32_t>(c0), a);
+          tmem_ld16(d + static_cast<uint32_t>(NT + c0), b);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (c0 + c < t.rows && col < p.n)
+              out[static_cast<size_t>(c0 + c) * p.ldo] = __float2bfloat16_rn(
+                  silu_f(__uint_as_float(a[c]) * f0) * (__uint_as_float(b[c]) * f1));
+        }
+      } else {
+        for (int i = 0; i < nt; ++i) {
+          const int col = (2 * t.nt + i) * 128 + r;
+          const size_t at = static_cast<size_t>(t.row0) * p.ldo + col;
+          for (int c0 = 0; c0 < t.rows; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(d + static_cast<uint32_t>(i * NT + c0), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if (c0 + c >= t.rows || col >= p.n) continue;
+              const float y = __uint_as_float(v[c]) * f0;
+              if (p.f32)
+                static_cast<float*>(p.out)[at + static_cast<size_t>(c0 + c) * p.ldo] = y;
+              else
+                static_cast<__nv_bfloat16*>(p.out)[at + static_cast<size_t>(c0 + c) * p.ldo] =
+                    __float2bfloat16_rn(y);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[db]);
+      if (++db == kDBufs) {
+        db = 0;
+        dphase ^= 1u;
+      }
+    }
+    if (!ok && lane == 0) fail(s_abort, p.status);
+  }
+
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_sync_all();          // every partial sum has arrived
+    if (first < total && *s_abort == 0) {
+      const Tile t = decode_tile<NT>(first, p.blocks, p.n_groups, s_prefix, s_offs);
+      const float* part = reinterpret_cast<const float*>(smem + Cfg::kOffPart);
+      const int per = (t.rows + 15) / 16 * 16 / p.splits;
+      const int rows = p.swiglu ? 128 : 256;
+      for (int i = threadIdx.x; i < per * rows; i += blockDim.x) {
+        const int c = i / rows, r = i - c * rows;
+        const int token = c * p.splits + rank, col = t.nt * rows + r;
+        if (token >= t.rows || col >= p.n) continue;
+        float y = 0.f, v = 0.f;
+        for (int s = 0; s < p.splits; ++s) {
+          y += part[(s * per + c) * 256 + r];
+          if (p.swiglu) v += part[(s * per + c) * 256 + 128 + r];
+        }
+        if (p.swiglu) y = silu_f(y) * v;
+        const size_t at = static_cast<size_t>(t.row0 + token) * p.ldo + col;
+        if (p.f32)
+          static_cast<float*>(p.out)[at] = y;
+        else
+          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // out_t = sum_{j < k_t} w_{t,j} y[inv_row(t,j)] (+ y_shared[t]) of fp32 rows, in j
@@ -168,32 +619,92 @@ __global__ void __launch_bounds__(128) combine_f32_kernel(
       make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
+template <int NT, bool GATHER, bool SPLIT>
+cudaError_t launch_tile(const CUtensorMap& tm16, const CUtensorMap& tm64, const TileParams& p,
+                        unsigned grid, cudaStream_t s) {
+  using Cfg = TileCfg<NT, SPLIT>;
+  static bool done[64] = {false};
+  auto kern = quant_tile_kernel<NT, GATHER, SPLIT>;
+  const cudaError_t e = set_smem_once(kern, static_cast<int>(Cfg::kSmem), done);
+  if (e != cudaSuccess) return e;
+  const dim3 block(GATHER ? kBaseThreads + kGatherThreads : kBaseThreads);
+  if (!SPLIT) return launch_pdl(kern, dim3(grid), block, Cfg::kSmem, s, tm16, tm64, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, tm16, tm64, p);
+}
+
 }  // namespace
 
 cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
-  RowsParams p{};
+  TileParams p{};
   const QuantShape q = quant_shape(a.n, a.K, a.group);
-  p.x = static_cast<const __nv_bfloat16*>(a.x);
-  p.token = a.token;
-  p.offsets = a.offsets;
   p.w = static_cast<const uint8_t*>(a.w);
   p.factor = reinterpret_cast<const float*>(p.w + q.bytes * a.n_groups * (a.swiglu ? 2 : 1));
+  p.x = static_cast<const uint4*>(a.x);
+  p.token = a.token;
+  p.offsets = a.offsets;
   p.out = a.out;
   p.ldx = a.ldx;
   p.ldo = a.ldo;
   p.out_rows = a.out_rows;
   p.matrix = q.bytes;
+  p.record = quant_record(a.group);
+  p.n_groups = a.n_groups;
   p.dense_rows = a.dense_rows;
   p.x_rows = a.x_rows;
   p.n = a.n;
   p.K = a.K;
   p.kb = q.kb;
+  p.rt = q.rt;
+  p.blocks = a.swiglu ? q.rt : (q.rt + 1) / 2;
+  p.code = a.code;
+  p.group = a.group;
+  p.swiglu = a.swiglu != 0;
+  p.f32 = a.out_f32;
+  p.early = a.early && a.token == nullptr;
+  p.splits = 1;
   p.status = a.status;
-  if (a.code == MOE_QUANT_INT)
-    return a.group == 16 ? launch_code<MOE_QUANT_INT, 16>(a, p, s)
-                         : launch_code<MOE_QUANT_INT, 32>(a, p, s);
-  return a.group == 16 ? launch_code<MOE_QUANT_E2M1, 16>(a, p, s)
-                       : launch_code<MOE_QUANT_E2M1, 32>(a, p, s);
+  CUtensorMap tm16{}, tm64{};
+  if (a.token == nullptr) {
+    const bool ok = a.ldx == a.K ? make_tmap_bf16(&tm16, a.x, a.x_rows, a.K, 16) &&
+                                       make_tmap_bf16(&tm64, a.x, a.x_rows, a.K, 64)
+                                 : encode_tmap(&tm16, a.x, 2, a.x_rows, a.K, a.ldx, 16, 64) &&
+                                       encode_tmap(&tm64, a.x, 2, a.x_rows, a.K, a.ldx, 64, 64);
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  // chunks of tokens there can be: every group may end inside one
+  const bool wide = a.out_rows > 64ll * a.n_groups;
+  const int nt = wide ? 128 : 64;
+  const long long chunks = a.offsets == nullptr ? (a.dense_rows + nt - 1) / nt
+                                                : a.out_rows / nt + std::min(a.out_rows, static_cast<long long>(a.n_groups));
+  const long long items = chunks * p.blocks;
+  if (a.token == nullptr && a.offsets == nullptr && !wide) {
+    int splits = 1;
+    while (splits < 8 && items * splits * 2 <= a.sm_count && p.kb >= 2 * splits) splits *= 2;
+    if (splits > 1) {
+      p.splits = splits;
+      return launch_tile<64, false, true>(tm16, tm64, p, static_cast<unsigned>(items * splits), s);
+    }
+  }
+  const unsigned grid = static_cast<unsigned>(std::min(items, static_cast<long long>(a.sm_count)));
+  if (a.token != nullptr)
+    return wide ? launch_tile<128, true, false>(tm16, tm64, p, grid, s)
+                : launch_tile<64, true, false>(tm16, tm64, p, grid, s);
+  return wide ? launch_tile<128, false, false>(tm16, tm64, p, grid, s)
+              : launch_tile<64, false, false>(tm16, tm64, p, grid, s);
 }
 
 cudaError_t launch_combine_f32(const float* y, const float* y_shared, const int32_t* inv_row,
