@@ -52,9 +52,13 @@ __host__ __device__ inline QuantShape quant_shape(int rows, int K, int group) {
   return s;
 }
 
-// Place of the 16-byte piece c of row r within the codes of a tile, in bytes.
+// Place of the 16-byte piece c of row r within the codes of a tile, in bytes, and of
+// its word w.
 __host__ __device__ constexpr uint32_t quant_piece(int r, int c) {
   return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+__host__ __device__ constexpr uint32_t quant_word(int r, int c, int w) {
+  return quant_piece(r, c) + static_cast<uint32_t>(4 * w);
 }
 
 // ---------------------------------------------------------------- values

@@ -3,22 +3,26 @@
 //
 // 128 rows of weights are the M side of tcgen05.mma, a chunk of up to NT tokens the
 // N side, so every weight is expanded once per chunk.  The expanded weights never
-// see shared memory: a thread reads one row's 64 bytes of codes for 128 inputs
-// (four 16-byte loads), expands them in registers (quant.cuh) and stores them as
-// the A operand in TMEM; only the tokens come from shared memory.  Expanding into
-// shared memory instead would write and read 2 bytes a weight there, four times the
-// codes' own traffic and more than an SM's 128 bytes a clock carry at the rate HBM
-// delivers codes.
+// see shared memory: a thread reads one row's codes of 128 inputs (four 16-byte
+// loads), expands them in registers (quant.cuh) and stores them as the A operand in
+// TMEM; only the tokens come from shared memory.  Expanding into shared memory
+// instead would write and read 2 bytes a weight there, four times the codes' own
+// traffic and more than an SM's 128 bytes a clock carry at the rate HBM delivers
+// codes.
 //
 // An item is two 128-row tiles (of one matrix, or the gate and up rows of the same
 // 128 features) x one chunk of a group's tokens, the whole of K: both tiles share
 // the chunk's tokens, halving their traffic.
 // Roles of the warps, one CTA an SM, items dealt round robin:
-//   0       bulk copies of weight records and TMA loads of token rows into a ring
-//   1       TMEM, MMA issue
+//   0       bulk copies of weight records (128 inputs of both tiles) into a ring
+//   1, 22   MMA issue, a tile each, so that one's waits pass under the other's MMAs
+//           (warp 1 has the TMEM, too)
 //   2-5     epilogue (TMEM lane quarter = warp % 4)
-//   6-13    expansion: four warps a tile
-//   14-17   GATHER: copy the token rows that an index names, instead of TMA
+//   6-21    expansion: four warps a tile, for every other record
+//   23(-26) token rows into a ring of their own: by TMA, or GATHER: copies of the
+//           rows that an index names
+// The two rings free a record as soon as its codes are in registers; two TMEM
+// buffers let one record be expanded while the last one multiplies.
 // Every wait is bounded.
 #include <algorithm>
 
@@ -29,24 +33,30 @@
 namespace moe {
 namespace {
 
-constexpr int kExpandWarps = 8;
-constexpr int kBaseThreads = (6 + kExpandWarps) * 32;
+constexpr int kExpandWarps = 16;
+constexpr int kMmaWarp = 6 + kExpandWarps;        // of the second tile
+constexpr int kTokenWarp = kMmaWarp + 1;
 constexpr int kGatherThreads = 128;
+constexpr int kThreads = (kTokenWarp + 1) * 32;
+constexpr int kThreadsGather = kTokenWarp * 32 + kGatherThreads;
+constexpr int kHalf = 64;                         // inputs of a block of a token stage
 constexpr uint32_t kMaxRecord = quant_record(16);
 constexpr uint32_t kWStage = 2 * kMaxRecord;      // both tiles' records of 128 inputs
 constexpr int kABufs = 2;                         // TMEM buffers of expanded weights
 constexpr uint32_t kACols = 128;                  // columns of one: 2 tiles x 128 bf16 inputs
+constexpr uint32_t kTmemD = kABufs * kACols;      // the accumulators' first column
 
 template <int NT, bool SPLIT>
 struct TileCfg {
-  static constexpr int kStages = NT == 128 ? 4 : (SPLIT ? 4 : 6);
-  static constexpr uint32_t kTok = NT * kQK * 2;  // a stage's tokens: two blocks of 64 inputs
-  static constexpr uint32_t kOffW = kStages * kTok;
-  static constexpr uint32_t kOffPart = kOffW + kStages * kWStage;
+  static constexpr int kW = SPLIT || NT == 128 ? 4 : 6;    // records in flight, even
+  static constexpr int kB = 4;                             // token stages of 128 inputs
+  static constexpr uint32_t kTok = NT * kQK * 2;
+  static constexpr uint32_t kOffW = kB * kTok;
+  static constexpr uint32_t kOffPart = kOffW + kW * kWStage;
   static constexpr uint32_t kPart = SPLIT ? NT * 256 * 4 : 0;
   static constexpr uint32_t kOffBar = kOffPart + kPart;
   static constexpr int kDBufs = NT == 128 ? 1 : 2;
-  static constexpr int kBars = 3 * kStages + 2 * kABufs + 2 * kDBufs + 1;
+  static constexpr int kBars = 2 * kW + 2 * kB + 2 * kABufs + 2 * kDBufs + 1;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
   static constexpr uint32_t kOffPrefix = kOffMisc + 16;
   static constexpr uint32_t kOffOffs = kOffPrefix + (kMaxGroups + 1) * 4;
@@ -91,15 +101,43 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T: lane = row of A, a column two consecutive bf16 inputs.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T over 64 inputs, four MMAs: lane = row of A, a column
+// two consecutive bf16 inputs.  Called by a whole warp, which elects the issuing lane
+// here: under a branch that one lane takes, the operands are not uniform, and an MMA
+// took 47 clocks to issue in a probe and 107 among this kernel's busy warps, whatever
+// N; so it takes what it executes in, 14 at N 16, 32 at 64, 64 at 128.
+__device__ __forceinline__ void umma_bf16_ts64(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// umma_commit by a whole warp.  The lane elected is the same at every call.
+__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+// A value that all lanes have, in a uniform register: what an MMA's operands and the
+// loops around it are made of has to be there, or each MMA pays for moving it.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -114,44 +152,49 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// One row's 128 expanded weights to TMEM columns d .. d + 63, and the row's scales
-// (sc: a byte for every 16 inputs).
+// 64 expanded weights of a row to TMEM columns d .. d + 31: words w, w + 1 of every piece;
+// s4: a scale byte for every 16 inputs.
 template <int CODE>
-__device__ __forceinline__ void expand_row(const uint4 (&c)[4], uint2 sc, uint32_t d) {
+__device__ __forceinline__ void expand_half(const uint32_t (&c0)[4], const uint32_t (&c1)[4],
+                                            uint32_t s4, uint32_t d) {
+  uint32_t v[32];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[32];
-    const uint32_t s4 = h == 0 ? sc.x : sc.y;
+  for (int i = 0; i < 2; ++i) {
+    const QuantScale<CODE> q[2] = {QuantScale<CODE>((s4 >> (16 * i)) & 0xFFu),
+                                   QuantScale<CODE>((s4 >> (16 * i + 8)) & 0xFFu)};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {                    // word 2 h + i: 32 inputs
-      const QuantScale<CODE> q[2] = {QuantScale<CODE>((s4 >> (16 * i)) & 0xFFu),
-                                     QuantScale<CODE>((s4 >> (16 * i + 8)) & 0xFFu)};
+    for (int p = 0; p < 4; ++p) {
+      uint32_t e[4];
+      quant_expand<CODE>(i == 0 ? c0[p] : c1[p], q[p >> 1], e);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t w = h == 0 ? (i == 0 ? c[p].x : c[p].y) : (i == 0 ? c[p].z : c[p].w);
-        uint32_t e[4];
-        quant_expand<CODE>(w, q[p >> 1], e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
-      }
+      for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
     }
-    tmem_st32(d + 32u * h, v);
+  }
+  tmem_st32(d, v);
+}
+
+// Next slot of a ring of n, with the phase that a wait on its barrier goes by.
+__device__ __forceinline__ void advance(int& slot, uint32_t& phase, int n) {
+  if (++slot == n) {
+    slot = 0;
+    phase ^= 1u;
   }
 }
 
 template <int NT, bool GATHER, bool SPLIT>
-__global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBaseThreads, 1)
+__global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     quant_tile_kernel(const __grid_constant__ CUtensorMap tm16,
                       const __grid_constant__ CUtensorMap tm64, const TileParams p) {
   using Cfg = TileCfg<NT, SPLIT>;
-  constexpr int kStages = Cfg::kStages, kDBufs = Cfg::kDBufs;
+  constexpr int kW = Cfg::kW, kB = Cfg::kB, kDBufs = Cfg::kDBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* wfull = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBar);
-  uint64_t* bfull = wfull + kStages;
-  uint64_t* empty = bfull + kStages;
-  uint64_t* afull = empty + kStages;
+  uint64_t* wempty = wfull + kW;
+  uint64_t* bfull = wempty + kW;
+  uint64_t* bempty = bfull + kB;
+  uint64_t* afull = bempty + kB;
   uint64_t* aempty = afull + kABufs;
   uint64_t* dfull = aempty + kABufs;
   uint64_t* dempty = dfull + kDBufs;
@@ -161,27 +204,30 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
   int* s_total = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 8);
   int* s_prefix = reinterpret_cast<int*>(smem + Cfg::kOffPrefix);
   int* s_offs = reinterpret_cast<int*>(smem + Cfg::kOffOffs);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kW; ++s) {
       mbar_init(&wfull[s], 1);
+      mbar_init(&wempty[s], kExpandWarps / 2);
+    }
+    for (int s = 0; s < kB; ++s) {
       mbar_init(&bfull[s], GATHER ? kGatherThreads : 1);
-      mbar_init(&empty[s], kExpandWarps + 1);
+      mbar_init(&bempty[s], 2);
     }
     for (int i = 0; i < kABufs; ++i) {
-      mbar_init(&afull[i], kExpandWarps);
-      mbar_init(&aempty[i], 1);
+      mbar_init(&afull[i], kExpandWarps / 2);
+      mbar_init(&aempty[i], 2);
     }
     for (int i = 0; i < kDBufs; ++i) {
-      mbar_init(&dfull[i], 1);
+      mbar_init(&dfull[i], 2);
       mbar_init(&dempty[i], 4);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == 0 && lane == 0 && !GATHER) {
+  if (warp == kTokenWarp && lane == 0 && !GATHER) {
     tma_prefetch_desc(&tm16);
     tma_prefetch_desc(&tm64);
   }
@@ -190,8 +236,7 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
     tmem_relinquish();
   }
   // `early`: the offsets were written before the launch that this one follows, so
-  // only the token rows have to be waited for (the producer does, behind its first
-  // weights)
+  // weights may stream at once and only the token rows have to be waited for
   if (!p.early) pdl_wait_and_trigger();
   if (warp == 2)
     build_tile_table<NT>(p.offsets, p.n_groups, p.dense_rows, p.out_rows, s_prefix, s_offs, s_total,
@@ -202,158 +247,112 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
   else
     __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem, tmem_d = tmem + kABufs * kACols;
-  const int total = *s_total * p.blocks;
+  // All columns are this CTA's, so they start at 0; as a constant, that makes the MMAs'
+  // operands uniform.
+  if (*s_tmem != 0u && threadIdx.x == 0) report(p.status, MOE_ERR_CUDA);
+  const int total = static_cast<int>(uniform(*s_tmem == 0u ? static_cast<uint32_t>(*s_total * p.blocks) : 0u));
   const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
   const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits : static_cast<int>(blockIdx.x);
   const int step = SPLIT ? total : static_cast<int>(gridDim.x);   // a cluster has one item
+  // records, and halves of them with inputs, of this CTA
   const int kb0 = SPLIT ? p.kb * rank / p.splits : 0;
   const int kb1 = SPLIT ? p.kb * (rank + 1) / p.splits : p.kb;
+  const int halves = min(2 * kb1, (p.K + kHalf - 1) / kHalf) - 2 * kb0;
   // item w: chunk w / blocks; tiles of row block w % blocks
   auto tiles_of = [&](int b) { return p.swiglu ? 2 : min(2, p.rt - 2 * b); };
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, parity = 0, bparity = 0, issued = 0, bissued = 0;
-      bool ok = true, waited = !p.early;
-      auto tokens = [&](int st, uint32_t ph, int kb, const Tile& t) {
-        if (GATHER) return;
-        bissued |= 1u << st;
-        bparity = (bparity & ~(1u << st)) | (ph << st);
-        const int nb = (t.rows + 15) / 16;
-        const bool wide = nb > 2;
-        const int boxes = wide ? (t.rows + 63) / 64 : nb;
-        const int box = wide ? 64 : 16;
-        mbar_expect_tx(&bfull[st], static_cast<uint32_t>(2 * boxes * box * 128));
-        for (int j = 0; j < 2; ++j)
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(smem + st * Cfg::kTok + j * (NT * 128) + i * box * 128, wide ? &tm64 : &tm16,
-                        &bfull[st], kb * kQK + j * 64, t.row0 + i * box);
-      };
-      for (int w = first; w < total && ok; w += step) {
-        const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
-        const int nt = tiles_of(t.nt);
-        const uint8_t* src0 = p.w + p.matrix * (static_cast<size_t>(t.g) * (p.swiglu ? 2 : 1)) +
-                              static_cast<size_t>(p.swiglu ? t.nt : 2 * t.nt) * p.kb * p.record;
-        const size_t next = p.swiglu ? p.matrix : static_cast<size_t>(p.kb) * p.record;
-        int behind = kb0;                             // tokens loaded up to here
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!waited && kb - kb0 == kStages) {
-            pdl_wait_and_trigger();
-            waited = true;
-          }
-          if (waited)
-            for (; behind < kb; ++behind) {
-              // the first kStages weights of the CTA: all of phase 0
-              const int st = (stage + kStages - (kb - behind)) % kStages;
-              tokens(st, 0u, behind, t);
-            }
-          if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(&wfull[stage], p.record * nt);
-          for (int i = 0; i < nt; ++i)
-            bulk_load(smem + Cfg::kOffW + stage * kWStage + i * kMaxRecord,
-                      src0 + next * i + static_cast<size_t>(kb) * p.record, p.record, &wfull[stage]);
-          issued |= 1u << stage;
-          parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (waited) {
-            tokens(stage, phase, kb, t);
-            behind = kb + 1;
-          }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!waited) {
-          pdl_wait_and_trigger();
-          waited = true;
-        }
-        if (ok)
-          for (; behind < kb1; ++behind) tokens((stage + kStages - (kb1 - behind)) % kStages, 0u, behind, t);
-      }
-      if (!waited) pdl_wait_and_trigger();
-      if (!ok) fail(s_abort, p.status);
-      // nothing may be in flight into this shared memory when the CTA ends
-      for (int s = 0; s < kStages; ++s) {
-        if ((issued >> s) & 1u) mbar_wait(&wfull[s], (parity >> s) & 1u, nullptr);
-        if ((bissued >> s) & 1u) mbar_wait(&bfull[s], (bparity >> s) & 1u, nullptr);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (p.early) pdl_wait_and_trigger();
-    if (lane == 0) {
-      int stage = 0, ab = 0, db = 0;
-      uint32_t phase = 0, aphase = 0, dphase = 0;
+      int slot = 0;
+      uint32_t phase = 0, parity = 0, issued = 0;
       bool ok = true;
       for (int w = first; w < total && ok; w += step) {
         const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
         const int nt = tiles_of(t.nt);
-        const uint32_t idesc = idesc_bf16_f32(128, (t.rows + 15) / 16 * 16);
-        if (!mbar_wait(&dempty[db], dphase ^ 1u, s_abort)) {
-          ok = false;
-          break;
-        }
-        const uint32_t d = tmem_d + static_cast<uint32_t>(db * 2 * NT);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&bfull[stage], phase, s_abort) || !mbar_wait(&afull[ab], aphase, s_abort)) {
+        const uint8_t* src = p.w + p.matrix * (static_cast<size_t>(t.g) * (p.swiglu ? 2 : 1)) +
+                             (static_cast<size_t>(p.swiglu ? t.nt : 2 * t.nt) * p.kb + kb0) * p.record;
+        const size_t next = p.swiglu ? p.matrix : static_cast<size_t>(p.kb) * p.record;
+        for (int kb = kb0; kb < kb1; ++kb, src += p.record) {
+          if (!mbar_wait(&wempty[slot], phase ^ 1u, s_abort)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t sb = smem_u32(smem + stage * Cfg::kTok);
-          const uint64_t b[2] = {sdesc_sw128(sb), sdesc_sw128(sb + NT * 128)};
+          mbar_expect_tx(&wfull[slot], p.record * nt);
           for (int i = 0; i < nt; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_bf16_ts(d + static_cast<uint32_t>(i * NT),
-                           tmem + static_cast<uint32_t>(ab * kACols + i * 64 + k * 8),
-                           b[k >> 2] + 2u * (k & 3), idesc, (kb != kb0 || k != 0) ? 1u : 0u);
-          umma_commit(&empty[stage]);
-          umma_commit(&aempty[ab]);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (++ab == kABufs) {
-            ab = 0;
-            aphase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        umma_commit(&dfull[db]);
-        if (++db == kDBufs) {
-          db = 0;
-          dphase ^= 1u;
+            bulk_load(smem + Cfg::kOffW + slot * kWStage + i * kMaxRecord, src + next * i, p.record,
+                      &wfull[slot]);
+          issued |= 1u << slot;
+          parity = (parity & ~(1u << slot)) | (phase << slot);
+          advance(slot, phase, kW);
         }
       }
       if (!ok) fail(s_abort, p.status);
-      umma_commit(mma_done);
-      mbar_wait(mma_done, 0u, nullptr);
+      // nothing may be in flight into this shared memory when the CTA ends
+      for (int s = 0; s < kW; ++s)
+        if ((issued >> s) & 1u) mbar_wait(&wfull[s], (parity >> s) & 1u, nullptr);
     }
     __syncwarp();
-  } else if (warp >= 6 && warp < 6 + kExpandWarps) {
+  } else if (warp == 1 || warp == kMmaWarp) {
     if (p.early) pdl_wait_and_trigger();
-    const int tile = (warp - 6) >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int stage = 0, ab = 0;
+    const uint32_t tok0 = uniform(smem_u32(smem));
+    const uint32_t tile = warp == 1 ? 0u : 1u;
+    int bs = 0, ab = 0, db = 0;
+    uint32_t bphase = 0, aphase = 0, dphase = 0;
+    bool ok = true;
+    for (int w = first; w < total && ok; w += step) {
+      const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+      const bool mine = uniform(tile < tiles_of(t.nt)) != 0u;
+      const uint32_t idesc = uniform(idesc_bf16_f32(128, (t.rows + 15) / 16 * 16));
+      const uint32_t d = kTmemD + static_cast<uint32_t>(db * 2 + tile) * NT;
+      ok = warp_wait(&dempty[db], dphase ^ 1u, s_abort);
+      for (int h = 0; h < halves && ok; h += 2) {
+        ok = warp_wait(&bfull[bs], bphase, s_abort) && warp_wait(&afull[ab], aphase, s_abort);
+        if (!ok) break;
+        if (mine) {
+          tc_fence_after();
+          const uint64_t b = sdesc_sw128(tok0 + static_cast<uint32_t>(bs) * Cfg::kTok);
+          const uint32_t a = static_cast<uint32_t>(ab) * kACols + tile * 64;
+          umma_bf16_ts64(d, a, b, idesc, h != 0);
+          if (h + 1 < halves) umma_bf16_ts64(d, a + 32, b + (NT * 128 >> 4), idesc, 1u);
+        }
+        umma_commit_warp(&bempty[bs]);
+        umma_commit_warp(&aempty[ab]);
+        advance(bs, bphase, kB);
+        advance(ab, aphase, kABufs);
+      }
+      if (!ok) break;
+      umma_commit_warp(&dfull[db]);
+      advance(db, dphase, kDBufs);
+    }
+    if (!ok && lane == 0) fail(s_abort, p.status);
+    umma_commit_warp(mma_done);
+    mbar_wait(mma_done, 0u, nullptr);
+    __syncwarp();
+  } else if (warp >= 6 && warp < kMmaWarp) {
+    if (p.early) pdl_wait_and_trigger();
+    const int set = (warp - 6) >> 3, tile = ((warp - 6) >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const uint32_t d = (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                       static_cast<uint32_t>(set * kACols + tile * 64);
+    int slot = set, n = 0;                        // n: records before this item
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
     for (int w = first; w < total && ok; w += step) {
       const bool mine = tile < tiles_of(w % p.blocks);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&wfull[stage], phase, s_abort));
+      for (int kb = kb0 + ((n ^ set) & 1); kb < kb1; kb += 2) {
+        ok = warp_wait(&wfull[slot], phase, s_abort);
         if (!ok) break;
-        uint4 c[4];
+        uint32_t c[4][4];                         // [word][piece]
         uint2 sc = make_uint2(0u, 0u);
         if (mine) {
-          const uint8_t* rec = smem + Cfg::kOffW + stage * kWStage + tile * kMaxRecord;
+          const uint8_t* rec = smem + Cfg::kOffW + slot * kWStage + tile * kMaxRecord;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(rec + quant_piece(r, i));
+          for (int i = 0; i < 4; ++i) {
+            const uint4 q = *reinterpret_cast<const uint4*>(rec + quant_piece(r, i));
+            c[0][i] = q.x;
+            c[1][i] = q.y;
+            c[2][i] = q.z;
+            c[3][i] = q.w;
+          }
           if (p.group == 16) {
             sc = *reinterpret_cast<const uint2*>(rec + kQCodeBytes + r * 8);
           } else {       // a byte for every 32 inputs, twice
@@ -361,41 +360,75 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
             sc = make_uint2(__byte_perm(s, 0u, 0x1100), __byte_perm(s, 0u, 0x3322));
           }
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&aempty[ab], aphase ^ 1u, s_abort));
-        if (!ok) break;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (lane == 0) mbar_arrive(&wempty[slot]);
+        slot += 2;
+        if (slot >= kW) {
+          slot -= kW;
+          phase ^= 1u;
+        }
+        ok = warp_wait(&aempty[set], aphase ^ 1u, s_abort);
+        if (!ok) break;
+        aphase ^= 1u;
         if (mine) {
           tc_fence_after();
-          const uint32_t d = tmem + lanes + static_cast<uint32_t>(ab * kACols + tile * 64);
-          if (p.code == MOE_QUANT_INT)
-            expand_row<MOE_QUANT_INT>(c, sc, d);
-          else
-            expand_row<MOE_QUANT_E2M1>(c, sc, d);
+          if (p.code == MOE_QUANT_INT) {
+            expand_half<MOE_QUANT_INT>(c[0], c[1], sc.x, d);
+            expand_half<MOE_QUANT_INT>(c[2], c[3], sc.y, d + 32);
+          } else {
+            expand_half<MOE_QUANT_E2M1>(c[0], c[1], sc.x, d);
+            expand_half<MOE_QUANT_E2M1>(c[2], c[3], sc.y, d + 32);
+          }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&afull[ab]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (++ab == kABufs) {
-          ab = 0;
-          aphase ^= 1u;
-        }
+        if (lane == 0) mbar_arrive(&afull[set]);
       }
+      n += kb1 - kb0;
     }
     if (!ok && lane == 0) fail(s_abort, p.status);
-  } else if (GATHER && warp >= 6 + kExpandWarps) {
-    // Thread g copies the 16-byte piece g % 8 of token rows g / 8 + 16 i of both
-    // 64-input blocks of a stage; a piece lands at piece ^ (row % 8) of its 128-byte
-    // row.  Pieces past K are zero (their weights are, but zero times NaN is not).
+  } else if (!GATHER && warp == kTokenWarp) {
+    if (p.early) pdl_wait_and_trigger();
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t phase = 0, parity = 0, issued = 0;
+      bool ok = true;
+      for (int w = first; w < total && ok; w += step) {
+        const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+        const int nb = (t.rows + 15) / 16;
+        const bool wide = nb > 2;
+        const int boxes = wide ? (t.rows + 63) / 64 : nb, box = wide ? 64 : 16;
+        for (int h = 0; h < halves; h += 2) {
+          if (!mbar_wait(&bempty[slot], phase ^ 1u, s_abort)) {
+            ok = false;
+            break;
+          }
+          const int blocks = min(2, halves - h);
+          mbar_expect_tx(&bfull[slot], static_cast<uint32_t>(blocks * boxes * box * kHalf * 2));
+          for (int j = 0; j < blocks; ++j)
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(smem + slot * Cfg::kTok + j * (NT * 128) + i * box * kHalf * 2,
+                          wide ? &tm64 : &tm16, &bfull[slot], (2 * kb0 + h + j) * kHalf,
+                          t.row0 + i * box);
+          issued |= 1u << slot;
+          parity = (parity & ~(1u << slot)) | (phase << slot);
+          advance(slot, phase, kB);
+        }
+      }
+      if (!ok) fail(s_abort, p.status);
+      for (int s = 0; s < kB; ++s)
+        if ((issued >> s) & 1u) mbar_wait(&bfull[s], (parity >> s) & 1u, nullptr);
+    }
+    __syncwarp();
+  } else if (GATHER && warp >= kTokenWarp) {
+    // Thread g copies the 16-byte piece g % 8 of token rows g / 8 + 16 i of a stage; a
+    // piece lands at piece ^ (row % 8) of its 128-byte row.  Pieces past K are zero
+    // (their weights are, but zero times NaN is not), and so is a token out of range.
     // A stage's copies are one cp.async group, reported kLag groups later.
-    constexpr int kLag = kStages - 2, kPer = NT / 16;
-    const int g = threadIdx.x - kBaseThreads, piece = g & 7, rg = g >> 3;
-    int stage = 0, astage = 0, pending = 0;
+    constexpr int kLag = kB - 2, kPer = NT / 16;
+    const int g = threadIdx.x - kTokenWarp * 32, piece = g & 7, rg = g >> 3;
+    int slot = 0, aslot = 0, pending = 0;
     uint32_t phase = 0;
     bool ok = true, bad = false;
     for (int w = first; w < total && ok; w += step) {
@@ -414,22 +447,23 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
         }
         src[i] = tok >= 0 ? p.x + static_cast<size_t>(tok) * (p.ldx / 8) + piece : nullptr;
       }
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
+      for (int h = 0; h < halves; h += 2) {
+        if (!mbar_wait(&bempty[slot], phase ^ 1u, s_abort)) {
           ok = false;
           break;
         }
-        const uint32_t sb = smem_u32(smem + stage * Cfg::kTok);
+        const uint32_t sb = smem_u32(smem + slot * Cfg::kTok);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const bool in = kb * kQK + j * 64 + piece * 8 < p.K;
+          const int k = (2 * kb0 + h + j) * kHalf + piece * 8;
+          const bool in = k < p.K;
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const int row = rg + 16 * i;
-            if (row < t.rows)       // a token out of range reads as zeros
+            if (row < t.rows)
               asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                sb + j * (NT * 128) + row * 128 + ((piece ^ (row & 7)) << 4)),
-                           "l"(in && src[i] != nullptr ? src[i] + kb * (kQK / 8) + j * 8 : p.x),
+                           "l"(in && src[i] != nullptr ? src[i] + (2 * kb0 + h + j) * 8 : p.x),
                            "r"(in && src[i] != nullptr ? 16u : 0u)
                            : "memory");
           }
@@ -438,22 +472,19 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
         if (++pending > kLag) {
           asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
           fence_proxy_async_smem();
-          mbar_arrive(&bfull[astage]);
-          if (++astage == kStages) astage = 0;
+          mbar_arrive(&bfull[aslot]);
+          if (++aslot == kB) aslot = 0;
           --pending;
         }
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        advance(slot, phase, kB);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     if (ok) {
       for (; pending > 0; --pending) {
-        mbar_arrive(&bfull[astage]);
-        if (++astage == kStages) astage = 0;
+        mbar_arrive(&bfull[aslot]);
+        if (++aslot == kB) aslot = 0;
       }
     } else if (lane == 0) {
       fail(s_abort, p.status);
@@ -471,10 +502,10 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
       const float u = p.code == MOE_QUANT_E2M1 ? quant_unit<MOE_QUANT_E2M1>() : 1.f;
       const float f0 = __ldg(p.factor + (p.swiglu ? 2 * t.g : t.g)) * u;
       const float f1 = p.swiglu ? __ldg(p.factor + 2 * t.g + 1) * u : f0;
-      ok = __all_sync(0xffffffffu, mbar_wait(&dfull[db], dphase, s_abort));
+      ok = warp_wait(&dfull[db], dphase, s_abort);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem_d + (static_cast<uint32_t>(q * 32) << 16) +
+      const uint32_t d = kTmemD + (static_cast<uint32_t>(q * 32) << 16) +
                          static_cast<uint32_t>(db * 2 * NT);
       if constexpr (SPLIT) {
         // column c is summed by the CTA c % splits: its slot [rank][c / splits][256 rows]
@@ -531,10 +562,7 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&dempty[db]);
-      if (++db == kDBufs) {
-        db = 0;
-        dphase ^= 1u;
-      }
+      advance(db, dphase, kDBufs);
     }
     if (!ok && lane == 0) fail(s_abort, p.status);
   }
@@ -569,7 +597,7 @@ __global__ void __launch_bounds__(GATHER ? kBaseThreads + kGatherThreads : kBase
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*s_tmem, 512);
   }
 }
 
@@ -627,7 +655,7 @@ cudaError_t launch_tile(const CUtensorMap& tm16, const CUtensorMap& tm64, const 
   auto kern = quant_tile_kernel<NT, GATHER, SPLIT>;
   const cudaError_t e = set_smem_once(kern, static_cast<int>(Cfg::kSmem), done);
   if (e != cudaSuccess) return e;
-  const dim3 block(GATHER ? kBaseThreads + kGatherThreads : kBaseThreads);
+  const dim3 block(GATHER ? kThreadsGather : kThreads);
   if (!SPLIT) return launch_pdl(kern, dim3(grid), block, Cfg::kSmem, s, tm16, tm64, p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
