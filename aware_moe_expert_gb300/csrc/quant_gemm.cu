@@ -122,23 +122,52 @@ __device__ __forceinline__ void umma_bf16_ts64(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
+// Barriers by their shared-memory address.
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // umma_commit by a whole warp.  The lane elected is the same at every call.
-__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
+__device__ __forceinline__ void commit_at(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_u32(bar))
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
+}
+
+// mbar_wait's loop.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (try_wait_at(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// A wait of a whole warp; false where one of its lanes gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, try_wait_at(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_on(bar, parity, abort));
 }
 
 // A value that all lanes have, in a uniform register: what an MMA's operands and the
 // loops around it are made of has to be there, or each MMA pays for moving it.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -148,29 +177,41 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// 64 expanded weights of a row to TMEM columns d .. d + 31: words w, w + 1 of every piece;
-// s4: a scale byte for every 16 inputs.
+// 128 expanded weights of a row (c: its pieces, sc: a scale byte for every 16 inputs) to
+// TMEM columns d .. d + 63.
 template <int CODE>
-__device__ __forceinline__ void expand_half(const uint32_t (&c0)[4], const uint32_t (&c1)[4],
-                                            uint32_t s4, uint32_t d) {
-  uint32_t v[32];
+__device__ __forceinline__ void expand_row(const uint4 (&c)[4], uint2 sc, uint32_t d) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const QuantScale<CODE> q[2] = {QuantScale<CODE>((s4 >> (16 * i)) & 0xFFu),
-                                   QuantScale<CODE>((s4 >> (16 * i + 8)) & 0xFFu)};
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[32];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      uint32_t e[4];
-      quant_expand<CODE>(i == 0 ? c0[p] : c1[p], q[p >> 1], e);
+    for (int i = 0; i < 2; ++i) {                 // word 2 h + i of every piece
+      const uint32_t s2 = (h == 0 ? sc.x : sc.y) >> (16 * i);
+      const QuantScale<CODE> q[2] = {QuantScale<CODE>(s2 & 0xFFu), QuantScale<CODE>((s2 >> 8) & 0xFFu)};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t w = h == 0 ? (i == 0 ? c[p].x : c[p].y) : (i == 0 ? c[p].z : c[p].w);
+        uint32_t e[4];
+        quant_expand<CODE>(w, q[p >> 1], e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
+      }
     }
+    tmem_st32(d + 32u * h, v);
   }
-  tmem_st32(d, v);
 }
 
 // Next slot of a ring of n, with the phase that a wait on its barrier goes by.
@@ -205,6 +246,11 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
   int* s_prefix = reinterpret_cast<int*>(smem + Cfg::kOffPrefix);
   int* s_offs = reinterpret_cast<int*>(smem + Cfg::kOffOffs);
   const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t sbase = uniform(smem_u32(smem));
+  const uint32_t b_wfull = sbase + Cfg::kOffBar, b_wempty = b_wfull + 8 * kW;
+  const uint32_t b_bfull = b_wempty + 8 * kW, b_bempty = b_bfull + 8 * kB;
+  const uint32_t b_afull = b_bempty + 8 * kB, b_aempty = b_afull + 8 * kABufs;
+  const uint32_t b_dfull = b_aempty + 8 * kABufs, b_dempty = b_dfull + 8 * kDBufs;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kW; ++s) {
@@ -294,7 +340,6 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     __syncwarp();
   } else if (warp == 1 || warp == kMmaWarp) {
     if (p.early) pdl_wait_and_trigger();
-    const uint32_t tok0 = uniform(smem_u32(smem));
     const uint32_t tile = warp == 1 ? 0u : 1u;
     int bs = 0, ab = 0, db = 0;
     uint32_t bphase = 0, aphase = 0, dphase = 0;
@@ -304,28 +349,28 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
       const bool mine = uniform(tile < tiles_of(t.nt)) != 0u;
       const uint32_t idesc = uniform(idesc_bf16_f32(128, (t.rows + 15) / 16 * 16));
       const uint32_t d = kTmemD + static_cast<uint32_t>(db * 2 + tile) * NT;
-      ok = warp_wait(&dempty[db], dphase ^ 1u, s_abort);
+      ok = warp_wait(b_dempty + 8 * db, dphase ^ 1u, s_abort);
       for (int h = 0; h < halves && ok; h += 2) {
-        ok = warp_wait(&bfull[bs], bphase, s_abort) && warp_wait(&afull[ab], aphase, s_abort);
+        ok = warp_wait(b_bfull + 8 * bs, bphase, s_abort) && warp_wait(b_afull + 8 * ab, aphase, s_abort);
         if (!ok) break;
         if (mine) {
           tc_fence_after();
-          const uint64_t b = sdesc_sw128(tok0 + static_cast<uint32_t>(bs) * Cfg::kTok);
+          const uint64_t b = sdesc_sw128(sbase + static_cast<uint32_t>(bs) * Cfg::kTok);
           const uint32_t a = static_cast<uint32_t>(ab) * kACols + tile * 64;
           umma_bf16_ts64(d, a, b, idesc, h != 0);
           if (h + 1 < halves) umma_bf16_ts64(d, a + 32, b + (NT * 128 >> 4), idesc, 1u);
         }
-        umma_commit_warp(&bempty[bs]);
-        umma_commit_warp(&aempty[ab]);
+        commit_at(b_bempty + 8 * bs);
+        commit_at(b_aempty + 8 * ab);
         advance(bs, bphase, kB);
         advance(ab, aphase, kABufs);
       }
       if (!ok) break;
-      umma_commit_warp(&dfull[db]);
+      commit_at(b_dfull + 8 * db);
       advance(db, dphase, kDBufs);
     }
     if (!ok && lane == 0) fail(s_abort, p.status);
-    umma_commit_warp(mma_done);
+    commit_at(smem_u32(mma_done));
     mbar_wait(mma_done, 0u, nullptr);
     __syncwarp();
   } else if (warp >= 6 && warp < kMmaWarp) {
@@ -333,57 +378,51 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     const int set = (warp - 6) >> 3, tile = ((warp - 6) >> 2) & 1, r = (warp & 3) * 32 + lane;
     const uint32_t d = (static_cast<uint32_t>((warp & 3) * 32) << 16) +
                        static_cast<uint32_t>(set * kACols + tile * 64);
+    const uint32_t swap = static_cast<uint32_t>((r >> 1) & 3) << 4;
+    const uint32_t codes = sbase + Cfg::kOffW + tile * kMaxRecord + r * 64;
+    const uint32_t scales = sbase + Cfg::kOffW + tile * kMaxRecord + kQCodeBytes +
+                            r * (p.group == 16 ? 8 : 4);
     int slot = set, n = 0;                        // n: records before this item
-    uint32_t phase = 0, aphase = 0;
+    uint32_t phase = 0, aphase = 1;
     bool ok = true;
     for (int w = first; w < total && ok; w += step) {
-      const bool mine = tile < tiles_of(w % p.blocks);
+      const bool mine = uniform(tile < tiles_of(w % p.blocks)) != 0u;
       for (int kb = kb0 + ((n ^ set) & 1); kb < kb1; kb += 2) {
-        ok = warp_wait(&wfull[slot], phase, s_abort);
+        ok = warp_wait(b_wfull + 8 * slot, phase, s_abort);
         if (!ok) break;
-        uint32_t c[4][4];                         // [word][piece]
+        uint4 c[4];                               // pieces
         uint2 sc = make_uint2(0u, 0u);
         if (mine) {
-          const uint8_t* rec = smem + Cfg::kOffW + slot * kWStage + tile * kMaxRecord;
+          const uint32_t at = codes + slot * kWStage;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 q = *reinterpret_cast<const uint4*>(rec + quant_piece(r, i));
-            c[0][i] = q.x;
-            c[1][i] = q.y;
-            c[2][i] = q.z;
-            c[3][i] = q.w;
-          }
-          if (p.group == 16) {
-            sc = *reinterpret_cast<const uint2*>(rec + kQCodeBytes + r * 8);
-          } else {       // a byte for every 32 inputs, twice
-            const uint32_t s = *reinterpret_cast<const uint32_t*>(rec + kQCodeBytes + r * 4);
-            sc = make_uint2(__byte_perm(s, 0u, 0x1100), __byte_perm(s, 0u, 0x3322));
-          }
+          for (uint32_t i = 0; i < 4; ++i) c[i] = lds128(at + ((i << 4) ^ swap));
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc.x) : "r"(scales + slot * kWStage) : "memory");
+          if (p.group == 16)
+            asm volatile("ld.shared.b32 %0, [%1+4];" : "=r"(sc.y) : "r"(scales + slot * kWStage) : "memory");
+          else           // a byte for every 32 inputs, twice
+            sc = make_uint2(__byte_perm(sc.x, 0u, 0x1100), __byte_perm(sc.x, 0u, 0x3322));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&wempty[slot]);
+        if (lane == 0) arrive_at(b_wempty + 8 * slot);
         slot += 2;
         if (slot >= kW) {
           slot -= kW;
           phase ^= 1u;
         }
-        ok = warp_wait(&aempty[set], aphase ^ 1u, s_abort);
+        ok = warp_wait(b_aempty + 8 * set, aphase, s_abort);
         if (!ok) break;
         aphase ^= 1u;
         if (mine) {
           tc_fence_after();
-          if (p.code == MOE_QUANT_INT) {
-            expand_half<MOE_QUANT_INT>(c[0], c[1], sc.x, d);
-            expand_half<MOE_QUANT_INT>(c[2], c[3], sc.y, d + 32);
-          } else {
-            expand_half<MOE_QUANT_E2M1>(c[0], c[1], sc.x, d);
-            expand_half<MOE_QUANT_E2M1>(c[2], c[3], sc.y, d + 32);
-          }
+          if (p.code == MOE_QUANT_INT)
+            expand_row<MOE_QUANT_INT>(c, sc, d);
+          else
+            expand_row<MOE_QUANT_E2M1>(c, sc, d);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&afull[set]);
+        if (lane == 0) arrive_at(b_afull + 8 * set);
       }
       n += kb1 - kb0;
     }
@@ -434,39 +473,43 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     for (int w = first; w < total && ok; w += step) {
       const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
       const uint4* src[kPer];
+      uint32_t size[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int row = rg + 16 * i;
-        int tok = -1;
+        src[i] = p.x;
+        size[i] = 0u;
         if (row < t.rows) {
-          tok = __ldg(p.token + t.row0 + row);
-          if (tok < 0 || tok >= p.x_rows) {
+          const int tok = __ldg(p.token + t.row0 + row);
+          if (tok >= 0 && tok < p.x_rows) {
+            src[i] = p.x + static_cast<size_t>(tok) * (p.ldx / 8) + kb0 * (kQK / 8) + piece;
+            size[i] = 16u;
+          } else {
             bad = true;
-            tok = -1;
           }
         }
-        src[i] = tok >= 0 ? p.x + static_cast<size_t>(tok) * (p.ldx / 8) + piece : nullptr;
       }
       for (int h = 0; h < halves; h += 2) {
-        if (!mbar_wait(&bempty[slot], phase ^ 1u, s_abort)) {
+        if (!try_wait_at(b_bempty + 8 * slot, phase ^ 1u) &&
+            !wait_on(b_bempty + 8 * slot, phase ^ 1u, s_abort)) {
           ok = false;
           break;
         }
-        const uint32_t sb = smem_u32(smem + slot * Cfg::kTok);
+        const uint32_t sb = sbase + slot * Cfg::kTok + rg * 128 + ((piece ^ (rg & 7)) << 4);
+        const int k = (2 * kb0 + h) * kHalf + piece * 8;
+        const uint32_t in0 = k < p.K ? 16u : 0u, in1 = k + kHalf < p.K ? 16u : 0u;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int k = (2 * kb0 + h + j) * kHalf + piece * 8;
-          const bool in = k < p.K;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int row = rg + 16 * i;
-            if (row < t.rows)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                               sb + j * (NT * 128) + row * 128 + ((piece ^ (row & 7)) << 4)),
-                           "l"(in && src[i] != nullptr ? src[i] + (2 * kb0 + h + j) * 8 : p.x),
-                           "r"(in && src[i] != nullptr ? 16u : 0u)
-                           : "memory");
+        for (int i = 0; i < kPer; ++i) {
+          if (16 * i >= t.rows) break;
+          if (rg + 16 * i < t.rows) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + i * 16 * 128),
+                         "l"(src[i]), "r"(size[i] & in0)
+                         : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + NT * 128 + i * 16 * 128),
+                         "l"(src[i] + kHalf / 8), "r"(size[i] & in1)
+                         : "memory");
           }
+          src[i] += kQK / 8;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (++pending > kLag) {
@@ -502,7 +545,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
       const float u = p.code == MOE_QUANT_E2M1 ? quant_unit<MOE_QUANT_E2M1>() : 1.f;
       const float f0 = __ldg(p.factor + (p.swiglu ? 2 * t.g : t.g)) * u;
       const float f1 = p.swiglu ? __ldg(p.factor + 2 * t.g + 1) * u : f0;
-      ok = warp_wait(&dfull[db], dphase, s_abort);
+      ok = warp_wait(b_dfull + 8 * db, dphase, s_abort);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = kTmemD + (static_cast<uint32_t>(q * 32) << 16) +
