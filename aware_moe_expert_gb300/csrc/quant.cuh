@@ -17,8 +17,9 @@
 //   integer codes  nibble i of the low half is input 2i, of the high half 2i + 1;
 //                  0x4300 | q is 128 + q, and fma(128 + q, s, -136 s) = s (q - 8)
 //   e2m1           sign, exponent and mantissa stand so that pair i, moved to the
-//                  bits 15 and 8-6 of a half word, reads as code * 2^-126 (a
-//                  subnormal for 0.5); times s * 2^117 that is code * s * 2^-9
+//                  bits 15 and 8-6 of a half word by one shift (i 0, 1) or two, reads
+//                  as code * 2^-126 (a subnormal for 0.5); times s * 2^117 that is
+//                  code * s * 2^-9
 // Both are exact: s has four significant bits, a code at most three, 136 s eight.
 // The factor 2^9 joins the matrix's own in the epilogue.
 //
@@ -65,12 +66,6 @@ __host__ __device__ constexpr uint32_t quant_word(int r, int c, int w) {
 constexpr uint32_t kScaleBase = 0x37803780u;     // exponent field of 2^-16: s
 constexpr uint32_t kScaleBase117 = 0x72007200u;  // of 2^101: s * 2^117
 
-// A scale byte as a pair of equal bf16.
-template <int CODE>
-__device__ __forceinline__ uint32_t quant_scale(uint32_t byte) {
-  return byte * 0x00100010u + (CODE == MOE_QUANT_E2M1 ? kScaleBase117 : kScaleBase);
-}
-
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -83,13 +78,25 @@ __device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t 
   return d;
 }
 
-// What a word's expansion needs of its group's scale.
+// (a & b) | c in one operation.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// What a word's expansion needs of its group's scale: byte I of `bytes` as a pair of
+// equal bf16, and -136 times it.
 template <int CODE>
 struct QuantScale {
   uint32_t s, c;
-  __device__ __forceinline__ explicit QuantScale(uint32_t byte) {
-    s = quant_scale<CODE>(byte);
-    c = CODE == MOE_QUANT_INT ? hmul2_bf16(s, 0xC308C308u) : 0u;   // -136 s
+  template <int I>
+  __device__ __forceinline__ static QuantScale at(uint32_t bytes) {
+    QuantScale q;
+    q.s = __byte_perm(bytes, 0u, 0x4040 | I << 8 | I) * 16u +
+          (CODE == MOE_QUANT_E2M1 ? kScaleBase117 : kScaleBase);
+    q.c = CODE == MOE_QUANT_INT ? hmul2_bf16(q.s, 0xC308C308u) : 0u;
+    return q;
   }
 };
 
@@ -100,14 +107,12 @@ __device__ __forceinline__ void quant_expand(uint32_t w, const QuantScale<CODE>&
   if (CODE == MOE_QUANT_INT) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = hfma2_bf16(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, q.s, q.c);
+      v[i] = hfma2_bf16(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), q.s, q.c);
   } else {
     v[0] = hmul2_bf16(w & 0x81C081C0u, q.s);
     v[1] = hmul2_bf16((w << 3) & 0x81C081C0u, q.s);
-    v[2] = hmul2_bf16((w << 6) & 0x81C081C0u, q.s);
-    v[3] = hmul2_bf16(((w << 1) & 0x80008000u) | ((w >> 5) & 0x01000100u) |
-                          ((w >> 4) & 0x00C000C0u),
-                      q.s);
+    v[2] = hmul2_bf16(and_or(w << 6, 0x01C001C0u, (w << 1) & 0x80008000u), q.s);
+    v[3] = hmul2_bf16(and_or(w >> 3, 0x01C001C0u, (w << 2) & 0x80008000u), q.s);
   }
 }
 
@@ -121,7 +126,7 @@ __device__ __forceinline__ constexpr float quant_unit() {
 __host__ __device__ inline uint32_t quant_place(int code, uint32_t q, int pair, int half) {
   if (code == MOE_QUANT_INT) return q << (4 * pair + 16 * half);
   // bits of sign, exponent high, exponent low, mantissa for each pair
-  const uint32_t at[4] = {0x0F080706u, 0x0C050403u, 0x09020100u, 0x0E0D0B0Au};
+  const uint32_t at[4] = {0x0F080706u, 0x0C050403u, 0x0E020100u, 0x0D0B0A09u};
   uint32_t v = 0;
   for (int b = 0; b < 4; ++b)
     v |= ((q >> b) & 1u) << (((at[pair] >> (8 * b)) & 31u) + 16u * half);

@@ -199,8 +199,10 @@ __device__ __forceinline__ void expand_row(const uint4 (&c)[4], uint2 sc, uint32
     uint32_t v[32];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {                 // word 2 h + i of every piece
-      const uint32_t s2 = (h == 0 ? sc.x : sc.y) >> (16 * i);
-      const QuantScale<CODE> q[2] = {QuantScale<CODE>(s2 & 0xFFu), QuantScale<CODE>((s2 >> 8) & 0xFFu)};
+      const uint32_t s4 = h == 0 ? sc.x : sc.y;
+      const QuantScale<CODE> q[2] = {
+          i == 0 ? QuantScale<CODE>::template at<0>(s4) : QuantScale<CODE>::template at<2>(s4),
+          i == 0 ? QuantScale<CODE>::template at<1>(s4) : QuantScale<CODE>::template at<3>(s4)};
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const uint32_t w = h == 0 ? (i == 0 ? c[p].x : c[p].y) : (i == 0 ? c[p].z : c[p].w);

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(const PackParams p
         *reinterpret_cast<const uint32_t*>(rec + quant_word(r, (k % 32) / 8, k / 32));
     uint32_t e[4];
     quant_expand<CODE>(
-        w, QuantScale<CODE>(rec[kQCodeBytes + r * (kQK / p.group) + k / p.group]), e);
+        w, QuantScale<CODE>::template at<0>(rec[kQCodeBytes + r * (kQK / p.group) + k / p.group]), e);
     const float f = factor[m], u = quant_unit<CODE>();
     uint32_t o[4];
     for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(bf16lo(e[i]) * u * f, bf16hi(e[i]) * u * f);
