@@ -21,10 +21,11 @@
 //   6-21    expansion: four warps a tile, for every other record
 //   23(-26) token rows into a ring of their own: by TMA, or GATHER: copies of the
 //           rows that an index names
-// The two rings free a record as soon as its codes are in registers; two TMEM
-// buffers let one record be expanded while the last one multiplies.
+// The two rings free a record as soon as its codes are in registers; two records'
+// TMEM buffers let one be expanded while the last one multiplies.
 // Every wait is bounded.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.cuh"
 #include "moe_internal.h"
@@ -42,9 +43,7 @@ constexpr int kThreadsGather = kTokenWarp * 32 + kGatherThreads;
 constexpr int kHalf = 64;                         // inputs of a block of a token stage
 constexpr uint32_t kMaxRecord = quant_record(16);
 constexpr uint32_t kWStage = 2 * kMaxRecord;      // both tiles' records of 128 inputs
-constexpr int kABufs = 2;                         // TMEM buffers of expanded weights
-constexpr uint32_t kACols = 128;                  // columns of one: 2 tiles x 128 bf16 inputs
-constexpr uint32_t kTmemD = kABufs * kACols;      // the accumulators' first column
+constexpr uint32_t kTmemD = 256;                  // the accumulators' first column, behind A
 
 template <int NT, bool SPLIT>
 struct TileCfg {
@@ -55,14 +54,22 @@ struct TileCfg {
   static constexpr uint32_t kOffPart = kOffW + kW * kWStage;
   static constexpr uint32_t kPart = SPLIT ? NT * 256 * 4 : 0;
   static constexpr uint32_t kOffBar = kOffPart + kPart;
+  // TMEM buffers of expanded weights (a tile's columns, then the other's), kParts a
+  // record.  One of 128 inputs takes fewer barriers, which count where the expansion
+  // bounds; of 64, the MMAs start earlier, which counts where they do (16384 tokens of K
+  // 7168 642 us, 685 with one part; layer of 64 tokens 255 us with two parts, 222 with one).
+  static constexpr int kParts = NT == 128 ? 2 : 1;
+  static constexpr int kABufs = 2 * kParts;
+  static constexpr uint32_t kACols = 128 / kParts;
   static constexpr int kDBufs = NT == 128 ? 1 : 2;
   static constexpr int kBars = 2 * kW + 2 * kB + 2 * kABufs + 2 * kDBufs + 1;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
-  static constexpr uint32_t kOffPrefix = kOffMisc + 16;
+  static constexpr uint32_t kOffOut = (kOffMisc + 16 + 127) / 128 * 128;   // 1 KB an epilogue warp
+  static constexpr uint32_t kOffPrefix = kOffOut + 4 * 1024;
   static constexpr uint32_t kOffOffs = kOffPrefix + (kMaxGroups + 1) * 4;
   static constexpr uint32_t kSmem = kOffOffs + (kMaxGroups + 1) * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(kABufs * kACols + kDBufs * 2 * NT <= 512, "TMEM columns");
+  static_assert(kABufs * kACols <= kTmemD && kTmemD + kDBufs * 2 * NT <= 512, "TMEM columns");
 };
 
 struct TileParams {
@@ -75,7 +82,7 @@ struct TileParams {
   long long ldx, ldo, out_rows;
   size_t matrix;
   uint32_t record;
-  int n_groups, dense_rows, x_rows, n, K, kb, rt, blocks, code, group, swiglu, f32, early, splits;
+  int n_groups, dense_rows, x_rows, n, K, kb, rt, blocks, code, group, swiglu, f32, vec, early, splits;
   int32_t* status;
 };
 
@@ -88,6 +95,27 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+
+// 16 lanes x 16 fp32 columns: thread i has lanes i / 4 (r[0], r[1] and r[4], r[5]) and
+// i / 4 + 8, columns 2 (i % 4) and the next of each block of eight.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(taddr));
+}
+
+// Four 8x8 blocks of bf16, transposed: a row of the block that lane i names gets column
+// i % 8 of block i / 8.
+__device__ __forceinline__ void stmatrix_trans(uint32_t a, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
+// SiLU by the approximate exponential and reciprocal: within (4 + 1.2 |g|) 2^-23 of its
+// value (0 below -87).
+__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -190,30 +218,26 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// 128 expanded weights of a row (c: its pieces, sc: a scale byte for every 16 inputs) to
-// TMEM columns d .. d + 63.
-template <int CODE>
-__device__ __forceinline__ void expand_row(const uint4 (&c)[4], uint2 sc, uint32_t d) {
+// 64 expanded weights of a row (words H, H + 1 of its pieces c; s4: a scale byte for
+// every 16 inputs) to TMEM columns d .. d + 31.
+template <int CODE, int H>
+__device__ __forceinline__ void expand_half(const uint4 (&c)[4], uint32_t s4, uint32_t d) {
+  uint32_t v[32];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[32];
+  for (int i = 0; i < 2; ++i) {
+    const QuantScale<CODE> q[2] = {
+        i == 0 ? QuantScale<CODE>::template at<0>(s4) : QuantScale<CODE>::template at<2>(s4),
+        i == 0 ? QuantScale<CODE>::template at<1>(s4) : QuantScale<CODE>::template at<3>(s4)};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {                 // word 2 h + i of every piece
-      const uint32_t s4 = h == 0 ? sc.x : sc.y;
-      const QuantScale<CODE> q[2] = {
-          i == 0 ? QuantScale<CODE>::template at<0>(s4) : QuantScale<CODE>::template at<2>(s4),
-          i == 0 ? QuantScale<CODE>::template at<1>(s4) : QuantScale<CODE>::template at<3>(s4)};
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t w = H == 0 ? (i == 0 ? c[p].x : c[p].y) : (i == 0 ? c[p].z : c[p].w);
+      uint32_t e[4];
+      quant_expand<CODE>(w, q[p >> 1], e);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t w = h == 0 ? (i == 0 ? c[p].x : c[p].y) : (i == 0 ? c[p].z : c[p].w);
-        uint32_t e[4];
-        quant_expand<CODE>(w, q[p >> 1], e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
-      }
+      for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
     }
-    tmem_st32(d + 32u * h, v);
   }
+  tmem_st32(d, v);
 }
 
 // Next slot of a ring of n, with the phase that a wait on its barrier goes by.
@@ -229,7 +253,8 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     quant_tile_kernel(const __grid_constant__ CUtensorMap tm16,
                       const __grid_constant__ CUtensorMap tm64, const TileParams p) {
   using Cfg = TileCfg<NT, SPLIT>;
-  constexpr int kW = Cfg::kW, kB = Cfg::kB, kDBufs = Cfg::kDBufs;
+  constexpr int kW = Cfg::kW, kB = Cfg::kB, kDBufs = Cfg::kDBufs, kABufs = Cfg::kABufs, kParts = Cfg::kParts;
+  constexpr uint32_t kACols = Cfg::kACols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -302,10 +327,9 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
   const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
   const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits : static_cast<int>(blockIdx.x);
   const int step = SPLIT ? total : static_cast<int>(gridDim.x);   // a cluster has one item
-  // records, and halves of them with inputs, of this CTA
+  // records of this CTA; a half of the last one may be past K: zero weights, zero tokens
   const int kb0 = SPLIT ? p.kb * rank / p.splits : 0;
   const int kb1 = SPLIT ? p.kb * (rank + 1) / p.splits : p.kb;
-  const int halves = min(2 * kb1, (p.K + kHalf - 1) / kHalf) - 2 * kb0;
   // item w: chunk w / blocks; tiles of row block w % blocks
   auto tiles_of = [&](int b) { return p.swiglu ? 2 : min(2, p.rt - 2 * b); };
 
@@ -352,20 +376,24 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
       const uint32_t idesc = uniform(idesc_bf16_f32(128, (t.rows + 15) / 16 * 16));
       const uint32_t d = kTmemD + static_cast<uint32_t>(db * 2 + tile) * NT;
       ok = warp_wait(b_dempty + 8 * db, dphase ^ 1u, s_abort);
-      for (int h = 0; h < halves && ok; h += 2) {
-        ok = warp_wait(b_bfull + 8 * bs, bphase, s_abort) && warp_wait(b_afull + 8 * ab, aphase, s_abort);
-        if (!ok) break;
-        if (mine) {
-          tc_fence_after();
-          const uint64_t b = sdesc_sw128(sbase + static_cast<uint32_t>(bs) * Cfg::kTok);
-          const uint32_t a = static_cast<uint32_t>(ab) * kACols + tile * 64;
-          umma_bf16_ts64(d, a, b, idesc, h != 0);
-          if (h + 1 < halves) umma_bf16_ts64(d, a + 32, b + (NT * 128 >> 4), idesc, 1u);
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        ok = warp_wait(b_bfull + 8 * bs, bphase, s_abort);
+        const uint64_t b = sdesc_sw128(sbase + static_cast<uint32_t>(bs) * Cfg::kTok);
+        for (int i = 0; i < kParts && ok; ++i) {
+          ok = warp_wait(b_afull + 8 * ab, aphase, s_abort);
+          if (!ok) break;
+          if (mine) {
+            tc_fence_after();
+            const uint32_t a = static_cast<uint32_t>(ab) * kACols + tile * (kACols / 2);
+            umma_bf16_ts64(d, a, b + static_cast<uint32_t>(i) * (NT * 128 >> 4), idesc, kb != kb0 || i != 0);
+            if (kParts == 1) umma_bf16_ts64(d, a + 32, b + (NT * 128 >> 4), idesc, 1u);
+          }
+          commit_at(b_aempty + 8 * ab);
+          advance(ab, aphase, kABufs);
         }
+        if (!ok) break;
         commit_at(b_bempty + 8 * bs);
-        commit_at(b_aempty + 8 * ab);
         advance(bs, bphase, kB);
-        advance(ab, aphase, kABufs);
       }
       if (!ok) break;
       commit_at(b_dfull + 8 * db);
@@ -379,7 +407,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     if (p.early) pdl_wait_and_trigger();
     const int set = (warp - 6) >> 3, tile = ((warp - 6) >> 2) & 1, r = (warp & 3) * 32 + lane;
     const uint32_t d = (static_cast<uint32_t>((warp & 3) * 32) << 16) +
-                       static_cast<uint32_t>(set * kACols + tile * 64);
+                       static_cast<uint32_t>(kParts * set * kACols + tile * (kACols / 2));
     const uint32_t swap = static_cast<uint32_t>((r >> 1) & 3) << 4;
     const uint32_t codes = sbase + Cfg::kOffW + tile * kMaxRecord + r * 64;
     const uint32_t scales = sbase + Cfg::kOffW + tile * kMaxRecord + kQCodeBytes +
@@ -411,20 +439,31 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
           slot -= kW;
           phase ^= 1u;
         }
-        ok = warp_wait(b_aempty + 8 * set, aphase, s_abort);
+        auto store = [&](auto half) {             // 64 inputs of the row
+          constexpr int H = decltype(half)::value;
+          constexpr uint32_t buf = kParts == 2 ? 8 * H : 0;
+          if (H == 0 || kParts == 2) ok = warp_wait(b_aempty + 8 * kParts * set + buf, aphase, s_abort);
+          if (!ok) return;
+          if (mine) {
+            if (H == 0 || kParts == 2) tc_fence_after();
+            const uint32_t to = d + H * (kParts == 2 ? kACols : 32);
+            if (p.code == MOE_QUANT_INT)
+              expand_half<MOE_QUANT_INT, H>(c, H == 0 ? sc.x : sc.y, to);
+            else
+              expand_half<MOE_QUANT_E2M1, H>(c, H == 0 ? sc.x : sc.y, to);
+          }
+          if (H == 1 || kParts == 2) {
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(b_afull + 8 * kParts * set + buf);
+          }
+        };
+        store(std::integral_constant<int, 0>());
+        if (!ok) break;
+        store(std::integral_constant<int, 1>());
         if (!ok) break;
         aphase ^= 1u;
-        if (mine) {
-          tc_fence_after();
-          if (p.code == MOE_QUANT_INT)
-            expand_row<MOE_QUANT_INT>(c, sc, d);
-          else
-            expand_row<MOE_QUANT_E2M1>(c, sc, d);
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) arrive_at(b_afull + 8 * set);
       }
       n += kb1 - kb0;
     }
@@ -440,17 +479,16 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
         const int nb = (t.rows + 15) / 16;
         const bool wide = nb > 2;
         const int boxes = wide ? (t.rows + 63) / 64 : nb, box = wide ? 64 : 16;
-        for (int h = 0; h < halves; h += 2) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&bempty[slot], phase ^ 1u, s_abort)) {
             ok = false;
             break;
           }
-          const int blocks = min(2, halves - h);
-          mbar_expect_tx(&bfull[slot], static_cast<uint32_t>(blocks * boxes * box * kHalf * 2));
-          for (int j = 0; j < blocks; ++j)
+          mbar_expect_tx(&bfull[slot], static_cast<uint32_t>(2 * boxes * box * kHalf * 2));
+          for (int j = 0; j < 2; ++j)
             for (int i = 0; i < boxes; ++i)
               tma_load_2d(smem + slot * Cfg::kTok + j * (NT * 128) + i * box * kHalf * 2,
-                          wide ? &tm64 : &tm16, &bfull[slot], (2 * kb0 + h + j) * kHalf,
+                          wide ? &tm64 : &tm16, &bfull[slot], kb * kQK + j * kHalf,
                           t.row0 + i * box);
           issued |= 1u << slot;
           parity = (parity & ~(1u << slot)) | (phase << slot);
@@ -491,14 +529,14 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
           }
         }
       }
-      for (int h = 0; h < halves; h += 2) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!try_wait_at(b_bempty + 8 * slot, phase ^ 1u) &&
             !wait_on(b_bempty + 8 * slot, phase ^ 1u, s_abort)) {
           ok = false;
           break;
         }
         const uint32_t sb = sbase + slot * Cfg::kTok + rg * 128 + ((piece ^ (rg & 7)) << 4);
-        const int k = (2 * kb0 + h) * kHalf + piece * 8;
+        const int k = kb * kQK + piece * 8;
         const uint32_t in0 = k < p.K ? 16u : 0u, in1 = k + kHalf < p.K ? 16u : 0u;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -569,37 +607,71 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
                              __uint_as_float(v[c]) * (i == 0 ? f0 : f1));
             }
           }
-      } else if (p.swiglu) {
-        const int col = t.nt * 128 + r;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(t.row0) * p.ldo + col;
-        for (int c0 = 0; c0 < t.rows; c0 += 16) {
-          uint32_t a[16], b[16];
-          tmem_ld16(d + static_cast<uint32_t>(c0), a);
-          tmem_ld16(d + static_cast<uint32_t>(NT + c0), b);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (c0 + c < t.rows && col < p.n)
-              out[static_cast<size_t>(c0 + c) * p.ldo] = __float2bfloat16_rn(
-                  silu_f(__uint_as_float(a[c]) * f0) * (__uint_as_float(b[c]) * f1));
-        }
-      } else {
+      } else if (p.f32) {
         for (int i = 0; i < nt; ++i) {
           const int col = (2 * t.nt + i) * 128 + r;
-          const size_t at = static_cast<size_t>(t.row0) * p.ldo + col;
+          float* out = static_cast<float*>(p.out) + static_cast<size_t>(t.row0) * p.ldo + col;
           for (int c0 = 0; c0 < t.rows; c0 += 16) {
             uint32_t v[16];
             tmem_ld16(d + static_cast<uint32_t>(i * NT + c0), v);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              if (c0 + c >= t.rows || col >= p.n) continue;
-              const float y = __uint_as_float(v[c]) * f0;
-              if (p.f32)
-                static_cast<float*>(p.out)[at + static_cast<size_t>(c0 + c) * p.ldo] = y;
-              else
-                static_cast<__nv_bfloat16*>(p.out)[at + static_cast<size_t>(c0 + c) * p.ldo] =
-                    __float2bfloat16_rn(y);
+            for (int c = 0; c < 16; ++c, out += p.ldo)
+              if (c0 + c < t.rows && col < p.n) *out = __uint_as_float(v[c]) * f0;
+          }
+        }
+      } else {
+        // 32 features of 16 tokens at a time: as bf16 through shared memory, where a token
+        // has its features in a row, in 16-byte pieces (octets of features) to memory
+        const uint32_t stage = sbase + Cfg::kOffOut + q * 1024;
+        const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+        const uint32_t get = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+        const int outs = p.swiglu ? 1 : nt;
+        for (int i = 0; i < outs; ++i) {
+          const int col = (p.swiglu ? t.nt : 2 * t.nt + i) * 128 + q * 32 + (lane & 3) * 8;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                               static_cast<size_t>(t.row0 + (lane >> 2)) * p.ldo + col;
+          const bool whole = p.vec && col + 8 <= p.n;
+          for (int c0 = 0; c0 < t.rows; c0 += 16) {
+            float v[2][8];                        // [lanes 0-15, 16-31]
+            tmem_ld_frag(d + static_cast<uint32_t>(i * NT + c0), v[0]);
+            tmem_ld_frag(d + (16u << 16) + static_cast<uint32_t>(i * NT + c0), v[1]);
+            if (p.swiglu) {
+              float up[2][8];
+              tmem_ld_frag(d + static_cast<uint32_t>(NT + c0), up[0]);
+              tmem_ld_frag(d + (16u << 16) + static_cast<uint32_t>(NT + c0), up[1]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                v[j / 8][j % 8] = silu_fast(v[j / 8][j % 8] * f0) * (up[j / 8][j % 8] * f1);
+            } else {
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j / 8][j % 8] *= f0;
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {         // eight tokens each
+              const uint32_t m[4] = {pack_bf16x2(v[0][4 * b], v[0][4 * b + 1]),
+                                     pack_bf16x2(v[0][4 * b + 2], v[0][4 * b + 3]),
+                                     pack_bf16x2(v[1][4 * b], v[1][4 * b + 1]),
+                                     pack_bf16x2(v[1][4 * b + 2], v[1][4 * b + 3])};
+              __syncwarp();                       // this buffer's last tokens have been read
+              stmatrix_trans(put + b * 512, m);
+              __syncwarp();
+              const uint4 o = lds128(get + b * 512);
+              const int left = t.rows - c0 - 8 * b - (lane >> 2);
+              if (left > 0) {
+                if (whole) {
+                  *reinterpret_cast<uint4*>(out) = o;
+                } else {
+                  const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    if (col + j < p.n)
+                      out[j] = __ushort_as_bfloat16(static_cast<unsigned short>(w[j / 2] >> (16 * (j & 1))));
+                }
+              }
+              out += 8 * p.ldo;
             }
           }
         }
@@ -629,7 +701,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
           y += part[(s * per + c) * 256 + r];
           if (p.swiglu) v += part[(s * per + c) * 256 + 128 + r];
         }
-        if (p.swiglu) y = silu_f(y) * v;
+        if (p.swiglu) y = silu_fast(y) * v;
         const size_t at = static_cast<size_t>(t.row0 + token) * p.ldo + col;
         if (p.f32)
           static_cast<float*>(p.out)[at] = y;
@@ -747,6 +819,7 @@ cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
   p.group = a.group;
   p.swiglu = a.swiglu != 0;
   p.f32 = a.out_f32;
+  p.vec = a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   p.early = a.early && a.token == nullptr;
   p.splits = 1;
   p.status = a.status;
