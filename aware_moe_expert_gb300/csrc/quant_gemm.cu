@@ -504,31 +504,35 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     // Thread g copies the 16-byte piece g % 8 of token rows g / 8 + 16 i of a stage; a
     // piece lands at piece ^ (row % 8) of its 128-byte row.  Pieces past K are zero
     // (their weights are, but zero times NaN is not), and so is a token out of range.
-    // A stage's copies are one cp.async group, reported kLag groups later.
-    constexpr int kLag = kB - 2, kPer = NT / 16;
+    // A stage's copies are one cp.async group, reported kLag groups later (8192 tokens of 128
+    // experts 600 us, 609 with a lag of 2).
+    constexpr int kLag = 1, kPer = NT / 16;
     const int g = threadIdx.x - kTokenWarp * 32, piece = g & 7, rg = g >> 3;
     int slot = 0, aslot = 0, pending = 0;
     uint32_t phase = 0;
     bool ok = true, bad = false;
+    // an item's tokens are loaded while the rows of the one before it are copied
+    Tile t{};
+    int tok[kPer];
+    auto look = [&](int w) {
+      t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        tok[i] = rg + 16 * i < t.rows ? __ldg(p.token + t.row0 + rg + 16 * i) : 0;
+    };
+    if (first < total) look(first);
     for (int w = first; w < total && ok; w += step) {
-      const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+      const int rows = t.rows;
       const uint4* src[kPer];
       uint32_t size[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int row = rg + 16 * i;
-        src[i] = p.x;
-        size[i] = 0u;
-        if (row < t.rows) {
-          const int tok = __ldg(p.token + t.row0 + row);
-          if (tok >= 0 && tok < p.x_rows) {
-            src[i] = p.x + static_cast<size_t>(tok) * (p.ldx / 8) + kb0 * (kQK / 8) + piece;
-            size[i] = 16u;
-          } else {
-            bad = true;
-          }
-        }
+        const bool fine = tok[i] >= 0 && tok[i] < p.x_rows;
+        bad |= !fine;
+        src[i] = p.x + static_cast<size_t>(fine ? tok[i] : 0) * (p.ldx / 8) + kb0 * (kQK / 8) + piece;
+        size[i] = fine ? 16u : 0u;
       }
+      if (w + step < total) look(w + step);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!try_wait_at(b_bempty + 8 * slot, phase ^ 1u) &&
             !wait_on(b_bempty + 8 * slot, phase ^ 1u, s_abort)) {
@@ -540,8 +544,8 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
         const uint32_t in0 = k < p.K ? 16u : 0u, in1 = k + kHalf < p.K ? 16u : 0u;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          if (16 * i >= t.rows) break;
-          if (rg + 16 * i < t.rows) {
+          if (16 * i >= rows) break;
+          if (rg + 16 * i < rows) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + i * 16 * 128),
                          "l"(src[i]), "r"(size[i] & in0)
                          : "memory");
