@@ -1596,6 +1596,8 @@ moe_status moe_quant_project(const moe_quant_project_desc* desc, const void* x, 
   a.early = 1;
   a.status = dev_status;
   a.sm_count = sm_count();
+  if (desc->T <= moe::kQuantFewTokens)
+    return cuda_status(moe::launch_quant_project_few(a, static_cast<cudaStream_t>(stream)));
   return cuda_status(moe::launch_quant_gemm(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1672,6 +1674,30 @@ moe_status moe_layer_forward_quant(const moe_layer_desc* desc, const moe_group_r
   } else {
     MOE_TRY(do_route(desc, x, router_w, nullptr, k_per_token, nullptr, topk_idx, topk_w,
                      dev_status, workspace, s, &bitmap_done));
+  }
+  if (d.T <= moe::kQuantFewTokens) {
+    moe::QuantFewArgs a{};
+    a.x = x;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.gate_up = weights->gate_up;
+    a.down = weights->down;
+    a.shared_gate_up = weights->shared_gate_up;
+    a.shared_down = weights->shared_down;
+    a.act = at<void>(workspace, l.act);
+    a.act_shared = at<void>(workspace, l.act_sh);
+    a.out = out;
+    a.T = d.T;
+    a.H = d.H;
+    a.E = E_r_of(desc);
+    a.I = d.I_sub;
+    a.I_shared = desc->I_shared;
+    a.k_max = d.k_max;
+    a.code = weights->code;
+    a.group = weights->group;
+    a.status = dev_status;
+    a.sm_count = sm_count();
+    return cuda_status(moe::launch_quant_ffn_few(a, s));
   }
   MOE_TRY(do_permute(desc, topk_idx, k_used, counts, offsets, sorted_token, inv_row, dev_status,
                      workspace, s, bitmap_done));

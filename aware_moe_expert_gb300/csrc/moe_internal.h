@@ -347,6 +347,30 @@ struct QuantGemmArgs {
   int sm_count;
 };
 cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s);
+
+// ---- quant_few.cu: the same for up to kQuantFewTokens tokens
+constexpr int kQuantFewTokens = 8;
+// Dense, bf16 out.
+cudaError_t launch_quant_project_few(const QuantGemmArgs& a, cudaStream_t s);
+struct QuantFewArgs {
+  const void* x;               // bf16 [T, H]
+  const int32_t* topk_idx;     // [T, k_max], -1: none; written before the launch that this follows
+  const float* topk_w;
+  const void* gate_up;         // packed, as in moe_quant_weights
+  const void* down;
+  const void* shared_gate_up;  // with I_shared > 0
+  const void* shared_down;
+  void* act;                   // bf16 [T * k_max, I]
+  void* act_shared;            // bf16 [T, I_shared]
+  void* out;                   // bf16 [T, H]
+  int T, H, E, I, I_shared, k_max, code, group;
+  int32_t* status;
+  int sm_count;
+};
+// The experts, the shared expert and their weighted sum.
+cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s);
+
+// ---- quant_gemm.cu
 // The weighted sum of fp32 rows y (and fp32 y_shared, nullable), like launch_combine's.
 cudaError_t launch_combine_f32(const float* y, const float* y_shared, const int32_t* inv_row,
                                const float* topk_w, const int32_t* k_per_token, int T, int H,

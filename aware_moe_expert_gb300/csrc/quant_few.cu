@@ -1,0 +1,425 @@
+// Products of up to eight tokens with packed 4-bit weights: the projection, and the
+// MoE layer's experts in two launches, without a permutation.
+//
+// A handful of tokens is bound by the weights' bytes and by latency, so the weights
+// go from memory to registers to mma.m16n8k16 and nowhere else: a lane holds the
+// 16-byte pieces of two rows (32 inputs each), which word by word are the A operands
+// of two MMAs (quant.cuh); the tokens are the N side, all eight columns whatever
+// their number, and a lane reads their inputs as they lie (16 bytes a word).  A warp
+// multiplies 16 rows (or 16 gate and 16 up rows) by 128 inputs a step, kAhead steps
+// in flight; the warps of a group split a task's steps and add their sums in shared
+// memory in warp order.
+//
+// Experts: every CTA lists the distinct units of the batch itself, from the router's
+// selection.  The first launch computes act[t, j] = w_tj f_u silu(g) u of token t's
+// j-th unit (its gate and its down matrix's factor with it, one rounding); the second
+// one, whose weights stream while the first ends, multiplies 16 rows of W_down of ALL
+// units and the shared expert with them, one long sum: the weighted sum over a token's
+// units is part of it.
+#include <type_traits>
+
+#include "gemm_common.cuh"
+#include "moe_internal.h"
+#include "quant.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTokens = kQuantFewTokens;
+
+enum Mode { PROJECT, GATE_UP, DOWN };
+
+struct FewParams {
+  const uint8_t* w;            // PROJECT, or the units' matrices
+  const uint8_t* w_shared;
+  const float* factor;         // of w's matrices
+  const float* factor_shared;
+  const float* factor_down;    // GATE_UP: of the matrices that the activations go to
+  const float* factor_down_shared;
+  const __nv_bfloat16* x;      // PROJECT, GATE_UP
+  const __nv_bfloat16* act;    // DOWN: [T * k_max, I], act_shared [T, I_shared]
+  const __nv_bfloat16* act_shared;
+  __nv_bfloat16* out;          // PROJECT, DOWN
+  __nv_bfloat16* out_act;      // GATE_UP
+  __nv_bfloat16* out_act_shared;
+  const int32_t* topk_idx;     // [T, k_max]
+  const float* topk_w;
+  long long ldx, ldo;
+  size_t matrix, matrix_shared;
+  int T, n, K, kb;             // outputs of a matrix, its inputs, their records
+  int n_shared, kb_shared, K_shared;   // GATE_UP: outputs; DOWN: inputs of the shared expert
+  int E, k_max, swiglu;
+  int32_t* status;
+};
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint4 ldg_nc(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 rows of one record as a lane holds them: pieces `lane % 4` of rows lane / 4 and
+// lane / 4 + 8, and their four scales (of words 0 .. 3).
+struct Rows {
+  uint4 c[2];
+  uint32_t s[2];
+};
+
+template <int GROUP>
+__device__ __forceinline__ void load_rows(Rows& q, const uint8_t* rec, int row, int lane) {
+  const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = row + g + 8 * i;
+    q.c[i] = ldg_stream(rec + quant_piece(r, tig));
+    if (GROUP == 32) {
+      q.s[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + kQCodeBytes + r * 4));
+    } else {
+      const uint2 s = __ldg(reinterpret_cast<const uint2*>(rec + kQCodeBytes + r * 8));
+      q.s[i] = __byte_perm(s.x, s.y, tig >= 2 ? 0x7531 : 0x6420);
+    }
+  }
+}
+
+// d += rows x tokens over a record's 128 inputs; x: word w of the token's piece, four each.
+template <int CODE>
+__device__ __forceinline__ void multiply(float (&d)[4], const Rows& q, const uint4 (&x)[4]) {
+  auto word = [&](auto index) {
+    constexpr int W = decltype(index)::value;
+    const uint32_t a = W == 0 ? q.c[0].x : W == 1 ? q.c[0].y : W == 2 ? q.c[0].z : q.c[0].w;
+    const uint32_t b = W == 0 ? q.c[1].x : W == 1 ? q.c[1].y : W == 2 ? q.c[1].z : q.c[1].w;
+    uint32_t ea[4], eb[4];
+    quant_expand<CODE>(a, QuantScale<CODE>::template at<W>(q.s[0]), ea);
+    quant_expand<CODE>(b, QuantScale<CODE>::template at<W>(q.s[1]), eb);
+    mma_16816(d, ea[0], eb[0], ea[1], eb[1], x[W].x, x[W].y);
+    mma_16816(d, ea[2], eb[2], ea[3], eb[3], x[W].z, x[W].w);
+  };
+  word(std::integral_constant<int, 0>());
+  word(std::integral_constant<int, 1>());
+  word(std::integral_constant<int, 2>());
+  word(std::integral_constant<int, 3>());
+}
+
+// The batch's distinct units, ascending, and where each token has them.
+struct Units {
+  __align__(16) uint8_t slot[kMaxGroups][kTokens];   // j of token t's selection, 255: none
+  uint8_t list[kMaxGroups];
+  int warp_count[kWarps];
+  int count;
+};
+static_assert(kMaxGroups == kWarps * 32, "a thread a unit");
+
+__device__ __forceinline__ void list_units(Units& u, const FewParams& p, bool complain) {
+  uint32_t* slots = reinterpret_cast<uint32_t*>(u.slot);
+  for (int i = threadIdx.x; i < kMaxGroups * kTokens / 4; i += kWarps * 32) slots[i] = 0xFFFFFFFFu;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.T * p.k_max; i += kWarps * 32) {
+    const int t = i / p.k_max, e = p.topk_idx[i];
+    if (e >= 0 && e < p.E) u.slot[e][t] = static_cast<uint8_t>(i - t * p.k_max);
+    // a token without units gets the shared expert alone
+    if (complain && e < 0 && i == t * p.k_max) report(p.status, MOE_ERR_K_RANGE);
+  }
+  __syncthreads();
+  // thread = unit (256 of both)
+  const uint2 s = *reinterpret_cast<const uint2*>(u.slot[threadIdx.x]);
+  const bool used = (s.x & s.y) != 0xFFFFFFFFu;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t m = __ballot_sync(0xffffffffu, used);
+  if (lane == 0) u.warp_count[warp] = __popc(m);
+  __syncthreads();
+  int at = __popc(m & ((1u << lane) - 1u));
+  for (int w = 0; w < warp; ++w) at += u.warp_count[w];
+  if (used) u.list[at] = static_cast<uint8_t>(threadIdx.x);
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int w = 0; w < kWarps; ++w) n += u.warp_count[w];
+    u.count = n;
+  }
+  __syncthreads();
+}
+
+// Warps of a task: what makes the longest warp's steps fewest, with half a step for
+// starting a task; the wider group on ties.
+__device__ __forceinline__ int task_warps(int tasks, int steps, int ctas) {
+  int best = kWarps;
+  long long cost = 0x7fffffffffffll;
+  for (int w = kWarps; w >= 1; w >>= 1) {
+    const int at_once = ctas * (kWarps / w);
+    const long long c = static_cast<long long>((tasks + at_once - 1) / at_once) * (2 * ((steps + w - 1) / w) + 1);
+    if (c < cost) {
+      cost = c;
+      best = w;
+    }
+  }
+  return best;
+}
+
+template <int MODE, int CODE, int GROUP, bool PAIR>
+__global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewParams p) {
+  constexpr uint32_t kRec = quant_record(GROUP);
+  constexpr int kTiles = PAIR ? 2 : 1;
+  constexpr int kAhead = PAIR ? 2 : 3;          // steps in flight
+  __shared__ Units units;
+  __shared__ float sums[kWarps][kTiles][16 * kTokens];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tig = lane & 3;
+  bool waited = false;
+  // The selection was written before the launch that a DOWN launch follows, so it may
+  // list the units and fetch weights at once.
+  if (MODE == GATE_UP) {
+    pdl_wait_and_trigger();
+    waited = true;
+  }
+  int D = 1;
+  if (MODE != PROJECT) {
+    list_units(units, p, MODE == GATE_UP && blockIdx.x == 0);
+    D = units.count;
+  }
+  const int tiles = (p.n + 15) / 16;            // of a matrix
+  const int shared_tiles = MODE == GATE_UP ? (p.n_shared + 15) / 16 : 0;
+  const int tasks = MODE == GATE_UP ? D * tiles + shared_tiles : tiles;
+  const int steps = MODE == DOWN ? D * p.kb + p.kb_shared : p.kb;
+  const int ways = task_warps(tasks, steps, gridDim.x);
+  const int group = warp / ways, part = warp - group * ways;
+  const int groups = kWarps / ways;
+
+  for (int t0 = blockIdx.x * groups; t0 < tasks; t0 += gridDim.x * groups) {
+    const int task = t0 + group;
+    const bool some = task < tasks;
+    const bool shared = MODE == GATE_UP && task >= D * tiles;
+    const int d = MODE == GATE_UP && !shared ? task / tiles : 0;
+    const int tile = shared ? task - D * tiles : MODE == GATE_UP ? task - d * tiles : task;
+    const int unit = MODE == GATE_UP && !shared && some ? units.list[d] : 0;
+    const int row = tile * 16 % kQRows;
+    // records of the task's row tile within the first matrix that it reads
+    const size_t at = static_cast<size_t>(tile * 16 / kQRows) * p.kb * kRec;
+    const uint8_t* base = shared ? p.w_shared + at : p.w + p.matrix * (static_cast<size_t>(unit) * kTiles) + at;
+    const size_t up = shared ? p.matrix_shared : p.matrix;
+
+    float acc[kTiles][4] = {};
+    Rows rows[kAhead][kTiles];
+    uint4 x[kAhead][4];
+    // step s of the task: its record and the tokens' inputs.  DOWN counts through the
+    // units' records, then the shared expert's.
+    int ws = part, wd = 0, wk = part;            // the next weights to load
+    int xs = part, xd = 0, xk = part;            // the next inputs
+    if (MODE == DOWN)
+      while (wd < D && wk >= p.kb) {
+        wk -= p.kb;
+        ++wd;
+      }
+    xd = wd;
+    xk = wk;
+    auto forward = [&](int& s, int& sd, int& sk) {
+      s += ways;
+      sk += ways;
+      if (MODE == DOWN)
+        while (sd < D && sk >= p.kb) {
+          sk -= p.kb;
+          ++sd;
+        }
+    };
+    auto load_w = [&](Rows (&q)[kTiles]) {
+      if (!some || ws >= steps) return;
+      const uint8_t* rec;
+      if (MODE != DOWN) {
+        rec = base + static_cast<size_t>(wk) * kRec;
+      } else if (wd < D) {
+        rec = base + p.matrix * units.list[wd] + static_cast<size_t>(wk) * kRec;
+      } else {
+        rec = p.w_shared + (static_cast<size_t>(tile * 16 / kQRows) * p.kb_shared + wk) * kRec;
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) load_rows<GROUP>(q[i], rec + up * i, row, lane);
+      forward(ws, wd, wk);
+    };
+    auto load_x = [&](uint4 (&v)[4]) {
+      if (!some || xs >= steps) return;
+      const __nv_bfloat16* src = nullptr;
+      int K = p.K;
+      if (MODE != DOWN) {
+        if (g < p.T) src = p.x + g * p.ldx;
+      } else if (xd < D) {
+        const int e = units.list[xd];
+        const int j = units.slot[e][g];
+        if (j != 255) src = p.act + (static_cast<size_t>(g) * p.k_max + j) * p.K;
+      } else {
+        K = p.K_shared;
+        if (g < p.T) src = p.act_shared + static_cast<size_t>(g) * K;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int k = xk * kQK + 32 * w + 8 * tig;
+        v[w] = src != nullptr && k < K ? ldg_nc(src + k) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      forward(xs, xd, xk);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_w(rows[i]);
+    if (!waited) {
+      pdl_wait_and_trigger();
+      waited = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_x(x[i]);
+    if (some)
+      for (int s = part; s < steps; s += kAhead * ways) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (s + i * ways >= steps) break;
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j) multiply<CODE>(acc[j], rows[i][j], x[i]);
+          load_w(rows[i]);
+          load_x(x[i]);
+        }
+      }
+    // the group's sums: [row][token]
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      float2* to = reinterpret_cast<float2*>(sums[warp][j]);
+      to[g * 4 + tig] = make_float2(acc[j][0], acc[j][1]);
+      to[(g + 8) * 4 + tig] = make_float2(acc[j][2], acc[j][3]);
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ways * 32) : "memory");
+    // rows fastest: neighbouring threads store neighbouring features
+    for (int i = part * 32 + lane; some && i < 16 * kTokens; i += ways * 32) {
+      const int r = i % 16, t = i / 16, feature = tile * 16 + r;
+      float v[kTiles] = {};
+      for (int w = 0; w < ways; ++w)
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) v[j] += sums[group * ways + w][j][r * kTokens + t];
+      if (t >= p.T || feature >= (shared ? p.n_shared : p.n)) continue;
+      constexpr float u = CODE == MOE_QUANT_E2M1 ? 512.f : 1.f;
+      if (MODE == DOWN) {      // the factors came with the activations
+        p.out[t * p.ldo + feature] = __float2bfloat16_rn(v[0]);
+      } else if (MODE == PROJECT) {
+        float y = v[0] * (p.factor[0] * u);
+        if (PAIR) y = y / (1.f + expf(-y)) * (v[kTiles - 1] * (p.factor[1] * u));
+        p.out[t * p.ldo + feature] = __float2bfloat16_rn(y);
+      } else {
+        const float* f = shared ? p.factor_shared : p.factor + 2 * unit;
+        const float gate = v[0] * (f[0] * u), lift = v[kTiles - 1] * (f[1] * u);
+        const float y = gate / (1.f + expf(-gate)) * lift * u;
+        if (shared) {
+          p.out_act_shared[static_cast<size_t>(t) * p.n_shared + feature] =
+              __float2bfloat16_rn(y * p.factor_down_shared[0]);
+        } else {
+          const int j = units.slot[unit][t];
+          if (j != 255) {
+            const size_t at_row = static_cast<size_t>(t) * p.k_max + j;
+            p.out_act[at_row * p.n + feature] =
+                __float2bfloat16_rn(y * p.factor_down[unit] * p.topk_w[at_row]);
+          }
+        }
+      }
+    }
+    // the next task's sums overwrite these
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ways * 32) : "memory");
+  }
+  if (!waited) pdl_wait_and_trigger();
+}
+
+template <int MODE, bool PAIR>
+cudaError_t launch_few(const FewParams& p, int code, int group, int grid, cudaStream_t s) {
+  const dim3 b(kWarps * 32);
+  if (code == MOE_QUANT_INT)
+    return group == 16 ? launch_pdl(quant_few_kernel<MODE, MOE_QUANT_INT, 16, PAIR>, dim3(grid), b, 0, s, p)
+                       : launch_pdl(quant_few_kernel<MODE, MOE_QUANT_INT, 32, PAIR>, dim3(grid), b, 0, s, p);
+  return group == 16 ? launch_pdl(quant_few_kernel<MODE, MOE_QUANT_E2M1, 16, PAIR>, dim3(grid), b, 0, s, p)
+                     : launch_pdl(quant_few_kernel<MODE, MOE_QUANT_E2M1, 32, PAIR>, dim3(grid), b, 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quant_project_few(const QuantGemmArgs& a, cudaStream_t s) {
+  const QuantShape q = quant_shape(a.n, a.K, a.group);
+  FewParams p{};
+  p.w = static_cast<const uint8_t*>(a.w);
+  p.factor = reinterpret_cast<const float*>(p.w + q.bytes * (a.swiglu ? 2 : 1));
+  p.x = static_cast<const __nv_bfloat16*>(a.x);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.ldx = a.ldx;
+  p.ldo = a.ldo;
+  p.matrix = q.bytes;
+  p.T = a.dense_rows;
+  p.n = a.n;
+  p.K = a.K;
+  p.kb = q.kb;
+  p.status = a.status;
+  const int tiles = (a.n + 15) / 16;
+  const int grid = tiles < 2 * a.sm_count ? tiles : 2 * a.sm_count;
+  return a.swiglu ? launch_few<PROJECT, true>(p, a.code, a.group, grid, s)
+                  : launch_few<PROJECT, false>(p, a.code, a.group, grid, s);
+}
+
+cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
+  const QuantShape gu = quant_shape(a.I, a.H, a.group), dn = quant_shape(a.H, a.I, a.group);
+  const QuantShape gus = quant_shape(a.I_shared, a.H, a.group), dns = quant_shape(a.H, a.I_shared, a.group);
+  FewParams p{};
+  p.w = static_cast<const uint8_t*>(a.gate_up);
+  p.w_shared = static_cast<const uint8_t*>(a.shared_gate_up);
+  p.factor = reinterpret_cast<const float*>(p.w + gu.bytes * 2 * a.E);
+  const uint8_t* down = static_cast<const uint8_t*>(a.down);
+  const uint8_t* shared_down = static_cast<const uint8_t*>(a.shared_down);
+  p.factor_down = reinterpret_cast<const float*>(down + dn.bytes * a.E);
+  if (a.I_shared > 0) {
+    p.factor_shared = reinterpret_cast<const float*>(p.w_shared + gus.bytes * 2);
+    p.factor_down_shared = reinterpret_cast<const float*>(shared_down + dns.bytes);
+  }
+  p.x = static_cast<const __nv_bfloat16*>(a.x);
+  p.out_act = static_cast<__nv_bfloat16*>(a.act);
+  p.out_act_shared = static_cast<__nv_bfloat16*>(a.act_shared);
+  p.topk_idx = a.topk_idx;
+  p.topk_w = a.topk_w;
+  p.ldx = a.H;
+  p.matrix = gu.bytes;
+  p.matrix_shared = gus.bytes;
+  p.T = a.T;
+  p.n = a.I;
+  p.K = a.H;
+  p.kb = gu.kb;
+  p.n_shared = a.I_shared;
+  p.E = a.E;
+  p.k_max = a.k_max;
+  p.status = a.status;
+  const int grid = 2 * a.sm_count;
+  const cudaError_t e = launch_few<GATE_UP, true>(p, a.code, a.group, grid, s);
+  if (e != cudaSuccess) return e;
+  FewParams d = p;
+  d.w = down;
+  d.w_shared = shared_down;
+  d.act = p.out_act;
+  d.act_shared = p.out_act_shared;
+  d.out = static_cast<__nv_bfloat16*>(a.out);
+  d.ldo = a.H;
+  d.matrix = dn.bytes;
+  d.n = a.H;
+  d.K = a.I;
+  d.kb = dn.kb;
+  d.n_shared = 0;
+  d.K_shared = a.I_shared;
+  d.kb_shared = a.I_shared > 0 ? dns.kb : 0;
+  return launch_few<DOWN, false>(d, a.code, a.group, grid, s);
+}
+
+}  // namespace moe
