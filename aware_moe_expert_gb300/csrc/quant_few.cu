@@ -8,7 +8,8 @@
 // their number, and a lane reads their inputs as they lie (16 bytes a word).  A warp
 // multiplies 16 rows (or 16 gate and 16 up rows) by 128 inputs a step, kAhead steps
 // in flight; the warps of a group split a task's steps and add their sums in shared
-// memory in warp order.
+// memory in warp order, and where there are fewer tasks than CTAs, a cluster's CTAs
+// split them further.
 //
 // Experts: every CTA lists the distinct units of the batch itself, from the router's
 // selection.  The first launch computes act[t, j] = w_tj f_u silu(g) u of token t's
@@ -27,6 +28,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTokens = kQuantFewTokens;
+constexpr int kMaxCluster = 8;
 
 enum Mode { PROJECT, GATE_UP, DOWN };
 
@@ -49,7 +51,8 @@ struct FewParams {
   size_t matrix, matrix_shared;
   int T, n, K, kb;             // outputs of a matrix, its inputs, their records
   int n_shared, kb_shared, K_shared;   // GATE_UP: outputs; DOWN: inputs of the shared expert
-  int E, k_max, swiglu;
+  int E, k_max;
+  int cluster;                 // CTAs that share a task
   int32_t* status;
 };
 
@@ -174,13 +177,17 @@ __device__ __forceinline__ int task_warps(int tasks, int steps, int ctas) {
   return best;
 }
 
-template <int MODE, int CODE, int GROUP, bool PAIR>
+template <int MODE, int CODE, int GROUP, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewParams p) {
   constexpr uint32_t kRec = quant_record(GROUP);
   constexpr int kTiles = PAIR ? 2 : 1;
-  constexpr int kAhead = PAIR ? 2 : 3;          // steps in flight
+  // Steps of weights in flight, and of tokens: those of DOWN come from L2, the others
+  // from L1.
+  constexpr int kAhead = 3;
+  constexpr int kAheadX = MODE == DOWN ? kAhead : 1;
   __shared__ Units units;
   __shared__ float sums[kWarps][kTiles][16 * kTokens];
+  __shared__ float parts[CLUSTER ? kMaxCluster : 1][kTiles][16 * kTokens];   // of the cluster's CTAs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tig = lane & 3;
   bool waited = false;
@@ -199,11 +206,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
   const int shared_tiles = MODE == GATE_UP ? (p.n_shared + 15) / 16 : 0;
   const int tasks = MODE == GATE_UP ? D * tiles + shared_tiles : tiles;
   const int steps = MODE == DOWN ? D * p.kb + p.kb_shared : p.kb;
-  const int ways = task_warps(tasks, steps, gridDim.x);
+  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
+  const int ways = CLUSTER ? kWarps : task_warps(tasks, steps, gridDim.x);
   const int group = warp / ways, part = warp - group * ways;
-  const int groups = kWarps / ways;
+  const int groups = kWarps / ways, stride = CLUSTER ? ways * p.cluster : ways;
+  if (CLUSTER) cluster_sync_all();              // the peers run: their shared memory may be written
 
-  for (int t0 = blockIdx.x * groups; t0 < tasks; t0 += gridDim.x * groups) {
+  for (int t0 = (CLUSTER ? blockIdx.x / p.cluster : blockIdx.x) * groups; t0 < tasks;
+       t0 += (CLUSTER ? gridDim.x / p.cluster : gridDim.x) * groups) {
     const int task = t0 + group;
     const bool some = task < tasks;
     const bool shared = MODE == GATE_UP && task >= D * tiles;
@@ -218,11 +228,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
 
     float acc[kTiles][4] = {};
     Rows rows[kAhead][kTiles];
-    uint4 x[kAhead][4];
+    uint4 x[kAheadX][4];
     // step s of the task: its record and the tokens' inputs.  DOWN counts through the
     // units' records, then the shared expert's.
-    int ws = part, wd = 0, wk = part;            // the next weights to load
-    int xs = part, xd = 0, xk = part;            // the next inputs
+    const int start = rank * ways + part;
+    int ws = start, wd = 0, wk = start;          // the next weights to load
+    int xs = start, xd = 0, xk = start;          // the next inputs
     if (MODE == DOWN)
       while (wd < D && wk >= p.kb) {
         wk -= p.kb;
@@ -231,8 +242,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
     xd = wd;
     xk = wk;
     auto forward = [&](int& s, int& sd, int& sk) {
-      s += ways;
-      sk += ways;
+      s += stride;
+      sk += stride;
       if (MODE == DOWN)
         while (sd < D && sk >= p.kb) {
           sk -= p.kb;
@@ -280,17 +291,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
       pdl_wait_and_trigger();
       waited = true;
     }
+    if (kAheadX > 1)
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_x(x[i]);
+      for (int i = 0; i < kAheadX; ++i) load_x(x[i]);
     if (some)
-      for (int s = part; s < steps; s += kAhead * ways) {
+      for (int s = start; s < steps; s += kAhead * stride) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          if (s + i * ways >= steps) break;
+          if (s + i * stride >= steps) break;
+          if (kAheadX == 1) load_x(x[0]);
 #pragma unroll
-          for (int j = 0; j < kTiles; ++j) multiply<CODE>(acc[j], rows[i][j], x[i]);
+          for (int j = 0; j < kTiles; ++j) multiply<CODE>(acc[j], rows[i][j], x[kAheadX > 1 ? i : 0]);
           load_w(rows[i]);
-          load_x(x[i]);
+          if (kAheadX > 1) load_x(x[i]);
         }
       }
     // the group's sums: [row][token]
@@ -301,13 +314,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
       to[(g + 8) * 4 + tig] = make_float2(acc[j][2], acc[j][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ways * 32) : "memory");
+    if (CLUSTER) {       // this CTA's sums to the first one's slots
+      for (int i = threadIdx.x; i < kTiles * 16 * kTokens; i += kWarps * 32) {
+        const int j = i / (16 * kTokens), k = i - j * (16 * kTokens);
+        float v = 0.f;
+        for (int w = 0; w < kWarps; ++w) v += sums[w][j][k];
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&parts[rank][j][k]), 0u)),
+                     "f"(v)
+                     : "memory");
+      }
+      cluster_sync_all();
+    }
     // rows fastest: neighbouring threads store neighbouring features
-    for (int i = part * 32 + lane; some && i < 16 * kTokens; i += ways * 32) {
+    for (int i = part * 32 + lane; some && rank == 0 && i < 16 * kTokens; i += ways * 32) {
       const int r = i % 16, t = i / 16, feature = tile * 16 + r;
       float v[kTiles] = {};
-      for (int w = 0; w < ways; ++w)
+      for (int w = 0; w < (CLUSTER ? p.cluster : ways); ++w)
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) v[j] += sums[group * ways + w][j][r * kTokens + t];
+        for (int j = 0; j < kTiles; ++j)
+          v[j] += CLUSTER ? parts[w][j][r * kTokens + t] : sums[group * ways + w][j][r * kTokens + t];
       if (t >= p.T || feature >= (shared ? p.n_shared : p.n)) continue;
       constexpr float u = CODE == MOE_QUANT_E2M1 ? 512.f : 1.f;
       if (MODE == DOWN) {      // the factors came with the activations
@@ -334,19 +359,59 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
       }
     }
     // the next task's sums overwrite these
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ways * 32) : "memory");
+    if (CLUSTER)
+      cluster_sync_all();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ways * 32) : "memory");
   }
   if (!waited) pdl_wait_and_trigger();
 }
 
-template <int MODE, bool PAIR>
-cudaError_t launch_few(const FewParams& p, int code, int group, int grid, cudaStream_t s) {
+template <int MODE, int CODE, int GROUP, bool PAIR>
+cudaError_t launch_kind(const FewParams& p, int grid, cudaStream_t s) {
   const dim3 b(kWarps * 32);
+  if (p.cluster == 1) return launch_pdl(quant_few_kernel<MODE, CODE, GROUP, PAIR, false>, dim3(grid), b, 0, s, p);
+  if constexpr (MODE == GATE_UP) return cudaErrorInvalidValue;   // has tasks enough
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = b;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, quant_few_kernel<MODE, CODE, GROUP, PAIR, MODE != GATE_UP>, p);
+}
+
+// `tasks` of `steps` records (0: many) on two CTAs an SM: the CTAs of a cluster that
+// share a task are what makes the longest CTA's steps fewest.
+template <int MODE, bool PAIR>
+cudaError_t launch_few(FewParams p, int code, int group, int tasks, int steps, int sm_count, cudaStream_t s) {
+  const int ctas = 2 * sm_count;
+  p.cluster = 1;
+  if (MODE != GATE_UP) {
+    double best = 0;
+    for (int c = 1; c <= kMaxCluster; c *= 2) {
+      const int rounds = (tasks * c + ctas - 1) / ctas;
+      const double each = steps > 0 ? (steps + kWarps * c - 1) / (kWarps * c) + (c > 1 ? 1.0 : 0.5) : 1.0 / c;
+      if (c == 1 || rounds * each < 0.95 * best) {
+        best = rounds * each;
+        p.cluster = c;
+      }
+    }
+  }
+  const int most = ctas / p.cluster * p.cluster;
+  const int grid = MODE != GATE_UP && tasks * p.cluster < most ? tasks * p.cluster : most;
   if (code == MOE_QUANT_INT)
-    return group == 16 ? launch_pdl(quant_few_kernel<MODE, MOE_QUANT_INT, 16, PAIR>, dim3(grid), b, 0, s, p)
-                       : launch_pdl(quant_few_kernel<MODE, MOE_QUANT_INT, 32, PAIR>, dim3(grid), b, 0, s, p);
-  return group == 16 ? launch_pdl(quant_few_kernel<MODE, MOE_QUANT_E2M1, 16, PAIR>, dim3(grid), b, 0, s, p)
-                     : launch_pdl(quant_few_kernel<MODE, MOE_QUANT_E2M1, 32, PAIR>, dim3(grid), b, 0, s, p);
+    return group == 16 ? launch_kind<MODE, MOE_QUANT_INT, 16, PAIR>(p, grid, s)
+                       : launch_kind<MODE, MOE_QUANT_INT, 32, PAIR>(p, grid, s);
+  return group == 16 ? launch_kind<MODE, MOE_QUANT_E2M1, 16, PAIR>(p, grid, s)
+                     : launch_kind<MODE, MOE_QUANT_E2M1, 32, PAIR>(p, grid, s);
 }
 
 }  // namespace
@@ -367,9 +432,8 @@ cudaError_t launch_quant_project_few(const QuantGemmArgs& a, cudaStream_t s) {
   p.kb = q.kb;
   p.status = a.status;
   const int tiles = (a.n + 15) / 16;
-  const int grid = tiles < 2 * a.sm_count ? tiles : 2 * a.sm_count;
-  return a.swiglu ? launch_few<PROJECT, true>(p, a.code, a.group, grid, s)
-                  : launch_few<PROJECT, false>(p, a.code, a.group, grid, s);
+  return a.swiglu ? launch_few<PROJECT, true>(p, a.code, a.group, tiles, q.kb, a.sm_count, s)
+                  : launch_few<PROJECT, false>(p, a.code, a.group, tiles, q.kb, a.sm_count, s);
 }
 
 cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
@@ -402,8 +466,7 @@ cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
   p.E = a.E;
   p.k_max = a.k_max;
   p.status = a.status;
-  const int grid = 2 * a.sm_count;
-  const cudaError_t e = launch_few<GATE_UP, true>(p, a.code, a.group, grid, s);
+  const cudaError_t e = launch_few<GATE_UP, true>(p, a.code, a.group, 0, 0, a.sm_count, s);
   if (e != cudaSuccess) return e;
   FewParams d = p;
   d.w = down;
@@ -419,7 +482,7 @@ cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
   d.n_shared = 0;
   d.K_shared = a.I_shared;
   d.kb_shared = a.I_shared > 0 ? dns.kb : 0;
-  return launch_few<DOWN, false>(d, a.code, a.group, grid, s);
+  return launch_few<DOWN, false>(d, a.code, a.group, (a.H + 15) / 16, 0, a.sm_count, s);
 }
 
 }  // namespace moe
