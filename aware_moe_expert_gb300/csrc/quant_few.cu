@@ -32,6 +32,12 @@ constexpr int kMaxCluster = 8;
 
 enum Mode { PROJECT, GATE_UP, DOWN };
 
+// Steps of weights in flight, and of tokens: those of DOWN come from L2, the others
+// from L1.  Two CTAs an SM (registers).
+__host__ __device__ constexpr int ahead_of(int mode) { return mode == DOWN ? 2 : 3; }
+__host__ __device__ constexpr int ahead_x_of(int mode) { return mode == DOWN ? 2 : 1; }
+constexpr int kCtas = 2;
+
 struct FewParams {
   const uint8_t* w;            // PROJECT, or the units' matrices
   const uint8_t* w_shared;
@@ -81,39 +87,45 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 rows of one record as a lane holds them: pieces `lane % 4` of rows lane / 4 and
-// lane / 4 + 8, and their four scales (of words 0 .. 3).
+// Two rows of a record as a lane holds them: a piece of each and the rows' scales.
+template <int GROUP>
 struct Rows {
   uint4 c[2];
-  uint32_t s[2];
+  uint32_t s[2][GROUP == 16 ? 2 : 1];
 };
 
+// codes and scales: those of the lane's first row; its second one is eight rows on.
 template <int GROUP>
-__device__ __forceinline__ void load_rows(Rows& q, const uint8_t* rec, int row, int lane) {
-  const int g = lane >> 2, tig = lane & 3;
+__device__ __forceinline__ void load_rows(Rows<GROUP>& q, const uint8_t* codes, const uint8_t* scales) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = row + g + 8 * i;
-    q.c[i] = ldg_stream(rec + quant_piece(r, tig));
+    q.c[i] = ldg_stream(codes + i * 8 * 64);
+    const uint8_t* at = scales + i * 8 * (kQK / GROUP);
     if (GROUP == 32) {
-      q.s[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + kQCodeBytes + r * 4));
+      q.s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
     } else {
-      const uint2 s = __ldg(reinterpret_cast<const uint2*>(rec + kQCodeBytes + r * 8));
-      q.s[i] = __byte_perm(s.x, s.y, tig >= 2 ? 0x7531 : 0x6420);
+      const uint2 s = __ldg(reinterpret_cast<const uint2*>(at));
+      q.s[i][0] = s.x;
+      q.s[i][GROUP == 16 ? 1 : 0] = s.y;
     }
   }
 }
 
 // d += rows x tokens over a record's 128 inputs; x: word w of the token's piece, four each.
-template <int CODE>
-__device__ __forceinline__ void multiply(float (&d)[4], const Rows& q, const uint4 (&x)[4]) {
+template <int CODE, int GROUP>
+__device__ __forceinline__ void multiply(float (&d)[4], const Rows<GROUP>& q, const uint4 (&x)[4],
+                                         uint32_t pick) {
+  uint32_t s[2];       // the scales of words 0 .. 3: with groups of 16, of the piece's half
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    s[i] = GROUP == 32 ? q.s[i][0] : __byte_perm(q.s[i][0], q.s[i][GROUP == 16 ? 1 : 0], pick);
   auto word = [&](auto index) {
     constexpr int W = decltype(index)::value;
     const uint32_t a = W == 0 ? q.c[0].x : W == 1 ? q.c[0].y : W == 2 ? q.c[0].z : q.c[0].w;
     const uint32_t b = W == 0 ? q.c[1].x : W == 1 ? q.c[1].y : W == 2 ? q.c[1].z : q.c[1].w;
     uint32_t ea[4], eb[4];
-    quant_expand<CODE>(a, QuantScale<CODE>::template at<W>(q.s[0]), ea);
-    quant_expand<CODE>(b, QuantScale<CODE>::template at<W>(q.s[1]), eb);
+    quant_expand<CODE>(a, QuantScale<CODE>::template at<W>(s[0]), ea);
+    quant_expand<CODE>(b, QuantScale<CODE>::template at<W>(s[1]), eb);
     mma_16816(d, ea[0], eb[0], ea[1], eb[1], x[W].x, x[W].y);
     mma_16816(d, ea[2], eb[2], ea[3], eb[3], x[W].z, x[W].w);
   };
@@ -178,18 +190,17 @@ __device__ __forceinline__ int task_warps(int tasks, int steps, int ctas) {
 }
 
 template <int MODE, int CODE, int GROUP, bool PAIR, bool CLUSTER>
-__global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const FewParams p) {
   constexpr uint32_t kRec = quant_record(GROUP);
-  constexpr int kTiles = PAIR ? 2 : 1;
-  // Steps of weights in flight, and of tokens: those of DOWN come from L2, the others
-  // from L1.
-  constexpr int kAhead = 3;
-  constexpr int kAheadX = MODE == DOWN ? kAhead : 1;
+  constexpr int kAhead = ahead_of(MODE);
+  constexpr int kAheadX = ahead_x_of(MODE);
+  constexpr int kRows = PAIR ? 16 : 32;         // features of a task
   __shared__ Units units;
-  __shared__ float sums[kWarps][kTiles][16 * kTokens];
-  __shared__ float parts[CLUSTER ? kMaxCluster : 1][kTiles][16 * kTokens];   // of the cluster's CTAs
+  __shared__ float sums[kWarps][32 * kTokens];
+  __shared__ float parts[CLUSTER ? kMaxCluster : 1][32 * kTokens];   // of the cluster's CTAs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tig = lane & 3;
+  const uint32_t pick = tig >= 2 ? 0x7531 : 0x6420;
   bool waited = false;
   // The selection was written before the launch that a DOWN launch follows, so it may
   // list the units and fetch weights at once.
@@ -202,8 +213,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
     list_units(units, p, MODE == GATE_UP && blockIdx.x == 0);
     D = units.count;
   }
-  const int tiles = (p.n + 15) / 16;            // of a matrix
-  const int shared_tiles = MODE == GATE_UP ? (p.n_shared + 15) / 16 : 0;
+  const int tiles = (p.n + kRows - 1) / kRows;  // of a matrix
+  const int shared_tiles = MODE == GATE_UP ? (p.n_shared + kRows - 1) / kRows : 0;
   const int tasks = MODE == GATE_UP ? D * tiles + shared_tiles : tiles;
   const int steps = MODE == DOWN ? D * p.kb + p.kb_shared : p.kb;
   const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
@@ -220,49 +231,47 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
     const int d = MODE == GATE_UP && !shared ? task / tiles : 0;
     const int tile = shared ? task - D * tiles : MODE == GATE_UP ? task - d * tiles : task;
     const int unit = MODE == GATE_UP && !shared && some ? units.list[d] : 0;
-    const int row = tile * 16 % kQRows;
-    // records of the task's row tile within the first matrix that it reads
-    const size_t at = static_cast<size_t>(tile * 16 / kQRows) * p.kb * kRec;
-    const uint8_t* base = shared ? p.w_shared + at : p.w + p.matrix * (static_cast<size_t>(unit) * kTiles) + at;
-    const size_t up = shared ? p.matrix_shared : p.matrix;
-
-    float acc[kTiles][4] = {};
-    Rows rows[kAhead][kTiles];
-    uint4 x[kAheadX][4];
-    // step s of the task: its record and the tokens' inputs.  DOWN counts through the
-    // units' records, then the shared expert's.
+    const int r = tile * kRows % kQRows + g, rt = tile * kRows / kQRows;
+    const uint32_t codes = quant_piece(r, tig), scales = kQCodeBytes + r * (kQK / GROUP);
+    // the task's rows in the first record that this warp reads
     const int start = rank * ways + part;
+    // from the first tile of 16 rows to the second one
+    const size_t next = !PAIR ? 16 * 64 : shared ? p.matrix_shared : p.matrix;
+    const size_t next_scale = !PAIR ? 16 * (kQK / GROUP) : next;
+    const uint8_t* rec = (shared ? p.w_shared : p.w + p.matrix * (static_cast<size_t>(unit) * (PAIR ? 2 : 1))) +
+                         (static_cast<size_t>(rt) * p.kb + start) * kRec;
+
+    float acc[2][4] = {};
+    Rows<GROUP> rows[kAhead][2];
+    uint4 x[kAheadX][4];
+    // DOWN counts through the units' records, then the shared expert's: unit, record, left
     int ws = start, wd = 0, wk = start;          // the next weights to load
     int xs = start, xd = 0, xk = start;          // the next inputs
-    if (MODE == DOWN)
-      while (wd < D && wk >= p.kb) {
-        wk -= p.kb;
-        ++wd;
+    auto settle = [&](int& sd, int& sk) {
+      while (sd < D && sk >= p.kb) {
+        sk -= p.kb;
+        ++sd;
       }
-    xd = wd;
-    xk = wk;
-    auto forward = [&](int& s, int& sd, int& sk) {
-      s += stride;
-      sk += stride;
-      if (MODE == DOWN)
-        while (sd < D && sk >= p.kb) {
-          sk -= p.kb;
-          ++sd;
-        }
     };
-    auto load_w = [&](Rows (&q)[kTiles]) {
+    if (MODE == DOWN) {
+      settle(wd, wk);
+      xd = wd;
+      xk = wk;
+    }
+    auto load_w = [&](Rows<GROUP> (&q)[2]) {
       if (!some || ws >= steps) return;
-      const uint8_t* rec;
+      const uint8_t* at = rec;
       if (MODE != DOWN) {
-        rec = base + static_cast<size_t>(wk) * kRec;
-      } else if (wd < D) {
-        rec = base + p.matrix * units.list[wd] + static_cast<size_t>(wk) * kRec;
+        rec += static_cast<size_t>(stride) * kRec;
       } else {
-        rec = p.w_shared + (static_cast<size_t>(tile * 16 / kQRows) * p.kb_shared + wk) * kRec;
+        at = wd < D ? p.w + p.matrix * units.list[wd] + (static_cast<size_t>(rt) * p.kb + wk) * kRec
+                    : p.w_shared + (static_cast<size_t>(rt) * p.kb_shared + wk) * kRec;
+        wk += stride;
+        settle(wd, wk);
       }
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) load_rows<GROUP>(q[i], rec + up * i, row, lane);
-      forward(ws, wd, wk);
+      load_rows<GROUP>(q[0], at + codes, at + scales);
+      load_rows<GROUP>(q[1], at + codes + next, at + scales + next_scale);
+      ws += stride;
     };
     auto load_x = [&](uint4 (&v)[4]) {
       if (!some || xs >= steps) return;
@@ -278,12 +287,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
         K = p.K_shared;
         if (g < p.T) src = p.act_shared + static_cast<size_t>(g) * K;
       }
+      const int k = xk * kQK + 8 * tig;
+      const int left = src != nullptr ? K - k : 0;
+      src += k;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int k = xk * kQK + 32 * w + 8 * tig;
-        v[w] = src != nullptr && k < K ? ldg_nc(src + k) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      forward(xs, xd, xk);
+      for (int w = 0; w < 4; ++w) v[w] = 32 * w < left ? ldg_nc(src + 32 * w) : make_uint4(0u, 0u, 0u, 0u);
+      xk += stride;
+      if (MODE == DOWN) settle(xd, xk);
+      xs += stride;
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load_w(rows[i]);
@@ -301,61 +312,56 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quant_few_kernel(const FewPara
           if (s + i * stride >= steps) break;
           if (kAheadX == 1) load_x(x[0]);
 #pragma unroll
-          for (int j = 0; j < kTiles; ++j) multiply<CODE>(acc[j], rows[i][j], x[kAheadX > 1 ? i : 0]);
+          for (int j = 0; j < 2; ++j) multiply<CODE, GROUP>(acc[j], rows[i][j], x[kAheadX > 1 ? i : 0], pick);
           load_w(rows[i]);
           if (kAheadX > 1) load_x(x[i]);
         }
       }
     // the group's sums: [row][token]
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-      float2* to = reinterpret_cast<float2*>(sums[warp][j]);
-      to[g * 4 + tig] = make_float2(acc[j][0], acc[j][1]);
-      to[(g + 8) * 4 + tig] = make_float2(acc[j][2], acc[j][3]);
+    for (int j = 0; j < 2; ++j) {
+      float2* to = reinterpret_cast<float2*>(sums[warp]) + (16 * j + g) * 4 + tig;
+      to[0] = make_float2(acc[j][0], acc[j][1]);
+      to[8 * 4] = make_float2(acc[j][2], acc[j][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ways * 32) : "memory");
     if (CLUSTER) {       // this CTA's sums to the first one's slots
-      for (int i = threadIdx.x; i < kTiles * 16 * kTokens; i += kWarps * 32) {
-        const int j = i / (16 * kTokens), k = i - j * (16 * kTokens);
+      for (int i = threadIdx.x; i < 32 * kTokens; i += kWarps * 32) {
         float v = 0.f;
-        for (int w = 0; w < kWarps; ++w) v += sums[w][j][k];
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&parts[rank][j][k]), 0u)),
-                     "f"(v)
+        for (int w = 0; w < kWarps; ++w) v += sums[w][i];
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&parts[rank][i]), 0u)), "f"(v)
                      : "memory");
       }
       cluster_sync_all();
     }
     // rows fastest: neighbouring threads store neighbouring features
-    for (int i = part * 32 + lane; some && rank == 0 && i < 16 * kTokens; i += ways * 32) {
-      const int r = i % 16, t = i / 16, feature = tile * 16 + r;
-      float v[kTiles] = {};
-      for (int w = 0; w < (CLUSTER ? p.cluster : ways); ++w)
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-          v[j] += CLUSTER ? parts[w][j][r * kTokens + t] : sums[group * ways + w][j][r * kTokens + t];
+    for (int i = part * 32 + lane; some && rank == 0 && i < kRows * kTokens; i += ways * 32) {
+      const int f = i % kRows, t = i / kRows, feature = tile * kRows + f;
+      float v = 0.f, lift = 0.f;
+      for (int w = 0; w < (CLUSTER ? p.cluster : ways); ++w) {
+        const float* from = CLUSTER ? parts[w] : sums[group * ways + w];
+        v += from[f * kTokens + t];
+        if (PAIR) lift += from[(16 + f % 16) * kTokens + t];
+      }
       if (t >= p.T || feature >= (shared ? p.n_shared : p.n)) continue;
       constexpr float u = CODE == MOE_QUANT_E2M1 ? 512.f : 1.f;
       if (MODE == DOWN) {      // the factors came with the activations
-        p.out[t * p.ldo + feature] = __float2bfloat16_rn(v[0]);
-      } else if (MODE == PROJECT) {
-        float y = v[0] * (p.factor[0] * u);
-        if (PAIR) y = y / (1.f + expf(-y)) * (v[kTiles - 1] * (p.factor[1] * u));
-        p.out[t * p.ldo + feature] = __float2bfloat16_rn(y);
+        p.out[t * p.ldo + feature] = __float2bfloat16_rn(v);
+        continue;
+      }
+      const float* factor = shared ? p.factor_shared : p.factor + 2 * unit;
+      v *= factor[0] * u;
+      if (PAIR) v = v / (1.f + expf(-v)) * (lift * (factor[1] * u));
+      if (MODE == PROJECT) {
+        p.out[t * p.ldo + feature] = __float2bfloat16_rn(v);
+      } else if (shared) {
+        p.out_act_shared[static_cast<size_t>(t) * p.n_shared + feature] =
+            __float2bfloat16_rn(v * (p.factor_down_shared[0] * u));
       } else {
-        const float* f = shared ? p.factor_shared : p.factor + 2 * unit;
-        const float gate = v[0] * (f[0] * u), lift = v[kTiles - 1] * (f[1] * u);
-        const float y = gate / (1.f + expf(-gate)) * lift * u;
-        if (shared) {
-          p.out_act_shared[static_cast<size_t>(t) * p.n_shared + feature] =
-              __float2bfloat16_rn(y * p.factor_down_shared[0]);
-        } else {
-          const int j = units.slot[unit][t];
-          if (j != 255) {
-            const size_t at_row = static_cast<size_t>(t) * p.k_max + j;
-            p.out_act[at_row * p.n + feature] =
-                __float2bfloat16_rn(y * p.factor_down[unit] * p.topk_w[at_row]);
-          }
-        }
+        const int j = units.slot[unit][t];
+        if (j == 255) continue;
+        const size_t row = static_cast<size_t>(t) * p.k_max + j;
+        p.out_act[row * p.n + feature] = __float2bfloat16_rn(v * (p.factor_down[unit] * u) * p.topk_w[row]);
       }
     }
     // the next task's sums overwrite these
@@ -388,19 +394,20 @@ cudaError_t launch_kind(const FewParams& p, int grid, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, quant_few_kernel<MODE, CODE, GROUP, PAIR, MODE != GATE_UP>, p);
 }
 
-// `tasks` of `steps` records (0: many) on two CTAs an SM: the CTAs of a cluster that
-// share a task are what makes the longest CTA's steps fewest.
+// `tasks` of about `steps` records: the CTAs of a cluster that share a task are what
+// makes the longest CTA's steps fewest, with a step for starting a task and another
+// for the cluster's barriers.
 template <int MODE, bool PAIR>
 cudaError_t launch_few(FewParams p, int code, int group, int tasks, int steps, int sm_count, cudaStream_t s) {
-  const int ctas = 2 * sm_count;
+  const int ctas = kCtas * sm_count;
   p.cluster = 1;
   if (MODE != GATE_UP) {
-    double best = 0;
+    long long best = 0;
     for (int c = 1; c <= kMaxCluster; c *= 2) {
-      const int rounds = (tasks * c + ctas - 1) / ctas;
-      const double each = steps > 0 ? (steps + kWarps * c - 1) / (kWarps * c) + (c > 1 ? 1.0 : 0.5) : 1.0 / c;
-      if (c == 1 || rounds * each < 0.95 * best) {
-        best = rounds * each;
+      const long long rounds = (static_cast<long long>(tasks) * c + ctas - 1) / ctas;
+      const long long cost = rounds * ((steps + kWarps * c - 1) / (kWarps * c) + (c > 1 ? 2 : 1));
+      if (c == 1 || cost < best) {
+        best = cost;
         p.cluster = c;
       }
     }
@@ -431,7 +438,7 @@ cudaError_t launch_quant_project_few(const QuantGemmArgs& a, cudaStream_t s) {
   p.K = a.K;
   p.kb = q.kb;
   p.status = a.status;
-  const int tiles = (a.n + 15) / 16;
+  const int tiles = a.swiglu ? (a.n + 15) / 16 : (a.n + 31) / 32;
   return a.swiglu ? launch_few<PROJECT, true>(p, a.code, a.group, tiles, q.kb, a.sm_count, s)
                   : launch_few<PROJECT, false>(p, a.code, a.group, tiles, q.kb, a.sm_count, s);
 }
@@ -482,7 +489,8 @@ cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
   d.n_shared = 0;
   d.K_shared = a.I_shared;
   d.kb_shared = a.I_shared > 0 ? dns.kb : 0;
-  return launch_few<DOWN, false>(d, a.code, a.group, (a.H + 15) / 16, 0, a.sm_count, s);
+    const int units = a.E < a.T * a.k_max ? a.E : a.T * a.k_max;       // at most
+  return launch_few<DOWN, false>(d, a.code, a.group, (a.H + 31) / 32, units * dn.kb + d.kb_shared, a.sm_count, s);
 }
 
 }  // namespace moe
