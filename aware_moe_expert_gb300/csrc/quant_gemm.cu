@@ -214,10 +214,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 // 64 expanded weights of a row (words H, H + 1 of its pieces c; s4: a scale byte for
 // every 16 inputs) to TMEM columns d .. d + 31.
 template <int CODE, int H>
@@ -595,20 +591,24 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
       const uint32_t d = kTmemD + (static_cast<uint32_t>(q * 32) << 16) +
                          static_cast<uint32_t>(db * 2 * NT);
       if constexpr (SPLIT) {
-        // column c is summed by the CTA c % splits: its slot [rank][c / splits][256 rows]
-        const uint32_t part = smem_u32(smem + Cfg::kOffPart);
+        // A CTA sums `per` of the chunk's columns: its slot [rank][per / 2][256 rows] of
+        // pairs
+        const uint32_t part = sbase + Cfg::kOffPart;
         const int per = (t.rows + 15) / 16 * 16 / p.splits;
         for (int i = 0; i < nt; ++i)
           for (int c0 = 0; c0 < t.rows; c0 += 16) {
             uint32_t v[16];
             tmem_ld16(d + static_cast<uint32_t>(i * NT + c0), v);
             tmem_ld_wait();
+            const float f = i == 0 ? f0 : f1;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const int col = c0 + c, to = col % p.splits;
-              st_cluster_f32(mapa_shared(part, static_cast<uint32_t>(to)) +
-                                 static_cast<uint32_t>(((rank * per + col / p.splits) * 256 + i * 128 + r) * 4),
-                             __uint_as_float(v[c]) * (i == 0 ? f0 : f1));
+            for (int c = 0; c < 16; c += 2) {     // pairs: per is even
+              const int to = (c0 + c) / per, in = c0 + c - to * per;
+              asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                               mapa_shared(part, static_cast<uint32_t>(to)) +
+                               static_cast<uint32_t>(((rank * (per / 2) + in / 2) * 256 + i * 128 + r) * 8)),
+                           "f"(__uint_as_float(v[c]) * f), "f"(__uint_as_float(v[c + 1]) * f)
+                           : "memory");
             }
           }
       } else if (p.f32) {
@@ -693,24 +693,35 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     cluster_sync_all();          // every partial sum has arrived
     if (first < total && *s_abort == 0) {
       const Tile t = decode_tile<NT>(first, p.blocks, p.n_groups, s_prefix, s_offs);
-      const float* part = reinterpret_cast<const float*>(smem + Cfg::kOffPart);
+      const float2* part = reinterpret_cast<const float2*>(smem + Cfg::kOffPart);
       const int per = (t.rows + 15) / 16 * 16 / p.splits;
       const int rows = p.swiglu ? 128 : 256;
-      for (int i = threadIdx.x; i < per * rows; i += blockDim.x) {
-        const int c = i / rows, r = i - c * rows;
-        const int token = c * p.splits + rank, col = t.nt * rows + r;
-        if (token >= t.rows || col >= p.n) continue;
-        float y = 0.f, v = 0.f;
+      // neighbouring threads: neighbouring features
+      for (int i = threadIdx.x; i < per / 2 * rows; i += blockDim.x) {
+        const int c = i / rows * 2, r = i % rows;
+        const int col = t.nt * rows + r;
+        float2 y = make_float2(0.f, 0.f), v = y;
         for (int s = 0; s < p.splits; ++s) {
-          y += part[(s * per + c) * 256 + r];
-          if (p.swiglu) v += part[(s * per + c) * 256 + 128 + r];
+          const float2 a = part[(s * (per / 2) + c / 2) * 256 + r];
+          y.x += a.x;
+          y.y += a.y;
+          if (p.swiglu) {
+            const float2 b = part[(s * (per / 2) + c / 2) * 256 + 128 + r];
+            v.x += b.x;
+            v.y += b.y;
+          }
         }
-        if (p.swiglu) y = silu_fast(y) * v;
-        const size_t at = static_cast<size_t>(t.row0 + token) * p.ldo + col;
-        if (p.f32)
-          static_cast<float*>(p.out)[at] = y;
-        else
-          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+        if (p.swiglu) y = make_float2(silu_fast(y.x) * v.x, silu_fast(y.y) * v.y);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int token = rank * per + c + k;
+          if (token >= t.rows || col >= p.n) continue;
+          const size_t at = static_cast<size_t>(t.row0 + token) * p.ldo + col;
+          if (p.f32)
+            static_cast<float*>(p.out)[at] = k == 0 ? y.x : y.y;
+          else
+            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(k == 0 ? y.x : y.y);
+        }
       }
     }
   }
@@ -795,6 +806,34 @@ cudaError_t launch_tile(const CUtensorMap& tm16, const CUtensorMap& tm64, const 
   return cudaLaunchKernelEx(&cfg, kern, tm16, tm64, p);
 }
 
+// Clusters of `size` CTAs of the splitting kernel that the device holds at once.
+int clusters_at_once(int size) {
+  static int cache[64][4] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int& n = cache[dev][size == 2 ? 1 : size == 4 ? 2 : 3];
+  if (n == 0) {
+    using Cfg = TileCfg<64, true>;
+    auto kern = quant_tile_kernel<64, false, true>;
+    static bool done[64] = {false};
+    if (set_smem_once(kern, static_cast<int>(Cfg::kSmem), done) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+    (void)cudaGetLastError();
+  }
+  return n;
+}
+
 }  // namespace
 
 cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
@@ -842,8 +881,10 @@ cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
                                                 : a.out_rows / nt + std::min(a.out_rows, static_cast<long long>(a.n_groups));
   const long long items = chunks * p.blocks;
   if (a.token == nullptr && a.offsets == nullptr && !wide) {
+    // as wide as clusters fit at once (152 SMs hold 15 of eight: 64 tokens of K 7168,
+    // N 4096 in 16 clusters of eight 25 us, of four 17)
     int splits = 1;
-    while (splits < 8 && items * splits * 2 <= a.sm_count && p.kb >= 2 * splits) splits *= 2;
+    while (splits < 8 && items <= clusters_at_once(2 * splits) && p.kb >= 2 * splits) splits *= 2;
     if (splits > 1) {
       p.splits = splits;
       return launch_tile<64, false, true>(tm16, tm64, p, static_cast<unsigned>(items * splits), s);
