@@ -37,6 +37,9 @@ enum Mode { PROJECT, GATE_UP, DOWN };
 __host__ __device__ constexpr int ahead_of(int mode) { return mode == DOWN ? 2 : 3; }
 __host__ __device__ constexpr int ahead_x_of(int mode) { return mode == DOWN ? 2 : 1; }
 constexpr int kCtas = 2;
+// Tiles of 16 rows of a task.  Two share the tokens' loads; a projection has few tasks
+// and takes one (one token, K 7168, N 4096: 6.4 us, with two 7.6).
+__host__ __device__ constexpr int tiles_of(int mode, bool pair) { return mode == PROJECT && !pair ? 1 : 2; }
 
 struct FewParams {
   const uint8_t* w;            // PROJECT, or the units' matrices
@@ -194,10 +197,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
   constexpr uint32_t kRec = quant_record(GROUP);
   constexpr int kAhead = ahead_of(MODE);
   constexpr int kAheadX = ahead_x_of(MODE);
-  constexpr int kRows = PAIR ? 16 : 32;         // features of a task
+  constexpr int kTiles = tiles_of(MODE, PAIR);
+  constexpr int kRows = PAIR ? 16 : 16 * kTiles;         // features of a task
   __shared__ Units units;
-  __shared__ float sums[kWarps][32 * kTokens];
-  __shared__ float parts[CLUSTER ? kMaxCluster : 1][32 * kTokens];   // of the cluster's CTAs
+  __shared__ float sums[kWarps][kTiles * 16 * kTokens];
+  __shared__ float parts[CLUSTER ? kMaxCluster : 1][kTiles * 16 * kTokens];   // of the cluster's CTAs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tig = lane & 3;
   const uint32_t pick = tig >= 2 ? 0x7531 : 0x6420;
@@ -241,8 +245,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
     const uint8_t* rec = (shared ? p.w_shared : p.w + p.matrix * (static_cast<size_t>(unit) * (PAIR ? 2 : 1))) +
                          (static_cast<size_t>(rt) * p.kb + start) * kRec;
 
-    float acc[2][4] = {};
-    Rows<GROUP> rows[kAhead][2];
+    float acc[kTiles][4] = {};
+    Rows<GROUP> rows[kAhead][kTiles];
     uint4 x[kAheadX][4];
     // DOWN counts through the units' records, then the shared expert's: unit, record, left
     int ws = start, wd = 0, wk = start;          // the next weights to load
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
       xd = wd;
       xk = wk;
     }
-    auto load_w = [&](Rows<GROUP> (&q)[2]) {
+    auto load_w = [&](Rows<GROUP> (&q)[kTiles]) {
       if (!some || ws >= steps) return;
       const uint8_t* at = rec;
       if (MODE != DOWN) {
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
         settle(wd, wk);
       }
       load_rows<GROUP>(q[0], at + codes, at + scales);
-      load_rows<GROUP>(q[1], at + codes + next, at + scales + next_scale);
+      if (kTiles == 2) load_rows<GROUP>(q[kTiles - 1], at + codes + next, at + scales + next_scale);
       ws += stride;
     };
     auto load_x = [&](uint4 (&v)[4]) {
@@ -312,21 +316,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
           if (s + i * stride >= steps) break;
           if (kAheadX == 1) load_x(x[0]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) multiply<CODE, GROUP>(acc[j], rows[i][j], x[kAheadX > 1 ? i : 0], pick);
+          for (int j = 0; j < kTiles; ++j) multiply<CODE, GROUP>(acc[j], rows[i][j], x[kAheadX > 1 ? i : 0], pick);
           load_w(rows[i]);
           if (kAheadX > 1) load_x(x[i]);
         }
       }
     // the group's sums: [row][token]
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < kTiles; ++j) {
       float2* to = reinterpret_cast<float2*>(sums[warp]) + (16 * j + g) * 4 + tig;
       to[0] = make_float2(acc[j][0], acc[j][1]);
       to[8 * 4] = make_float2(acc[j][2], acc[j][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ways * 32) : "memory");
     if (CLUSTER) {       // this CTA's sums to the first one's slots
-      for (int i = threadIdx.x; i < 32 * kTokens; i += kWarps * 32) {
+      for (int i = threadIdx.x; i < kTiles * 16 * kTokens; i += kWarps * 32) {
         float v = 0.f;
         for (int w = 0; w < kWarps; ++w) v += sums[w][i];
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&parts[rank][i]), 0u)), "f"(v)
@@ -395,7 +399,7 @@ cudaError_t launch_kind(const FewParams& p, int grid, cudaStream_t s) {
 }
 
 // `tasks` of about `steps` records: the CTAs of a cluster that share a task are what
-// makes the longest CTA's steps fewest, with a step for starting a task and another
+// makes the longest CTA's steps fewest, with a step for starting a task and two
 // for the cluster's barriers.
 template <int MODE, bool PAIR>
 cudaError_t launch_few(FewParams p, int code, int group, int tasks, int steps, int sm_count, cudaStream_t s) {
@@ -405,7 +409,7 @@ cudaError_t launch_few(FewParams p, int code, int group, int tasks, int steps, i
     long long best = 0;
     for (int c = 1; c <= kMaxCluster; c *= 2) {
       const long long rounds = (static_cast<long long>(tasks) * c + ctas - 1) / ctas;
-      const long long cost = rounds * ((steps + kWarps * c - 1) / (kWarps * c) + (c > 1 ? 2 : 1));
+      const long long cost = rounds * ((steps + kWarps * c - 1) / (kWarps * c) + (c > 1 ? 3 : 1));
       if (c == 1 || cost < best) {
         best = cost;
         p.cluster = c;
@@ -438,7 +442,7 @@ cudaError_t launch_quant_project_few(const QuantGemmArgs& a, cudaStream_t s) {
   p.K = a.K;
   p.kb = q.kb;
   p.status = a.status;
-  const int tiles = a.swiglu ? (a.n + 15) / 16 : (a.n + 31) / 32;
+  const int tiles = (a.n + 15) / 16;
   return a.swiglu ? launch_few<PROJECT, true>(p, a.code, a.group, tiles, q.kb, a.sm_count, s)
                   : launch_few<PROJECT, false>(p, a.code, a.group, tiles, q.kb, a.sm_count, s);
 }
