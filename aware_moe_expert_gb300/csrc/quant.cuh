@@ -6,11 +6,11 @@
 //   [128 rows][64 bytes of codes]     then     [128 rows][128 / group scales]
 // Rows and inputs past the matrix are zero weights.
 //
-// Codes: the 16-byte piece c of a row holds the inputs k with (k % 32) / 8 == c,
-// its 32-bit word w those of k / 32 == w: four lanes that read one piece each
-// have, word by word, 32 consecutive inputs (the K of two mma.m16n8k16), and a
-// thread that reads a whole row has all 128.  Piece c of row r lies at place
-// c ^ ((r / 2) % 4), which spreads eight rows' equal pieces over all banks.
+// Codes: the 16-byte piece c of a row holds its inputs 32 c .. 32 c + 31, so that a lane
+// with one piece needs one or two scales, and its 32-bit word w eight of them; four
+// lanes with a piece each have, word by word, the K of two mma.m16n8k16.  Piece c of
+// row r lies at place c ^ ((r / 2) % 4), which spreads eight rows' equal pieces over
+// all banks.
 //
 // Eight codes of a word are four pairs (k, k + 1), one in each half word, that
 // become bf16 pairs by a shift, a mask and one packed bf16 operation:
@@ -85,18 +85,20 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// What a word's expansion needs of its group's scale: byte I of `bytes` as a pair of
+// What a word's expansion needs of its group's scale: a byte of `bytes` as a pair of
 // equal bf16, and -136 times it.
 template <int CODE>
 struct QuantScale {
   uint32_t s, c;
-  template <int I>
-  __device__ __forceinline__ static QuantScale at(uint32_t bytes) {
+  __device__ __forceinline__ static QuantScale of(uint32_t twice) {   // the byte in both halves
     QuantScale q;
-    q.s = __byte_perm(bytes, 0u, 0x4040 | I << 8 | I) * 16u +
-          (CODE == MOE_QUANT_E2M1 ? kScaleBase117 : kScaleBase);
+    q.s = twice * 16u + (CODE == MOE_QUANT_E2M1 ? kScaleBase117 : kScaleBase);
     q.c = CODE == MOE_QUANT_INT ? hmul2_bf16(q.s, 0xC308C308u) : 0u;
     return q;
+  }
+  template <int I>
+  __device__ __forceinline__ static QuantScale at(uint32_t bytes) {
+    return of(__byte_perm(bytes, 0u, 0x4040 | I << 8 | I));
   }
 };
 

@@ -32,10 +32,9 @@ constexpr int kMaxCluster = 8;
 
 enum Mode { PROJECT, GATE_UP, DOWN };
 
-// Steps of weights in flight, and of tokens: those of DOWN come from L2, the others
-// from L1.  Two CTAs an SM (registers).
-__host__ __device__ constexpr int ahead_of(int mode) { return mode == DOWN ? 2 : 3; }
-__host__ __device__ constexpr int ahead_x_of(int mode) { return mode == DOWN ? 2 : 1; }
+// Steps in flight.  With two tiles of rows a third one spills (layer of eight tokens
+// 42 us, 47).
+__host__ __device__ constexpr int ahead_of(int mode, bool pair) { return mode == PROJECT && !pair ? 3 : 2; }
 constexpr int kCtas = 2;
 // Tiles of 16 rows of a task.  Two share the tokens' loads; a projection has few tasks
 // and takes one (one token, K 7168, N 4096: 6.4 us, with two 7.6).
@@ -90,45 +89,40 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two rows of a record as a lane holds them: a piece of each and the rows' scales.
-template <int GROUP>
+// Two rows of a record as a lane holds them: a piece of each and its scales, in the low
+// byte, or two.
 struct Rows {
   uint4 c[2];
-  uint32_t s[2][GROUP == 16 ? 2 : 1];
+  uint32_t s[2];
 };
 
 // codes and scales: those of the lane's first row; its second one is eight rows on.
 template <int GROUP>
-__device__ __forceinline__ void load_rows(Rows<GROUP>& q, const uint8_t* codes, const uint8_t* scales) {
+__device__ __forceinline__ void load_rows(Rows& q, const uint8_t* codes, const uint8_t* scales) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     q.c[i] = ldg_stream(codes + i * 8 * 64);
     const uint8_t* at = scales + i * 8 * (kQK / GROUP);
-    if (GROUP == 32) {
-      q.s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-    } else {
-      const uint2 s = __ldg(reinterpret_cast<const uint2*>(at));
-      q.s[i][0] = s.x;
-      q.s[i][GROUP == 16 ? 1 : 0] = s.y;
-    }
+    q.s[i] = GROUP == 32 ? __ldg(at) : __ldg(reinterpret_cast<const uint16_t*>(at));
   }
 }
 
 // d += rows x tokens over a record's 128 inputs; x: word w of the token's piece, four each.
 template <int CODE, int GROUP>
-__device__ __forceinline__ void multiply(float (&d)[4], const Rows<GROUP>& q, const uint4 (&x)[4],
-                                         uint32_t pick) {
-  uint32_t s[2];       // the scales of words 0 .. 3: with groups of 16, of the piece's half
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    s[i] = GROUP == 32 ? q.s[i][0] : __byte_perm(q.s[i][0], q.s[i][GROUP == 16 ? 1 : 0], pick);
+__device__ __forceinline__ void multiply(float (&d)[4], const Rows& q, const uint4 (&x)[4]) {
+  using Scale = QuantScale<CODE>;
+  Scale sa[2], sb[2];          // of words 0 and 1, 2 and 3
+  sa[0] = Scale::template at<0>(q.s[0]);
+  sb[0] = Scale::template at<0>(q.s[1]);
+  sa[1] = GROUP == 32 ? sa[0] : Scale::template at<1>(q.s[0]);
+  sb[1] = GROUP == 32 ? sb[0] : Scale::template at<1>(q.s[1]);
   auto word = [&](auto index) {
     constexpr int W = decltype(index)::value;
     const uint32_t a = W == 0 ? q.c[0].x : W == 1 ? q.c[0].y : W == 2 ? q.c[0].z : q.c[0].w;
     const uint32_t b = W == 0 ? q.c[1].x : W == 1 ? q.c[1].y : W == 2 ? q.c[1].z : q.c[1].w;
     uint32_t ea[4], eb[4];
-    quant_expand<CODE>(a, QuantScale<CODE>::template at<W>(s[0]), ea);
-    quant_expand<CODE>(b, QuantScale<CODE>::template at<W>(s[1]), eb);
+    quant_expand<CODE>(a, sa[W / 2], ea);
+    quant_expand<CODE>(b, sb[W / 2], eb);
     mma_16816(d, ea[0], eb[0], ea[1], eb[1], x[W].x, x[W].y);
     mma_16816(d, ea[2], eb[2], ea[3], eb[3], x[W].z, x[W].w);
   };
@@ -195,8 +189,7 @@ __device__ __forceinline__ int task_warps(int tasks, int steps, int ctas) {
 template <int MODE, int CODE, int GROUP, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const FewParams p) {
   constexpr uint32_t kRec = quant_record(GROUP);
-  constexpr int kAhead = ahead_of(MODE);
-  constexpr int kAheadX = ahead_x_of(MODE);
+  constexpr int kAhead = ahead_of(MODE, PAIR);
   constexpr int kTiles = tiles_of(MODE, PAIR);
   constexpr int kRows = PAIR ? 16 : 16 * kTiles;         // features of a task
   __shared__ Units units;
@@ -204,7 +197,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
   __shared__ float parts[CLUSTER ? kMaxCluster : 1][kTiles * 16 * kTokens];   // of the cluster's CTAs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tig = lane & 3;
-  const uint32_t pick = tig >= 2 ? 0x7531 : 0x6420;
   bool waited = false;
   // The selection was written before the launch that a DOWN launch follows, so it may
   // list the units and fetch weights at once.
@@ -236,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
     const int tile = shared ? task - D * tiles : MODE == GATE_UP ? task - d * tiles : task;
     const int unit = MODE == GATE_UP && !shared && some ? units.list[d] : 0;
     const int r = tile * kRows % kQRows + g, rt = tile * kRows / kQRows;
-    const uint32_t codes = quant_piece(r, tig), scales = kQCodeBytes + r * (kQK / GROUP);
+    const uint32_t codes = quant_piece(r, tig), scales = kQCodeBytes + r * (kQK / GROUP) + tig * (32 / GROUP);
     // the task's rows in the first record that this warp reads
     const int start = rank * ways + part;
     // from the first tile of 16 rows to the second one
@@ -246,8 +238,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
                          (static_cast<size_t>(rt) * p.kb + start) * kRec;
 
     float acc[kTiles][4] = {};
-    Rows<GROUP> rows[kAhead][kTiles];
-    uint4 x[kAheadX][4];
+    Rows rows[kAhead][kTiles];
+    uint4 x[kAhead][4];
     // DOWN counts through the units' records, then the shared expert's: unit, record, left
     int ws = start, wd = 0, wk = start;          // the next weights to load
     int xs = start, xd = 0, xk = start;          // the next inputs
@@ -262,7 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
       xd = wd;
       xk = wk;
     }
-    auto load_w = [&](Rows<GROUP> (&q)[kTiles]) {
+    auto load_w = [&](Rows (&q)[kTiles]) {
       if (!some || ws >= steps) return;
       const uint8_t* at = rec;
       if (MODE != DOWN) {
@@ -291,11 +283,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
         K = p.K_shared;
         if (g < p.T) src = p.act_shared + static_cast<size_t>(g) * K;
       }
-      const int k = xk * kQK + 8 * tig;
+      const int k = xk * kQK + 32 * tig;
       const int left = src != nullptr ? K - k : 0;
       src += k;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) v[w] = 32 * w < left ? ldg_nc(src + 32 * w) : make_uint4(0u, 0u, 0u, 0u);
+      for (int w = 0; w < 4; ++w) v[w] = 8 * w < left ? ldg_nc(src + 8 * w) : make_uint4(0u, 0u, 0u, 0u);
       xk += stride;
       if (MODE == DOWN) settle(xd, xk);
       xs += stride;
@@ -306,19 +298,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
       pdl_wait_and_trigger();
       waited = true;
     }
-    if (kAheadX > 1)
 #pragma unroll
-      for (int i = 0; i < kAheadX; ++i) load_x(x[i]);
+    for (int i = 0; i < kAhead; ++i) load_x(x[i]);
     if (some)
       for (int s = start; s < steps; s += kAhead * stride) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           if (s + i * stride >= steps) break;
-          if (kAheadX == 1) load_x(x[0]);
 #pragma unroll
-          for (int j = 0; j < kTiles; ++j) multiply<CODE, GROUP>(acc[j], rows[i][j], x[kAheadX > 1 ? i : 0], pick);
+          for (int j = 0; j < kTiles; ++j) multiply<CODE, GROUP>(acc[j], rows[i][j], x[i]);
           load_w(rows[i]);
-          if (kAheadX > 1) load_x(x[i]);
+          load_x(x[i]);
         }
       }
     // the group's sums: [row][token]

@@ -214,23 +214,29 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-// 64 expanded weights of a row (words H, H + 1 of its pieces c; s4: a scale byte for
-// every 16 inputs) to TMEM columns d .. d + 31.
-template <int CODE, int H>
-__device__ __forceinline__ void expand_half(const uint4 (&c)[4], uint32_t s4, uint32_t d) {
+// 64 expanded weights of a row (pieces c[0] and c[1]; s2: their scale bytes) to TMEM
+// columns d .. d + 31.
+template <int CODE, int GROUP>
+__device__ __forceinline__ void expand_half(const uint4& c0, const uint4& c1, uint32_t bytes, uint32_t d) {
   uint32_t v[32];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const QuantScale<CODE> q[2] = {
-        i == 0 ? QuantScale<CODE>::template at<0>(s4) : QuantScale<CODE>::template at<2>(s4),
-        i == 0 ? QuantScale<CODE>::template at<1>(s4) : QuantScale<CODE>::template at<3>(s4)};
+    const uint4& c = i == 0 ? c0 : c1;
+    const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+    using Scale = QuantScale<CODE>;
+    Scale q[2];
+    if (GROUP == 16) {
+      q[0] = i == 0 ? Scale::template at<0>(bytes) : Scale::template at<2>(bytes);
+      q[1] = i == 0 ? Scale::template at<1>(bytes) : Scale::template at<3>(bytes);
+    } else {
+      q[0] = q[1] = i == 0 ? Scale::template at<0>(bytes) : Scale::template at<1>(bytes);
+    }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t w = H == 0 ? (i == 0 ? c[p].x : c[p].y) : (i == 0 ? c[p].z : c[p].w);
+    for (int w = 0; w < 4; ++w) {
       uint32_t e[4];
-      quant_expand<CODE>(w, q[p >> 1], e);
+      quant_expand<CODE>(word[w], q[w >> 1], e);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[16 * i + 4 * p + j] = e[j];
+      for (int j = 0; j < 4; ++j) v[16 * i + 4 * w + j] = e[j];
     }
   }
   tmem_st32(d, v);
@@ -443,10 +449,11 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
           if (mine) {
             if (H == 0 || kParts == 2) tc_fence_after();
             const uint32_t to = d + H * (kParts == 2 ? kACols : 32);
+            const uint32_t bytes = H == 0 ? sc.x : sc.y;
             if (p.code == MOE_QUANT_INT)
-              expand_half<MOE_QUANT_INT, H>(c, H == 0 ? sc.x : sc.y, to);
+              expand_half<MOE_QUANT_INT, 16>(c[2 * H], c[2 * H + 1], bytes, to);
             else
-              expand_half<MOE_QUANT_E2M1, H>(c, H == 0 ? sc.x : sc.y, to);
+              expand_half<MOE_QUANT_E2M1, 16>(c[2 * H], c[2 * H + 1], bytes, to);
           }
           if (H == 1 || kParts == 2) {
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

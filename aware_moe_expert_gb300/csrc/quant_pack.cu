@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p,
         }
         w |= quant_place(p.code, q, i / 2, i & 1);
       }
-      *reinterpret_cast<uint32_t*>(rec + quant_word(r, (k % 32) / 8, k / 32)) = w;
+      *reinterpret_cast<uint32_t*>(rec + quant_word(r, k / 32, (k % 32) / 8)) = w;
     }
   }
 }
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(const PackParams p
     const uint8_t* rec = p.packed + p.shape.bytes * m +
                          (static_cast<size_t>(n / kQRows) * p.shape.kb + kb) * quant_record(p.group);
     const uint32_t w =
-        *reinterpret_cast<const uint32_t*>(rec + quant_word(r, (k % 32) / 8, k / 32));
+        *reinterpret_cast<const uint32_t*>(rec + quant_word(r, k / 32, (k % 32) / 8));
     uint32_t e[4];
     quant_expand<CODE>(
         w, QuantScale<CODE>::template at<0>(rec[kQCodeBytes + r * (kQK / p.group) + k / p.group]), e);
