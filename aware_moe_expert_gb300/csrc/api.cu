@@ -927,7 +927,9 @@ moe_status validate_quant_layer(const moe_layer_desc* d) {
   c.I_shared = 0;
   MOE_TRY(validate(&c));
   if (d->I_shared < 0) return MOE_ERR_INVALID_ARGUMENT;
-  return d->I_shared % 64 != 0 || d->I_shared > (1 << 20) ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+  return d->I_shared % 64 != 0 || d->I_shared > (1 << 20) || d->I_sub > (1 << 20)
+             ? MOE_ERR_UNSUPPORTED_SHAPE
+             : MOE_OK;
 }
 
 moe_status validate_quant_weights(const moe_layer_desc* d, const moe_quant_weights* w, bool routed,

@@ -14,6 +14,10 @@ namespace {
 
 constexpr int kPackThreads = 256;
 
+// Waits for the launch before, and does not let the next one start early: the products
+// read weights before they wait, as parameters.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct PackParams {
   const uint8_t* codes;        // [count, rows, K / 2]; null: quantise w
   const uint8_t* scales;       // [count, rows, groups]
@@ -55,7 +59,7 @@ __device__ __forceinline__ uint32_t nearest(int code, float v) {
 
 // Largest magnitude of each matrix, as ordered bits (all are >= 0).
 __global__ void __launch_bounds__(kPackThreads) amax_kernel(PackParams p, uint32_t* amax) {
-  pdl_wait_and_trigger();
+  pdl_wait();
   const size_t n = static_cast<size_t>(p.rows) * p.K;
   const __nv_bfloat16* w = p.w + n * blockIdx.y;
   float m = 0.f;
@@ -77,7 +81,7 @@ __device__ __forceinline__ float vmax_of(int code) { return code == MOE_QUANT_IN
 
 // amax -> factor: the largest weight is the largest scale times the largest code.
 __global__ void __launch_bounds__(kPackThreads) factor_kernel(PackParams p, float* factor) {
-  pdl_wait_and_trigger();
+  pdl_wait();
   const int i = blockIdx.x * kPackThreads + threadIdx.x;
   if (i >= p.count) return;
   if (p.codes != nullptr) {
@@ -94,7 +98,7 @@ __global__ void __launch_bounds__(kPackThreads) factor_kernel(PackParams p, floa
 // so that a scale is looked at once.
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p,
                                                             const float* factor) {
-  pdl_wait_and_trigger();
+  pdl_wait();
   const int per_row = kQK / p.group, words = p.group / 8;
   const size_t per_tile = static_cast<size_t>(kQRows) * per_row;
   const size_t per_matrix = per_tile * p.shape.rt * p.shape.kb;
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p,
 template <int CODE>
 __global__ void __launch_bounds__(kPackThreads) unpack_kernel(const PackParams p,
                                                               const float* factor) {
-  pdl_wait_and_trigger();
+  pdl_wait();
   const int words = p.shape.kb * (kQK / 8);
   const size_t per_matrix = static_cast<size_t>(p.rows) * words;
   const size_t id = static_cast<size_t>(blockIdx.x) * kPackThreads + threadIdx.x;
