@@ -6,13 +6,16 @@
     residual, h = norm(residual, routed + shared)     post-norm, residual, next pre-norm
 
 Every step is a call of the library on the caller's stream; the block owns the
-workspaces and the buffers between the steps.
+workspaces and the buffers between the steps.  The experts, and the shared expert
+where no request has an adapter, may be 4-bit weights (`quantized`).
 
 ``python -m aware_moe_expert_gb300.block`` runs a few steps of a small block on
-synthetic inputs and balances its experts.
+synthetic inputs and balances its experts; ``--quant e2m1`` or ``int4`` with 4-bit
+experts.
 """
 from __future__ import annotations
 
+import argparse
 import contextlib
 import ctypes
 from dataclasses import dataclass, replace
@@ -42,26 +45,48 @@ class BlockWeights:
     ffn_post_norm: torch.Tensor           # [H]: norm of the block's output
     next_pre_norm: torch.Tensor           # [H]: the next block's input norm
     router: torch.Tensor                  # [E_r, H]
-    w_gate_up: torch.Tensor               # [E_r, 2 I, H]
-    w_down: torch.Tensor                  # [E_r, H, I]
-    shared_gate_up: torch.Tensor          # [2 I_shared, H]
-    shared_down: torch.Tensor             # [H, I_shared]
+    w_gate_up: Optional[torch.Tensor]     # [E_r, 2 I, H]; None with `quant`
+    w_down: Optional[torch.Tensor]        # [E_r, H, I]; None with `quant`
+    shared_gate_up: Optional[torch.Tensor]   # [2 I_shared, H]; None where `quant` has it
+    shared_down: Optional[torch.Tensor]      # [H, I_shared]; None where `quant` has it
     select_bias: torch.Tensor             # fp32 [E_r], moved by balance()
+    quant: Optional[B.QuantWeights] = None   # packed experts, with or without the shared one
+
+
+def quantized(w: BlockWeights, code: str = "e2m1", group: int = 16,
+              shared: bool = False) -> BlockWeights:
+    """The block's experts (and its shared expert, which then takes no adapters) as 4-bit
+    weights, packed once; the bf16 ones are left out of the result.  Synchronises."""
+    status = torch.zeros(1, dtype=torch.int32, device=w.router.device)
+
+    def pack(t, count):
+        d = B.QuantDesc(count, t.numel() // (count * t.shape[-1]), t.shape[-1], code, group)
+        packed = torch.empty(B.moe_quant_size(d), dtype=torch.uint8, device=t.device)
+        B.check(B.moe_quant_quantize(d, t, packed, status), "moe_quant_quantize")
+        return packed
+
+    E = w.w_gate_up.shape[0]
+    q = B.QuantWeights(code, group, pack(w.w_gate_up, 2 * E), pack(w.w_down, E))
+    if shared:
+        q.shared_gate_up, q.shared_down = pack(w.shared_gate_up, 2), pack(w.shared_down, 1)
+        w = replace(w, shared_gate_up=None, shared_down=None)
+    B.check(B.moe_get_device_status(status), "quantized")
+    return replace(w, w_gate_up=None, w_down=None, quant=q)
 
 
 MAX_RANK = 128       # of a pool, the largest r_max
 
 
-def _workspace_bytes(layer: B.LayerDesc) -> int:
+def _workspace_bytes(layer: B.LayerDesc, size_of: str = "moe_workspace_size") -> int:
     """Bytes of workspace that do for a step of any number of tokens up to layer.T.
     A step of fewer tokens can need more than one of layer.T does: it takes other
     kernels and splits its reductions further."""
-    d, size = layer.c(), B.lib().moe_workspace_size
+    d, size = layer.c(), getattr(B.lib(), size_of)
     n = 0
     for d.T in range(layer.T + 1):
         n = max(n, size(ctypes.byref(d)))
     if n == 0:
-        raise B.MoeError(2, "moe_workspace_size")
+        raise B.MoeError(2, size_of)
     return n
 
 
@@ -97,20 +122,36 @@ class MoeBlock:
                  adapters: Optional[Adapters] = None, *, eps: float = 1e-6,
                  residual_scale: float = 1.0, branch_scale: float = 1.0, device="cuda"):
         """layer.T is the largest number of tokens of a step; layer.I_shared is
-        taken from the weights (the shared expert runs here, with adapters)."""
+        taken from the weights (the shared expert runs here, with adapters), unless
+        these have a packed shared expert, of layer.I_shared."""
         self.device = torch.device(device)
         self.layer, self.weights = layer, weights
         # this block's bias in a copy: blocks may be built from one GroupRoute
         self.groups = replace(groups, select_bias=weights.select_bias)
         self.eps, self.residual_scale, self.branch_scale = eps, residual_scale, branch_scale
         T, H, k = layer.T, layer.H, layer.k_max
-        self.shared = weights.shared_down.shape[1]
+        q = weights.quant
+        self.shared_packed = q is not None and q.shared_gate_up is not None
+        self.shared = layer.I_shared if self.shared_packed else weights.shared_down.shape[1]
         E, I = layer.E_r, layer.I_sub  # noqa: E741
-        for name, shape in dict(attn_post_norm=(H,), pre_norm=(H,), ffn_post_norm=(H,),
-                                next_pre_norm=(H,), router=(E, H), w_gate_up=(E, 2 * I, H),
-                                w_down=(E, H, I), shared_gate_up=(2 * self.shared, H),
-                                shared_down=(H, self.shared)).items():
+        shapes = dict(attn_post_norm=(H,), pre_norm=(H,), ffn_post_norm=(H,), next_pre_norm=(H,),
+                      router=(E, H))
+        packed = {}
+        if q is None:
+            shapes.update(w_gate_up=(E, 2 * I, H), w_down=(E, H, I))
+        else:
+            packed.update(gate_up=(2 * E, I, H), down=(E, H, I))
+        if self.shared_packed:
+            packed.update(shared_gate_up=(2, self.shared, H), shared_down=(1, H, self.shared))
+        else:
+            shapes.update(shared_gate_up=(2 * self.shared, H), shared_down=(H, self.shared))
+        for name, shape in shapes.items():
             _want(name, getattr(weights, name), shape, BF16, self.device)
+        for name, shape in packed.items():
+            n = B.moe_quant_size(B.QuantDesc(*shape, q.code, q.group))
+            if n == 0:
+                raise B.MoeError(2, "moe_quant_size")
+            _want("quant." + name, getattr(q, name), (n,), (torch.uint8,), self.device)
         self.adapters = adapters
         new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=self.device)  # noqa: E731
         i32 = torch.int32
@@ -122,7 +163,9 @@ class MoeBlock:
         self.sorted_token, self.inv_row = new(T * k, dtype=i32), new(T * k, dtype=i32)
         self.y_perm = new(T * k, H)
         self.status = torch.zeros(1, dtype=i32, device=self.device)
-        self.workspace = new(_workspace_bytes(layer), dtype=torch.uint8)
+        size = _workspace_bytes(layer) if q is None else _workspace_bytes(
+            layer, "moe_quant_workspace_size")
+        self.workspace = new(size, dtype=torch.uint8)
         # for a pool of any rank: self.adapters may be replaced between steps
         n = min(B.moe_lora_workspace_size(replace(self._lora(T, first), r_max=MAX_RANK))
                 for first in (True, False))
@@ -136,6 +179,8 @@ class MoeBlock:
 
     @adapters.setter
     def adapters(self, a: Optional[Adapters]):
+        if a is not None and self.shared_packed:
+            raise ValueError("adapters: the shared expert is packed, and takes none")
         if a is not None:
             H, n = self.layer.H, a.ranks.shape[0]
             r, r2 = a.gate_up_a.shape[1], a.down_a.shape[1]
@@ -188,14 +233,25 @@ class MoeBlock:
         d.T = T
         h = self.h[:T]
         self._norm(residual, attn, w.attn_post_norm, w.pre_norm, residual, h)
+        if self.shared_packed:           # routing, experts, shared expert and their sum
+            y = self.y[:T]
+            B.check(B.moe_layer_forward_quant(d, self.groups, w.quant, h, w.router, k_per_token,
+                                              self.load, y, st, ws), "moe_layer_forward_quant")
+            out = torch.empty_like(y)
+            self._norm(residual, y, w.ffn_post_norm, w.next_pre_norm, residual, out)
+            return out
         idx, tw, k_used = self.topk_idx[:T], self.topk_w[:T], self.k_used[:T]
         B.check(B.moe_route_groups(d, self.groups, h, w.router, None, k_per_token,
                                    self.logits[:T], idx, tw, k_used, self.load, st, ws),
                 "moe_route_groups")
         B.check(B.moe_permute(d, idx, k_used, self.counts, self.offsets, self.sorted_token,
                               self.inv_row, st, ws), "moe_permute")
-        B.check(B.moe_grouped_ffn(d, h, self.sorted_token, self.offsets, w.w_gate_up, w.w_down,
-                                  self.y_perm, st, ws), "moe_grouped_ffn")
+        if w.quant is None:
+            B.check(B.moe_grouped_ffn(d, h, self.sorted_token, self.offsets, w.w_gate_up, w.w_down,
+                                      self.y_perm, st, ws), "moe_grouped_ffn")
+        else:
+            B.check(B.moe_grouped_ffn_quant(d, w.quant, h, self.sorted_token, self.offsets,
+                                            self.y_perm, st, ws), "moe_grouped_ffn_quant")
         act, y_shared = self.act[:T], self.y_shared[:T]
         pool = lambda x, y: (x, y, a.ranks, a.scales, adapter_idx)  # noqa: E731
         none = (None,) * 5
@@ -224,8 +280,10 @@ class MoeBlock:
 
 
 def synthetic(T=64, H=256, experts=32, I=128, shared=256, n_adapters=6, rank=16, seed=0,  # noqa: E741
-              device="cuda"):
-    """A small block with random weights: (block, residual, attn, k, adapter_idx)."""
+              device="cuda", quant=None, group=16, shared_quant=False):
+    """A small block with random weights, in 4 bits with `quant` ("e2m1" or "int4"; the
+    shared expert, too, and no adapters, with shared_quant): (block, residual, attn, k,
+    adapter_idx)."""
     g = torch.Generator(device=device).manual_seed(seed)
     bf = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=device) * std).bfloat16()  # noqa: E731
     norm = lambda: (1 + 0.1 * torch.randn(H, generator=g, device=device)).bfloat16()  # noqa: E731
@@ -242,6 +300,10 @@ def synthetic(T=64, H=256, experts=32, I=128, shared=256, n_adapters=6, rank=16,
                     0.5 + torch.rand(n_adapters, generator=g, device=device))
     layer = B.LayerDesc(T=T, H=H, n_experts=experts, n_sub=1, I_sub=I, k_max=6, score="sigmoid",
                         renorm=True, route_scale=2.5)
+    if quant is not None:
+        w = quantized(w, quant, group, shared_quant)
+    if shared_quant:
+        layer, pool = replace(layer, I_shared=shared), None
     block = MoeBlock(layer, B.GroupRoute(n_groups=8, groups_kept=4, group_best=2), w, pool,
                      device=device)
     k = torch.randint(3, 7, (T,), generator=g, device=device, dtype=torch.int32)
@@ -250,7 +312,9 @@ def synthetic(T=64, H=256, experts=32, I=128, shared=256, n_adapters=6, rank=16,
 
 
 def main():
-    block, residual, attn, k, adapter = synthetic(T=512)
+    a = argparse.ArgumentParser(description="a few steps of a small block on synthetic inputs")
+    a.add_argument("--quant", choices=("e2m1", "int4"), help="experts of 4-bit weights")
+    block, residual, attn, k, adapter = synthetic(T=512, quant=a.parse_args().quant)
     for step in range(200):
         h = block.forward(residual.clone(), attn, k, adapter)
         load = block.load.float()
