@@ -83,6 +83,7 @@ def _layer(d=None, w=None, groups=None, x=FAKE, router=FAKE, k=FAKE, load=None, 
 @pytest.mark.parametrize("kw,code", [
     (dict(d=_desc(H=100)), SHAPE), (dict(d=_desc(T=-1)), INVALID), (dict(d=_desc(k_max=33)), SHAPE),
     (dict(d=_desc(I_shared=-64)), INVALID), (dict(d=_desc(I_shared=100)), SHAPE),
+    (dict(d=_desc(I_sub=(1 << 20) + 64)), SHAPE),
     (dict(d=_desc(I_shared=64)), INVALID),               # no packed shared expert
     (dict(d=_desc(I_shared=64), w=_weights(shared_gate_up=FAKE)), INVALID),
     (dict(w=_weights(gate_up=None)), INVALID), (dict(w=_weights(down=FAKE + 8)), INVALID),
