@@ -881,15 +881,22 @@ cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
                                        encode_tmap(&tm64, a.x, 2, a.x_rows, a.K, a.ldx, 64, 64);
     if (!ok) return cudaErrorInvalidValue;
   }
-  // chunks of tokens there can be: every group may end inside one
-  const bool wide = a.out_rows > 64ll * a.n_groups;
-  const int nt = wide ? 128 : 64;
-  const long long chunks = a.offsets == nullptr ? (a.dense_rows + nt - 1) / nt
-                                                : a.out_rows / nt + std::min(a.out_rows, static_cast<long long>(a.n_groups));
-  const long long items = chunks * p.blocks;
+  // chunks of nt tokens that there can be, as every group may end inside one
+  auto items_of = [&](int nt) {
+    const long long chunks = a.offsets == nullptr ? (a.dense_rows + nt - 1) / nt
+                                                  : a.out_rows / nt + std::min(a.out_rows, static_cast<long long>(a.n_groups));
+    return chunks * p.blocks;
+  };
+  // Chunks of 128 tokens where the groups' mean passes 64, as a weight is expanded for a
+  // chunk (8192 tokens of 128 experts 602 us, 783 in chunks of 64), but not where chunks of
+  // 64 are at most an item an SM: there an item's length counts (512 tokens of K 7168,
+  // N 4096 36 us, in chunks of 128 44; 333 tokens of 12 experts 13, 17).
+  const bool wide = a.out_rows > 64ll * a.n_groups && items_of(64) > a.sm_count;
+  const long long items = items_of(wide ? 128 : 64);
   if (a.token == nullptr && a.offsets == nullptr && !wide) {
-    // as wide as clusters fit at once (152 SMs hold 15 of eight: 64 tokens of K 7168,
-    // N 4096 in 16 clusters of eight 25 us, of four 17)
+    // A cluster's CTAs split K where whole items leave SMs idle, as wide as clusters fit at
+    // once (64, 128 and 256 tokens of K 7168, N 4096 15, 16 and 25 us, an item a CTA 42; 152
+    // SMs hold 15 clusters of eight: 64 tokens in 16 of eight 25 us, of four 17).
     int splits = 1;
     while (splits < 8 && items <= clusters_at_once(2 * splits) && p.kb >= 2 * splits) splits *= 2;
     if (splits > 1) {
