@@ -14,18 +14,21 @@
 //
 // Eight codes of a word are four pairs (k, k + 1), one in each half word, that
 // become bf16 pairs by a shift, a mask and one packed bf16 operation:
-//   integer codes  nibble i of the low half is input 2i, of the high half 2i + 1;
-//                  0x4300 | q is 128 + q, and fma(128 + q, s, -136 s) = s (q - 8)
+//   integer codes  nibble i of the low half is input 2i, of the high half 2i + 1.  The
+//                  low eight bits of a bf16, a subnormal or just above, count 2^-133
+//                  each, so pair 0 masked is q * 2^-133 and pair 1 in its place
+//                  q * 2^-129 without a shift (pairs 2 and 3 take one together);
+//                  fma(q * 2^-133, s * 2^117, -8 s * 2^-16) = (q - 8) s * 2^-16
 //   e2m1           sign, exponent and mantissa stand so that pair i, moved to the
 //                  bits 15 and 8-6 of a half word by one shift (i 0, 1) or two, reads
 //                  as code * 2^-126 (a subnormal for 0.5); times s * 2^117 that is
 //                  code * s * 2^-9
-// Both are exact: s has four significant bits, a code at most three, 136 s eight.
-// The factor 2^9 joins the matrix's own in the epilogue.
+// Both are exact: s has four significant bits, a code at most three, 8 s four.
+// The factor 2^16 or 2^9 joins the matrix's own in the epilogue.
 //
 // Scales are e4m3 without its sign, stored with a fifth exponent bit so that
 // subnormals are like the others: s = 2^E (1 + m / 8) is the byte (E + 16) << 3 | m,
-// and (byte << 4) + a constant is s (or s * 2^117) in bf16.  A scale of zero is
+// and (byte << 4) + a constant is s * 2^117 in bf16.  A scale of zero is
 // stored as any, with zero codes.
 #pragma once
 
@@ -63,8 +66,8 @@ __host__ __device__ constexpr uint32_t quant_word(int r, int c, int w) {
 }
 
 // ---------------------------------------------------------------- values
-constexpr uint32_t kScaleBase = 0x37803780u;     // exponent field of 2^-16: s
-constexpr uint32_t kScaleBase117 = 0x72007200u;  // of 2^101: s * 2^117
+constexpr uint32_t kScaleBase117 = 0x72007200u;  // exponent field of 2^101: s * 2^117
+constexpr uint32_t kScaleBase113 = 0x70007000u;
 
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -85,15 +88,16 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// What a word's expansion needs of its group's scale: a byte of `bytes` as a pair of
-// equal bf16, and -136 times it.
+// What a word's expansion needs of its group's scale, a byte of `bytes`, as pairs of
+// equal bf16: s * 2^117, and for integer codes s * 2^113 and -8 s * 2^-16.
 template <int CODE>
 struct QuantScale {
-  uint32_t s, c;
+  uint32_t s, t, c;
   __device__ __forceinline__ static QuantScale of(uint32_t twice) {   // the byte in both halves
     QuantScale q;
-    q.s = twice * 16u + (CODE == MOE_QUANT_E2M1 ? kScaleBase117 : kScaleBase);
-    q.c = CODE == MOE_QUANT_INT ? hmul2_bf16(q.s, 0xC308C308u) : 0u;
+    q.s = twice * 16u + kScaleBase117;
+    q.t = twice * 16u + kScaleBase113;
+    q.c = CODE == MOE_QUANT_INT ? hmul2_bf16(q.s, 0x80088008u) : 0u;  // -2^-130
     return q;
   }
   template <int I>
@@ -107,9 +111,11 @@ template <int CODE>
 __device__ __forceinline__ void quant_expand(uint32_t w, const QuantScale<CODE>& q,
                                              uint32_t (&v)[4]) {
   if (CODE == MOE_QUANT_INT) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = hfma2_bf16(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), q.s, q.c);
+    const uint32_t h = w >> 8;
+    v[0] = hfma2_bf16(w & 0x000F000Fu, q.s, q.c);
+    v[1] = hfma2_bf16(w & 0x00F000F0u, q.t, q.c);
+    v[2] = hfma2_bf16(h & 0x000F000Fu, q.s, q.c);
+    v[3] = hfma2_bf16(h & 0x00F000F0u, q.t, q.c);
   } else {
     v[0] = hmul2_bf16(w & 0x81C081C0u, q.s);
     v[1] = hmul2_bf16((w << 3) & 0x81C081C0u, q.s);
@@ -121,7 +127,7 @@ __device__ __forceinline__ void quant_expand(uint32_t w, const QuantScale<CODE>&
 // What the sums of expanded weights are multiplied by, beside the matrix's factor.
 template <int CODE>
 __device__ __forceinline__ constexpr float quant_unit() {
-  return CODE == MOE_QUANT_E2M1 ? 512.f : 1.f;
+  return CODE == MOE_QUANT_E2M1 ? 512.f : 65536.f;
 }
 
 // Where code q of the input pair's half h (0: even input) goes in its word.

@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
         if (PAIR) lift += from[(16 + f % 16) * kTokens + t];
       }
       if (t >= p.T || feature >= (shared ? p.n_shared : p.n)) continue;
-      constexpr float u = CODE == MOE_QUANT_E2M1 ? 512.f : 1.f;
+      constexpr float u = quant_unit<CODE>();
       if (MODE == DOWN) {      // the factors came with the activations
         p.out[t * p.ldo + feature] = __float2bfloat16_rn(v);
         continue;

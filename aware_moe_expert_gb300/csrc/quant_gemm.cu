@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     for (int w = first; w < total; w += step) {
       const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
       const int nt = tiles_of(t.nt);
-      const float u = p.code == MOE_QUANT_E2M1 ? quant_unit<MOE_QUANT_E2M1>() : 1.f;
+      const float u = p.code == MOE_QUANT_E2M1 ? quant_unit<MOE_QUANT_E2M1>() : quant_unit<MOE_QUANT_INT>();
       const float f0 = __ldg(p.factor + (p.swiglu ? 2 * t.g : t.g)) * u;
       const float f1 = p.swiglu ? __ldg(p.factor + 2 * t.g + 1) * u : f0;
       ok = warp_wait(b_dfull + 8 * db, dphase, s_abort);
