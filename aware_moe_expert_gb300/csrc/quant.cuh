@@ -20,7 +20,7 @@
 //                  q * 2^-129 without a shift (pairs 2 and 3 take one together);
 //                  fma(q * 2^-133, s * 2^117, -8 s * 2^-16) = (q - 8) s * 2^-16
 //   e2m1           sign, exponent and mantissa stand so that pair i, moved to the
-//                  bits 15 and 8-6 of a half word by one shift (i 0, 1) or two, reads
+//                  bits 15 and 8-6 of a half word by one shift (i 0, 1) or a product, reads
 //                  as code * 2^-126 (a subnormal for 0.5); times s * 2^117 that is
 //                  code * s * 2^-9
 // Both are exact: s has four significant bits, a code at most three, 8 s four.
@@ -119,8 +119,8 @@ __device__ __forceinline__ void quant_expand(uint32_t w, const QuantScale<CODE>&
   } else {
     v[0] = hmul2_bf16(w & 0x81C081C0u, q.s);
     v[1] = hmul2_bf16((w << 3) & 0x81C081C0u, q.s);
-    v[2] = hmul2_bf16(and_or(w << 6, 0x01C001C0u, (w << 1) & 0x80008000u), q.s);
-    v[3] = hmul2_bf16(and_or(w >> 3, 0x01C001C0u, (w << 2) & 0x80008000u), q.s);
+    v[2] = hmul2_bf16((w & 0x40074007u) * (64u + 2u) & 0x81C081C0u, q.s);
+    v[3] = hmul2_bf16((w >> 3 & 0x05C005C0u) * (32u + 1u) & 0x81C081C0u, q.s);
   }
 }
 

@@ -379,10 +379,13 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
       const uint32_t d = kTmemD + static_cast<uint32_t>(db * 2 + tile) * NT;
       ok = warp_wait(b_dempty + 8 * db, dphase ^ 1u, s_abort);
       for (int kb = kb0; kb < kb1 && ok; ++kb) {
-        ok = warp_wait(b_bfull + 8 * bs, bphase, s_abort);
+        // both in one vote, as a wait on a barrier that is ready costs 100 clocks and more
+        const bool both = __all_sync(0xffffffffu, try_wait_at(b_bfull + 8 * bs, bphase) &
+                                                      try_wait_at(b_afull + 8 * ab, aphase));
+        ok = both || warp_wait(b_bfull + 8 * bs, bphase, s_abort);
         const uint64_t b = sdesc_sw128(sbase + static_cast<uint32_t>(bs) * Cfg::kTok);
         for (int i = 0; i < kParts && ok; ++i) {
-          ok = warp_wait(b_afull + 8 * ab, aphase, s_abort);
+          ok = (both && i == 0) || warp_wait(b_afull + 8 * ab, aphase, s_abort);
           if (!ok) break;
           if (mine) {
             tc_fence_after();
