@@ -41,9 +41,21 @@ constexpr int kGatherThreads = 128;
 constexpr int kThreads = (kTokenWarp + 1) * 32;
 constexpr int kThreadsGather = kTokenWarp * 32 + kGatherThreads;
 constexpr int kHalf = 64;                         // inputs of a block of a token stage
+constexpr int kMaxSplits = 8;                     // CTAs of a cluster
 constexpr uint32_t kMaxRecord = quant_record(16);
 constexpr uint32_t kWStage = 2 * kMaxRecord;      // both tiles' records of 128 inputs
 constexpr uint32_t kTmemD = 256;                  // the accumulators' first column, behind A
+
+// Columns of a chunk that each of `splits` CTAs sums: even, and splits times it covers
+// the 16s that the rows fill.
+__host__ __device__ constexpr int columns_of(int rows, int splits) {
+  return ((rows + 15) / 16 * 16 + 2 * splits - 1) / (2 * splits) * 2;
+}
+constexpr int most_columns(int nt) {       // all CTAs' together
+  int m = 0;
+  for (int s = 2; s <= kMaxSplits; ++s) m = std::max(m, s * columns_of(nt, s));
+  return m;
+}
 
 template <int NT, bool SPLIT>
 struct TileCfg {
@@ -52,7 +64,7 @@ struct TileCfg {
   static constexpr uint32_t kTok = NT * kQK * 2;
   static constexpr uint32_t kOffW = kB * kTok;
   static constexpr uint32_t kOffPart = kOffW + kW * kWStage;
-  static constexpr uint32_t kPart = SPLIT ? NT * 256 * 4 : 0;
+  static constexpr uint32_t kPart = SPLIT ? most_columns(NT) * 256 * 4 : 0;
   static constexpr uint32_t kOffBar = kOffPart + kPart;
   // TMEM buffers of expanded weights (a tile's columns, then the other's), kParts a
   // record.  One of 128 inputs takes fewer barriers, which count where the expansion
@@ -604,7 +616,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
         // A CTA sums `per` of the chunk's columns: its slot [rank][per / 2][256 rows] of
         // pairs
         const uint32_t part = sbase + Cfg::kOffPart;
-        const int per = (t.rows + 15) / 16 * 16 / p.splits;
+        const int per = columns_of(t.rows, p.splits);
         for (int i = 0; i < nt; ++i)
           for (int c0 = 0; c0 < t.rows; c0 += 16) {
             uint32_t v[16];
@@ -704,7 +716,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     if (first < total && *s_abort == 0) {
       const Tile t = decode_tile<NT>(first, p.blocks, p.n_groups, s_prefix, s_offs);
       const float2* part = reinterpret_cast<const float2*>(smem + Cfg::kOffPart);
-      const int per = (t.rows + 15) / 16 * 16 / p.splits;
+      const int per = columns_of(t.rows, p.splits);
       const int rows = p.swiglu ? 128 : 256;
       // neighbouring threads: neighbouring features
       for (int i = threadIdx.x; i < per / 2 * rows; i += blockDim.x) {
@@ -818,10 +830,10 @@ cudaError_t launch_tile(const CUtensorMap& tm16, const CUtensorMap& tm64, const 
 
 // Clusters of `size` CTAs of the splitting kernel that the device holds at once.
 int clusters_at_once(int size) {
-  static int cache[64][4] = {};
+  static int cache[64][kMaxSplits + 1] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int& n = cache[dev][size == 2 ? 1 : size == 4 ? 2 : 3];
+  int& n = cache[dev][size];
   if (n == 0) {
     using Cfg = TileCfg<64, true>;
     auto kern = quant_tile_kernel<64, false, true>;
@@ -898,10 +910,11 @@ cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
   const long long items = items_of(wide ? 128 : 64);
   if (a.token == nullptr && a.offsets == nullptr && !wide) {
     // A cluster's CTAs split K where whole items leave SMs idle, as wide as clusters fit at
-    // once (64, 128 and 256 tokens of K 7168, N 4096 15, 16 and 25 us, an item a CTA 42; 152
-    // SMs hold 15 clusters of eight: 64 tokens in 16 of eight 25 us, of four 17).
-    int splits = 1;
-    while (splits < 8 && items <= clusters_at_once(2 * splits) && p.kb >= 2 * splits) splits *= 2;
+    // once (64, 128 and 256 tokens of K 7168, N 4096 13, 16 and 25 us, an item a CTA 42; 152
+    // SMs hold 15 clusters of eight, so 64 tokens take 25 us in 16 of eight, 14.6 in
+    // clusters of four).
+    int splits = kMaxSplits;
+    while (splits > 1 && (items > clusters_at_once(splits) || p.kb < splits)) --splits;
     if (splits > 1) {
       p.splits = splits;
       return launch_tile<64, false, true>(tm16, tm64, p, static_cast<unsigned>(items * splits), s);

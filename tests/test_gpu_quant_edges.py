@@ -160,6 +160,24 @@ def test_outputs_at_any_two_byte_address(T, N, swiglu):
             assert (gaps == 7.0).all()
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("T,K,N", [(64, 1024, 4096), (65, 520, 700), (100, 640, 2048), (128, 264, 256), (129, 1160, 3584),
+                                   (190, 1032, 1300), (300, 904, 1280), (321, 2056, 514), (1000, 136, 2050)])
+def test_sums_split_over_clusters_of_every_width(T, K, N, swiglu):
+    """Chunks of 64 tokens x blocks of outputs: from one item to more than a device holds."""
+    rng = np.random.default_rng(T + N)
+    halves = 2 if swiglu else 1
+    kind, group = ("int4", 32) if T % 2 else ("e2m1", 16)
+    w, x = random_weights(rng, halves, N // halves, K, kind, group), _bf(rng, T, K)
+    d = B.QuantProject(T, K, N, kind, group, swiglu)
+    st, ws = status(), torch.empty(256, dtype=torch.uint8, device=DEV)
+    y = torch.full((T + 1, N // halves), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.check(B.moe_quant_project(d, x, pack(w, kind, group), y, st, ws))
+    assert B.moe_get_device_status(st) == 0 and (y[T:] == 7.0).all()
+    w64, x64 = Q.weights(*w, kind, group), to64(x)
+    within(y[:T], *(Q.swiglu(*Q.product(x64, w64[0]), *Q.product(x64, w64[1])) if swiglu else Q.product(x64, w64[0])))
+
+
 def _grouped(layer, T, k, token, offsets, rows=None):
     x = _bf(np.random.default_rng(5), T, layer.H)
     d = B.LayerDesc(T=T, H=layer.H, n_experts=layer.E, n_sub=1, I_sub=layer.I, k_max=k)
