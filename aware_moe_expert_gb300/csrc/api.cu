@@ -942,9 +942,10 @@ moe_status validate_quant_weights(const moe_layer_desc* d, const moe_quant_weigh
   return MOE_OK;
 }
 
-// Behind the layer's own workspace: fp32 outputs of the experts and the shared expert.
+// Behind the layer's own workspace: fp32 outputs of the experts and the shared expert, or a
+// few tokens' second parts of the activations.
 struct QuantLayout {
-  size_t y, ysh, total;
+  size_t y, ysh, low, low_sh, total;
 };
 QuantLayout quant_layout_of(const moe_layer_desc& d) {
   QuantLayout q;
@@ -953,6 +954,11 @@ QuantLayout quant_layout_of(const moe_layer_desc& d) {
   o = align_up(o + static_cast<size_t>(d.T) * d.k_max * d.H * 4);
   q.ysh = o;
   o = align_up(o + (d.I_shared > 0 ? static_cast<size_t>(d.T) * d.H * 4 : 0));
+  const size_t pairs = d.T <= moe::kQuantPairTokens ? static_cast<size_t>(d.T) : 0;
+  q.low = o;
+  o = align_up(o + pairs * d.k_max * d.I_sub * 2);
+  q.low_sh = o;
+  o = align_up(o + pairs * std::max(d.I_shared, 0) * 2);
   q.total = o;
   return q;
 }
@@ -983,7 +989,9 @@ moe_status do_quant_ffn(const moe_layer_desc* d, const moe_quant_weights* w, boo
   a.early = shared;
   a.status = status;
   a.sm_count = sm_count();
-  MOE_TRY(cuda_status(moe::launch_quant_gemm(a, s)));
+  const auto launch =
+      shared && d->T <= moe::kQuantFewTokens ? moe::launch_quant_project_few : moe::launch_quant_gemm;
+  MOE_TRY(cuda_status(launch(a, s)));
   moe::QuantGemmArgs b = a;
   b.early = 1;
   b.x = a.out;
@@ -996,8 +1004,8 @@ moe_status do_quant_ffn(const moe_layer_desc* d, const moe_quant_weights* w, boo
   b.swiglu = 0;
   b.out = y;
   b.ldo = d->H;
-  b.out_f32 = f32;
-  return cuda_status(moe::launch_quant_gemm(b, s));
+  b.out_f32 = f32;             // never set up to kQuantFewTokens
+  return cuda_status(launch(b, s));
 }
 
 }  // namespace
@@ -1688,6 +1696,8 @@ moe_status moe_layer_forward_quant(const moe_layer_desc* desc, const moe_group_r
     a.shared_down = weights->shared_down;
     a.act = at<void>(workspace, l.act);
     a.act_shared = at<void>(workspace, l.act_sh);
+    a.act_low = at<void>(workspace, q.low);
+    a.act_shared_low = at<void>(workspace, q.low_sh);
     a.out = out;
     a.T = d.T;
     a.H = d.H;

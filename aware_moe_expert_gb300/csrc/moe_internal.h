@@ -348,8 +348,11 @@ struct QuantGemmArgs {
 };
 cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s);
 
-// ---- quant_few.cu: the same for up to kQuantFewTokens tokens
+// ---- quant_few.cu: the same for up to kQuantFewTokens tokens, the columns of its MMAs
+// (K 7168, N 4096: 8 tokens 7.4 us there, 10.5 in quant_gemm.cu, which runs from 9 on; layer of 8
+// tokens, 256 units of 384: 41 us, 57).
 constexpr int kQuantFewTokens = 8;
+constexpr int kQuantPairTokens = 4;      // whose activations have two columns each
 // Dense, bf16 out.
 cudaError_t launch_quant_project_few(const QuantGemmArgs& a, cudaStream_t s);
 struct QuantFewArgs {
@@ -362,6 +365,8 @@ struct QuantFewArgs {
   const void* shared_down;
   void* act;                   // bf16 [T * k_max, I]
   void* act_shared;            // bf16 [T, I_shared]
+  void* act_low;               // like act and act_shared, for T <= kQuantPairTokens
+  void* act_shared_low;
   void* out;                   // bf16 [T, H]
   int T, H, E, I, I_shared, k_max, code, group;
   int32_t* status;

@@ -13,10 +13,19 @@
 //
 // Experts: every CTA lists the distinct units of the batch itself, from the router's
 // selection.  The first launch computes act[t, j] = w_tj f_u silu(g) u of token t's
-// j-th unit (its gate and its down matrix's factor with it, one rounding); the second
-// one, whose weights stream while the first ends, multiplies 16 rows of W_down of ALL
+// j-th unit (its gate and its down matrix's factor with it, one rounding; up to four tokens
+// what it leaves is another bf16, in the columns that they leave free: the error of one token's
+// outputs is then their own rounding's, 0.0016, 0.0025 without); the second
+// one, whose weights stream while the first ends, multiplies 32 rows of W_down of ALL
 // units and the shared expert with them, one long sum: the weighted sum over a token's
 // units is part of it.
+//
+// Measured on a GB300: one token of K 7168, N 4096 5.7 us (2.9 TB/s); layers of 1, 8 and 3
+// tokens (256 units of 384, k 16; the same; 256 of 2048 and a shared expert, k 8) 17.9, 40.8
+// and 134 us.  Loads of the codes alone, without products and tokens, take 3.8 us there, and
+// 28 and 86 of the layers' 40.8 and 134: what is left is the expansion (issue slots 50-60%
+// busy, ALU 40-54%), the tokens' loads, and for one token three launches' latencies.
+#include <cfloat>
 #include <type_traits>
 
 #include "gemm_common.cuh"
@@ -28,6 +37,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTokens = kQuantFewTokens;
+constexpr int kPairTokens = kQuantPairTokens;
+static_assert(2 * kPairTokens == kTokens, "a second column for each");
 constexpr int kMaxCluster = 8;
 
 enum Mode { PROJECT, GATE_UP, DOWN };
@@ -50,9 +61,13 @@ struct FewParams {
   const __nv_bfloat16* x;      // PROJECT, GATE_UP
   const __nv_bfloat16* act;    // DOWN: [T * k_max, I], act_shared [T, I_shared]
   const __nv_bfloat16* act_shared;
+  const __nv_bfloat16* act_low;        // up to kPairTokens: what the roundings left
+  const __nv_bfloat16* act_shared_low;
   __nv_bfloat16* out;          // PROJECT, DOWN
   __nv_bfloat16* out_act;      // GATE_UP
   __nv_bfloat16* out_act_shared;
+  __nv_bfloat16* out_act_low;
+  __nv_bfloat16* out_act_shared_low;
   const int32_t* topk_idx;     // [T, k_max]
   const float* topk_w;
   long long ldx, ldo;
@@ -197,6 +212,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
   __shared__ float parts[CLUSTER ? kMaxCluster : 1][kTiles * 16 * kTokens];   // of the cluster's CTAs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tig = lane & 3;
+  // DOWN: token and part of the activations in this lane's column
+  const bool pairs = p.T <= kPairTokens, low = pairs && g >= kPairTokens;
+  const int token = pairs ? g & (kPairTokens - 1) : g;
   bool waited = false;
   // The selection was written before the launch that a DOWN launch follows, so it may
   // list the units and fetch weights at once.
@@ -277,11 +295,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
         if (g < p.T) src = p.x + g * p.ldx;
       } else if (xd < D) {
         const int e = units.list[xd];
-        const int j = units.slot[e][g];
-        if (j != 255) src = p.act + (static_cast<size_t>(g) * p.k_max + j) * p.K;
+        const int j = units.slot[e][token];
+        if (j != 255) src = (low ? p.act_low : p.act) + (static_cast<size_t>(token) * p.k_max + j) * p.K;
       } else {
         K = p.K_shared;
-        if (g < p.T) src = p.act_shared + static_cast<size_t>(g) * K;
+        if (token < p.T) src = (low ? p.act_shared_low : p.act_shared) + static_cast<size_t>(token) * K;
       }
       const int k = xk * kQK + 32 * tig;
       const int left = src != nullptr ? K - k : 0;
@@ -335,6 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
       for (int w = 0; w < (CLUSTER ? p.cluster : ways); ++w) {
         const float* from = CLUSTER ? parts[w] : sums[group * ways + w];
         v += from[f * kTokens + t];
+        if (MODE == DOWN && pairs && t < kPairTokens) v += from[f * kTokens + t + kPairTokens];
         if (PAIR) lift += from[(16 + f % 16) * kTokens + t];
       }
       if (t >= p.T || feature >= (shared ? p.n_shared : p.n)) continue;
@@ -348,14 +367,19 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const Few
       if (PAIR) v = v / (1.f + expf(-v)) * (lift * (factor[1] * u));
       if (MODE == PROJECT) {
         p.out[t * p.ldo + feature] = __float2bfloat16_rn(v);
-      } else if (shared) {
-        p.out_act_shared[static_cast<size_t>(t) * p.n_shared + feature] =
-            __float2bfloat16_rn(v * (p.factor_down_shared[0] * u));
       } else {
-        const int j = units.slot[unit][t];
+        const int j = shared ? 0 : units.slot[unit][t];
         if (j == 255) continue;
-        const size_t row = static_cast<size_t>(t) * p.k_max + j;
-        p.out_act[row * p.n + feature] = __float2bfloat16_rn(v * (p.factor_down[unit] * u) * p.topk_w[row]);
+        const size_t row = shared ? t : static_cast<size_t>(t) * p.k_max + j;
+        const size_t at = row * (shared ? p.n_shared : p.n) + feature;
+        v *= shared ? p.factor_down_shared[0] * u : p.factor_down[unit] * u * p.topk_w[row];
+        const __nv_bfloat16 high = __float2bfloat16_rn(v);
+        (shared ? p.out_act_shared : p.out_act)[at] = high;
+        if (pairs) {           // 0, not NaN, where the rounding left infinity
+          const float left = v - __bfloat162float(high);
+          (shared ? p.out_act_shared_low : p.out_act_low)[at] =
+              __float2bfloat16_rn(fabsf(left) <= FLT_MAX ? left : 0.f);
+        }
       }
     }
     // the next task's sums overwrite these
@@ -454,6 +478,8 @@ cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
   p.x = static_cast<const __nv_bfloat16*>(a.x);
   p.out_act = static_cast<__nv_bfloat16*>(a.act);
   p.out_act_shared = static_cast<__nv_bfloat16*>(a.act_shared);
+  p.out_act_low = static_cast<__nv_bfloat16*>(a.act_low);
+  p.out_act_shared_low = static_cast<__nv_bfloat16*>(a.act_shared_low);
   p.topk_idx = a.topk_idx;
   p.topk_w = a.topk_w;
   p.ldx = a.H;
@@ -474,6 +500,8 @@ cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
   d.w_shared = shared_down;
   d.act = p.out_act;
   d.act_shared = p.out_act_shared;
+  d.act_low = p.out_act_low;
+  d.act_shared_low = p.out_act_shared_low;
   d.out = static_cast<__nv_bfloat16*>(a.out);
   d.ldo = a.H;
   d.matrix = dn.bytes;
@@ -483,7 +511,7 @@ cudaError_t launch_quant_ffn_few(const QuantFewArgs& a, cudaStream_t s) {
   d.n_shared = 0;
   d.K_shared = a.I_shared;
   d.kb_shared = a.I_shared > 0 ? dns.kb : 0;
-    const int units = a.E < a.T * a.k_max ? a.E : a.T * a.k_max;       // at most
+  const int units = a.E < a.T * a.k_max ? a.E : a.T * a.k_max;       // at most
   return launch_few<DOWN, false>(d, a.code, a.group, (a.H + 31) / 32, units * dn.kb + d.kb_shared, a.sm_count, s);
 }
 

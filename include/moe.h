@@ -541,8 +541,12 @@ moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void
  * checkpoint with e8m0 scales has them as e4m3 and a factor where a matrix spans
  * up to 18 powers of two, one with groups of 64 or 128 by repeating scales.
  * Products take the codes times their scale (exact in bf16), sum in fp32 and
- * multiply the sums by the factor: no weight is rounded.
+ * multiply the sums by the factor: no weight is rounded.  (Inside a product weights
+ * are scaled by a power of two down to 2^-16, so sums below 2^-110 can lose bits.)
  * moe_quant_pack lays weights out once; only the packed form is used after.
+ * Pointers are 16-byte aligned, where no other alignment is given (status words, factors,
+ * indexes: 4 bytes).  A workspace is 256-byte aligned and holds nothing between calls;
+ * calls that may run at once, captured graphs among them, need one each.
  */
 typedef enum { MOE_QUANT_E2M1 = 0, MOE_QUANT_INT = 1 } moe_quant_code;
 
@@ -617,8 +621,12 @@ moe_status moe_shared_ffn_quant(const moe_layer_desc* desc, const moe_quant_weig
                                 void* workspace, void* stream);
 
 /* The whole layer on packed weights: moe_layer_forward's router (groups null) or
- * moe_layer_forward_groups' (load nullable; null without groups).  The experts'
- * outputs stay fp32 up to the weighted sum. */
+ * moe_layer_forward_groups' (load nullable; null without groups).  A token whose
+ * selection is empty gets the shared expert alone and reports MOE_ERR_K_RANGE.  Activations
+ * are rounded to bf16, from more than eight tokens as silu(gate) * up, with fp32
+ * outputs of the experts up to the weighted sum; up to eight tokens with the routing weight
+ * and the down factor in them (up to four as a sum of two bf16), and the weighted sum is one
+ * fp32 sum over all experts. */
 moe_status moe_layer_forward_quant(const moe_layer_desc* desc, const moe_group_route* groups,
                                    const moe_quant_weights* weights, const void* x,
                                    const void* router_w, const int32_t* k_per_token,
