@@ -349,8 +349,8 @@ struct QuantGemmArgs {
 cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s);
 
 // ---- quant_few.cu: the same for up to kQuantFewTokens tokens, the columns of its MMAs
-// (K 7168, N 4096: 8 tokens 7.4 us there, 10.5 in quant_gemm.cu, which runs from 9 on; layer of 8
-// tokens, 256 units of 384: 41 us, 57).
+// (K 7168, N 4096: 1 and 8 tokens 5.7 and 7.1 us there, 10.4 and 10.5 in quant_gemm.cu,
+// which runs from 9 on; layers of 1 and 8 tokens, 256 units of 384: 18 and 41 us, 34 and 56).
 constexpr int kQuantFewTokens = 8;
 constexpr int kQuantPairTokens = 4;      // whose activations have two columns each
 // Dense, bf16 out.

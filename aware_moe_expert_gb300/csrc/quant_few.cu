@@ -43,12 +43,12 @@ constexpr int kMaxCluster = 8;
 
 enum Mode { PROJECT, GATE_UP, DOWN };
 
-// Steps in flight.  With two tiles of rows a third one spills (layer of eight tokens
-// 42 us, 47).
-__host__ __device__ constexpr int ahead_of(int mode, bool pair) { return mode == PROJECT && !pair ? 3 : 2; }
+// Steps in flight.  Three spill beside two tiles of rows (layer of eight tokens 41 us, 50) and
+// gain nothing beside one (one token, K 7168, N 4096 5.7 us with both).
+constexpr int kAhead = 2;
 constexpr int kCtas = 2;
 // Tiles of 16 rows of a task.  Two share the tokens' loads; a projection has few tasks
-// and takes one (one token, K 7168, N 4096: 6.4 us, with two 7.6).
+// and takes one (one token, K 7168, N 4096: 5.7 us, with two 6.5; eight tokens 7.1, 7.0).
 __host__ __device__ constexpr int tiles_of(int mode, bool pair) { return mode == PROJECT && !pair ? 1 : 2; }
 
 struct FewParams {
@@ -204,7 +204,6 @@ __device__ __forceinline__ int task_warps(int tasks, int steps, int ctas) {
 template <int MODE, int CODE, int GROUP, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) quant_few_kernel(const FewParams p) {
   constexpr uint32_t kRec = quant_record(GROUP);
-  constexpr int kAhead = ahead_of(MODE, PAIR);
   constexpr int kTiles = tiles_of(MODE, PAIR);
   constexpr int kRows = PAIR ? 16 : 16 * kTiles;         // features of a task
   __shared__ Units units;

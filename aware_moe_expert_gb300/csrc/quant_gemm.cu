@@ -25,10 +25,10 @@
 // TMEM buffers let one be expanded while the last one multiplies.
 // Every wait is bounded.
 //
-// Measured on a GB300: 64 tokens of K 7168, N 4096 13.2 us, 16384 tokens 571 (1.68 PFLOP/s);
-// a layer of 64 tokens on 32 units of 3584 185 us (4.05 TB/s), experts of 1024 and 8192
-// tokens (128 of 768, k 8) 134 and 591.  Of 185, 134 and 591, without the MMAs 169, 116 and
-// 500 are left, without the expansion's arithmetic 159, 109 and 531, without either 147, 96
+// Measured on a GB300: 64 tokens of K 7168, N 4096 12.6 us, 16384 tokens 573 (1.68 PFLOP/s);
+// a layer of 64 tokens on 32 units of 3584 183 us (4.1 TB/s), experts of 1024 and 8192
+// tokens (128 of 768, k 8) 130 and 580.  Without the MMAs 169, 116 and 500 were left of 185,
+// 134 and 593, without the expansion's arithmetic 159, 109 and 531, without either 147, 96
 // and 438: issue slots (71% busy) and the wait for a record's stores, barriers and MMAs
 // bound the first two, the rows' way from L2 (about 10 TB/s) and the one set of
 // accumulators of a wide chunk the last.
@@ -52,7 +52,12 @@ constexpr int kHalf = 64;                         // inputs of a block of a toke
 constexpr int kMaxSplits = 8;                     // CTAs of a cluster
 constexpr uint32_t kMaxRecord = quant_record(16);
 constexpr uint32_t kWStage = 2 * kMaxRecord;      // both tiles' records of 128 inputs
-constexpr uint32_t kTmemD = 256;                  // the accumulators' first column, behind A
+// TMEM buffers of expanded weights, a record each (a tile's columns, then the other's).  Halves
+// of a record let its MMAs start earlier, but take twice the barriers (layer of 64 tokens 218
+// us, 183 so; 16384 tokens of K 7168, N 4096 575, 573).
+constexpr int kABufs = 2;
+constexpr uint32_t kACols = 128;
+constexpr uint32_t kTmemD = kABufs * kACols;      // the accumulators' first column
 
 // Columns of a chunk that each of `splits` CTAs sums: even, and splits times it covers
 // the 16s that the rows fill.
@@ -74,13 +79,6 @@ struct TileCfg {
   static constexpr uint32_t kOffPart = kOffW + kW * kWStage;
   static constexpr uint32_t kPart = SPLIT ? most_columns(NT) * 256 * 4 : 0;
   static constexpr uint32_t kOffBar = kOffPart + kPart;
-  // TMEM buffers of expanded weights (a tile's columns, then the other's), kParts a
-  // record.  One of 128 inputs takes fewer barriers, which count where the expansion
-  // bounds; of 64, the MMAs start earlier, which counts where they do (16384 tokens of K
-  // 7168 642 us, 685 with one part; layer of 64 tokens 255 us with two parts, 222 with one).
-  static constexpr int kParts = NT == 128 ? 2 : 1;
-  static constexpr int kABufs = 2 * kParts;
-  static constexpr uint32_t kACols = 128 / kParts;
   static constexpr int kDBufs = NT == 128 ? 1 : 2;
   static constexpr int kBars = 2 * kW + 2 * kB + 2 * kABufs + 2 * kDBufs + 1;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
@@ -89,7 +87,7 @@ struct TileCfg {
   static constexpr uint32_t kOffOffs = kOffPrefix + (kMaxGroups + 1) * 4;
   static constexpr uint32_t kSmem = kOffOffs + (kMaxGroups + 1) * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(kABufs * kACols <= kTmemD && kTmemD + kDBufs * 2 * NT <= 512, "TMEM columns");
+  static_assert(kTmemD + kDBufs * 2 * NT <= 512, "TMEM columns");
 };
 
 struct TileParams {
@@ -236,7 +234,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 
 // 64 expanded weights of a row (pieces c[0] and c[1]; s2: their scale bytes) to TMEM
 // columns d .. d + 31.
-template <int CODE, int GROUP>
+template <int CODE>
 __device__ __forceinline__ void expand_half(const uint4& c0, const uint4& c1, uint32_t bytes, uint32_t d) {
   uint32_t v[32];
 #pragma unroll
@@ -245,12 +243,8 @@ __device__ __forceinline__ void expand_half(const uint4& c0, const uint4& c1, ui
     const uint32_t word[4] = {c.x, c.y, c.z, c.w};
     using Scale = QuantScale<CODE>;
     Scale q[2];
-    if (GROUP == 16) {
-      q[0] = i == 0 ? Scale::template at<0>(bytes) : Scale::template at<2>(bytes);
-      q[1] = i == 0 ? Scale::template at<1>(bytes) : Scale::template at<3>(bytes);
-    } else {
-      q[0] = q[1] = i == 0 ? Scale::template at<0>(bytes) : Scale::template at<1>(bytes);
-    }
+    q[0] = i == 0 ? Scale::template at<0>(bytes) : Scale::template at<2>(bytes);
+    q[1] = i == 0 ? Scale::template at<1>(bytes) : Scale::template at<3>(bytes);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint32_t e[4];
@@ -275,8 +269,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     quant_tile_kernel(const __grid_constant__ CUtensorMap tm16,
                       const __grid_constant__ CUtensorMap tm64, const TileParams p) {
   using Cfg = TileCfg<NT, SPLIT>;
-  constexpr int kW = Cfg::kW, kB = Cfg::kB, kDBufs = Cfg::kDBufs, kABufs = Cfg::kABufs, kParts = Cfg::kParts;
-  constexpr uint32_t kACols = Cfg::kACols;
+  constexpr int kW = Cfg::kW, kB = Cfg::kB, kDBufs = Cfg::kDBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -402,21 +395,17 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
         // both in one vote, as a wait on a barrier that is ready costs 100 clocks and more
         const bool both = __all_sync(0xffffffffu, try_wait_at(b_bfull + 8 * bs, bphase) &
                                                       try_wait_at(b_afull + 8 * ab, aphase));
-        ok = both || warp_wait(b_bfull + 8 * bs, bphase, s_abort);
-        const uint64_t b = sdesc_sw128(sbase + static_cast<uint32_t>(bs) * Cfg::kTok);
-        for (int i = 0; i < kParts && ok; ++i) {
-          ok = (both && i == 0) || warp_wait(b_afull + 8 * ab, aphase, s_abort);
-          if (!ok) break;
-          if (mine) {
-            tc_fence_after();
-            const uint32_t a = static_cast<uint32_t>(ab) * kACols + tile * (kACols / 2);
-            umma_bf16_ts64(d, a, b + static_cast<uint32_t>(i) * (NT * 128 >> 4), idesc, kb != kb0 || i != 0);
-            if (kParts == 1) umma_bf16_ts64(d, a + 32, b + (NT * 128 >> 4), idesc, 1u);
-          }
-          commit_at(b_aempty + 8 * ab);
-          advance(ab, aphase, kABufs);
-        }
+        ok = both || (warp_wait(b_bfull + 8 * bs, bphase, s_abort) && warp_wait(b_afull + 8 * ab, aphase, s_abort));
         if (!ok) break;
+        if (mine) {
+          tc_fence_after();
+          const uint64_t b = sdesc_sw128(sbase + static_cast<uint32_t>(bs) * Cfg::kTok);
+          const uint32_t a = static_cast<uint32_t>(ab) * kACols + tile * (kACols / 2);
+          umma_bf16_ts64(d, a, b, idesc, kb != kb0);
+          umma_bf16_ts64(d, a + 32, b + (NT * 128 >> 4), idesc, 1u);
+        }
+        commit_at(b_aempty + 8 * ab);
+        advance(ab, aphase, kABufs);
         commit_at(b_bempty + 8 * bs);
         advance(bs, bphase, kB);
       }
@@ -432,7 +421,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     if (p.early) pdl_wait_and_trigger();
     const int set = (warp - 6) >> 3, tile = ((warp - 6) >> 2) & 1, r = (warp & 3) * 32 + lane;
     const uint32_t d = (static_cast<uint32_t>((warp & 3) * 32) << 16) +
-                       static_cast<uint32_t>(kParts * set * kACols + tile * (kACols / 2));
+                       static_cast<uint32_t>(set * kACols + tile * (kACols / 2));
     const uint32_t swap = static_cast<uint32_t>((r >> 1) & 3) << 4;
     const uint32_t codes = sbase + Cfg::kOffW + tile * kMaxRecord + r * 64;
     const uint32_t scales = sbase + Cfg::kOffW + tile * kMaxRecord + kQCodeBytes +
@@ -464,31 +453,22 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
           slot -= kW;
           phase ^= 1u;
         }
-        auto store = [&](auto half) {             // 64 inputs of the row
-          constexpr int H = decltype(half)::value;
-          constexpr uint32_t buf = kParts == 2 ? 8 * H : 0;
-          if (H == 0 || kParts == 2) ok = warp_wait(b_aempty + 8 * kParts * set + buf, aphase, s_abort);
-          if (!ok) return;
-          if (mine) {
-            if (H == 0 || kParts == 2) tc_fence_after();
-            const uint32_t to = d + H * (kParts == 2 ? kACols : 32);
-            const uint32_t bytes = H == 0 ? sc.x : sc.y;
-            if (p.code == MOE_QUANT_INT)
-              expand_half<MOE_QUANT_INT, 16>(c[2 * H], c[2 * H + 1], bytes, to);
-            else
-              expand_half<MOE_QUANT_E2M1, 16>(c[2 * H], c[2 * H + 1], bytes, to);
-          }
-          if (H == 1 || kParts == 2) {
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(b_afull + 8 * kParts * set + buf);
-          }
-        };
-        store(std::integral_constant<int, 0>());
+        ok = warp_wait(b_aempty + 8 * set, aphase, s_abort);
         if (!ok) break;
-        store(std::integral_constant<int, 1>());
-        if (!ok) break;
+        if (mine) {
+          tc_fence_after();
+          if (p.code == MOE_QUANT_INT) {
+            expand_half<MOE_QUANT_INT>(c[0], c[1], sc.x, d);
+            expand_half<MOE_QUANT_INT>(c[2], c[3], sc.y, d + 32);
+          } else {
+            expand_half<MOE_QUANT_E2M1>(c[0], c[1], sc.x, d);
+            expand_half<MOE_QUANT_E2M1>(c[2], c[3], sc.y, d + 32);
+          }
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(b_afull + 8 * set);
         aphase ^= 1u;
       }
       n += kb1 - kb0;
@@ -911,15 +891,15 @@ cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
     return chunks * p.blocks;
   };
   // Chunks of 128 tokens where the groups' mean passes 64, as a weight is expanded for a
-  // chunk (8192 tokens of 128 experts 602 us, 783 in chunks of 64), but not where chunks of
+  // chunk (8192 tokens of 128 experts 580 us, 736 in chunks of 64), but not where chunks of
   // 64 are at most an item an SM: there an item's length counts (512 tokens of K 7168,
-  // N 4096 36 us, in chunks of 128 44; 333 tokens of 12 experts 13, 17).
+  // N 4096 35 us, in chunks of 128 43; 333 tokens of 12 experts 13, 17).
   const bool wide = a.out_rows > 64ll * a.n_groups && items_of(64) > a.sm_count;
   const long long items = items_of(wide ? 128 : 64);
   if (a.token == nullptr && a.offsets == nullptr && !wide) {
     // A cluster's CTAs split K where whole items leave SMs idle, as wide as clusters fit at
     // once (64, 128 and 256 tokens of K 7168, N 4096 13, 16 and 25 us, an item a CTA 42; 152
-    // SMs hold 15 clusters of eight, so 64 tokens take 25 us in 16 of eight, 14.6 in
+    // SMs hold 15 clusters of eight, so 64 tokens take 22 us in 16 of eight, 14.6 in
     // clusters of four).
     int splits = kMaxSplits;
     while (splits > 1 && (items > clusters_at_once(splits) || p.kb < splits)) --splits;
