@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     // piece lands at piece ^ (row % 8) of its 128-byte row.  Pieces past K are zero
     // (their weights are, but zero times NaN is not), and so is a token out of range.
     // A stage's copies are one cp.async group, reported kLag groups later (8192 tokens of 128
-    // experts 600 us, 609 with a lag of 2).
+    // experts 593 us, 600 with a lag of 2).
     constexpr int kLag = 1, kPer = NT / 16;
     const int g = threadIdx.x - kTokenWarp * 32, piece = g & 7, rg = g >> 3;
     int slot = 0, aslot = 0, pending = 0;
