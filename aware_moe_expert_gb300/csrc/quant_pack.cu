@@ -44,7 +44,6 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t b) {
   return static_cast<uint32_t>(top + 7) << 3 | ((m << (3 - top)) & 7u);
 }
 
-
 __device__ __forceinline__ uint32_t zero_code(int code) { return code == MOE_QUANT_INT ? 8u : 0u; }
 
 // The code whose value is nearest to v (ties: the even code, as the formats round).
@@ -114,7 +113,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p,
     const bool real = n < p.rows && k0 < p.K;
     const size_t row = static_cast<size_t>(m) * p.rows + n;
     uint32_t sb = 0u;
-    float inv = 0.f;
+    float step = 1.f;
     if (real && p.codes != nullptr) {
       const uint32_t b = p.scales[row * p.groups + k0 / p.group];
       // a scale is not negative, and not NaN (e4m3 has one, all exponent and mantissa bits)
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p,
       const float want = a / (vmax_of(p.code) * factor[m]);
       const uint32_t b = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
       sb = scale_byte(b & 0x7Fu);
-      if (sb != 0u) inv = 1.f / (e4m3_value(b & 0x7Fu) * factor[m]);
+      step = e4m3_value(b & 0x7Fu) * factor[m];
     }
     rec[kQCodeBytes + r * per_row + g] = static_cast<uint8_t>(sb != 0u ? sb : 16u << 3);
     for (int j = 0; j < words; ++j) {
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p,
             q = (kk & 1) != 0 ? byte >> 4 : byte & 15u;
           } else {
             const float v = __bfloat162float(p.w[row * p.K + kk]);
-            if (fabsf(v) < INFINITY) q = nearest(p.code, v * inv);
+            if (fabsf(v) < INFINITY) q = nearest(p.code, v / step);   // its reciprocal may be infinite
           }
         }
         w |= quant_place(p.code, q, i / 2, i & 1);

@@ -99,3 +99,20 @@ def test_quantize_reports_what_is_not_finite():
     assert B.moe_get_device_status(st) == 6
     got = _unpack(d, packed)
     assert got[0, 1, 3] == 0 and got[0, 2, 5] == 0 and (got == 1).sum() == 4 * 64 - 2
+
+
+@pytest.mark.parametrize("kind,group", KINDS)
+def test_quantize_weights_near_the_smallest(kind, group):
+    """Largest weight 2^-120: the groups' steps are subnormal, their reciprocals infinite."""
+    w = torch.zeros(1, 3, 64, dtype=torch.bfloat16, device=DEV)
+    w[0, 0, 0] = 2.0 ** -120
+    w[0, 1, ::2] = 2.0 ** -127
+    d = B.QuantDesc(1, 3, 64, kind, group)
+    packed, st = torch.empty(B.moe_quant_size(d), dtype=torch.uint8, device=DEV), status()
+    B.check(B.moe_quant_quantize(d, w, packed, st))
+    assert B.moe_get_device_status(st) == 0
+    got = _unpack(d, packed)
+    assert ((got == 0) == (w == 0)).all()
+    # the factor (2^-131) has 18 bits, a scale off by up to 2^-4, a product rounded to a bf16
+    # subnormal (2^-134, 2^-7 of 2^-127)
+    assert (np.abs(to64(got) - to64(w)) <= (2.0 ** -4 + 2.0 ** -7 + 2.0 ** -17) * np.abs(to64(w))).all()
