@@ -25,9 +25,9 @@
 // TMEM buffers let one be expanded while the last one multiplies.
 // Every wait is bounded.
 //
-// Measured on a GB300: 64 tokens of K 7168, N 4096 12.6 us, 16384 tokens 573 (1.68 PFLOP/s);
-// a layer of 64 tokens on 32 units of 3584 183 us (4.1 TB/s), experts of 1024 and 8192
-// tokens (128 of 768, k 8) 130 and 580.  Without the MMAs 169, 116 and 500 were left of 185,
+// Measured on a GB300: 64 tokens of K 7168, N 4096 12.5 us, 16384 tokens 553 (1.74 PFLOP/s);
+// a layer of 64 tokens on 32 units of 3584 181 us (4.15 TB/s), experts of 1024 and 8192
+// tokens (128 of 768, k 8) 128 and 580.  Without the MMAs 169, 116 and 500 were left of 185,
 // 134 and 593, without the expansion's arithmetic 159, 109 and 531, without either 147, 96
 // and 438: issue slots (71% busy) and the wait for a record's stores, barriers and MMAs
 // bound the first two, the rows' way from L2 (about 10 TB/s) and the one set of
@@ -346,18 +346,27 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
   const int kb0 = SPLIT ? p.kb * rank / p.splits : 0;
   const int kb1 = SPLIT ? p.kb * (rank + 1) / p.splits : p.kb;
   // item w: chunk w / blocks; tiles of row block w % blocks
-  auto tiles_of = [&](int b) { return p.swiglu ? 2 : min(2, p.rt - 2 * b); };
+  // The items of the last round go to twice as many CTAs, a tile each, where these are
+  // idle otherwise (K 7168, N 4096: 16384 tokens 560 us, 572; 1536 tokens 75, 83).
+  const int rest = GATHER || SPLIT || p.swiglu ? 0 : total % static_cast<int>(gridDim.x);
+  const int whole = total - (2 * rest <= static_cast<int>(gridDim.x) ? rest : 0);
+  const int count = 2 * total - whole;
+  auto chunk_of = [&](int w) { return w < whole ? w : whole + (w - whole) / 2; };
+  auto first_tile = [&](int w) { return w < whole ? 0 : (w - whole) & 1; };
+  auto tiles_of = [&](int w, int b) {
+    return p.swiglu ? 2 : max(0, min(w < whole ? 2 : 1, p.rt - 2 * b - first_tile(w)));
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0;
       uint32_t phase = 0, parity = 0, issued = 0;
       bool ok = true;
-      for (int w = first; w < total && ok; w += step) {
-        const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
-        const int nt = tiles_of(t.nt);
+      for (int w = first; w < count && ok; w += step) {
+        const Tile t = decode_tile<NT>(chunk_of(w), p.blocks, p.n_groups, s_prefix, s_offs);
+        const int nt = tiles_of(w, t.nt);
         const uint8_t* src = p.w + p.matrix * (static_cast<size_t>(t.g) * (p.swiglu ? 2 : 1)) +
-                             (static_cast<size_t>(p.swiglu ? t.nt : 2 * t.nt) * p.kb + kb0) * p.record;
+                             (static_cast<size_t>(p.swiglu ? t.nt : 2 * t.nt + first_tile(w)) * p.kb + kb0) * p.record;
         const size_t next = p.swiglu ? p.matrix : static_cast<size_t>(p.kb) * p.record;
         for (int kb = kb0; kb < kb1; ++kb, src += p.record) {
           if (!mbar_wait(&wempty[slot], phase ^ 1u, s_abort)) {
@@ -385,9 +394,9 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     int bs = 0, ab = 0, db = 0;
     uint32_t bphase = 0, aphase = 0, dphase = 0;
     bool ok = true;
-    for (int w = first; w < total && ok; w += step) {
-      const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
-      const bool mine = uniform(tile < tiles_of(t.nt)) != 0u;
+    for (int w = first; w < count && ok; w += step) {
+      const Tile t = decode_tile<NT>(chunk_of(w), p.blocks, p.n_groups, s_prefix, s_offs);
+      const bool mine = uniform(tile < tiles_of(w, t.nt)) != 0u;
       const uint32_t idesc = uniform(idesc_bf16_f32(128, (t.rows + 15) / 16 * 16));
       const uint32_t d = kTmemD + static_cast<uint32_t>(db * 2 + tile) * NT;
       ok = warp_wait(b_dempty + 8 * db, dphase ^ 1u, s_abort);
@@ -429,8 +438,8 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     int slot = set, n = 0;                        // n: records before this item
     uint32_t phase = 0, aphase = 1;
     bool ok = true;
-    for (int w = first; w < total && ok; w += step) {
-      const bool mine = uniform(tile < tiles_of(w % p.blocks)) != 0u;
+    for (int w = first; w < count && ok; w += step) {
+      const bool mine = uniform(tile < tiles_of(w, chunk_of(w) % p.blocks)) != 0u;
       for (int kb = kb0 + ((n ^ set) & 1); kb < kb1; kb += 2) {
         ok = warp_wait(b_wfull + 8 * slot, phase, s_abort);
         if (!ok) break;
@@ -480,8 +489,8 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
       int slot = 0;
       uint32_t phase = 0, parity = 0, issued = 0;
       bool ok = true;
-      for (int w = first; w < total && ok; w += step) {
-        const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+      for (int w = first; w < count && ok; w += step) {
+        const Tile t = decode_tile<NT>(chunk_of(w), p.blocks, p.n_groups, s_prefix, s_offs);
         const int nb = (t.rows + 15) / 16;
         const bool wide = nb > 2;
         const int boxes = wide ? (t.rows + 63) / 64 : nb, box = wide ? 64 : 16;
@@ -521,13 +530,13 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     Tile t{};
     int tok[kPer];
     auto look = [&](int w) {
-      t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
+      t = decode_tile<NT>(chunk_of(w), p.blocks, p.n_groups, s_prefix, s_offs);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         tok[i] = rg + 16 * i < t.rows ? __ldg(p.token + t.row0 + rg + 16 * i) : 0;
     };
-    if (first < total) look(first);
-    for (int w = first; w < total && ok; w += step) {
+    if (first < count) look(first);
+    for (int w = first; w < count && ok; w += step) {
       const int rows = t.rows;
       const uint4* src[kPer];
       uint32_t size[kPer];
@@ -538,7 +547,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
         src[i] = p.x + static_cast<size_t>(fine ? tok[i] : 0) * (p.ldx / 8) + kb0 * (kQK / 8) + piece;
         size[i] = fine ? 16u : 0u;
       }
-      if (w + step < total) look(w + step);
+      if (w + step < count) look(w + step);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!try_wait_at(b_bempty + 8 * slot, phase ^ 1u) &&
             !wait_on(b_bempty + 8 * slot, phase ^ 1u, s_abort)) {
@@ -589,9 +598,9 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     int db = 0;
     uint32_t dphase = 0;
     bool ok = true;
-    for (int w = first; w < total; w += step) {
-      const Tile t = decode_tile<NT>(w, p.blocks, p.n_groups, s_prefix, s_offs);
-      const int nt = tiles_of(t.nt);
+    for (int w = first; w < count; w += step) {
+      const Tile t = decode_tile<NT>(chunk_of(w), p.blocks, p.n_groups, s_prefix, s_offs);
+      const int nt = tiles_of(w, t.nt);
       const float u = p.code == MOE_QUANT_E2M1 ? quant_unit<MOE_QUANT_E2M1>() : quant_unit<MOE_QUANT_INT>();
       const float f0 = __ldg(p.factor + (p.swiglu ? 2 * t.g : t.g)) * u;
       const float f1 = p.swiglu ? __ldg(p.factor + 2 * t.g + 1) * u : f0;
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
           }
       } else if (p.f32) {
         for (int i = 0; i < nt; ++i) {
-          const int col = (2 * t.nt + i) * 128 + r;
+          const int col = (2 * t.nt + first_tile(w) + i) * 128 + r;
           float* out = static_cast<float*>(p.out) + static_cast<size_t>(t.row0) * p.ldo + col;
           for (int c0 = 0; c0 < t.rows; c0 += 16) {
             uint32_t v[16];
@@ -642,7 +651,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
         const uint32_t get = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
         const int outs = p.swiglu ? 1 : nt;
         for (int i = 0; i < outs; ++i) {
-          const int col = (p.swiglu ? t.nt : 2 * t.nt + i) * 128 + q * 32 + (lane & 3) * 8;
+          const int col = (p.swiglu ? t.nt : 2 * t.nt + first_tile(w) + i) * 128 + q * 32 + (lane & 3) * 8;
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
                                static_cast<size_t>(t.row0 + (lane >> 2)) * p.ldo + col;
           const bool whole = p.vec && col + 8 <= p.n;

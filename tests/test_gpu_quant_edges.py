@@ -188,6 +188,39 @@ def _grouped(layer, T, k, token, offsets, rows=None):
     return to64(x), y, B.moe_get_device_status(st)
 
 
+@pytest.mark.parametrize("T,N", [(2300, 2100), (2300, 2304), (2432, 4096), (1300, 3585)])
+def test_last_rounds_of_a_dense_product(T, N):
+    """Some items more than SMs, with an odd number of row tiles and an even one."""
+    rng = np.random.default_rng(N)
+    w, x = random_weights(rng, 1, N, 72, "e2m1", 16), _bf(rng, T, 72)
+    st, ws = status(), torch.empty(256, dtype=torch.uint8, device=DEV)
+    y = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.check(B.moe_quant_project(B.QuantProject(T, 72, N, "e2m1", 16), x, pack(w, "e2m1", 16), y, st, ws))
+    assert B.moe_get_device_status(st) == 0 and (y[T:] == 7.0).all()
+    within(y[:T], *Q.product(to64(x), Q.weights(*w, "e2m1", 16)[0]))
+
+
+@pytest.mark.parametrize("E", [17, 18])
+def test_last_rounds_of_experts(E):
+    """Nine blocks of outputs of 17 or 18 experts on 152 SMs, the last block of one tile."""
+    layer = Layer(E, 2112, E, 64, "int4", 32)
+    x, y, code = _grouped(layer, 3 * E, 1, list(range(3 * E)), list(range(0, 3 * E + 1, 3)))
+    assert code == 0
+    for e in range(E):
+        within(y[3 * e:3 * e + 3], *layer.expert(e, x[3 * e:3 * e + 3]))
+    c = _Call(layer, 100, 6, seed=E)            # fp32 rows between the products
+    only, many = [], c.run().clone()
+    for t0 in range(0, 100, 4):                 # the few-token kernels on the same tokens
+        part = _Call(layer, 4, 6)
+        part.x, part.router, part.k = c.x[t0:t0 + 4], c.router, c.k[t0:t0 + 4].contiguous()
+        only.append(part.run().clone())
+    few = torch.cat(only)
+    assert c.code() == 0
+    # both are within a rounding of the output and one of the activations of the same sums
+    off = (many.double() - few.double()).norm() / few.double().norm()
+    assert float(off) <= (2 + 1) ** 0.5 * 2.0 ** -8 / 3 ** 0.5
+
+
 @pytest.mark.parametrize("T", [3, 200])
 def test_all_tokens_to_one_expert_and_none(T):
     layer = Layer(7, 128, 5, 64, "e2m1", 32)
