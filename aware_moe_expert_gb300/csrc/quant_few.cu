@@ -21,9 +21,9 @@
 // units is part of it.
 //
 // Measured on a GB300: one token of K 7168, N 4096 5.7 us (2.9 TB/s); layers of 1, 8 and 3
-// tokens (256 units of 384, k 16; the same; 256 of 2048 and a shared expert, k 8) 17.9, 40.8
-// and 134 us.  Loads of the codes alone, without products and tokens, take 3.8 us there, and
-// 28 and 86 of the layers' 40.8 and 134: what is left is the expansion (issue slots 50-60%
+// tokens (256 units of 384, k 16; the same; 256 of 2048 and a shared expert, k 8) 18.1, 40.9
+// and 126 us.  Loads of the codes alone, without products and tokens, take 3.8 us there, and
+// 28 and 86 of the layers' 40.9 and 126: what is left is the expansion (issue slots 50-60%
 // busy, ALU 40-54%), the tokens' loads, and for one token three launches' latencies.
 #include <cfloat>
 #include <type_traits>
@@ -412,8 +412,10 @@ cudaError_t launch_kind(const FewParams& p, int grid, cudaStream_t s) {
 }
 
 // `tasks` of about `steps` records: the CTAs of a cluster that share a task are what
-// makes the longest CTA's steps fewest, with a step for starting a task and two
-// for the cluster's barriers.
+// makes the longest CTA's steps fewest, with three for starting a task and three more for
+// the cluster's barriers (clusters of 1, 2, 4 and 8: layer of 3 tokens, 224 tasks of 400 records,
+// 126, 128, 134 and 161 us; layers of 8 and 1 tokens, 64 tasks of 384 and 48 records, 64, 48, 41
+// and 47, and 19.8, 17.9, 18.2 and 21.2).
 template <int MODE, bool PAIR>
 cudaError_t launch_few(FewParams p, int code, int group, int tasks, int steps, int sm_count, cudaStream_t s) {
   const int ctas = kCtas * sm_count;
@@ -422,7 +424,7 @@ cudaError_t launch_few(FewParams p, int code, int group, int tasks, int steps, i
     long long best = 0;
     for (int c = 1; c <= kMaxCluster; c *= 2) {
       const long long rounds = (static_cast<long long>(tasks) * c + ctas - 1) / ctas;
-      const long long cost = rounds * ((steps + kWarps * c - 1) / (kWarps * c) + (c > 1 ? 3 : 1));
+      const long long cost = rounds * ((steps + kWarps * c - 1) / (kWarps * c) + (c > 1 ? 6 : 3));
       if (c == 1 || cost < best) {
         best = cost;
         p.cluster = c;
