@@ -25,9 +25,9 @@
 // TMEM buffers let one be expanded while the last one multiplies.
 // Every wait is bounded.
 //
-// Measured on a GB300: 64 tokens of K 7168, N 4096 12.5 us, 16384 tokens 553 (1.74 PFLOP/s);
-// a layer of 64 tokens on 32 units of 3584 181 us (4.15 TB/s), experts of 1024 and 8192
-// tokens (128 of 768, k 8) 128 and 580.  Without the MMAs 169, 116 and 500 were left of 185,
+// Measured on a GB300: 64 tokens of K 7168, N 4096 12.5 us, 16384 tokens 560 (1.72 PFLOP/s);
+// a layer of 64 tokens on 32 units of 3584 180 us (4.17 TB/s), experts of 1024 and 8192
+// tokens (128 of 768, k 8) 128 and 583.  Without the MMAs 169, 116 and 500 were left of 185,
 // 134 and 593, without the expansion's arithmetic 159, 109 and 531, without either 147, 96
 // and 438: issue slots (71% busy) and the wait for a record's stores, barriers and MMAs
 // bound the first two, the rows' way from L2 (about 10 TB/s) and the one set of
@@ -72,8 +72,10 @@ constexpr int most_columns(int nt) {       // all CTAs' together
 
 template <int NT, bool SPLIT>
 struct TileCfg {
-  static constexpr int kW = SPLIT || NT == 128 ? 4 : 6;    // records in flight, even
-  static constexpr int kB = 4;                             // token stages of 128 inputs
+  // Records in flight, even, and token stages of 128 inputs (layer of 64 tokens 180.0 us, 180.9
+  // with 6 and 4, 183.7 with 8 and 4; chunks of 128: 8192 tokens 583, with 6 and 3 594).
+  static constexpr int kW = 4;
+  static constexpr int kB = SPLIT || NT == 128 ? 4 : 6;
   static constexpr uint32_t kTok = NT * kQK * 2;
   static constexpr uint32_t kOffW = kB * kTok;
   static constexpr uint32_t kOffPart = kOffW + kW * kWStage;
@@ -900,7 +902,7 @@ cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
     return chunks * p.blocks;
   };
   // Chunks of 128 tokens where the groups' mean passes 64, as a weight is expanded for a
-  // chunk (8192 tokens of 128 experts 580 us, 736 in chunks of 64), but not where chunks of
+  // chunk (8192 tokens of 128 experts 583 us, 736 in chunks of 64), but not where chunks of
   // 64 are at most an item an SM: there an item's length counts (512 tokens of K 7168,
   // N 4096 35 us, in chunks of 128 43; 333 tokens of 12 experts 13, 17).
   const bool wide = a.out_rows > 64ll * a.n_groups && items_of(64) > a.sm_count;
