@@ -76,6 +76,18 @@ def test_two_calls_at_once_on_two_streams(T):
         assert torch.equal(c.out, w) and c.code() == 0
 
 
+@pytest.mark.parametrize("T", [1, 2, 4])
+def test_few_tokens_lose_their_outputs_rounding_only(T):
+    """One expert of weight 1 and the shared one.  A rounding moves values by 2^-8 / sqrt(3) of
+    them at the most in the mean square; activations rounded once to bf16 would double the square."""
+    layer = Layer(T, 2048, 1, 512, "e2m1", 16, shared=256)
+    c = _Call(layer, T, 1)
+    x = to64(c.x)
+    want = layer.expert(0, x)[0] + layer.shared_expert(x)[0]
+    off = np.linalg.norm(to64(c.run()) - want) / np.linalg.norm(want)
+    assert c.code() == 0 and off <= 2.0 ** -8 / 3 ** 0.5
+
+
 @pytest.mark.parametrize("T", [5, 20])
 def test_tokens_without_units(T):
     """A bias of -inf takes every unit out: the shared expert alone, and the status says so."""
