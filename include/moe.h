@@ -606,7 +606,8 @@ typedef struct {
 } moe_quant_weights;
 
 /* Workspace bytes for the calls below (0 on a bad desc).  Of desc they use the shape,
- * the routing and I_shared; not w_shared_gate_up, w_shared_down and path. */
+ * the routing and I_shared; not w_shared_gate_up, w_shared_down and path.  Fewer tokens
+ * can need more, so a workspace for several T has the largest of their sizes. */
 size_t moe_quant_workspace_size(const moe_layer_desc* desc);
 
 /* moe_grouped_ffn on packed weights. */
