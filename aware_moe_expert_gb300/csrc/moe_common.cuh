@@ -42,8 +42,11 @@ __device__ __forceinline__ void pdl_wait_and_trigger() {
 // right behind a launch of the same call whose threads all wait before they
 // trigger: then everything before that launch is complete, and the kernel waits
 // only for what that launch writes (group_route_kernel behind zero_load_kernel,
-// the projections of lora.cu behind the kernel that computes v).  Either way all
-// of a kernel's CTAs have waited by the time it completes, so that one kernel's
+// the projections of lora.cu behind the kernel that computes v).  What it may read before
+// either is parameters (router_w, expert_bias, packed 4-bit weights): no kernel right
+// before the call writes them but the library's own packing, which ends with a launch
+// whose thread waits for it and triggers then (packed_kernel).  In every case some thread of
+// each of a kernel's CTAs has waited by the time it completes, so that one kernel's
 // completion implies every earlier one's.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,

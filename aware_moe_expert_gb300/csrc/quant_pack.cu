@@ -14,8 +14,7 @@ namespace {
 
 constexpr int kPackThreads = 256;
 
-// Waits for the launch before, and does not let the next one start early: the products
-// read weights before they wait, as parameters.
+// Waits for the launch before.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct PackParams {
@@ -184,6 +183,11 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(const PackParams p
   }
 }
 
+// Ends a packing.  Products read packed weights before they wait, and only a wait makes a
+// launch's writes visible: that the packing does not trigger is not enough.  This thread waits
+// for the packing, then triggers, so what starts behind it finds the weights complete.
+__global__ void packed_kernel() { pdl_wait_and_trigger(); }
+
 PackParams params_of(const QuantPackArgs& a) {
   PackParams p{};
   p.codes = static_cast<const uint8_t*>(a.codes);
@@ -232,8 +236,9 @@ cudaError_t launch_quant_pack(const QuantPackArgs& a, cudaStream_t s) {
   e = launch_pdl(factor_kernel, dim3(blocks(p.count)), dim3(kPackThreads), 0, s, p, factor);
   if (e != cudaSuccess) return e;
   const size_t n = static_cast<size_t>(p.shape.rt) * p.shape.kb * kQRows * (kQK / p.group);
-  return launch_pdl(pack_kernel, dim3(blocks(n), p.count < 65535 ? p.count : 65535),
-                    dim3(kPackThreads), 0, s, p, static_cast<const float*>(factor));
+  e = launch_pdl(pack_kernel, dim3(blocks(n), p.count < 65535 ? p.count : 65535),
+                 dim3(kPackThreads), 0, s, p, static_cast<const float*>(factor));
+  return e != cudaSuccess ? e : launch_pdl(packed_kernel, dim3(1), dim3(1), 0, s);
 }
 
 cudaError_t launch_quant_unpack(const QuantPackArgs& a, cudaStream_t s) {

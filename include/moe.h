@@ -23,11 +23,14 @@
  *    synchronises).
  *  - Kernels are launched with programmatic dependent launch: the first
  *    kernel of a call may start while the previous kernel on `stream`
- *    finishes.  It reads the layer's parameters (router_w, expert_bias)
- *    before it waits for that kernel and every other input after; so a
- *    parameter must not be written by a kernel on the same stream that is
- *    still running when the call starts (one that lets its dependents launch
- *    early).  Inputs written by the preceding kernel (x, k_per_token, ...)
+ *    finishes.  It reads the layer's parameters (router_w, expert_bias,
+ *    packed 4-bit weights) before it waits for that kernel and every other
+ *    input after; so the kernel right before a call on its stream must not
+ *    write them, whether it lets its dependents launch early or not, as only
+ *    that wait makes its writes visible (a copy, a memset or a kernel that is
+ *    launched the ordinary way between the two is enough).  moe_quant_pack and
+ *    moe_quant_quantize need nothing between: they end with a launch of their
+ *    own that waits.  Inputs written by the preceding kernel (x, k_per_token, ...)
  *    are always read after it has finished.
  *  - `workspace` is caller-owned device memory of at least
  *    moe_workspace_size(desc) bytes, 256-byte aligned.  Calls on the same
@@ -543,7 +546,9 @@ moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void
  * Products take the codes times their scale (exact in bf16), sum in fp32 and
  * multiply the sums by the factor: no weight is rounded.  (Inside a product weights
  * are scaled by a power of two down to 2^-16, so sums below 2^-110 can lose bits.)
- * moe_quant_pack lays weights out once; only the packed form is used after.
+ * moe_quant_pack lays weights out once; only the packed form is used after, by calls that
+ * may follow at once.  Packed weights are parameters: read before a call waits for the
+ * kernel right before it, which must not write them (copying them by a kernel, for one).
  * Pointers are 16-byte aligned, where no other alignment is given (status words, factors,
  * indexes: 4 bytes).  A workspace is 256-byte aligned and holds nothing between calls;
  * calls that may run at once, captured graphs among them, need one each.
