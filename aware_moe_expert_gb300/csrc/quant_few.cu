@@ -419,6 +419,7 @@ cudaError_t launch_kind(const FewParams& p, int grid, cudaStream_t s) {
 template <int MODE, bool PAIR>
 cudaError_t launch_few(FewParams p, int code, int group, int tasks, int steps, int sm_count, cudaStream_t s) {
   const int ctas = kCtas * sm_count;
+  if (ctas < 1) return cudaErrorNoDevice;      // the device could not be asked
   p.cluster = 1;
   if (MODE != GATE_UP) {
     long long best = 0;
