@@ -56,21 +56,39 @@ class BlockWeights:
 def quantized(w: BlockWeights, code: str = "e2m1", group: int = 16,
               shared: bool = False) -> BlockWeights:
     """The block's experts (and its shared expert, which then takes no adapters) as 4-bit
-    weights, packed once; the bf16 ones are left out of the result.  Synchronises."""
-    status = torch.zeros(1, dtype=torch.int32, device=w.router.device)
+    weights, packed once; the bf16 ones are left out of the result.  They are what MoeBlock
+    takes, on a GPU: contiguous bf16 of the router's shape; others are refused (ValueError),
+    as packed bytes no longer show what they were made from.  Synchronises."""
+    if w.quant is not None:
+        raise ValueError("quantized: the weights are packed already")
+    if w.router.dim() != 2:
+        raise ValueError("router: a tensor of 2 dimensions wanted")
+    (E, H), dev = w.router.shape, w.router.device
+    for gate_up, down, count in (("w_gate_up", "w_down", (E,)), ("shared_gate_up", "shared_down", ()))[:1 + shared]:
+        t = getattr(w, down)
+        n = max(t.shape[-1], 1) if isinstance(t, torch.Tensor) and t.dim() else 1     # which down decides
+        for name, shape in ((down, (*count, H, n)), (gate_up, (*count, 2 * n, H))):
+            t = getattr(w, name)
+            _want(name, t, shape, BF16, dev)
+            if t.device != dev:
+                raise ValueError(f"{name}: on {t.device}, the router on {dev}")
+    if dev.type != "cuda":
+        raise ValueError(f"quantized: weights on cuda wanted, not on {dev}")
 
-    def pack(t, count):
+    def pack(name, count):
+        t = getattr(w, name)
         d = B.QuantDesc(count, t.numel() // (count * t.shape[-1]), t.shape[-1], code, group)
-        packed = torch.empty(B.moe_quant_size(d), dtype=torch.uint8, device=t.device)
+        packed = torch.empty(B.moe_quant_size(d), dtype=torch.uint8, device=dev)
         B.check(B.moe_quant_quantize(d, t, packed, status), "moe_quant_quantize")
         return packed
 
-    E = w.w_gate_up.shape[0]
-    q = B.QuantWeights(code, group, pack(w.w_gate_up, 2 * E), pack(w.w_down, E))
-    if shared:
-        q.shared_gate_up, q.shared_down = pack(w.shared_gate_up, 2), pack(w.shared_down, 1)
-        w = replace(w, shared_gate_up=None, shared_down=None)
-    B.check(B.moe_get_device_status(status), "quantized")
+    with torch.cuda.device(dev):
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        q = B.QuantWeights(code, group, pack("w_gate_up", 2 * E), pack("w_down", E))
+        if shared:
+            q.shared_gate_up, q.shared_down = pack("shared_gate_up", 2), pack("shared_down", 1)
+            w = replace(w, shared_gate_up=None, shared_down=None)
+        B.check(B.moe_get_device_status(status), "quantized")
     return replace(w, w_gate_up=None, w_down=None, quant=q)
 
 
