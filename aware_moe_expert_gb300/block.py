@@ -143,7 +143,6 @@ class MoeBlock:
         taken from the weights (the shared expert runs here, with adapters), unless
         these have a packed shared expert, of layer.I_shared."""
         self.device = torch.device(device)
-        self.layer, self.weights = layer, weights
         # this block's bias in a copy: blocks may be built from one GroupRoute
         self.groups = replace(groups, select_bias=weights.select_bias)
         self.eps, self.residual_scale, self.branch_scale = eps, residual_scale, branch_scale
@@ -151,6 +150,9 @@ class MoeBlock:
         q = weights.quant
         self.shared_packed = q is not None and q.shared_gate_up is not None
         self.shared = layer.I_shared if self.shared_packed else weights.shared_down.shape[1]
+        if not self.shared_packed and layer.I_shared != 0:
+            layer = replace(layer, I_shared=0)       # the layer's steps have no shared expert
+        self.layer, self.weights = layer, weights
         E, I = layer.E_r, layer.I_sub  # noqa: E741
         shapes = dict(attn_post_norm=(H,), pre_norm=(H,), ffn_post_norm=(H,), next_pre_norm=(H,),
                       router=(E, H))

@@ -57,3 +57,22 @@ def test_weights_in_host_memory_or_packed_already_are_refused():
         K.quantized(_weights(quant=B.QuantWeights("e2m1", 16)))
     with pytest.raises(ValueError, match="router"):
         K.quantized(_weights(router=bf(E * H)))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_layer_that_names_its_shared_expert(monkeypatch, packed):
+    """The shared expert in bf16 is the block's own step: the layer's calls get no I_shared."""
+    layer = B.LayerDesc(T=20, H=H, n_experts=E, n_sub=1, I_sub=I, k_max=3, I_shared=S)
+    w = _weights()
+    if packed:
+        size = lambda *s: torch.zeros(B.moe_quant_size(B.QuantDesc(*s, "e2m1", 16)), dtype=torch.uint8)  # noqa: E731
+        w = dataclasses.replace(w, w_gate_up=None, w_down=None,
+                                quant=B.QuantWeights("e2m1", 16, size(2 * E, I, H), size(E, H, I)))
+    block = K.MoeBlock(layer, B.GroupRoute(), w, device="cpu")
+    assert block.shared == S and block.workspace.numel() >= B.moe_workspace_size(dataclasses.replace(layer, I_shared=0))
+    descs = []
+    for name in B.EXPORTS:
+        monkeypatch.setattr(B, name, lambda d, *a: descs.append(d) or 0)
+    block.forward(torch.zeros(5, H), bf(5, H), torch.ones(5, dtype=torch.int32))
+    layers = [d for d in descs if isinstance(d, B.MoeLayerDesc)]
+    assert len(layers) == 4 and all(d.I_shared == 0 and d.T == 5 for d in layers)
