@@ -84,8 +84,9 @@ __global__ void __launch_bounds__(kPackThreads) factor_kernel(PackParams p, floa
   if (i >= p.count) return;
   if (p.codes != nullptr) {
     const float f = p.factors[i];
-    if (!(fabsf(f) < INFINITY)) report(p.status, MOE_ERR_NONFINITE);
-    factor[i] = f;
+    const bool bad = !(fabsf(f) < INFINITY);
+    if (bad) report(p.status, MOE_ERR_NONFINITE);
+    factor[i] = bad ? 0.f : f;                   // as a bad scale's weights
   } else {
     const float f = factor[i] / (448.f * vmax_of(p.code));
     factor[i] = f > 0.f ? f : 1.f;

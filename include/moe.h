@@ -567,7 +567,7 @@ size_t moe_quant_size(const moe_quant_desc* desc);
 /*   codes    uint8 [count, rows, K / 2]: two a byte, the even input in the low half
  *   scales   e4m3 [count, rows, ceil(K / group)]; a negative or NaN one is reported
  *            (MOE_ERR_NONFINITE) and its weights are 0
- *   factors  fp32 [count]; one that is not finite is reported
+ *   factors  fp32 [count]; one that is not finite is reported (the same) and its matrix is 0
  *   packed   moe_quant_size bytes, 16-byte aligned */
 moe_status moe_quant_pack(const moe_quant_desc* desc, const void* codes, const void* scales,
                           const float* factors, void* packed, int32_t* dev_status, void* stream);
