@@ -942,16 +942,19 @@ moe_status validate_quant_weights(const moe_layer_desc* d, const moe_quant_weigh
   return MOE_OK;
 }
 
-// Behind the layer's own workspace: fp32 outputs of the experts and the shared expert, or a
-// few tokens' second parts of the activations.
+// The experts' fp32 outputs lie where the bf16 layer has x_perm, act and y_perm (twice 2 bytes
+// a value and more), which these calls do not use.  Behind the layer's workspace: the
+// activations, the shared expert's fp32 outputs, a few tokens' second parts of the activations.
 struct QuantLayout {
-  size_t y, ysh, low, low_sh, total;
+  size_t y, act, ysh, low, low_sh, total;
 };
 QuantLayout quant_layout_of(const moe_layer_desc& d) {
   QuantLayout q;
-  size_t o = layout_of(d).total;
-  q.y = o;
-  o = align_up(o + static_cast<size_t>(d.T) * d.k_max * d.H * 4);
+  const Layout l = layout_of(d);
+  size_t o = l.total;
+  q.y = l.xperm;
+  q.act = o;
+  o = align_up(o + static_cast<size_t>(d.T) * d.k_max * d.I_sub * 2);
   q.ysh = o;
   o = align_up(o + (d.I_shared > 0 ? static_cast<size_t>(d.T) * d.H * 4 : 0));
   const size_t pairs = d.T <= moe::kQuantPairTokens ? static_cast<size_t>(d.T) : 0;
@@ -983,7 +986,7 @@ moe_status do_quant_ffn(const moe_layer_desc* d, const moe_quant_weights* w, boo
   a.n = I;
   a.K = d->H;
   a.swiglu = 1;
-  a.out = at<void>(ws, shared ? l.act_sh : l.act);
+  a.out = at<void>(ws, shared ? l.act_sh : quant_layout_of(*d).act);
   a.ldo = I;
   a.out_rows = rows;
   a.early = shared;
@@ -1694,7 +1697,7 @@ moe_status moe_layer_forward_quant(const moe_layer_desc* desc, const moe_group_r
     a.down = weights->down;
     a.shared_gate_up = weights->shared_gate_up;
     a.shared_down = weights->shared_down;
-    a.act = at<void>(workspace, l.act);
+    a.act = at<void>(workspace, q.act);
     a.act_shared = at<void>(workspace, l.act_sh);
     a.act_low = at<void>(workspace, q.low);
     a.act_shared_low = at<void>(workspace, q.low_sh);
