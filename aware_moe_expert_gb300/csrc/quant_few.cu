@@ -13,17 +13,18 @@
 //
 // Experts: every CTA lists the distinct units of the batch itself, from the router's
 // selection.  The first launch computes act[t, j] = w_tj f_u silu(g) u of token t's
-// j-th unit (its gate and its down matrix's factor with it, one rounding; up to four tokens
-// what it leaves is another bf16, in the columns that they leave free: the error of one token's
-// outputs is then their own rounding's, 0.0016, 0.0025 without); the second
+// j-th unit (its gate and its down matrix's factor with it, one rounding to bf16, as the bf16
+// layer's activations have one; up to four tokens what it leaves is another bf16, in the
+// columns that they leave free: the error of the outputs is then their own rounding's,
+// 0.0016; from five tokens on there is no column for it, and the error 0.0023); the second
 // one, whose weights stream while the first ends, multiplies 32 rows of W_down of ALL
 // units and the shared expert with them, one long sum: the weighted sum over a token's
 // units is part of it.
 //
 // Measured on a GB300: one token of K 7168, N 4096 5.7 us (2.9 TB/s); layers of 1, 8 and 3
-// tokens (256 units of 384, k 16; the same; 256 of 2048 and a shared expert, k 8) 18.1, 40.9
-// and 126 us.  Loads of the codes alone, without products and tokens, take 3.8 us there, and
-// 28 and 86 of the layers' 40.9 and 126: what is left is the expansion (issue slots 50-60%
+// tokens (256 units of 384, k 16; the same; 256 of 2048 and a shared expert, k 8) 18.1, 41.0
+// and 126 us; a shared expert alone (H 7168, 2048) of 1 and 8 tokens 12.4 and 14.2.  Loads of the codes alone, without products and tokens, take 3.8 us there, and
+// 28 and 86 of the layers' 41.0 and 126: what is left is the expansion (issue slots 50-60%
 // busy, ALU 40-54%), the tokens' loads, and for one token three launches' latencies.
 #include <cfloat>
 #include <type_traits>

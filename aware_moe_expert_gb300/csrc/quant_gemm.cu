@@ -25,13 +25,14 @@
 // TMEM buffers let one be expanded while the last one multiplies.
 // Every wait is bounded.
 //
-// Measured on a GB300: 64 tokens of K 7168, N 4096 12.5 us, 16384 tokens 560 (1.72 PFLOP/s);
+// Measured on a GB300, calls in a graph: 64 tokens of K 7168, N 4096 12.5 us, 16384 tokens
+// 557 (1.73 PFLOP/s; call by call for long 620, as the power cap lowers the clock);
 // a layer of 64 tokens on 32 units of 3584 180 us (4.17 TB/s), experts of 1024 and 8192
-// tokens (128 of 768, k 8) 128 and 583.  Without the MMAs 169, 116 and 500 were left of 185,
-// 134 and 593, without the expansion's arithmetic 159, 109 and 531, without either 147, 96
-// and 438: issue slots (71% busy) and the wait for a record's stores, barriers and MMAs
-// bound the first two, the rows' way from L2 (about 10 TB/s) and the one set of
-// accumulators of a wide chunk the last.
+// tokens (128 of 768, k 8) 128 and 581.  When these took 185, 134 and 593, 169, 116 and 500
+// were left without the MMAs, 159, 109 and 531 without the expansion's arithmetic, 147, 96
+// and 438 without either: issue slots (72% busy) and the wait for a record's stores,
+// barriers and MMAs bound the first two, the rows' way from L2 (about 10 TB/s) and the one
+// set of accumulators of a wide chunk the last.
 #include <algorithm>
 #include <type_traits>
 
@@ -134,7 +135,7 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t a, const uint32_t (&v)[4
 }
 
 // SiLU by the approximate exponential and reciprocal: within (4 + 1.2 |g|) 2^-23 of its
-// value (0 below -87).
+// value (0 below -87), far below the bf16 that it is rounded to.
 __device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -266,6 +267,8 @@ __device__ __forceinline__ void advance(int& slot, uint32_t& phase, int n) {
   }
 }
 
+// 768 threads leave 80 registers each, 864 with the gathering warps 72.  Of the three ungathered
+// variants the two that do not split spill 72 bytes a thread (124 of loads).
 template <int NT, bool GATHER, bool SPLIT>
 __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     quant_tile_kernel(const __grid_constant__ CUtensorMap tm16,
@@ -349,7 +352,8 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
   const int kb1 = SPLIT ? p.kb * (rank + 1) / p.splits : p.kb;
   // item w: chunk w / blocks; tiles of row block w % blocks
   // The items of the last round go to twice as many CTAs, a tile each, where these are
-  // idle otherwise (K 7168, N 4096: 16384 tokens 560 us, 572; 1536 tokens 75, 83).
+  // idle otherwise (K 7168, N 4096: 16384 tokens 557 us, 569; 1536 tokens 75, 82).  With an odd
+  // number of row tiles the last block's second item has none: its CTA loads tokens only.
   const int rest = GATHER || SPLIT || p.swiglu ? 0 : total % static_cast<int>(gridDim.x);
   const int whole = total - (2 * rest <= static_cast<int>(gridDim.x) ? rest : 0);
   const int count = 2 * total - whole;
@@ -661,6 +665,10 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
             float v[2][8];                        // [lanes 0-15, 16-31]
             tmem_ld_frag(d + static_cast<uint32_t>(i * NT + c0), v[0]);
             tmem_ld_frag(d + (16u << 16) + static_cast<uint32_t>(i * NT + c0), v[1]);
+            // Activations leave as one bf16, as the bf16 layer's do, though the next product
+            // sums them in fp32: a second bf16 with what is left would double that product's
+            // MMAs and token rows, which bound it for many tokens.  The error of the outputs
+            // is 0.0023 so, their own rounding's 0.0016 without.
             if (p.swiglu) {
               float up[2][8];
               tmem_ld_frag(d + static_cast<uint32_t>(NT + c0), up[0]);
@@ -902,16 +910,17 @@ cudaError_t launch_quant_gemm(const QuantGemmArgs& a, cudaStream_t s) {
     return chunks * p.blocks;
   };
   // Chunks of 128 tokens where the groups' mean passes 64, as a weight is expanded for a
-  // chunk (8192 tokens of 128 experts 583 us, 736 in chunks of 64), but not where chunks of
-  // 64 are at most an item an SM: there an item's length counts (512 tokens of K 7168,
-  // N 4096 35 us, in chunks of 128 43; 333 tokens of 12 experts 13, 17).
+  // chunk (8192 tokens of 128 experts 581 us, 709 in chunks of 64; 16384 tokens of K 7168, N 4096
+  // 557, 856; but 900 tokens of the experts, 56 a group, 122 in 64, 130 in 128), nor where chunks
+  // of 64 are at most an item an SM: there an item's length counts (512 tokens of K 7168,
+  // N 4096 36 us, in chunks of 128 41; 333 tokens of 12 experts 12.4, 16.3).
   const bool wide = a.out_rows > 64ll * a.n_groups && items_of(64) > a.sm_count;
   const long long items = items_of(wide ? 128 : 64);
   if (a.token == nullptr && a.offsets == nullptr && !wide) {
     // A cluster's CTAs split K where whole items leave SMs idle, as wide as clusters fit at
-    // once (64, 128 and 256 tokens of K 7168, N 4096 13, 16 and 25 us, an item a CTA 42; 152
-    // SMs hold 15 clusters of eight, so 64 tokens take 22 us in 16 of eight, 14.6 in
-    // clusters of four).
+    // once (64, 128 and 256 tokens of K 7168, N 4096 12.5, 15.5 and 23.3 us, an item a CTA 35;
+    // 152 SMs hold 15 clusters of eight, so 64 tokens took 22 us in 16 of eight, 14.6 in
+    // clusters of four, 13 in six).
     int splits = kMaxSplits;
     while (splits > 1 && (items > clusters_at_once(splits) || p.kb < splits)) --splits;
     if (splits > 1) {

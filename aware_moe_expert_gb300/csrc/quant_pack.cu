@@ -1,9 +1,13 @@
 // Packing of 4-bit weights (the layout is quant.cuh's): from a checkpoint's
 // codes, scales and factors, from bf16 weights, and back to bf16.
 //
-// Set-up work, one thread per 32-bit word of eight codes, bound by its reads
-// and writes: a warp reads 8 consecutive bytes of codes (16 of bf16) per lane
-// quartet and row and writes whole 16-byte pieces of neighbouring rows.
+// Set-up work, once a checkpoint.  A thread packs a scale group of a row: it loads codes a
+// byte for each and sets a word's bits one by one; unpacking has a thread per word of
+// eight weights.  Issue slots bound all three, not memory.  256 matrices of 768 x 2048, e2m1,
+// groups of 16: packing 502 us (0.9 TB/s, issue slots 82% busy), quantising 1466 (the largest
+// magnitudes 594, two bytes a lane at a time, 64 CTAs a matrix; then packing at 88%),
+// unpacking 329 (3.1 TB/s, 81%).  One matrix of 4096 x 7168: 41, 864, where those 64 CTAs read
+// it alone, and 25 us.
 #include <cuda_fp8.h>
 
 #include "moe_internal.h"

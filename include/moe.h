@@ -546,9 +546,12 @@ moe_status moe_lora_project(const moe_lora_desc* desc, const void* x, const void
  * Products take the codes times their scale (exact in bf16), sum in fp32 and
  * multiply the sums by the factor: no weight is rounded.  (Inside a product weights
  * are scaled by a power of two down to 2^-16, so sums below 2^-110 can lose bits.)
+ * Integers have no zero point but 8.
  * moe_quant_pack lays weights out once; only the packed form is used after, by calls that
  * may follow at once.  Packed weights are parameters: read before a call waits for the
  * kernel right before it, which must not write them (copying them by a kernel, for one).
+ * The packed bytes do not say what they hold: a call gives the code, group and shape that
+ * they were packed with.
  * Pointers are 16-byte aligned, where no other alignment is given (status words, factors,
  * indexes: 4 bytes).  A workspace is 256-byte aligned and holds nothing between calls;
  * calls that may run at once, captured graphs among them, need one each.
